@@ -255,6 +255,166 @@ LT_API lt_status latent_tail_forward_host(const uint16_t* routed_host,
                                           float eps, void* workspace, size_t workspace_bytes,
                                           lt_stream stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Operators around the tail in a latent-MoE block. The tail turns the experts'
+ * latent outputs into the block's output; these produce its routed operand and
+ * consume its result:
+ *
+ *   latent tokens -> latent_tail_dispatch -> experts (latent_tail_expert_matvec4)
+ *     -> latent_tail_combine -> routed partial -> latent_tail_forward
+ *     -> latent_tail_residual_norm -> the next block
+ *
+ * The conventions at the top of this file hold (device arrays, contiguous,
+ * 16-byte aligned, caller-owned, nothing launched on a non-OK status, outputs
+ * must not overlap inputs or one another unless stated). Arrays that a device
+ * kernel indexes by (expert ids, positions, offsets) are bounds-checked on the
+ * device: a value out of range never leads to an access out of range. Results
+ * are the same bits from run to run.
+ */
+
+/*
+ * Bytes of device workspace latent_tail_dispatch needs for T tokens with K
+ * choices among E experts: 0 where one kernel does the whole call (up to 2048
+ * choices), else the per-chunk expert counts. Returns 0 for T <= 0 or invalid
+ * shapes. Host-only.
+ */
+LT_API size_t latent_tail_dispatch_workspace_size(int T, int K, int E);
+
+/*
+ * Sorts the T * K choices of an expert router by expert and copies each token's
+ * row to its choices' places. With i = t * K + k the flat index of a choice,
+ * key(i) = ids[i] where 0 <= ids[i] < E and E otherwise (no expert: the choice
+ * is not routed), and row(i) the place of i when the choices are ordered by key
+ * and, within one key, by i:
+ *   order[row(i)]  = i
+ *   position[i]    = row(i) if routed, else -1 - row(i)
+ *   offsets[e]     = number of choices with key < e, e = 0 .. E (expert e owns
+ *                    rows offsets[e] .. offsets[e+1] - 1; offsets[E] rows in all)
+ *   rows[row(i),:] = x[t,:] if routed, else zero (the rows past offsets[E])
+ *   x [T, L] bf16, expert_ids [T, K] int32; rows [T*K, L] bf16, offsets [E+1],
+ *   order [T*K], position [T, K] int32 (outputs). x and rows may both be NULL:
+ *   the sort alone (L is then ignored).
+ * Limits: 1 <= K <= 64, 1 <= E <= 1024, T * K <= 2^24, L as for the tail.
+ * With T == 0 only offsets is written (zeros).
+ * The gradient of x is latent_tail_combine of the rows' gradients without weights.
+ */
+LT_API lt_status latent_tail_dispatch(const uint16_t* x, const int32_t* expert_ids,
+                                      uint16_t* rows, int32_t* offsets, int32_t* order,
+                                      int32_t* position, int T, int K, int E, int L,
+                                      void* workspace, size_t workspace_bytes,
+                                      lt_stream stream);
+
+/*
+ * Brings rows sorted by expert back to their tokens: out[t,:] = sum over the
+ * routed choices k, ascending, of weights[t,k] * rows[position[t,k],:] (FP32,
+ * rounded once to bf16). Choices with position outside [0, T*K) are skipped
+ * (their weights are not read into the sum); a token without a routed choice
+ * gives zeros.
+ *   rows [T*K, L] bf16, position [T, K] int32, weights [T, K] fp32 or NULL
+ *   (all 1), out [T, L] bf16 (e.g. one plane of the tail's routed operand).
+ */
+LT_API lt_status latent_tail_combine(const uint16_t* rows, const int32_t* position,
+                                     const float* weights, uint16_t* out, int T, int K, int L,
+                                     lt_stream stream);
+
+/*
+ * Gradient of latent_tail_combine: for each routed choice, with r = position[t,k],
+ *   grad_rows[r,:]    = weights[t,k] * grad_out[t,:]
+ *   grad_weights[t,k] = sum_l grad_out[t,l] * rows[r,l]      (FP32)
+ * and for each choice that is not routed (position = -1 - r, as
+ * latent_tail_dispatch writes it) grad_rows[r,:] = 0 and grad_weights[t,k] = 0.
+ * Every row of grad_rows is written when position comes from latent_tail_dispatch.
+ *   grad_out [T, L] bf16, rows [T*K, L] bf16, position [T, K], weights [T, K] fp32
+ *   or NULL (all 1); grad_rows [T*K, L] bf16, grad_weights [T, K] fp32 or NULL
+ *   (not wanted; rows is then not read and may be NULL too).
+ */
+LT_API lt_status latent_tail_combine_backward(const uint16_t* grad_out, const uint16_t* rows,
+                                              const int32_t* position, const float* weights,
+                                              uint16_t* grad_rows, float* grad_weights, int T,
+                                              int K, int L, lt_stream stream);
+
+/*
+ * Products of expert-sorted rows with 4-bit weights: for row r of expert e,
+ *   out[r,m] = sum_c x[r,c] * (q[e,m,c] - 8) * scales[e,m,c/G]
+ * with q[e,m,c] the 4-bit value in byte packed[e,m,c/2] (low four bits: even c),
+ * products and sums in FP32, rounded once to bf16. Meant for the few rows of
+ * decode steps, where reading the weights bounds the call: each matrix with rows
+ * is read once for up to 32 of them.
+ *   x [N, C] bf16, packed [E, M, C/2] bytes, scales [E, M, C/G] bf16,
+ *   offsets [E+1] int32 (rows of expert e: offsets[e] .. offsets[e+1]-1, as
+ *   latent_tail_dispatch writes it; rows from offsets[E] on give zeros) or NULL
+ *   with E == 1 (every row); out [N, M] bf16.
+ * Limits: 0 <= N <= 2^24, 1 <= E <= 1024, 8 <= M <= 1048576 with M % 8 == 0,
+ * G = 32, 64 or 128, C a multiple of G and at most 16384.
+ */
+LT_API lt_status latent_tail_expert_matvec4(const uint16_t* x, const uint8_t* packed,
+                                            const uint16_t* scales, const int32_t* offsets,
+                                            uint16_t* out, int N, int E, int M, int C, int G,
+                                            lt_stream stream);
+
+/* What the gate of latent_tail_residual_norm holds. */
+typedef enum lt_gate {
+  LT_GATE_NONE = 0,    /* no gate (gate == NULL): 1                */
+  LT_GATE_TOKEN = 1,   /* gate [T] fp32, one factor per token      */
+  LT_GATE_CHANNEL = 2, /* gate [H] fp32, one factor per channel    */
+  LT_GATE_FULL = 3     /* gate [T, H] bf16, one factor per element */
+} lt_gate;
+
+/* Type of the residual stream (residual, residual_out and their gradients). */
+typedef enum lt_residual {
+  LT_RESIDUAL_BF16 = 0,
+  LT_RESIDUAL_FP32 = 1
+} lt_residual;
+
+/*
+ * The norm after a block, its gate, the scaled residual sum and the norm before
+ * the next block in one pass, in FP32:
+ *   u[t,h]            = block[t,h] * rsqrt(mean_h block[t,h]^2 + eps) * post_weight[h]
+ *                       (block[t,h] itself when post_weight is NULL)
+ *   v[t,h]            = residual_scale * residual[t,h] + gate * u[t,h]
+ *   residual_out[t,h] = v rounded to the residual's type
+ *   next_out[t,h]     = bf16_rn(v[t,h] * rsqrt(mean_h v[t,h]^2 + eps) * next_weight[h])
+ *                       (not computed when next_weight and next_out are NULL; the
+ *                       norm takes v before its rounding)
+ *   block [T, H] bf16 (e.g. the tail's out), residual [T, H], post_weight and
+ *   next_weight [H] fp32 or NULL; residual_out may be exactly residual (in place).
+ * Limits: 8 <= H <= 16384, H % 8 == 0, 0 <= T <= 2^24; residual_scale finite.
+ */
+LT_API lt_status latent_tail_residual_norm(const uint16_t* block, const void* residual,
+                                           const float* post_weight, const void* gate,
+                                           const float* next_weight, void* residual_out,
+                                           uint16_t* next_out, int T, int H,
+                                           lt_gate gate_kind, lt_residual residual_type,
+                                           float residual_scale, float eps, lt_stream stream);
+
+/*
+ * Bytes of device workspace latent_tail_residual_norm_backward needs: the partial
+ * sums of the gradients that add up over tokens (post_weight, next_weight, a
+ * channel gate). The size covers every choice of optional arguments. Returns 0
+ * for T <= 0 or invalid shapes. Host-only.
+ */
+LT_API size_t latent_tail_residual_norm_backward_workspace_size(int T, int H);
+
+/*
+ * Gradient of latent_tail_residual_norm at its inputs, from the gradients of its
+ * outputs and the stored residual_out (which stands for v):
+ *   grad_residual_out [T, H] (residual's type) or NULL (zero), grad_next [T, H]
+ *   bf16 (given exactly when next_weight is; at least one of the two), block,
+ *   residual_out, post_weight, gate and next_weight as in the forward call;
+ *   grad_block [T, H] bf16, grad_residual [T, H] (residual's type),
+ *   grad_post_weight, grad_next_weight [H] fp32 (given exactly when the weight is),
+ *   grad_gate (shape and type of the gate; given exactly when the gate is).
+ * With T == 0 the gradients of the weights and of a channel gate are zeros.
+ */
+LT_API lt_status latent_tail_residual_norm_backward(
+    const void* grad_residual_out, const uint16_t* grad_next, const uint16_t* block,
+    const void* residual_out, const float* post_weight, const void* gate,
+    const float* next_weight, uint16_t* grad_block, void* grad_residual,
+    float* grad_post_weight, void* grad_gate, float* grad_next_weight, int T, int H,
+    lt_gate gate_kind, lt_residual residual_type, float residual_scale, float eps,
+    void* workspace, size_t workspace_bytes, lt_stream stream);
+
 /* Static, human-readable name of a status code. Never NULL. */
 LT_API const char* latent_tail_status_string(lt_status status);
 

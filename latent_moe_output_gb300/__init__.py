@@ -5,7 +5,8 @@
 
 The computation runs in the CUDA library built from ``csrc/`` and exposed
 through the C ABI in ``include/latent_tail.h``; ``binding`` is the thin ctypes
-layer over it. Importing this package does not load the library; the first
+layer over it, and ``block`` the same for the operators around the tail (expert
+dispatch and combine, 4-bit expert products, fused residual norms). Importing this package does not load the library; the first
 call does, and fails loudly if it was not built.
 """
 
@@ -25,4 +26,16 @@ from .binding import (  # noqa: F401
     latent_tail_workspace_size,
     library_path,
     load_library,
+)
+from .block import (  # noqa: F401
+    Dispatched,
+    combine,
+    combine_backward,
+    dispatch,
+    dispatch_workspace_size,
+    expert_matvec4,
+    quantize4,
+    residual_norm,
+    residual_norm_backward,
+    residual_norm_backward_workspace_size,
 )

@@ -59,6 +59,22 @@ _SIGNATURES = {
     "latent_tail_forward_host": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int] * 4
                                  + [ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t,
                                     ctypes.c_void_p]),
+    "latent_tail_dispatch_workspace_size": (ctypes.c_size_t, [ctypes.c_int] * 3),
+    "latent_tail_dispatch": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int] * 4
+                             + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "latent_tail_combine": (ctypes.c_int, [ctypes.c_void_p] * 4 + [ctypes.c_int] * 3
+                            + [ctypes.c_void_p]),
+    "latent_tail_combine_backward": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int] * 3
+                                     + [ctypes.c_void_p]),
+    "latent_tail_expert_matvec4": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int] * 5
+                                   + [ctypes.c_void_p]),
+    "latent_tail_residual_norm": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int] * 4
+                                  + [ctypes.c_float] * 2 + [ctypes.c_void_p]),
+    "latent_tail_residual_norm_backward_workspace_size": (ctypes.c_size_t, [ctypes.c_int] * 2),
+    "latent_tail_residual_norm_backward": (ctypes.c_int, [ctypes.c_void_p] * 12
+                                           + [ctypes.c_int] * 4 + [ctypes.c_float] * 2
+                                           + [ctypes.c_void_p, ctypes.c_size_t,
+                                              ctypes.c_void_p]),
     "latent_tail_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
 

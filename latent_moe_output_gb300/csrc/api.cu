@@ -4,12 +4,23 @@
 // kernels (the single-GPU counterpart of `_select_tail_tier` in PR #50383,
 // which picks the tail implementation from num_tokens alone).
 #include "latent_tail.h"
+#include "block_launch.h"
+#include "host_checks.h"
 #include "launch.h"
 
 #include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
+
+using lt::aligned16;
+using lt::check_ptrs;
+using lt::current_device;
+using lt::launch_status;
+using lt::overlaps;
+using lt::round256;
+using lt::Span;
+using lt::span;
 
 namespace {
 
@@ -69,36 +80,12 @@ lt_status init_device(int dev, DeviceSlot& slot) {
     g_ptr_attr = reinterpret_cast<PointerGetAttributeFn>(fn);
   }
   if (lt::setup_norm(d) != cudaSuccess || lt::setup_decode(d) != cudaSuccess ||
-      lt::setup_prefill(d) != cudaSuccess || lt::setup_gemv(d) != cudaSuccess)
+      lt::setup_prefill(d) != cudaSuccess || lt::setup_gemv(d) != cudaSuccess ||
+      lt::setup_dispatch(d) != cudaSuccess || lt::setup_matvec4(d) != cudaSuccess ||
+      lt::setup_residual_norm(d) != cudaSuccess)
     return LT_ERR_CUDA;
   return LT_OK;
 }
-
-// Per-device state of the current device; set up on first use.
-lt_status current_device(const lt::DeviceInfo** out) {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return LT_ERR_CUDA;
-  if (dev < 0 || dev >= kMaxDevices) return LT_ERR_UNSUPPORTED;
-  std::lock_guard<std::mutex> lock(g_mutex);
-  DeviceSlot& slot = g_devices[dev];
-  if (!slot.initialized) {
-    slot.status = init_device(dev, slot);
-    slot.initialized = true;
-  }
-  *out = &slot.info;
-  return slot.status;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Span {
-  uintptr_t lo, hi;
-};
-Span span(const void* p, size_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Span{a, a + bytes};
-}
-bool overlaps(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
 
 // out may be exactly one of the P shared partials (in-place beta-add): every
 // kernel reads all partials of an output element before writing it, and no
@@ -146,19 +133,7 @@ lt_status check_range(int H, int c0, int c1) {
   return LT_OK;
 }
 
-lt_status check_ptrs(std::initializer_list<const void*> ptrs) {
-  for (const void* p : ptrs)
-    if (p == nullptr) return LT_ERR_INVALID_ARG;
-  for (const void* p : ptrs)
-    if (!aligned16(p)) return LT_ERR_ALIGNMENT;
-  return LT_OK;
-}
-
 size_t latent_bytes(int T, int L) { return static_cast<size_t>(T) * L * 2; }
-
-size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
-
-lt_status launch_status(cudaError_t e) { return e == cudaSuccess ? LT_OK : LT_ERR_CUDA; }
 
 // Whether a call of T tokens at latent width L runs the decode kernel (else the
 // prefill kernel).
@@ -228,6 +203,20 @@ lt_status forward_impl(const uint16_t* routed, const uint16_t* shared, const flo
 }  // namespace
 
 namespace lt {
+
+lt_status current_device(const DeviceInfo** out) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return LT_ERR_CUDA;
+  if (dev < 0 || dev >= kMaxDevices) return LT_ERR_UNSUPPORTED;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  DeviceSlot& slot = g_devices[dev];
+  if (!slot.initialized) {
+    slot.status = init_device(dev, slot);
+    slot.initialized = true;
+  }
+  *out = &slot.info;
+  return slot.status;
+}
 
 bool make_map_bf16_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                          uint32_t box_rows) {

@@ -1,0 +1,115 @@
+// Library-internal host interface between the C-ABI layer (block_api.cu) and
+// the kernels of the operators around the tail. Not installed, not part of the ABI.
+#pragma once
+
+#include "launch.h"
+
+namespace lt {
+
+constexpr int kMaxChoices = 64;            // K
+constexpr int kMaxExperts = 1024;          // E
+constexpr int kMaxSlots = 1 << 24;         // T * K
+
+struct DispatchArgs {
+  const uint16_t* x;    // [T,L] or null (sort alone)
+  const int32_t* ids;   // [T,K]
+  uint16_t* rows;       // [T*K,L] or null
+  int32_t* offsets;     // [E+1]
+  int32_t* order;       // [T*K]
+  int32_t* position;    // [T,K]
+  int T, K, E, L;
+  uint16_t* counts;     // workspace: [chunks][counts_stride(E)]
+};
+
+// Up to this many choices one kernel sorts and copies (see dispatch.cu).
+constexpr int kDispatchOneLaunch = 2048;
+// Most chunks the choices of a larger call are cut into.
+constexpr int kDispatchMaxChunks = 304;
+// Counts per chunk: one per expert and one for choices without an expert,
+// padded to whole 16-byte vectors.
+constexpr int dispatch_counts_stride(int E) { return (E + 1 + 7) / 8 * 8; }
+
+struct CombineArgs {
+  const uint16_t* rows;     // [T*K,L]
+  const int32_t* position;  // [T,K]
+  const float* weights;     // [T,K] or null
+  uint16_t* out;            // [T,L]
+  int T, K, L;
+};
+
+struct CombineBackwardArgs {
+  const uint16_t* grad_out;  // [T,L]
+  const uint16_t* rows;      // [T*K,L] or null (no grad_weights)
+  const int32_t* position;   // [T,K]
+  const float* weights;      // [T,K] or null
+  uint16_t* grad_rows;       // [T*K,L]
+  float* grad_weights;       // [T,K] or null
+  int T, K, L;
+};
+
+struct Matvec4Args {
+  const uint16_t* x;       // [N,C]
+  const uint8_t* packed;   // [E,M,C/2]
+  const uint16_t* scales;  // [E,M,C/G]
+  const int32_t* offsets;  // [E+1] or null (E == 1)
+  uint16_t* out;           // [N,M]
+  int N, E, M, C, G;
+};
+
+enum GateKind { kGateNone = 0, kGateToken = 1, kGateChannel = 2, kGateFull = 3 };
+
+struct ResidualNormArgs {
+  const uint16_t* block;   // [T,H]
+  const void* residual;    // [T,H]
+  const float* post;       // [H] or null
+  const void* gate;        // by gate_kind, or null
+  const float* next;       // [H] or null
+  void* residual_out;      // [T,H]
+  uint16_t* next_out;      // [T,H] or null
+  int T, H;
+  int gate_kind;
+  bool residual_f32;
+  float scale, eps;
+};
+
+struct ResidualNormBackwardArgs {
+  const void* grad_residual_out;  // [T,H] or null
+  const uint16_t* grad_next;      // [T,H] or null
+  const uint16_t* block;          // [T,H]
+  const void* residual_out;       // [T,H]
+  const float* post;              // [H] or null
+  const void* gate;
+  const float* next;              // [H] or null
+  uint16_t* grad_block;           // [T,H]
+  void* grad_residual;            // [T,H]
+  float* grad_post;               // [H] or null
+  void* grad_gate;
+  float* grad_next_weight;        // [H] or null
+  int T, H;
+  int gate_kind;
+  bool residual_f32;
+  float scale, eps;
+  float* partials;                // workspace: [3][rows][H]
+};
+
+// Most partial rows the backward kernel writes per summed gradient.
+constexpr int kResidualNormMaxPartials = 304 * 8;
+// Rows of partial sums that a call of T tokens of width H may write (bounds the
+// workspace without knowing the device).
+int residual_norm_partial_rows(int T, int H);
+
+cudaError_t launch_dispatch(const DispatchArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_combine(const CombineArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_combine_backward(const CombineBackwardArgs& a, const DeviceInfo& dev,
+                                    cudaStream_t stream);
+cudaError_t launch_matvec4(const Matvec4Args& a, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_residual_norm(const ResidualNormArgs& a, const DeviceInfo& dev,
+                                 cudaStream_t stream);
+cudaError_t launch_residual_norm_backward(const ResidualNormBackwardArgs& a,
+                                          const DeviceInfo& dev, cudaStream_t stream);
+
+cudaError_t setup_dispatch(const DeviceInfo& dev);
+cudaError_t setup_matvec4(const DeviceInfo& dev);
+cudaError_t setup_residual_norm(const DeviceInfo& dev);
+
+}  // namespace lt

@@ -1,0 +1,62 @@
+// Small device helpers shared by the row-wise kernels: 8-element vectors in
+// FP32, warp and thread-group sums, programmatic-dependent launches.
+#pragma once
+
+#include "ptx.cuh"
+
+#include <utility>
+
+namespace lt {
+
+__device__ __forceinline__ float warp_sum_f(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// 16-byte load of data that this kernel may overwrite afterwards (an in-place
+// residual), so not through the read-only path.
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&a)[8]) {
+  a[0] = bf16_lo(v.x);
+  a[1] = bf16_hi(v.x);
+  a[2] = bf16_lo(v.y);
+  a[3] = bf16_hi(v.y);
+  a[4] = bf16_lo(v.z);
+  a[5] = bf16_hi(v.z);
+  a[6] = bf16_lo(v.w);
+  a[7] = bf16_hi(v.w);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&a)[8]) {
+  return make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                    pack_bf16x2(a[6], a[7]));
+}
+
+// One kernel launch as a programmatic dependent of the work before it on the
+// stream: the kernel may start early and must call pdl_wait() before it reads
+// or writes memory.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+}  // namespace lt
