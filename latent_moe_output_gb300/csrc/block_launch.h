@@ -47,6 +47,11 @@ struct CombineBackwardArgs {
   int T, K, L;
 };
 
+// 2-D map of bytes, row-major [rows, bytes], with a (128 x box_rows) box and 128-byte
+// swizzle. Returns false if the driver rejects it.
+bool make_map_u8_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t bytes,
+                       uint32_t box_rows);
+
 struct Matvec4Args {
   const uint16_t* x;       // [N,C]
   const uint8_t* packed;   // [E,M,C/2]
