@@ -5,14 +5,18 @@
 //            = sum_groups s[e,m,g] * ( sum_{c in g} x[r,c] * (q[e,m,c] - 8) )
 //
 // With the few rows per expert of a decode step the weights are read once and
-// used at most a few times, so their stream bounds the call; the work per weight
-// is the unpacking. A 4-bit value plus 128 is one bit operation away from a bf16
-// number (0x4300 | q = 128 + q), and 136 less is exactly q - 8, so the inner sums
-// run on the tensor cores with exact bf16 operands and FP32 accumulators: 16 weight
-// rows x 16 columns against 8 rows of x per instruction. These warp-level
-// instructions take their operands from registers, where the unpacked weights are;
-// the tcgen05 ones would need them written back to shared memory first, and at 8
-// to 32 rows the tensor rate does not matter. Scales multiply the FP32 group sums.
+// used at most a few times, so their stream bounds the call, and after it the
+// unpacking: at the measured copy rate an SM receives 41 weights per clock at
+// G = 32 and has 64 lanes per clock for logic operations.
+// A 4-bit value masked out at bit 0 or 4 of a bf16 pattern is that integer times
+// 2^-133 (subnormals and the first binade are one linear range), so one masking and
+// one exact bf16 fused multiply-add per two weights give (q - 8) / 64: five logic
+// operations for eight weights. The inner sums run on the tensor cores with these
+// exact operands and FP32 accumulators: 16 weight rows x 16 columns against 8 rows
+// of x per instruction. These warp-level instructions take their operands from
+// registers, where the unpacked weights are; the tcgen05 ones would need them
+// written back to shared memory first, and at 8 to 32 rows the tensor rate does not
+// matter. Scales multiply the FP32 group sums; the factor 64 is applied at the end.
 //
 // Layout of the work. A tile is kRows = 128 / kSplit weight rows of one expert,
 // against up to 8 * kTiles rows of x (a pass). The CTAs walk over the tiles of
@@ -20,9 +24,10 @@
 // One warp streams weights and x through a ring of stages with TMA: a stage holds
 // kSplit boxes of 256 columns (kRows x 128 bytes of weights, swizzled so that the
 // eight rows of a fragment lie in different banks, and 8 * kTiles rows of x). The
-// eight other warps each own 16 weight rows and one of the kSplit column parts of
-// every stage; the parts are added in order through shared memory at the end of a
-// tile. kSplit = 4 gives enough tiles to fill the GPU from one matrix.
+// eight other warps each own 32 weight rows and half of one box's columns (a
+// fragment of x then serves two of weights); the 2 * kSplit column parts are added
+// in order through shared memory at the end of a tile. kSplit = 4 gives enough tiles
+// to fill the GPU from one matrix.
 #include "block_launch.h"
 #include "rows.cuh"
 
@@ -35,21 +40,20 @@ constexpr int kConsumers = 8;  // warps
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kBoxCols = 256;  // columns per box: 128 bytes of weights
 constexpr int kMaxStages = 8;
-constexpr int kSmemBudget = 102 * 1024;  // dynamic, two CTAs per SM
+constexpr int kSmemPerSm = 204 * 1024;  // dynamic
 
 template <int kSplit, int kTiles>
 struct Config {
   static constexpr int kRows = 128 / kSplit;
+  static constexpr int kCtasPerSm = kTiles == 4 ? 1 : 2;  // four need more than 96 registers
   static constexpr int kWeightBytes = 128 * 128;
   static constexpr int kXBoxBytes = 8 * 128;  // 8 rows x 64 columns
   static constexpr int kStageBytes = kWeightBytes + kSplit * kTiles * 4 * kXBoxBytes;
-  // Column parts 1.. of a tile's sums, double-buffered.
-  static constexpr int kSumFloats = (kSplit - 1) * kRows * 8 * kTiles;
-  static constexpr int kSumBytes = 2 * kSumFloats * 4;
-  static constexpr int kStages =
-      (kSmemBudget - kSumBytes - 1024) / kStageBytes > kMaxStages
-          ? kMaxStages
-          : (kSmemBudget - kSumBytes - 1024) / kStageBytes;
+  static constexpr int kParts = 2 * kSplit;
+  // Column parts 1.. of a tile's sums.
+  static constexpr int kSumBytes = (kParts - 1) * kRows * 8 * kTiles * 4;
+  static constexpr int kFit = (kSmemPerSm / kCtasPerSm - kSumBytes - 1024) / kStageBytes;
+  static constexpr int kStages = kFit > kMaxStages ? kMaxStages : kFit;
   static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes + kSumBytes + 1024;
   static_assert(kStages >= 2, "a ring needs two stages");
 };
@@ -76,21 +80,27 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
-// Values i and i + 4 of the eight in w, minus 8, as two bf16 numbers (exact).
-__device__ __forceinline__ uint32_t weight_pair(uint32_t w, int i) {
-  const uint32_t biased = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;  // 128 + q
+// Two of the eight values of a word, in the low four bits of each half (kHigh
+// false) or the four bits above them: (q - 8) / 64 as two bf16 numbers, exact.
+template <bool kHigh>
+__device__ __forceinline__ uint32_t weight_pair(uint32_t w) {
+  const uint32_t bits = w & (kHigh ? 0x00F000F0u : 0x000F000Fu);  // q * 2^-133 (* 16)
   uint32_t v;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(biased), "r"(0x43084308u));  // - 136
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+      : "=r"(v)
+      : "r"(bits), "r"(kHigh ? 0x7D007D00u : 0x7F007F00u),  // 2^123, 2^127
+        "r"(0xBE00BE00u));                                  // -8 / 64
   return v;
 }
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1, const float (&c)[4]) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+        "f"(c[2]), "f"(c[3]));
 }
 
 __device__ __forceinline__ void consumer_barrier() {
@@ -123,7 +133,7 @@ __device__ __forceinline__ Tile tile_at(int64_t tile, int mblocks, int rows_per_
 }
 
 template <int kGroup, int kSplit, int kTiles>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
     matvec4_kernel(const __grid_constant__ CUtensorMap w_map,
                    const __grid_constant__ CUtensorMap x_map, const Params p) {
   using Cfg = Config<kSplit, kTiles>;
@@ -234,8 +244,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   } else {
-    const int part = warp / (kConsumers / kSplit);       // column part of every stage
-    const int mrow = warp % (kConsumers / kSplit) * 16;  // first weight row in the tile
+    constexpr int kRowWarps = Cfg::kRows / 32;
+    constexpr int kHalf = kScales / 2;              // scales per row and half box
+    constexpr int kWords = (kHalf + 1) / 2;
+    const int part = warp / kRowWarps;              // column part of every stage
+    const int box_in = part >> 1, half = part & 1;  // its box and half
+    const int mrow = warp % kRowWarps * 32;         // first weight row in the tile
     const int g = lane >> 2, c4 = lane & 3;
     // Column n of a fragment holds row (n >> 1) + 4 (n & 1) of the eight: lanes of
     // one quarter of the warp then read different halves of the swizzled rows.
@@ -243,144 +257,165 @@ __global__ void __launch_bounds__(kThreads, 2)
     float* sums = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) +
                                            Cfg::kStages * Cfg::kStageBytes);
     const int pitch = p.C / kGroup;  // scales per row
-    const bool vec = pitch % kScales == 0;
+    const bool vec = pitch % kHalf == 0;
     uint32_t it = 0;
     bool ok = true;
-    int parity = 0;
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
       const Tile t = tile_at(tile, mblocks, Cfg::kRows, kPass, s_first, s_unit, p.E);
-      const int n_tiles = (t.rows + 7) / 8;
-      const uint16_t* srow[2];
+      const int n_tiles = kTiles == 1 ? 1 : (t.rows + 7) / 8;
+      const uint16_t* stile = p.scales + (static_cast<size_t>(t.e) * p.M + t.m0) * pitch;
+      int srow[4];  // weight rows mrow + g + 8 h
 #pragma unroll
-      for (int h = 0; h < 2; ++h)  // (rows past the matrix are read from its last row)
-        srow[h] = p.scales + (static_cast<size_t>(t.e) * p.M +
-                              min(p.M - 1, t.m0 + mrow + g + h * 8)) * pitch;
-      // Scales of one box: kScales per row, two per register.
-      auto load_scales = [&](int box, uint32_t (&sc)[2][kScales / 2]) {
-        const int first = box * kScales;
+      for (int h = 0; h < 4; ++h)  // (rows past the matrix are read from its last row)
+        srow[h] = min(p.M - 1 - t.m0, mrow + g + h * 8) * pitch;
+      // Scales of half a box: kHalf per row, two per register.
+      auto load_scales = [&](int box, uint32_t (&sc)[4][kWords]) {
+        const int first = box * kScales + half * kHalf;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 4; ++h) {
           if (vec) {
             if (first < pitch) {
-              if constexpr (kScales == 8) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(srow[h] + first));
-                sc[h][0] = v.x; sc[h][1] = v.y; sc[h][2] = v.z; sc[h][3] = v.w;
-              } else if constexpr (kScales == 4) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(srow[h] + first));
+              if constexpr (kHalf == 4) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(stile + srow[h] + first));
                 sc[h][0] = v.x; sc[h][1] = v.y;
+              } else if constexpr (kHalf == 2) {
+                sc[h][0] = __ldg(reinterpret_cast<const uint32_t*>(stile + srow[h] + first));
               } else {
-                sc[h][0] = __ldg(reinterpret_cast<const uint32_t*>(srow[h] + first));
+                sc[h][0] = __ldg(stile + srow[h] + first);
               }
             }
           } else {
 #pragma unroll
-            for (int q = 0; q < kScales / 2; ++q) {
-              const uint32_t a = first + 2 * q < pitch ? __ldg(srow[h] + first + 2 * q) : 0;
-              const uint32_t b = first + 2 * q + 1 < pitch ? __ldg(srow[h] + first + 2 * q + 1) : 0;
+            for (int q = 0; q < kWords; ++q) {
+              const uint32_t a = first + 2 * q < pitch ? __ldg(stile + srow[h] + first + 2 * q) : 0;
+              const uint32_t b = first + 2 * q + 1 < pitch ? __ldg(stile + srow[h] + first + 2 * q + 1) : 0;
               sc[h][q] = a | (b << 16);
             }
           }
         }
       };
-      float total[kTiles][4];
+      float total[2][kTiles][4];
 #pragma unroll
       for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) total[n][j] = 0.f;
+        for (int j = 0; j < 4; ++j) total[0][n][j] = total[1][n][j] = 0.f;
 
-      uint32_t next[2][kScales / 2] = {};
-      load_scales(part, next);
+      uint32_t next[4][kWords] = {};
+      load_scales(box_in, next);
       for (int i = 0; i < steps; ++i, ++it) {
-        uint32_t sc[2][kScales / 2];
+        uint32_t sc[4][kWords];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 4; ++h)
 #pragma unroll
-          for (int q = 0; q < kScales / 2; ++q) sc[h][q] = next[h][q];
-        if (i + 1 < steps) load_scales((i + 1) * kSplit + part, next);
+          for (int q = 0; q < kWords; ++q) sc[h][q] = next[h][q];
+        if (i + 1 < steps) load_scales((i + 1) * kSplit + box_in, next);
         const uint32_t s = it % Cfg::kStages;
         if (ok) ok = mbar_wait(smem_u32(&full_bar[s]), (it / Cfg::kStages) & 1u, p.err, abort_v);
-        const int box = i * kSplit + part;
-        if (ok && box < boxes) {
-          const uint32_t st = ring + s * Cfg::kStageBytes;
-          const uint32_t wa = st + part * Cfg::kRows * 128 + (mrow + g) * 128 + c4 * 4;
-          const uint32_t xa = st + Cfg::kWeightBytes + part * kTiles * 4 * Cfg::kXBoxBytes +
-                              xrow * 128;
-          const int runs = min(8, (p.C - box * kBoxCols) / 32);  // runs of 32 columns
-          float acc[kTiles][4];
+        const int box = i * kSplit + box_in;
+        // Runs of 32 columns in this half box.
+        const int runs = min(4, (p.C - box * kBoxCols) / 32 - half * 4);
+        const uint32_t st = ring + s * Cfg::kStageBytes;
+        const uint32_t wa = st + box_in * Cfg::kRows * 128 + (mrow + g) * 128 + c4 * 4;
+        const uint32_t xa =
+            st + Cfg::kWeightBytes + box_in * kTiles * 4 * Cfg::kXBoxBytes + xrow * 128;
+        float acc[2][kTiles][4];
+        auto run = [&](int j) {  // j: run in the half box, known at compile time
+          constexpr int kRunsPerGroup = kGroup / 32;
+          const bool opens = j % kRunsPerGroup == 0, closes = (j + 1) % kRunsPerGroup == 0;
+          const int chunk = half * 4 + j;
+          uint32_t lo[2][4], hi[2][4];  // fragments: values 0, 1, 4, 5 and 2, 3, 6, 7
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (j >= runs) break;
-            constexpr int kRunsPerGroup = kGroup / 32;
-            const uint32_t w0 = lds32(wa + ((j ^ g) << 4));
-            const uint32_t w1 = lds32(wa + 8 * 128 + ((j ^ g) << 4));
-            uint32_t a0[4], a1[4];
+          for (int m = 0; m < 2; ++m) {
+            const uint32_t at = wa + m * 16 * 128 + ((chunk ^ g) << 4);
+            const uint32_t w0 = lds32(at), w1 = lds32(at + 8 * 128);
+            lo[m][0] = weight_pair<false>(w0);
+            lo[m][1] = weight_pair<false>(w1);
+            lo[m][2] = weight_pair<true>(w0);
+            lo[m][3] = weight_pair<true>(w1);
+            hi[m][0] = weight_pair<false>(w0 >> 8);
+            hi[m][1] = weight_pair<false>(w1 >> 8);
+            hi[m][2] = weight_pair<true>(w0 >> 8);
+            hi[m][3] = weight_pair<true>(w1 >> 8);
+          }
+          const float zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              a0[q] = weight_pair(w0, q);
-              a1[q] = weight_pair(w1, q);
-            }
+          for (int n = 0; n < kTiles; ++n) {
+            if (kTiles > 1 && n >= n_tiles) break;
+            const uint4 v = lds128(xa + (n * 4 + (chunk >> 1)) * Cfg::kXBoxBytes +
+                                   ((((chunk & 1) * 4 + c4) ^ xrow) << 4));
+            const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410), b1 = __byte_perm(v.x, v.z, 0x7632);
+            const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410), b3 = __byte_perm(v.y, v.w, 0x7632);
 #pragma unroll
-            for (int n = 0; n < kTiles; ++n) {
-              if (n >= n_tiles) break;
-              if (j % kRunsPerGroup == 0) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-              const uint4 v = lds128(xa + (n * 4 + (j >> 1)) * Cfg::kXBoxBytes +
-                                     ((((j & 1) * 4 + c4) ^ xrow) << 4));
-              mma_bf16(acc[n], a0[0], a1[0], a0[1], a1[1], __byte_perm(v.x, v.z, 0x5410),
-                       __byte_perm(v.x, v.z, 0x7632));
-              mma_bf16(acc[n], a0[2], a1[2], a0[3], a1[3], __byte_perm(v.y, v.w, 0x5410),
-                       __byte_perm(v.y, v.w, 0x7632));
-              if (j % kRunsPerGroup == kRunsPerGroup - 1) {
-                constexpr int kShift = kRunsPerGroup;
-                const int q = j / kShift;
-                const float s0 = (q & 1) ? bf16_hi(sc[0][q >> 1]) : bf16_lo(sc[0][q >> 1]);
-                const float s1 = (q & 1) ? bf16_hi(sc[1][q >> 1]) : bf16_lo(sc[1][q >> 1]);
-                total[n][0] = fmaf(s0, acc[n][0], total[n][0]);
-                total[n][1] = fmaf(s0, acc[n][1], total[n][1]);
-                total[n][2] = fmaf(s1, acc[n][2], total[n][2]);
-                total[n][3] = fmaf(s1, acc[n][3], total[n][3]);
+            for (int m = 0; m < 2; ++m) {
+              if (opens)
+                mma_bf16(acc[m][n], lo[m], b0, b1, zero);
+              else
+                mma_bf16(acc[m][n], lo[m], b0, b1, acc[m][n]);
+              mma_bf16(acc[m][n], hi[m], b2, b3, acc[m][n]);
+              if (closes) {
+                const int q = j / kRunsPerGroup;
+                const uint32_t u0 = sc[2 * m][q >> 1], u1 = sc[2 * m + 1][q >> 1];
+                const float s0 = (q & 1) ? bf16_hi(u0) : bf16_lo(u0);
+                const float s1 = (q & 1) ? bf16_hi(u1) : bf16_lo(u1);
+                total[m][n][0] = fmaf(s0, acc[m][n][0], total[m][n][0]);
+                total[m][n][1] = fmaf(s0, acc[m][n][1], total[m][n][1]);
+                total[m][n][2] = fmaf(s1, acc[m][n][2], total[m][n][2]);
+                total[m][n][3] = fmaf(s1, acc[m][n][3], total[m][n][3]);
               }
             }
           }
+        };
+        if (ok && runs == 4) {
+          run(0);
+          run(1);
+          run(2);
+          run(3);
+        } else if (ok && runs > 0) {  // (whole groups: C is a multiple of the group)
+          run(0);
+          if (runs > 1) run(1);
+          if (runs > 2) run(2);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&empty_bar[s]));
       }
 
+      // The column parts of a row are added in order by part 0's warp.
+      consumer_barrier();  // the last tile's sums have been read
+      constexpr int kPerWarp = 32 * 8 * kTiles;
+      if (part > 0) {
+        float* dst = sums + ((part - 1) * kRowWarps + warp % kRowWarps) * kPerWarp + lane;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dst[((m * kTiles + n) * 4 + j) * 32] = total[m][n][j];
+      }
+      consumer_barrier();
+      if (part > 0) continue;
+      for (int q = 0; q < Cfg::kParts - 1; ++q) {
+        const float* src = sums + (q * kRowWarps + warp) * kPerWarp + lane;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) total[m][n][j] += src[((m * kTiles + n) * 4 + j) * 32];
+      }
       // Element (j, lane) of a fragment: weight row g + 8 (j >> 1), column
       // 2 c4 + (j & 1), i.e. row c4 + 4 (j & 1) of x.
-      if constexpr (kSplit > 1) {
-        float* buf = sums + parity * Cfg::kSumFloats;
-        parity ^= 1;
-        if (part > 0) {
-          float* dst = buf + ((part - 1) * Cfg::kRows + mrow) * kPass;
 #pragma unroll
-          for (int n = 0; n < kTiles; ++n)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dst[(n * 4 + j) * 32 + lane] = total[n][j];
-        }
-        // One barrier per tile: the buffer of the tile before last is read by part
-        // 0 before it arrives here for the last one.
-        consumer_barrier();
-        if (part > 0) continue;
+        for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-        for (int q = 1; q < kSplit; ++q) {
-          const float* src = buf + ((q - 1) * Cfg::kRows + mrow) * kPass;
-#pragma unroll
-          for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) total[n][j] += src[(n * 4 + j) * 32 + lane];
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int m = t.m0 + mrow + g + (j >> 1) * 8;
-          const int r = n * 8 + c4 + (j & 1) * 4;
-          if (m < p.M && r < t.rows)
-            p.out[static_cast<size_t>(t.row0 + r) * p.M + m] =
-                static_cast<uint16_t>(pack_bf16x2(total[n][j], 0.f) & 0xffffu);
-        }
+          for (int j = 0; j < 4; ++j) {
+            const int col = t.m0 + mrow + m * 16 + g + (j >> 1) * 8;
+            const int r = n * 8 + c4 + (j & 1) * 4;
+            if (col < p.M && r < t.rows)
+              p.out[static_cast<size_t>(t.row0 + r) * p.M + col] =
+                  static_cast<uint16_t>(pack_bf16x2(64.f * total[m][n][j], 0.f) & 0xffffu);
+          }
     }
     // Rows that no expert owns.
     const int mvec = p.M / 8;
@@ -396,13 +431,13 @@ typedef void (*Kernel)(const CUtensorMap, const CUtensorMap, const Params);
 struct Variant {
   Kernel kernel;
   size_t smem;
-  int rows;
+  int rows, ctas_per_sm;
 };
 
 template <int kGroup, int kSplit, int kTiles>
 Variant variant() {
   return Variant{matvec4_kernel<kGroup, kSplit, kTiles>, Config<kSplit, kTiles>::kSmem,
-                 Config<kSplit, kTiles>::kRows};
+                 Config<kSplit, kTiles>::kRows, Config<kSplit, kTiles>::kCtasPerSm};
 }
 
 template <int kGroup>
@@ -446,7 +481,7 @@ cudaError_t launch_matvec4(const Matvec4Args& a, const DeviceInfo& dev, cudaStre
     return cudaErrorInvalidValue;
   const int64_t most = (static_cast<int64_t>(matrices) + a.N / 8 + 1) *
                        ((a.M + v.rows - 1) / v.rows);
-  const int grid = static_cast<int>(std::min<int64_t>(2 * dev.num_sms, most));
+  const int grid = static_cast<int>(std::min<int64_t>(v.ctas_per_sm * dev.num_sms, most));
   const Params p{a.scales, a.offsets, a.out, a.N, a.E, a.M, a.C, dev.err_word};
   return launch_dependent(v.kernel, dim3(grid), dim3(kThreads), v.smem, stream, w_map, x_map, p);
 }
