@@ -218,16 +218,17 @@ lt_status current_device(const DeviceInfo** out) {
   return slot.status;
 }
 
-bool make_map_u8_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t bytes,
-                       uint32_t box_rows) {
+bool make_map_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t bytes,
+                 uint32_t box_bytes, uint32_t box_rows) {
   if (g_encode == nullptr) return false;
   const cuuint64_t dims[2] = {bytes, rows};
   const cuuint64_t strides[1] = {bytes};
-  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t box[2] = {box_bytes, box_rows};
   const cuuint32_t estrides[2] = {1, 1};
   const CUresult r =
       g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
-               estrides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               estrides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }

@@ -47,10 +47,10 @@ struct CombineBackwardArgs {
   int T, K, L;
 };
 
-// 2-D map of bytes, row-major [rows, bytes], with a (128 x box_rows) box and 128-byte
-// swizzle. Returns false if the driver rejects it.
-bool make_map_u8_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t bytes,
-                       uint32_t box_rows);
+// 2-D map of bytes, row-major [rows, bytes], with a (box_bytes x box_rows) box: 128
+// bytes with 128-byte swizzle, else none. Returns false if the driver rejects it.
+bool make_map_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t bytes,
+                 uint32_t box_bytes, uint32_t box_rows);
 
 struct Matvec4Args {
   const uint16_t* x;       // [N,C]

@@ -23,7 +23,7 @@
 // the experts that have rows (found from the offsets at the start of the kernel).
 // One warp streams weights and x through a ring of stages with TMA: a stage holds
 // kSplit boxes of 256 columns (kRows x 128 bytes of weights, swizzled so that the
-// eight rows of a fragment lie in different banks, and 8 * kTiles rows of x). The
+// eight rows of a fragment lie in different banks, 8 * kTiles rows of x, the scales). The
 // eight other warps each own 32 weight rows and half of one box's columns (a
 // fragment of x then serves two of weights); the 2 * kSplit column parts are added
 // in order through shared memory at the end of a tile. kSplit = 4 gives enough tiles
@@ -48,7 +48,9 @@ struct Config {
   static constexpr int kCtasPerSm = kTiles == 4 ? 1 : 2;  // four need more than 96 registers
   static constexpr int kWeightBytes = 128 * 128;
   static constexpr int kXBoxBytes = 8 * 128;  // 8 rows x 64 columns
-  static constexpr int kStageBytes = kWeightBytes + kSplit * kTiles * 4 * kXBoxBytes;
+  static constexpr int kXBytes = kSplit * kTiles * 4 * kXBoxBytes;
+  static constexpr int kScaleBytes = 128 * 16;  // eight scales per row and box
+  static constexpr int kStageBytes = kWeightBytes + kXBytes + kScaleBytes;
   static constexpr int kParts = 2 * kSplit;
   // Column parts 1.. of a tile's sums.
   static constexpr int kSumBytes = (kParts - 1) * kRows * 8 * kTiles * 4;
@@ -63,12 +65,25 @@ struct Params {
   const int32_t* offsets;
   uint16_t* out;
   int N, E, M, C;
+  bool staged_scales;  // the scales come through the ring (their rows are whole 16-byte pieces)
   uint32_t* err;
 };
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
 
@@ -135,7 +150,8 @@ __device__ __forceinline__ Tile tile_at(int64_t tile, int mblocks, int rows_per_
 template <int kGroup, int kSplit, int kTiles>
 __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
     matvec4_kernel(const __grid_constant__ CUtensorMap w_map,
-                   const __grid_constant__ CUtensorMap x_map, const Params p) {
+                   const __grid_constant__ CUtensorMap x_map,
+                   const __grid_constant__ CUtensorMap s_map, const Params p) {
   using Cfg = Config<kSplit, kTiles>;
   constexpr int kPass = 8 * kTiles;
   constexpr int kScales = kBoxCols / kGroup;  // per row and box
@@ -220,10 +236,14 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
           const uint32_t bar = smem_u32(&full_bar[s]);
           const uint32_t st = ring + s * Cfg::kStageBytes;
           mbar_arrive_expect_tx(bar, static_cast<uint32_t>(live) *
-                                         (Cfg::kRows * 128 + n_tiles * 4 * Cfg::kXBoxBytes));
+                                         (Cfg::kRows * (p.staged_scales ? 144 : 128) +
+                                          n_tiles * 4 * Cfg::kXBoxBytes));
           for (int j = 0; j < live; ++j) {
             const int c0 = (i * kSplit + j) * kBoxCols;
             tma_load_2d(st + j * Cfg::kRows * 128, &w_map, bar, c0 / 2, t.e * p.M + t.m0);
+            if (p.staged_scales)  // whole 16-byte pieces, from the one that holds the box's first
+              tma_load_2d(st + Cfg::kWeightBytes + Cfg::kXBytes + j * Cfg::kRows * 16, &s_map, bar,
+                          (c0 / kGroup & ~7) * 2, t.e * p.M + t.m0);
             const uint32_t xs = st + Cfg::kWeightBytes + j * kTiles * 4 * Cfg::kXBoxBytes;
             for (int n = 0; n < n_tiles; ++n)
 #pragma unroll
@@ -257,7 +277,6 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
     float* sums = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) +
                                            Cfg::kStages * Cfg::kStageBytes);
     const int pitch = p.C / kGroup;  // scales per row
-    const bool vec = pitch % kHalf == 0;
     uint32_t it = 0;
     bool ok = true;
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -268,47 +287,13 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
 #pragma unroll
       for (int h = 0; h < 4; ++h)  // (rows past the matrix are read from its last row)
         srow[h] = min(p.M - 1 - t.m0, mrow + g + h * 8) * pitch;
-      // Scales of half a box: kHalf per row, two per register.
-      auto load_scales = [&](int box, uint32_t (&sc)[4][kWords]) {
-        const int first = box * kScales + half * kHalf;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          if (vec) {
-            if (first < pitch) {
-              if constexpr (kHalf == 4) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(stile + srow[h] + first));
-                sc[h][0] = v.x; sc[h][1] = v.y;
-              } else if constexpr (kHalf == 2) {
-                sc[h][0] = __ldg(reinterpret_cast<const uint32_t*>(stile + srow[h] + first));
-              } else {
-                sc[h][0] = __ldg(stile + srow[h] + first);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < kWords; ++q) {
-              const uint32_t a = first + 2 * q < pitch ? __ldg(stile + srow[h] + first + 2 * q) : 0;
-              const uint32_t b = first + 2 * q + 1 < pitch ? __ldg(stile + srow[h] + first + 2 * q + 1) : 0;
-              sc[h][q] = a | (b << 16);
-            }
-          }
-        }
-      };
       float total[2][kTiles][4];
 #pragma unroll
       for (int n = 0; n < kTiles; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) total[0][n][j] = total[1][n][j] = 0.f;
 
-      uint32_t next[4][kWords] = {};
-      load_scales(box_in, next);
       for (int i = 0; i < steps; ++i, ++it) {
-        uint32_t sc[4][kWords];
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-#pragma unroll
-          for (int q = 0; q < kWords; ++q) sc[h][q] = next[h][q];
-        if (i + 1 < steps) load_scales((i + 1) * kSplit + box_in, next);
         const uint32_t s = it % Cfg::kStages;
         if (ok) ok = mbar_wait(smem_u32(&full_bar[s]), (it / Cfg::kStages) & 1u, p.err, abort_v);
         const int box = i * kSplit + box_in;
@@ -318,6 +303,32 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
         const uint32_t wa = st + box_in * Cfg::kRows * 128 + (mrow + g) * 128 + c4 * 4;
         const uint32_t xa =
             st + Cfg::kWeightBytes + box_in * kTiles * 4 * Cfg::kXBoxBytes + xrow * 128;
+        // Scales of half a box: kHalf per row, two per register.
+        uint32_t sc[4][kWords] = {};
+        if (p.staged_scales) {
+          const uint32_t sa = st + Cfg::kWeightBytes + Cfg::kXBytes +
+                              (box_in * Cfg::kRows + mrow + g) * 16 +
+                              ((box * kScales & 7) + half * kHalf) * 2;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            if constexpr (kHalf == 4) {
+              const uint2 v = lds64(sa + h * 128);
+              sc[h][0] = v.x;
+              sc[h][1] = v.y;
+            } else {
+              sc[h][0] = kHalf == 2 ? lds32(sa + h * 128) : lds16(sa + h * 128);
+            }
+          }
+        } else if (ok && runs > 0) {
+          const int first = box * kScales + half * kHalf;
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int q = 0; q < kHalf; ++q)
+              if (first + q < pitch)
+                sc[h][q >> 1] |= static_cast<uint32_t>(__ldg(stile + srow[h] + first + q))
+                                 << (16 * (q & 1));
+        }
         float acc[2][kTiles][4];
         auto run = [&](int j) {  // j: run in the half box, known at compile time
           constexpr int kRunsPerGroup = kGroup / 32;
@@ -426,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
   }
 }
 
-typedef void (*Kernel)(const CUtensorMap, const CUtensorMap, const Params);
+typedef void (*Kernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const Params);
 
 struct Variant {
   Kernel kernel;
@@ -475,15 +486,24 @@ cudaError_t launch_matvec4(const Matvec4Args& a, const DeviceInfo& dev, cudaStre
   const int64_t large = static_cast<int64_t>(matrices) * ((a.M + 127) / 128);
   const int split = tiles <= 2 && large < 4 * dev.num_sms ? 2 : 1;
   const Variant v = pick(a.G, split, tiles);
-  CUtensorMap w_map, x_map;
-  if (!make_map_u8_sw128(&w_map, a.packed, static_cast<uint64_t>(a.E) * a.M, a.C / 2, v.rows) ||
+  const uint64_t rows = static_cast<uint64_t>(a.E) * a.M;
+  const uint64_t pitch = static_cast<uint64_t>(a.C / a.G) * 2;
+  const bool staged = pitch % 16 == 0;
+  CUtensorMap w_map, x_map, s_map;
+  if (!make_map_u8(&w_map, a.packed, rows, a.C / 2, 128, v.rows) ||
       !make_map_bf16_sw128(&x_map, a.x, a.N, a.C, 8))
+    return cudaErrorInvalidValue;
+  if (!staged)
+    s_map = w_map;  // not used
+  else if (!make_map_u8(&s_map, a.scales, rows, pitch, 16, v.rows))
     return cudaErrorInvalidValue;
   const int64_t most = (static_cast<int64_t>(matrices) + a.N / 8 + 1) *
                        ((a.M + v.rows - 1) / v.rows);
   const int grid = static_cast<int>(std::min<int64_t>(v.ctas_per_sm * dev.num_sms, most));
-  const Params p{a.scales, a.offsets, a.out, a.N, a.E, a.M, a.C, dev.err_word};
-  return launch_dependent(v.kernel, dim3(grid), dim3(kThreads), v.smem, stream, w_map, x_map, p);
+  const Params p{a.scales, a.offsets, a.out, a.N, a.E, a.M, a.C, staged,
+                 dev.err_word};
+  return launch_dependent(v.kernel, dim3(grid), dim3(kThreads), v.smem, stream, w_map, x_map,
+                          s_map, p);
 }
 
 }  // namespace lt
