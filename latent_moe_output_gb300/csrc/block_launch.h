@@ -52,6 +52,12 @@ struct CombineBackwardArgs {
 bool make_map_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t bytes,
                  uint32_t box_bytes, uint32_t box_rows);
 
+// 3-D map of a row-major bf16 [rows, cols] array, cols a multiple of 64, as
+// (64 columns, rows, 64-column chunks): one box brings box_chunks chunks of box_rows
+// rows, each chunk a 128-byte-swizzled block. Returns false if the driver rejects it.
+bool make_map_bf16_rows64(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                          uint32_t box_rows, uint32_t box_chunks);
+
 struct Matvec4Args {
   const uint16_t* x;       // [N,C]
   const uint8_t* packed;   // [E,M,C/2]

@@ -40,12 +40,13 @@ constexpr int kConsumers = 8;  // warps
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kBoxCols = 256;  // columns per box: 128 bytes of weights
 constexpr int kMaxStages = 8;
-constexpr int kSmemPerSm = 204 * 1024;  // dynamic
+constexpr int kSmemPerSm = 204 * 1024;  // dynamic, without the experts' table
+constexpr int table_bytes(int E) { return (E + 1) * 2 * static_cast<int>(sizeof(int)); }
 
 template <int kSplit, int kTiles>
 struct Config {
   static constexpr int kRows = 128 / kSplit;
-  static constexpr int kCtasPerSm = kTiles == 4 ? 1 : 2;  // four need more than 96 registers
+  static constexpr int kCtasPerSm = kTiles == 4 ? 1 : 2;  // registers: 96 at two
   static constexpr int kWeightBytes = 128 * 128;
   static constexpr int kXBoxBytes = 8 * 128;  // 8 rows x 64 columns
   static constexpr int kXBytes = kSplit * kTiles * 4 * kXBoxBytes;
@@ -66,6 +67,7 @@ struct Params {
   uint16_t* out;
   int N, E, M, C;
   bool staged_scales;  // the scales come through the ring (their rows are whole 16-byte pieces)
+  bool x_chunks;       // x has whole 64-column chunks: one copy brings a box's four
   uint32_t* err;
 };
 
@@ -130,7 +132,9 @@ struct Tile {
 __device__ __forceinline__ Tile tile_at(int64_t tile, int mblocks, int rows_per_tile,
                                         int rows_per_pass, const int* s_first,
                                         const int* s_unit, int E) {
-  const int unit = static_cast<int>(tile / mblocks);
+  // (a 64-bit division costs as much as the rest of this function)
+  const int unit = tile >> 32 == 0 ? static_cast<uint32_t>(tile) / static_cast<uint32_t>(mblocks)
+                                   : static_cast<int>(tile / mblocks);
   int lo = 0, hi = E - 1;  // the expert with s_unit[e] <= unit < s_unit[e + 1]
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -143,7 +147,7 @@ __device__ __forceinline__ Tile tile_at(int64_t tile, int mblocks, int rows_per_
   t.e = lo;
   t.row0 = s_first[lo] + (unit - s_unit[lo]) * rows_per_pass;
   t.rows = min(rows_per_pass, s_first[lo + 1] - t.row0);
-  t.m0 = static_cast<int>(tile % mblocks) * rows_per_tile;
+  t.m0 = static_cast<int>(tile - static_cast<int64_t>(unit) * mblocks) * rows_per_tile;
   return t;
 }
 
@@ -157,12 +161,14 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
   constexpr int kScales = kBoxCols / kGroup;  // per row and box
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full_bar[Cfg::kStages], empty_bar[Cfg::kStages];
-  __shared__ int s_first[kMaxExperts + 1];  // first row of each expert
-  __shared__ int s_unit[kMaxExperts + 1];   // passes before each expert
   __shared__ int abort_flag;
   volatile int* abort_v = &abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  float* sums = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) +
+                                         Cfg::kStages * Cfg::kStageBytes);
+  int* s_first = reinterpret_cast<int*>(sums) + Cfg::kSumBytes / 4;  // first row of each expert
+  int* s_unit = s_first + p.E + 1;                                   // passes before each expert
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::kStages; ++s) {
@@ -245,11 +251,16 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
               tma_load_2d(st + Cfg::kWeightBytes + Cfg::kXBytes + j * Cfg::kRows * 16, &s_map, bar,
                           (c0 / kGroup & ~7) * 2, t.e * p.M + t.m0);
             const uint32_t xs = st + Cfg::kWeightBytes + j * kTiles * 4 * Cfg::kXBoxBytes;
-            for (int n = 0; n < n_tiles; ++n)
+            for (int n = 0; n < n_tiles; ++n) {
+              const uint32_t dst = xs + n * 4 * Cfg::kXBoxBytes;
+              if (p.x_chunks) {
+                tma_load_3d(dst, &x_map, bar, 0, t.row0 + n * 8, c0 / 64);
+              } else {
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                tma_load_2d(xs + (n * 4 + c) * Cfg::kXBoxBytes, &x_map, bar, c0 + c * 64,
-                            t.row0 + n * 8);
+                for (int c = 0; c < 4; ++c)
+                  tma_load_2d(dst + c * Cfg::kXBoxBytes, &x_map, bar, c0 + c * 64, t.row0 + n * 8);
+              }
+            }
           }
         }
       }
@@ -274,8 +285,6 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
     // Column n of a fragment holds row (n >> 1) + 4 (n & 1) of the eight: lanes of
     // one quarter of the warp then read different halves of the swizzled rows.
     const int xrow = (g >> 1) + (g & 1) * 4;
-    float* sums = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) +
-                                           Cfg::kStages * Cfg::kStageBytes);
     const int pitch = p.C / kGroup;  // scales per row
     uint32_t it = 0;
     bool ok = true;
@@ -471,7 +480,8 @@ cudaError_t setup_matvec4(const DeviceInfo&) {
       for (int tiles : {1, 2, 4}) {
         const Variant v = pick(group, split, tiles);
         const cudaError_t e = cudaFuncSetAttribute(
-            v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(v.smem));
+            v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            static_cast<int>(v.smem) + table_bytes(kMaxExperts));
         if (e != cudaSuccess) return e;
       }
   return cudaSuccess;
@@ -489,9 +499,11 @@ cudaError_t launch_matvec4(const Matvec4Args& a, const DeviceInfo& dev, cudaStre
   const uint64_t rows = static_cast<uint64_t>(a.E) * a.M;
   const uint64_t pitch = static_cast<uint64_t>(a.C / a.G) * 2;
   const bool staged = pitch % 16 == 0;
+  const bool x_chunks = a.C % 64 == 0;
   CUtensorMap w_map, x_map, s_map;
   if (!make_map_u8(&w_map, a.packed, rows, a.C / 2, 128, v.rows) ||
-      !make_map_bf16_sw128(&x_map, a.x, a.N, a.C, 8))
+      !(x_chunks ? make_map_bf16_rows64(&x_map, a.x, a.N, a.C, 8, 4)
+                 : make_map_bf16_sw128(&x_map, a.x, a.N, a.C, 8)))
     return cudaErrorInvalidValue;
   if (!staged)
     s_map = w_map;  // not used
@@ -500,9 +512,10 @@ cudaError_t launch_matvec4(const Matvec4Args& a, const DeviceInfo& dev, cudaStre
   const int64_t most = (static_cast<int64_t>(matrices) + a.N / 8 + 1) *
                        ((a.M + v.rows - 1) / v.rows);
   const int grid = static_cast<int>(std::min<int64_t>(v.ctas_per_sm * dev.num_sms, most));
-  const Params p{a.scales, a.offsets, a.out, a.N, a.E, a.M, a.C, staged,
+  const Params p{a.scales, a.offsets, a.out, a.N, a.E, a.M, a.C, staged, x_chunks,
                  dev.err_word};
-  return launch_dependent(v.kernel, dim3(grid), dim3(kThreads), v.smem, stream, w_map, x_map,
+  return launch_dependent(v.kernel, dim3(grid), dim3(kThreads),
+                          v.smem + table_bytes(a.E), stream, w_map, x_map,
                           s_map, p);
 }
 
