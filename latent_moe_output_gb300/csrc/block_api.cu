@@ -219,7 +219,7 @@ LT_API lt_status latent_tail_residual_norm(const uint16_t* block, const void* re
 
 LT_API size_t latent_tail_residual_norm_backward_workspace_size(int T, int H) {
   if (T <= 0 || T > (1 << 24) || check_width(H, 16384) != LT_OK) return 0;
-  return round256(3 * static_cast<size_t>(residual_norm_partial_rows(T, H)) * H * sizeof(float));
+  return round256(2 * static_cast<size_t>(residual_norm_partial_rows(T, H)) * H * sizeof(float));
 }
 
 LT_API lt_status latent_tail_residual_norm_backward(

@@ -100,11 +100,11 @@ struct ResidualNormBackwardArgs {
   int gate_kind;
   bool residual_f32;
   float scale, eps;
-  float* partials;                // workspace: [3][rows][H]
+  float* partials;                // workspace: [2][rows][H]
 };
 
-// Most partial rows the backward kernel writes per summed gradient.
-constexpr int kResidualNormMaxPartials = 304 * 8;
+// SMs that a workspace size computed without a device allows for.
+constexpr int kMaxSms = 304;
 // Rows of partial sums that a call of T tokens of width H may write (bounds the
 // workspace without knowing the device).
 int residual_norm_partial_rows(int T, int H);

@@ -20,7 +20,7 @@
 namespace lt {
 namespace {
 
-constexpr int kMaxThreads = 1024;
+constexpr int kMaxThreads = 512;
 constexpr int kReduceCols = 32;    // float4 columns per CTA of the column sum
 constexpr int kReduceSlices = 16;  // parts of the partial rows per CTA
 
@@ -34,12 +34,12 @@ struct Shape {
 Shape shape_of(int H) {
   const int nch = H / 8;
   Shape s;
-  s.pieces = nch > kMaxThreads ? 2 : 1;
+  s.pieces = nch <= 256 ? 1 : nch <= 1024 ? 2 : 4;
   if (nch <= 128) {
     s.tpr = nch <= 32 ? 32 : nch <= 64 ? 64 : 128;
     s.threads = 256;
   } else {
-    s.tpr = std::min(kMaxThreads, (nch + 31) / 32 * 32);
+    s.tpr = ((nch + s.pieces - 1) / s.pieces + 31) / 32 * 32;
     s.threads = s.tpr;
   }
   s.per_cta = s.threads / s.tpr;
@@ -51,11 +51,10 @@ Shape shape_of(int H) {
 __device__ __forceinline__ float row_sum(float v, float* red, int row_in_cta, int warps_per_row) {
   v = warp_sum_f(v);
   if (warps_per_row == 1) return v;
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  float s = 0.f;
-  for (int w = 0; w < warps_per_row; ++w) s += red[row_in_cta * warps_per_row + w];
-  return s;
+  return warp_sum_f(lane < warps_per_row ? red[row_in_cta * warps_per_row + lane] : 0.f);
 }
 
 __device__ __forceinline__ void load8(const float* p, float (&a)[8]) {
@@ -104,8 +103,36 @@ __device__ __forceinline__ void gate8(const void* gate, int kind, int t, int col
   }
 }
 
+template <bool kF32>
+struct Raw;
+template <>
+struct Raw<false> {
+  uint4 v;
+  __device__ __forceinline__ void load(const void* base, size_t at) {
+    v = ld_once_v4(static_cast<const uint16_t*>(base) + at);
+  }
+  __device__ __forceinline__ void get(float (&a)[8]) const { unpack8(v, a); }
+};
+template <>
+struct Raw<true> {
+  uint4 lo, hi;
+  __device__ __forceinline__ void load(const void* base, size_t at) {
+    lo = ld_once_v4(static_cast<const float*>(base) + at);
+    hi = ld_once_v4(static_cast<const float*>(base) + at + 4);
+  }
+  __device__ __forceinline__ void get(float (&a)[8]) const {
+    a[0] = __uint_as_float(lo.x); a[1] = __uint_as_float(lo.y);
+    a[2] = __uint_as_float(lo.z); a[3] = __uint_as_float(lo.w);
+    a[4] = __uint_as_float(hi.x); a[5] = __uint_as_float(hi.y);
+    a[6] = __uint_as_float(hi.z); a[7] = __uint_as_float(hi.w);
+  }
+};
+
+// One row per group of `tpr` threads. A row's loads, two reductions and stores
+// follow one another, so several CTAs per SM keep the memory busy; rows are held
+// as they were loaded to keep the registers for that.
 template <int kPieces, bool kF32>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(kMaxThreads, kPieces == 4 ? 1 : 2)
     residual_norm_kernel(const ResidualNormArgs a, int tpr) {
   __shared__ float red[2][kMaxThreads / 32];
   pdl_launch_dependents();
@@ -116,41 +143,52 @@ __global__ void __launch_bounds__(kMaxThreads)
   const size_t base = static_cast<size_t>(t) * a.H;
   const float inv_h = 1.0f / static_cast<float>(a.H);
 
-  float y[kPieces][8], x[kPieces][8], ss = 0.f;
+  uint4 y[kPieces];
+  Raw<kF32> x[kPieces];
 #pragma unroll
   for (int q = 0; q < kPieces; ++q) {
     const int col = (lane + q * tpr) * 8;
     if (live && col < a.H) {
-      const uint4 raw = ld_stream_v4(a.block + base + col);
-      load_res8<kF32>(a.residual, base + col, x[q]);
-      unpack8(raw, y[q]);
+      y[q] = ld_stream_v4(a.block + base + col);
+      x[q].load(a.residual, base + col);
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[q][i] = y[q][i] = 0.f;
+      y[q] = make_uint4(0, 0, 0, 0);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(y[q][i], y[q][i], ss);
   }
-  float r1 = 1.f;
-  if (a.post != nullptr) r1 = 1.0f / sqrtf(row_sum(ss, red[0], row, wpr) * inv_h + a.eps);
+  float r1 = 1.f, ss = 0.f;
+  if (a.post != nullptr) {
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) {
+      float f[8];
+      unpack8(y[q], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+    }
+    r1 = 1.0f / sqrtf(row_sum(ss, red[0], row, wpr) * inv_h + a.eps);
+  }
   ss = 0.f;
+  float v[kPieces][8];
 #pragma unroll
   for (int q = 0; q < kPieces; ++q) {
     const int col = (lane + q * tpr) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[q][i] = 0.f;
     if (live && col < a.H) {
-      float w[8];
+      float u[8], w[8];
+      unpack8(y[q], u);
       if (a.post != nullptr) {
         load8(a.post + col, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[q][i] = y[q][i] * r1 * w[i];
+        for (int i = 0; i < 8; ++i) u[i] = u[i] * r1 * w[i];
       }
       gate8(a.gate, a.gate_kind, t, col, base + col, w);
+      x[q].get(v[q]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[q][i] = fmaf(w[i], y[q][i], a.scale * x[q][i]);
-      store_res8<kF32>(a.residual_out, base + col, x[q]);
+      for (int i = 0; i < 8; ++i) v[q][i] = fmaf(w[i], u[i], a.scale * v[q][i]);
+      store_res8<kF32>(a.residual_out, base + col, v[q]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[q][i], x[q][i], ss);
+    for (int i = 0; i < 8; ++i) ss = fmaf(v[q][i], v[q][i], ss);
   }
   if (a.next == nullptr) return;
   const float r2 = 1.0f / sqrtf(row_sum(ss, red[1], row, wpr) * inv_h + a.eps);
@@ -161,27 +199,29 @@ __global__ void __launch_bounds__(kMaxThreads)
       float w[8];
       load8(a.next + col, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = x[q][i] * r2 * w[i];
+      for (int i = 0; i < 8; ++i) w[i] = v[q][i] * r2 * w[i];
       *reinterpret_cast<uint4*>(a.next_out + base + col) = pack8(w);
     }
   }
 }
 
-// Each CTA walks over token rows and keeps the column sums of its threads'
-// columns: in registers for one piece per thread, else in shared memory.
+// The gradient for rows that the ring kernel below does not take. Each CTA walks
+// over token rows and keeps the column sums of its threads' columns: in registers
+// for one piece per thread, else in shared memory. With a channel gate one sum,
+// S = sum_t d * yh, gives both dgp = gate * S and dgate = gp * S.
 template <int kPieces, bool kF32>
 __global__ void __launch_bounds__(kMaxThreads)
-    residual_norm_backward_kernel(const ResidualNormBackwardArgs a, int tpr, int partial_rows) {
-  extern __shared__ float s_acc[];  // kPieces > 1: [3][H]
+    residual_norm_backward_kernel(const ResidualNormBackwardArgs a, int tpr) {
+  extern __shared__ float s_acc[];  // kPieces > 1: [2][H]
   __shared__ float red[4][kMaxThreads / 32];
   pdl_launch_dependents();
   pdl_wait();
   const int row = threadIdx.x / tpr, lane = threadIdx.x - row * tpr, wpr = tpr >> 5;
   const int per_cta = blockDim.x / tpr;
   const float inv_h = 1.0f / static_cast<float>(a.H);
-  float acc[3][8] = {};
+  float acc[2][8] = {};
   if constexpr (kPieces > 1)
-    for (int i = threadIdx.x; i < 3 * a.H; i += blockDim.x) s_acc[i] = 0.f;
+    for (int i = threadIdx.x; i < 2 * a.H; i += blockDim.x) s_acc[i] = 0.f;
   if constexpr (kPieces > 1) __syncthreads();
   auto add = [&](int which, int q, const float (&v)[8]) {
     if constexpr (kPieces == 1) {
@@ -262,7 +302,12 @@ __global__ void __launch_bounds__(kMaxThreads)
           o[i] = d[q][i] * u;
           sgate += o[i];
         }
-        if (a.gate_kind == kGateChannel) add(2, q, o);
+        if (a.gate_kind == kGateChannel) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            o[i] = d[q][i] * (a.post != nullptr ? y[q][i] * r1 : y[q][i]);
+          add(0, q, o);
+        }
         if (a.gate_kind == kGateFull)
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_gate) + base + col) = pack8(o);
 #pragma unroll
@@ -274,7 +319,7 @@ __global__ void __launch_bounds__(kMaxThreads)
             d[q][i] *= w[i];
             sby = fmaf(d[q][i], y[q][i], sby);
           }
-          add(0, q, o);
+          if (a.gate_kind != kGateChannel) add(0, q, o);
         }
       }
     }
@@ -299,41 +344,305 @@ __global__ void __launch_bounds__(kMaxThreads)
     __syncthreads();  // red is free for the next row
   }
 
-  const size_t plane = static_cast<size_t>(partial_rows) * a.H;
-  const size_t at = static_cast<size_t>(blockIdx.x * per_cta + row) * a.H;
-  const bool want[3] = {a.post != nullptr, a.next != nullptr, a.gate_kind == kGateChannel};
+  const size_t plane = static_cast<size_t>(gridDim.x) * a.H;
+  const size_t at = static_cast<size_t>(blockIdx.x) * a.H;
+  const bool want[2] = {a.post != nullptr || a.gate_kind == kGateChannel, a.next != nullptr};
+  if constexpr (kPieces == 1) {  // the rows that the CTA worked on at once add up in order
+    __shared__ float s_rows[256 * 8];
 #pragma unroll
-  for (int q = 0; q < kPieces; ++q) {
-    const int col = (lane + q * tpr) * 8;
-    if (col >= a.H) continue;
-#pragma unroll
-    for (int s = 0; s < 3; ++s) {
+    for (int s = 0; s < 2; ++s) {
       if (!want[s]) continue;
-      float o[8];
+      __syncthreads();
+      if (lane * 8 < a.H)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        o[i] = kPieces == 1 ? acc[s][i] : s_acc[static_cast<size_t>(s) * a.H + col + i];
-      store_res8<true>(a.partials + s * plane, at + col, o);
+        for (int i = 0; i < 8; ++i) s_rows[row * a.H + lane * 8 + i] = acc[s][i];
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
+        float o = 0.f;
+        for (int r = 0; r < per_cta; ++r) o += s_rows[r * a.H + c];
+        a.partials[s * plane + at + c] = o;
+      }
     }
+  } else {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (want[s])
+        for (int c = threadIdx.x; c < a.H; c += blockDim.x)
+          a.partials[s * plane + at + c] = s_acc[s * a.H + c];
   }
 }
 
-// Sums of the partial rows, in a fixed order: 16 slices of rows per CTA, then
-// the slices in order.
+// ------------------------------------------------------------ ring kernel
+// The gradient for 1024 < H <= 8192: one CTA per SM walks over token rows, one
+// 8-element piece of the row per thread. The rows (up to five arrays) come through
+// a ring of stages with bulk copies that run ahead of the arithmetic; a stage is
+// refilled once all threads are past the row's second barrier.
+constexpr int kRingMinH = 1032, kRingMaxH = 8192;
+constexpr int kRingMaxStages = 4;
+constexpr size_t kRingSmem = 224 * 1024;
+
+// Sums of up to four values over the CTA with one barrier: halving exchanges that
+// leave lane l with a part of value l / 8, one partial per warp in shared memory,
+// and each warp adds the warps' partials again. `red` is [4][32].
+__device__ __forceinline__ void cta_sum4(float (&v)[4], float (*red)[32], int warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool up16 = lane & 16, up8 = lane & 8;
+  // values 0, 1 stay with lanes 0-15, values 2, 3 with lanes 16-31
+  const float s0 = up16 ? v[0] : v[2], s1 = up16 ? v[1] : v[3];
+  float a = (up16 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, s0, 16);
+  float b = (up16 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, s1, 16);
+  float c = (up8 ? b : a) + __shfl_xor_sync(0xffffffffu, up8 ? a : b, 8);
+  c += __shfl_xor_sync(0xffffffffu, c, 4);
+  c += __shfl_xor_sync(0xffffffffu, c, 2);
+  c += __shfl_xor_sync(0xffffffffu, c, 1);
+  const int which = lane >> 3;  // value held: 0, 1, 2, 3 for lanes 0, 8, 16, 24
+  if ((lane & 7) == 0) red[which][warp] = c;
+  __syncthreads();
+  const float4 p = *reinterpret_cast<const float4*>(&red[which][(lane & 7) * 4]);
+  const int w = (lane & 7) * 4;
+  c = ((w < warps ? p.x : 0.f) + (w + 1 < warps ? p.y : 0.f)) +
+      ((w + 2 < warps ? p.z : 0.f) + (w + 3 < warps ? p.w : 0.f));
+  c += __shfl_xor_sync(0xffffffffu, c, 4);
+  c += __shfl_xor_sync(0xffffffffu, c, 2);
+  c += __shfl_xor_sync(0xffffffffu, c, 1);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, c, 8 * i);
+}
+
+template <bool kF32>
+__device__ __forceinline__ void lds_res8(const uint8_t* row, int lane, float (&a)[8]) {
+  if constexpr (kF32) {
+    const float4 lo = *reinterpret_cast<const float4*>(row + lane * 32);
+    const float4 hi = *reinterpret_cast<const float4*>(row + lane * 32 + 16);
+    a[0] = lo.x; a[1] = lo.y; a[2] = lo.z; a[3] = lo.w;
+    a[4] = hi.x; a[5] = hi.y; a[6] = hi.z; a[7] = hi.w;
+  } else {
+    unpack8(*reinterpret_cast<const uint4*>(row + lane * 16), a);
+  }
+}
+
+template <bool kF32, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1)
+    residual_norm_backward_ring_kernel(const ResidualNormBackwardArgs a, int stages,
+                                       int stage_bytes, uint32_t* err) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full_bar[kRingMaxStages];
+  __shared__ __align__(16) float red[2][4][32];
+  __shared__ int abort_flag;
+  volatile int* abort_v = &abort_flag;
+  const int lane = threadIdx.x;  // piece of the row
+  const int H = a.H, warps = blockDim.x >> 5;
+  const uint32_t h2 = static_cast<uint32_t>(H) * 2, hr = kF32 ? h2 * 2 : h2;
+  const bool has_dv = a.grad_residual_out != nullptr, has_next = a.next != nullptr;
+  const bool has_post = a.post != nullptr, full_gate = a.gate_kind == kGateFull;
+  // Arrays of a stage: y, v, dz, dv, gate.
+  const uint32_t at_v = h2, at_z = at_v + hr, at_d = at_z + (has_next ? h2 : 0),
+                 at_g = at_d + (has_dv ? hr : 0);
+  float* s_gate = reinterpret_cast<float*>(smem + static_cast<size_t>(stages) * stage_bytes);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(smem_u32(&full_bar[s]), 1);
+    abort_flag = 0;
+    mbar_fence_init();
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  __syncthreads();
+
+  auto fetch = [&](int t, int s) {  // one thread
+    const uint32_t bar = smem_u32(&full_bar[s]);
+    const uint32_t st = smem_u32(smem) + static_cast<uint32_t>(s) * stage_bytes;
+    const size_t base = static_cast<size_t>(t) * H;
+    const size_t rb = base * (kF32 ? 4 : 2);
+    mbar_arrive_expect_tx(bar, at_g + (full_gate ? h2 : 0));
+    bulk_load(st, a.block + base, h2, bar);
+    bulk_load(st + at_v, static_cast<const uint8_t*>(a.residual_out) + rb, hr, bar);
+    if (has_next) bulk_load(st + at_z, a.grad_next + base, h2, bar);
+    if (has_dv) bulk_load(st + at_d, static_cast<const uint8_t*>(a.grad_residual_out) + rb, hr, bar);
+    if (full_gate) bulk_load(st + at_g, static_cast<const uint16_t*>(a.gate) + base, h2, bar);
+  };
+  const int step = gridDim.x;
+  if (threadIdx.x == 0)
+    for (int s = 0; s < stages && static_cast<int>(blockIdx.x) + s * step < a.T; ++s)
+      fetch(blockIdx.x + s * step, s);
+
+  const int col = lane * 8;
+  const bool on = col < H;
+  float gp[8], gn[8], acc_p[8] = {}, acc_n[8] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) gp[i] = 1.f, gn[i] = 0.f;
+  if (on && has_post) load8(a.post + col, gp);
+  if (on && has_next) load8(a.next + col, gn);
+  if (on && a.gate_kind == kGateChannel) {
+    float g[8];
+    load8(static_cast<const float*>(a.gate) + col, g);
+    store_res8<true>(s_gate, col, g);  // read back by the same thread
+  }
+  const float inv_h = 1.0f / static_cast<float>(H);
+  int s = 0;
+  uint32_t parity = 0;
+  bool ok = true;
+  for (int t = blockIdx.x; t < a.T; t += step) {
+    const uint8_t* st = smem + static_cast<size_t>(s) * stage_bytes;
+    if (ok) ok = mbar_wait(smem_u32(&full_bar[s]), parity, err, abort_v);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};  // y y, v v, a v
+    uint4 y_raw = make_uint4(0, 0, 0, 0);
+    if (on) {
+      float f[8];
+      y_raw = *reinterpret_cast<const uint4*>(st + lane * 16);
+      unpack8(y_raw, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[0] = fmaf(f[i], f[i], sum[0]);
+      if (has_next) {
+        float z[8];
+        lds_res8<kF32>(st + at_v, lane, f);
+        unpack8(*reinterpret_cast<const uint4*>(st + at_z + lane * 16), z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sum[1] = fmaf(f[i], f[i], sum[1]);
+          sum[2] = fmaf(z[i] * gn[i], f[i], sum[2]);
+        }
+      }
+    }
+    cta_sum4(sum, red[0], warps);
+    const float r1 = has_post ? 1.0f / sqrtf(sum[0] * inv_h + a.eps) : 1.f;
+    const float r2 = 1.0f / sqrtf(sum[1] * inv_h + a.eps);
+    const float m = sum[2] * inv_h * r2;  // mean(a * vh)
+
+    const size_t base = static_cast<size_t>(t) * H + col;
+    float d[8], by[4] = {0.f, 0.f, 0.f, 0.f};  // b y, d u
+    if (on) {
+      if (has_dv) {
+        lds_res8<kF32>(st + at_d, lane, d);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = 0.f;
+      }
+      float f[8], g[8];
+      if (has_next) {
+        lds_res8<kF32>(st + at_v, lane, f);
+        unpack8(*reinterpret_cast<const uint4*>(st + at_z + lane * 16), g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float vh = f[i] * r2;
+          d[i] = fmaf(r2, fmaf(g[i], gn[i], -vh * m), d[i]);
+          acc_n[i] = fmaf(g[i], vh, acc_n[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = a.scale * d[i];
+      store_res8<kF32>(a.grad_residual, base, g);
+      unpack8(y_raw, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= r1;  // yh
+      if (a.gate_kind == kGateChannel) {
+        const float4 lo = *reinterpret_cast<const float4*>(s_gate + col);
+        const float4 hi = *reinterpret_cast<const float4*>(s_gate + col + 4);
+        g[0] = lo.x; g[1] = lo.y; g[2] = lo.z; g[3] = lo.w;
+        g[4] = hi.x; g[5] = hi.y; g[6] = hi.z; g[7] = hi.w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          acc_p[i] = fmaf(d[i], f[i], acc_p[i]);
+          d[i] *= g[i] * gp[i];
+        }
+      } else {
+        if (full_gate) {
+          unpack8(*reinterpret_cast<const uint4*>(st + at_g + lane * 16), g);
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = d[i] * (f[i] * gp[i]);
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_gate) + base) = pack8(o);
+        } else {
+          const float gt =
+              a.gate_kind == kGateToken ? __ldg(static_cast<const float*>(a.gate) + t) : 1.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            by[1] = fmaf(d[i], f[i] * gp[i], by[1]);
+            g[i] = gt;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          d[i] *= g[i];
+          acc_p[i] = fmaf(d[i], f[i], acc_p[i]);
+          d[i] *= gp[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) by[0] = fmaf(d[i], f[i], by[0]);
+    }
+    cta_sum4(by, red[1], warps);
+    // All threads are done with the stage.
+    if (threadIdx.x == 0 && ok && t + stages * step < a.T) fetch(t + stages * step, s);
+    if (a.gate_kind == kGateToken && threadIdx.x == 0) static_cast<float*>(a.grad_gate)[t] = by[1];
+    if (on) {
+      if (has_post) {
+        const float m1 = by[0] * inv_h;  // mean(b * yh)
+        float f[8];
+        unpack8(y_raw, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = r1 * fmaf(-f[i] * r1, m1, d[i]);
+      }
+      *reinterpret_cast<uint4*>(a.grad_block + base) = pack8(d);
+    }
+    if (++s == stages) s = 0, parity ^= 1;
+  }
+  if (on) {
+    const size_t plane = static_cast<size_t>(gridDim.x) * H;
+    const size_t at = static_cast<size_t>(blockIdx.x) * H + col;
+    if (has_post || a.gate_kind == kGateChannel) store_res8<true>(a.partials, at, acc_p);
+    if (has_next) store_res8<true>(a.partials + plane, at, acc_n);
+  }
+  if (*abort_v && threadIdx.x == 0) {  // let copies in flight land before the CTA exits
+    for (int i = 0; i < stages; ++i)
+      for (uint32_t q = 0; q < 2; ++q) {
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(smem_u32(&full_bar[i]), q) &&
+               global_timer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+  }
+}
+
+struct RingPlan {
+  int stages = 0, stage_bytes = 0, threads = 0;
+  size_t smem = 0;
+};
+
+// The ring for this call; stages == 0 when the direct kernel takes it.
+RingPlan ring_plan(const ResidualNormBackwardArgs& a) {
+  RingPlan r;
+  if (a.H < kRingMinH || a.H > kRingMaxH) return r;
+  const int h2 = a.H * 2, hr = a.residual_f32 ? h2 * 2 : h2;
+  const int bytes = h2 + hr + (a.next != nullptr ? h2 : 0) +
+                    (a.grad_residual_out != nullptr ? hr : 0) +
+                    (a.gate_kind == kGateFull ? h2 : 0);
+  const size_t gate = a.gate_kind == kGateChannel ? static_cast<size_t>(a.H) * 4 : 0;
+  r.stage_bytes = (bytes + 127) / 128 * 128;
+  r.stages = static_cast<int>(
+      std::min<size_t>(kRingMaxStages, (kRingSmem - gate) / r.stage_bytes));
+  r.threads = (a.H / 8 + 31) / 32 * 32;
+  r.smem = static_cast<size_t>(r.stages) * r.stage_bytes + gate;
+  return r;
+}
+
+// Sums of the partial rows, in a fixed order: 16 slices of rows per CTA, then the
+// slices in order. Plane 0 gives the gradients of the post weight and of a channel
+// gate, plane 1 that of the next weight.
 __global__ void __launch_bounds__(kReduceCols* kReduceSlices)
-    column_sum_kernel(const float* __restrict__ partials, float* __restrict__ o0,
-                      float* __restrict__ o1, float* __restrict__ o2, int partial_rows, int H) {
+    column_sum_kernel(const float* __restrict__ partials, const float* __restrict__ post,
+                      const float* __restrict__ gate, float* __restrict__ grad_post,
+                      float* __restrict__ grad_gate, float* __restrict__ grad_next,
+                      int partial_rows, int H) {
   __shared__ float4 s_part[kReduceSlices][kReduceCols];
   pdl_launch_dependents();
   pdl_wait();
-  float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
-  if (out == nullptr) return;
+  if (blockIdx.y == 0 ? grad_post == nullptr && grad_gate == nullptr : grad_next == nullptr) return;
   const int cx = threadIdx.x % kReduceCols, slice = threadIdx.x / kReduceCols;
   const int col = (blockIdx.x * kReduceCols + cx) * 4;
   const float* src = partials + blockIdx.y * static_cast<size_t>(partial_rows) * H + col;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (col < H) {
-#pragma unroll 4
+#pragma unroll 8
     for (int r = slice; r < partial_rows; r += kReduceSlices) {
       const float4 v = *reinterpret_cast<const float4*>(src + static_cast<size_t>(r) * H);
       s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
@@ -341,67 +650,112 @@ __global__ void __launch_bounds__(kReduceCols* kReduceSlices)
   }
   s_part[slice][cx] = s;
   __syncthreads();
-  if (slice == 0 && col < H) {
-    for (int i = 1; i < kReduceSlices; ++i) {
-      const float4 v = s_part[i][cx];
-      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-    }
-    *reinterpret_cast<float4*>(out + col) = s;
+  if (slice != 0 || col >= H) return;
+  for (int i = 1; i < kReduceSlices; ++i) {
+    const float4 v = s_part[i][cx];
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
   }
+  if (blockIdx.y == 1) {
+    *reinterpret_cast<float4*>(grad_next + col) = s;
+    return;
+  }
+  auto times = [&](const float* f) {
+    const float4 w = f == nullptr ? make_float4(1.f, 1.f, 1.f, 1.f)
+                                  : *reinterpret_cast<const float4*>(f + col);
+    return make_float4(s.x * w.x, s.y * w.y, s.z * w.z, s.w * w.w);
+  };
+  if (grad_post != nullptr) *reinterpret_cast<float4*>(grad_post + col) = times(gate);
+  if (grad_gate != nullptr) *reinterpret_cast<float4*>(grad_gate + col) = times(post);
 }
 
+// CTAs of the backward kernels: one per SM for the ring, about 1024 threads per SM
+// for the direct one.
 int backward_grid(int T, int H, int num_sms) {
+  if (H >= kRingMinH && H <= kRingMaxH) return std::min(T, num_sms);
   const Shape s = shape_of(H);
-  const int ctas = std::max(1, 2048 / s.threads);  // resident threads per SM
-  return std::max(1, std::min((T + s.per_cta - 1) / s.per_cta,
-                              std::min(num_sms * (ctas > 2 ? 2 : ctas), 304)));
+  return std::min((T + s.per_cta - 1) / s.per_cta, num_sms * std::max(1, 1024 / s.threads));
 }
 
 }  // namespace
 
 int residual_norm_partial_rows(int T, int H) {
-  return backward_grid(T, H, 304) * shape_of(H).per_cta;
+  return backward_grid(T, H, kMaxSms);
 }
 
+namespace {
+
+typedef void (*BackwardKernel)(const ResidualNormBackwardArgs, int);
+typedef void (*RingKernel)(const ResidualNormBackwardArgs, int, int, uint32_t*);
+
+BackwardKernel backward_kernel(int pieces, bool f32) {
+  switch (pieces) {
+    case 1: return f32 ? residual_norm_backward_kernel<1, true> : residual_norm_backward_kernel<1, false>;
+    default: return f32 ? residual_norm_backward_kernel<4, true> : residual_norm_backward_kernel<4, false>;
+  }
+}
+
+RingKernel ring_kernel(int threads, bool f32) {
+  if (threads <= 640)
+    return f32 ? residual_norm_backward_ring_kernel<true, 640>
+               : residual_norm_backward_ring_kernel<false, 640>;
+  if (threads <= 896)
+    return f32 ? residual_norm_backward_ring_kernel<true, 896>
+               : residual_norm_backward_ring_kernel<false, 896>;
+  return f32 ? residual_norm_backward_ring_kernel<true, 1024>
+             : residual_norm_backward_ring_kernel<false, 1024>;
+}
+
+}  // namespace
+
 cudaError_t setup_residual_norm(const DeviceInfo&) {
-  const int bytes = 3 * 16384 * static_cast<int>(sizeof(float));
-  cudaError_t e = cudaFuncSetAttribute(residual_norm_backward_kernel<2, false>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(residual_norm_backward_kernel<2, true>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  for (bool f32 : {false, true}) {
+    cudaError_t e = cudaFuncSetAttribute(backward_kernel(4, f32),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         2 * 16384 * static_cast<int>(sizeof(float)));
+    if (e != cudaSuccess) return e;
+    for (int threads : {640, 896, 1024})
+      if ((e = cudaFuncSetAttribute(ring_kernel(threads, f32),
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(kRingSmem))) != cudaSuccess)
+        return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, const DeviceInfo&,
                                  cudaStream_t stream) {
   const Shape s = shape_of(a.H);
   const dim3 grid((a.T + s.per_cta - 1) / s.per_cta);
-  auto* k = s.pieces == 1 ? (a.residual_f32 ? residual_norm_kernel<1, true>
-                                            : residual_norm_kernel<1, false>)
-                          : (a.residual_f32 ? residual_norm_kernel<2, true>
-                                            : residual_norm_kernel<2, false>);
+  void (*k)(const ResidualNormArgs, int) =
+      s.pieces == 1   ? (a.residual_f32 ? residual_norm_kernel<1, true> : residual_norm_kernel<1, false>)
+      : s.pieces == 2 ? (a.residual_f32 ? residual_norm_kernel<2, true> : residual_norm_kernel<2, false>)
+                      : (a.residual_f32 ? residual_norm_kernel<4, true> : residual_norm_kernel<4, false>);
   return launch_dependent(k, grid, dim3(s.threads), 0, stream, a, s.tpr);
 }
 
 cudaError_t launch_residual_norm_backward(const ResidualNormBackwardArgs& a,
                                           const DeviceInfo& dev, cudaStream_t stream) {
-  const Shape s = shape_of(a.H);
-  const int grid = backward_grid(a.T, a.H, dev.num_sms);
-  const int partial_rows = grid * s.per_cta;
-  auto* k = s.pieces == 1 ? (a.residual_f32 ? residual_norm_backward_kernel<1, true>
-                                            : residual_norm_backward_kernel<1, false>)
-                          : (a.residual_f32 ? residual_norm_backward_kernel<2, true>
-                                            : residual_norm_backward_kernel<2, false>);
-  const size_t smem = s.pieces == 1 ? 0 : 3 * static_cast<size_t>(a.H) * sizeof(float);
-  const cudaError_t e =
-      launch_dependent(k, dim3(grid), dim3(s.threads), smem, stream, a, s.tpr, partial_rows);
-  float* channel = a.gate_kind == kGateChannel ? static_cast<float*>(a.grad_gate) : nullptr;
-  if (e != cudaSuccess || (a.post == nullptr && a.next == nullptr && channel == nullptr)) return e;
+  const int grid = backward_grid(a.T, a.H, std::min(dev.num_sms, kMaxSms));
+  const RingPlan ring = ring_plan(a);
+  cudaError_t e;
+  if (ring.stages != 0) {
+    e = launch_dependent(ring_kernel(ring.threads, a.residual_f32), dim3(grid), dim3(ring.threads),
+                         ring.smem, stream, a, ring.stages, ring.stage_bytes, dev.err_word);
+  } else {
+    const Shape s = shape_of(a.H);
+    const size_t smem = s.pieces == 1 ? 0 : 2 * static_cast<size_t>(a.H) * sizeof(float);
+    e = launch_dependent(backward_kernel(s.pieces, a.residual_f32), dim3(grid), dim3(s.threads),
+                         smem, stream, a, s.tpr);
+  }
+  const bool channel = a.gate_kind == kGateChannel;
+  if (e != cudaSuccess || (a.post == nullptr && a.next == nullptr && !channel)) return e;
   const int cols = kReduceCols * 4;
-  return launch_dependent(column_sum_kernel, dim3((a.H + cols - 1) / cols, 3),
+  return launch_dependent(column_sum_kernel, dim3((a.H + cols - 1) / cols, 2),
                           dim3(kReduceCols * kReduceSlices), 0, stream,
-                          static_cast<const float*>(a.partials), a.grad_post, a.grad_next_weight,
-                          channel, partial_rows, a.H);
+                          static_cast<const float*>(a.partials), a.post,
+                          channel ? static_cast<const float*>(a.gate) : nullptr, a.grad_post,
+                          channel ? static_cast<float*>(a.grad_gate) : nullptr,
+                          a.grad_next_weight, grid, a.H);
 }
 
 }  // namespace lt
