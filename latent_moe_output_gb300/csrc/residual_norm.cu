@@ -90,6 +90,30 @@ __device__ __forceinline__ void store_res8(void* base, size_t at, const float (&
   }
 }
 
+// The same on register pairs; 32 bytes of FP32 at a time.
+__device__ __forceinline__ void pairs_of(const float4& lo, const float4& hi, f32x2 (&a)[4]) {
+  a[0] = pair(lo.x, lo.y);
+  a[1] = pair(lo.z, lo.w);
+  a[2] = pair(hi.x, hi.y);
+  a[3] = pair(hi.z, hi.w);
+}
+__device__ __forceinline__ void load8(const float* p, f32x2 (&a)[4]) {
+  pairs_of(__ldg(reinterpret_cast<const float4*>(p)), __ldg(reinterpret_cast<const float4*>(p) + 1),
+           a);
+}
+__device__ __forceinline__ void store8(float* p, const f32x2 (&a)[4]) {
+  ulonglong2* q = reinterpret_cast<ulonglong2*>(p);
+  q[0] = make_ulonglong2(a[0], a[1]);
+  q[1] = make_ulonglong2(a[2], a[3]);
+}
+template <bool kF32>
+__device__ __forceinline__ void store_res8(void* base, size_t at, const f32x2 (&a)[4]) {
+  if constexpr (kF32)
+    store8(static_cast<float*>(base) + at, a);
+  else
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = pack8(a);
+}
+
 __device__ __forceinline__ void gate8(const void* gate, int kind, int t, int col, size_t at,
                                       float (&a)[8]) {
   if (kind == kGateFull) {
@@ -378,51 +402,216 @@ __global__ void __launch_bounds__(kMaxThreads)
 // a ring of stages with bulk copies that run ahead of the arithmetic; a stage is
 // refilled once all threads are past the row's second barrier.
 constexpr int kRingMinH = 1032, kRingMaxH = 8192;
-constexpr int kRingMaxStages = 4;
-constexpr size_t kRingSmem = 224 * 1024;
+constexpr int kRingMaxStages = 6;
+constexpr int kRingMinWaves = 4;  // forward: rows per SM
+constexpr size_t kRingSmem = 224 * 1024;  // one CTA per SM
+constexpr int kForwardRingMinH = 4096;
 
-// Sums of up to four values over the CTA with one barrier: halving exchanges that
-// leave lane l with a part of value l / 8, one partial per warp in shared memory,
-// and each warp adds the warps' partials again. `red` is [4][32].
-__device__ __forceinline__ void cta_sum4(float (&v)[4], float (*red)[32], int warps) {
+// Narrow rows have few threads: several CTAs then share an SM (72 registers each).
+constexpr int ring_ctas_per_sm(int threads) { return threads <= 288 ? 3 : threads <= 448 ? 2 : 1; }
+constexpr size_t ring_smem(int threads) {
+  return ring_ctas_per_sm(threads) == 1 ? kRingSmem : kRingSmem / ring_ctas_per_sm(threads) - 2048;
+}
+constexpr int ring_threads(int H) { return (H / 8 + 31) / 32 * 32; }
+
+// Sums of one, two or four values over the CTA with one barrier: halving exchanges
+// leave a lane with a part of one value, one partial per warp goes to shared memory,
+// and each warp adds the warps' partials again. `red` is [kValues][32].
+template <int kValues>
+__device__ __forceinline__ void cta_sum(float (&v)[kValues], float (*red)[32], int warps) {
+  constexpr int kLanes = 32 / kValues;  // lanes per value
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool up16 = lane & 16, up8 = lane & 8;
-  // values 0, 1 stay with lanes 0-15, values 2, 3 with lanes 16-31
-  const float s0 = up16 ? v[0] : v[2], s1 = up16 ? v[1] : v[3];
-  float a = (up16 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, s0, 16);
-  float b = (up16 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, s1, 16);
-  float c = (up8 ? b : a) + __shfl_xor_sync(0xffffffffu, up8 ? a : b, 8);
-  c += __shfl_xor_sync(0xffffffffu, c, 4);
-  c += __shfl_xor_sync(0xffffffffu, c, 2);
-  c += __shfl_xor_sync(0xffffffffu, c, 1);
-  const int which = lane >> 3;  // value held: 0, 1, 2, 3 for lanes 0, 8, 16, 24
-  if ((lane & 7) == 0) red[which][warp] = c;
-  __syncthreads();
-  const float4 p = *reinterpret_cast<const float4*>(&red[which][(lane & 7) * 4]);
-  const int w = (lane & 7) * 4;
-  c = ((w < warps ? p.x : 0.f) + (w + 1 < warps ? p.y : 0.f)) +
-      ((w + 2 < warps ? p.z : 0.f) + (w + 3 < warps ? p.w : 0.f));
-  c += __shfl_xor_sync(0xffffffffu, c, 4);
-  c += __shfl_xor_sync(0xffffffffu, c, 2);
-  c += __shfl_xor_sync(0xffffffffu, c, 1);
+  float c = v[0];
+  if constexpr (kValues == 4) {
+    const bool up16 = lane & 16, up8 = lane & 8;
+    const float a = (up16 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up16 ? v[0] : v[2], 16);
+    const float b = (up16 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, up16 ? v[1] : v[3], 16);
+    c = (up8 ? b : a) + __shfl_xor_sync(0xffffffffu, up8 ? a : b, 8);
+  } else if constexpr (kValues == 2) {
+    const bool up16 = lane & 16;
+    c = (up16 ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up16 ? v[0] : v[1], 16);
+  }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, c, 8 * i);
+  for (int o = kLanes / 2; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+  const int which = lane / kLanes, at = (lane % kLanes) * kValues;
+  if (lane % kLanes == 0) red[which][warp] = c;
+  __syncthreads();
+  float p[kValues];  // kValues partials of this lane's value
+  if constexpr (kValues == 4)
+    *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(&red[which][at]);
+  else if constexpr (kValues == 2)
+    *reinterpret_cast<float2*>(p) = *reinterpret_cast<const float2*>(&red[which][at]);
+  else
+    p[0] = red[0][at];
+  c = 0.f;
+#pragma unroll
+  for (int i = 0; i < kValues; ++i) c += at + i < warps ? p[i] : 0.f;
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+#pragma unroll
+  for (int i = 0; i < kValues; ++i) v[i] = __shfl_sync(0xffffffffu, c, kLanes * i);
 }
 
+// A thread's piece of a row in shared memory.
+__device__ __forceinline__ void lds8(const float* row, int lane, f32x2 (&a)[4]) {
+  pairs_of(*reinterpret_cast<const float4*>(row + lane * 8),
+           *reinterpret_cast<const float4*>(row + lane * 8 + 4), a);
+}
+__device__ __forceinline__ void lds8(const uint8_t* row, int lane, f32x2 (&a)[4]) {
+  unpack8(*reinterpret_cast<const uint4*>(row + lane * 16), a);
+}
 template <bool kF32>
-__device__ __forceinline__ void lds_res8(const uint8_t* row, int lane, float (&a)[8]) {
-  if constexpr (kF32) {
-    const float4 lo = *reinterpret_cast<const float4*>(row + lane * 32);
-    const float4 hi = *reinterpret_cast<const float4*>(row + lane * 32 + 16);
-    a[0] = lo.x; a[1] = lo.y; a[2] = lo.z; a[3] = lo.w;
-    a[4] = hi.x; a[5] = hi.y; a[6] = hi.z; a[7] = hi.w;
-  } else {
-    unpack8(*reinterpret_cast<const uint4*>(row + lane * 16), a);
+__device__ __forceinline__ void lds_res8(const uint8_t* row, int lane, f32x2 (&a)[4]) {
+  if constexpr (kF32)
+    lds8(reinterpret_cast<const float*>(row), lane, a);
+  else
+    lds8(row, lane, a);
+}
+
+// After a wait that ran out: lets copies in flight land before the CTA exits.
+__device__ __noinline__ void drain_ring(uint64_t* full_bar, int stages) {
+  for (int i = 0; i < stages; ++i)
+    for (uint32_t q = 0; q < 2; ++q) {
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(smem_u32(&full_bar[i]), q) && global_timer_ns() - t0 < kWaitLimitNs) {
+      }
+    }
+}
+
+// The forward pass for many rows: like the gradient's ring kernel below, kRows
+// token rows at a time (adjacent in memory: one copy per array), which share the
+// two barriers.
+template <bool kF32, int kThreads, int kRows>
+__global__ void __launch_bounds__(kThreads, 1)
+    residual_norm_ring_kernel(const ResidualNormArgs a, int stages, int stage_bytes,
+                              uint32_t* err) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full_bar[kRingMaxStages];
+  __shared__ __align__(16) float red[2][kRows][32];
+  __shared__ int abort_flag;
+  volatile int* abort_v = &abort_flag;
+  const int lane = threadIdx.x;  // piece of the row
+  const int H = a.H, warps = blockDim.x >> 5;
+  const uint32_t h2 = static_cast<uint32_t>(H) * 2, hr = kF32 ? h2 * 2 : h2;
+  const bool has_post = a.post != nullptr, full_gate = a.gate_kind == kGateFull;
+  const uint32_t at_x = kRows * h2, at_g = at_x + kRows * hr;  // arrays of a stage: y, x, gate
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(smem_u32(&full_bar[s]), 1);
+    abort_flag = 0;
+    mbar_fence_init();
   }
+  pdl_launch_dependents();
+  pdl_wait();
+  __syncthreads();
+
+  auto fetch = [&](int t, int s) {  // one thread
+    const uint32_t bar = smem_u32(&full_bar[s]);
+    const uint32_t st = smem_u32(smem) + static_cast<uint32_t>(s) * stage_bytes;
+    const uint32_t n = min(kRows, a.T - t);
+    const size_t base = static_cast<size_t>(t) * H;
+    mbar_arrive_expect_tx(bar, n * (h2 + hr + (full_gate ? h2 : 0)));
+    bulk_load(st, a.block + base, n * h2, bar);
+    bulk_load(st + at_x, static_cast<const uint8_t*>(a.residual) + base * (kF32 ? 4 : 2), n * hr,
+              bar);
+    if (full_gate) bulk_load(st + at_g, static_cast<const uint16_t*>(a.gate) + base, n * h2, bar);
+  };
+  const int step = gridDim.x * kRows;
+  if (threadIdx.x == 0)
+    for (int s = 0; s < stages; ++s) {
+      const int64_t t = static_cast<int64_t>(blockIdx.x) * kRows + static_cast<int64_t>(s) * step;
+      if (t < a.T) fetch(static_cast<int>(t), s);
+    }
+
+  const int col = lane * 8;
+  const bool on = col < H;
+  f32x2 gp[4], gn[4];  // post weight (times a channel gate), next weight
+#pragma unroll
+  for (int i = 0; i < 4; ++i) gp[i] = both(1.f), gn[i] = both(0.f);
+  if (on && has_post) load8(a.post + col, gp);
+  if (on && a.next != nullptr) load8(a.next + col, gn);
+  if (on && a.gate_kind == kGateChannel) {
+    f32x2 g[4];
+    load8(static_cast<const float*>(a.gate) + col, g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) gp[i] = mul2(gp[i], g[i]);
+  }
+  const float inv_h = 1.0f / static_cast<float>(H);
+  const f32x2 scale = both(a.scale);
+  int s = 0;
+  uint32_t parity = 0;
+  bool ok = true;
+  for (int t = blockIdx.x * kRows; t < a.T; t += step) {
+    const uint8_t* st = smem + static_cast<size_t>(s) * stage_bytes;
+    if (ok) ok = mbar_wait(smem_u32(&full_bar[s]), parity, err, abort_v);
+    float sum[kRows], factor[kRows];  // of y: r1 and a token gate
+    uint4 y_raw[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      y_raw[r] = make_uint4(0, 0, 0, 0);
+      if (on && t + r < a.T) y_raw[r] = *reinterpret_cast<const uint4*>(st + r * h2 + lane * 16);
+      factor[r] = a.gate_kind == kGateToken && t + r < a.T
+                      ? __ldg(static_cast<const float*>(a.gate) + t + r)
+                      : 1.f;
+      f32x2 f[4], q = both(0.f);
+      unpack8(y_raw[r], f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q = fma2(f[i], f[i], q);
+      sum[r] = sum2(q);
+    }
+    if (has_post) {
+      cta_sum<kRows>(sum, red[0], warps);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) factor[r] *= 1.0f / sqrtf(sum[r] * inv_h + a.eps);
+    }
+    f32x2 v[kRows][4];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      f32x2 q = both(0.f);
+      if (on && t + r < a.T) {
+        f32x2 f[4];
+        const f32x2 c = both(factor[r]);
+        unpack8(y_raw[r], f);
+        lds_res8<kF32>(st + at_x + r * hr, lane, v[r]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = mul2(mul2(f[i], c), gp[i]);
+        if (full_gate) {
+          f32x2 g[4];
+          lds8(st + at_g + r * h2, lane, g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], g[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[r][i] = fma2(scale, v[r][i], f[i]);
+          q = fma2(v[r][i], v[r][i], q);
+        }
+        store_res8<kF32>(a.residual_out, static_cast<size_t>(t + r) * H + col, v[r]);
+      }
+      sum[r] = sum2(q);
+    }
+    // Also without a second norm: after this barrier all threads are done with the stage.
+    cta_sum<kRows>(sum, red[1], warps);
+    if (threadIdx.x == 0 && ok && t + static_cast<int64_t>(stages) * step < a.T)
+      fetch(t + stages * step, s);
+    if (a.next != nullptr) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const f32x2 r2 = both(1.0f / sqrtf(sum[r] * inv_h + a.eps));
+        if (on && t + r < a.T) {
+          f32x2 o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = mul2(mul2(v[r][i], r2), gn[i]);
+          *reinterpret_cast<uint4*>(a.next_out + static_cast<size_t>(t + r) * H + col) = pack8(o);
+        }
+      }
+    }
+    if (++s == stages) s = 0, parity ^= 1;
+  }
+  if (*abort_v && threadIdx.x == 0) drain_ring(full_bar, stages);
 }
 
 template <bool kF32, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
     residual_norm_backward_ring_kernel(const ResidualNormBackwardArgs a, int stages,
                                        int stage_bytes, uint32_t* err) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -438,7 +627,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Arrays of a stage: y, v, dz, dv, gate.
   const uint32_t at_v = h2, at_z = at_v + hr, at_d = at_z + (has_next ? h2 : 0),
                  at_g = at_d + (has_dv ? hr : 0);
-  float* s_gate = reinterpret_cast<float*>(smem + static_cast<size_t>(stages) * stage_bytes);
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(smem_u32(&full_bar[s]), 1);
     abort_flag = 0;
@@ -467,120 +655,120 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int col = lane * 8;
   const bool on = col < H;
-  float gp[8], gn[8], acc_p[8] = {}, acc_n[8] = {};
+  // gp: post weight, times a channel gate; gn: next weight. acc_p sums
+  // d * gate * yh (d * yh with a channel gate), acc_n dz * vh.
+  f32x2 gp[4], gn[4], acc_p[4], acc_n[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) gp[i] = 1.f, gn[i] = 0.f;
+  for (int i = 0; i < 4; ++i) gp[i] = both(1.f), gn[i] = acc_p[i] = acc_n[i] = both(0.f);
   if (on && has_post) load8(a.post + col, gp);
   if (on && has_next) load8(a.next + col, gn);
   if (on && a.gate_kind == kGateChannel) {
-    float g[8];
+    f32x2 g[4];
     load8(static_cast<const float*>(a.gate) + col, g);
-    store_res8<true>(s_gate, col, g);  // read back by the same thread
+#pragma unroll
+    for (int i = 0; i < 4; ++i) gp[i] = mul2(gp[i], g[i]);
   }
   const float inv_h = 1.0f / static_cast<float>(H);
+  const f32x2 scale = both(a.scale);
   int s = 0;
   uint32_t parity = 0;
   bool ok = true;
   for (int t = blockIdx.x; t < a.T; t += step) {
     const uint8_t* st = smem + static_cast<size_t>(s) * stage_bytes;
+    const float gt =
+        a.gate_kind == kGateToken ? __ldg(static_cast<const float*>(a.gate) + t) : 1.f;
     if (ok) ok = mbar_wait(smem_u32(&full_bar[s]), parity, err, abort_v);
     float sum[4] = {0.f, 0.f, 0.f, 0.f};  // y y, v v, a v
     uint4 y_raw = make_uint4(0, 0, 0, 0);
     if (on) {
-      float f[8];
+      f32x2 f[4], q = both(0.f);
       y_raw = *reinterpret_cast<const uint4*>(st + lane * 16);
       unpack8(y_raw, f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[0] = fmaf(f[i], f[i], sum[0]);
+      for (int i = 0; i < 4; ++i) q = fma2(f[i], f[i], q);
+      sum[0] = sum2(q);
       if (has_next) {
-        float z[8];
+        f32x2 z[4], av = both(0.f);
+        q = both(0.f);
         lds_res8<kF32>(st + at_v, lane, f);
-        unpack8(*reinterpret_cast<const uint4*>(st + at_z + lane * 16), z);
+        lds8(st + at_z, lane, z);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sum[1] = fmaf(f[i], f[i], sum[1]);
-          sum[2] = fmaf(z[i] * gn[i], f[i], sum[2]);
+        for (int i = 0; i < 4; ++i) {
+          q = fma2(f[i], f[i], q);
+          av = fma2(mul2(z[i], gn[i]), f[i], av);
         }
+        sum[1] = sum2(q);
+        sum[2] = sum2(av);
       }
     }
-    cta_sum4(sum, red[0], warps);
+    cta_sum<4>(sum, red[0], warps);
     const float r1 = has_post ? 1.0f / sqrtf(sum[0] * inv_h + a.eps) : 1.f;
-    const float r2 = 1.0f / sqrtf(sum[1] * inv_h + a.eps);
-    const float m = sum[2] * inv_h * r2;  // mean(a * vh)
 
     const size_t base = static_cast<size_t>(t) * H + col;
-    float d[8], by[4] = {0.f, 0.f, 0.f, 0.f};  // b y, d u
+    f32x2 d[4];
+    float by[1] = {0.f};  // r1 d gp y (times a full gate): a token gate's gradient
     if (on) {
+      f32x2 f[4];
       if (has_dv) {
         lds_res8<kF32>(st + at_d, lane, d);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = 0.f;
+        for (int i = 0; i < 4; ++i) d[i] = both(0.f);
       }
-      float f[8], g[8];
       if (has_next) {
+        // d = dv + r2 a - v (r2^2 mean(a vh)), with a = dz gn
+        const float r2 = 1.0f / sqrtf(sum[1] * inv_h + a.eps);
+        const f32x2 c = both(r2), k = both(-(sum[2] * inv_h * r2 * r2 * r2));
+        f32x2 z[4];
         lds_res8<kF32>(st + at_v, lane, f);
-        unpack8(*reinterpret_cast<const uint4*>(st + at_z + lane * 16), g);
+        lds8(st + at_z, lane, z);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float vh = f[i] * r2;
-          d[i] = fmaf(r2, fmaf(g[i], gn[i], -vh * m), d[i]);
-          acc_n[i] = fmaf(g[i], vh, acc_n[i]);
+        for (int i = 0; i < 4; ++i) {
+          z[i] = mul2(z[i], c);
+          d[i] = fma2(z[i], gn[i], fma2(k, f[i], d[i]));
+          acc_n[i] = fma2(z[i], f[i], acc_n[i]);
         }
       }
+      f32x2 g[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = a.scale * d[i];
+      for (int i = 0; i < 4; ++i) g[i] = mul2(scale, d[i]);
       store_res8<kF32>(a.grad_residual, base, g);
       unpack8(y_raw, f);
+      const f32x2 c = both(r1), cg = both(gt);
+      f32x2 q = both(0.f);
+      if (full_gate) lds8(st + at_g, lane, g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= r1;  // yh
-      if (a.gate_kind == kGateChannel) {
-        const float4 lo = *reinterpret_cast<const float4*>(s_gate + col);
-        const float4 hi = *reinterpret_cast<const float4*>(s_gate + col + 4);
-        g[0] = lo.x; g[1] = lo.y; g[2] = lo.z; g[3] = lo.w;
-        g[4] = hi.x; g[5] = hi.y; g[6] = hi.z; g[7] = hi.w;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          acc_p[i] = fmaf(d[i], f[i], acc_p[i]);
-          d[i] *= g[i] * gp[i];
-        }
-      } else {
+      for (int i = 0; i < 4; ++i) {
+        const f32x2 dr = mul2(d[i], c);
+        d[i] = mul2(dr, gp[i]);  // r1 d gp; times the gate below
         if (full_gate) {
-          unpack8(*reinterpret_cast<const uint4*>(st + at_g + lane * 16), g);
-          float o[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = d[i] * (f[i] * gp[i]);
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_gate) + base) = pack8(o);
+          acc_p[i] = fma2(mul2(dr, g[i]), f[i], acc_p[i]);
+          const f32x2 u = mul2(d[i], f[i]);  // d u
+          d[i] = mul2(d[i], g[i]);
+          g[i] = u;
         } else {
-          const float gt =
-              a.gate_kind == kGateToken ? __ldg(static_cast<const float*>(a.gate) + t) : 1.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            by[1] = fmaf(d[i], f[i] * gp[i], by[1]);
-            g[i] = gt;
-          }
+          acc_p[i] = fma2(mul2(dr, cg), f[i], acc_p[i]);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          d[i] *= g[i];
-          acc_p[i] = fmaf(d[i], f[i], acc_p[i]);
-          d[i] *= gp[i];
-        }
+        q = fma2(d[i], f[i], q);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) by[0] = fmaf(d[i], f[i], by[0]);
+      if (full_gate)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_gate) + base) = pack8(g);
+      by[0] = sum2(q);
     }
-    cta_sum4(by, red[1], warps);
+    cta_sum<1>(by, red[1], warps);
     // All threads are done with the stage.
-    if (threadIdx.x == 0 && ok && t + stages * step < a.T) fetch(t + stages * step, s);
-    if (a.gate_kind == kGateToken && threadIdx.x == 0) static_cast<float*>(a.grad_gate)[t] = by[1];
+    if (threadIdx.x == 0 && ok && t + static_cast<int64_t>(stages) * step < a.T)
+      fetch(t + stages * step, s);
+    if (a.gate_kind == kGateToken && threadIdx.x == 0) static_cast<float*>(a.grad_gate)[t] = by[0];
     if (on) {
-      if (has_post) {
-        const float m1 = by[0] * inv_h;  // mean(b * yh)
-        float f[8];
-        unpack8(y_raw, f);
+      // dy = gt (r1 b - y r1^2 mean(b yh)) with b = d gate gp
+      const f32x2 k = both(has_post ? -(by[0] * inv_h * r1 * r1 * gt) : 0.f), cg = both(gt);
+      f32x2 f[4];
+      unpack8(y_raw, f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = r1 * fmaf(-f[i] * r1, m1, d[i]);
+      for (int i = 0; i < 4; ++i) {
+        d[i] = mul2(d[i], cg);
+        if (has_post) d[i] = fma2(k, f[i], d[i]);
       }
       *reinterpret_cast<uint4*>(a.grad_block + base) = pack8(d);
     }
@@ -589,24 +777,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (on) {
     const size_t plane = static_cast<size_t>(gridDim.x) * H;
     const size_t at = static_cast<size_t>(blockIdx.x) * H + col;
-    if (has_post || a.gate_kind == kGateChannel) store_res8<true>(a.partials, at, acc_p);
-    if (has_next) store_res8<true>(a.partials + plane, at, acc_n);
+    if (has_post || a.gate_kind == kGateChannel) store8(a.partials + at, acc_p);
+    if (has_next) store8(a.partials + plane + at, acc_n);
   }
-  if (*abort_v && threadIdx.x == 0) {  // let copies in flight land before the CTA exits
-    for (int i = 0; i < stages; ++i)
-      for (uint32_t q = 0; q < 2; ++q) {
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(smem_u32(&full_bar[i]), q) &&
-               global_timer_ns() - t0 < kWaitLimitNs) {
-        }
-      }
-  }
+  if (*abort_v && threadIdx.x == 0) drain_ring(full_bar, stages);
 }
 
 struct RingPlan {
   int stages = 0, stage_bytes = 0, threads = 0;
   size_t smem = 0;
 };
+
+// The forward ring; stages == 0 when the direct kernel takes the call.
+RingPlan ring_plan(const ResidualNormArgs& a, int rows, int num_sms) {
+  RingPlan r;
+  if (a.H < kForwardRingMinH || a.H > kRingMaxH || a.T < kRingMinWaves * num_sms) return r;
+  const int h2 = a.H * 2;
+  const int bytes = h2 + (a.residual_f32 ? 2 * h2 : h2) + (a.gate_kind == kGateFull ? h2 : 0);
+  r.stage_bytes = (rows * bytes + 127) / 128 * 128;
+  r.threads = ring_threads(a.H);
+  r.stages = static_cast<int>(std::min<size_t>(kRingMaxStages, kRingSmem / r.stage_bytes));
+  r.smem = static_cast<size_t>(r.stages) * r.stage_bytes;
+  return r;
+}
 
 // The ring for this call; stages == 0 when the direct kernel takes it.
 RingPlan ring_plan(const ResidualNormBackwardArgs& a) {
@@ -616,12 +809,11 @@ RingPlan ring_plan(const ResidualNormBackwardArgs& a) {
   const int bytes = h2 + hr + (a.next != nullptr ? h2 : 0) +
                     (a.grad_residual_out != nullptr ? hr : 0) +
                     (a.gate_kind == kGateFull ? h2 : 0);
-  const size_t gate = a.gate_kind == kGateChannel ? static_cast<size_t>(a.H) * 4 : 0;
   r.stage_bytes = (bytes + 127) / 128 * 128;
-  r.stages = static_cast<int>(
-      std::min<size_t>(kRingMaxStages, (kRingSmem - gate) / r.stage_bytes));
-  r.threads = (a.H / 8 + 31) / 32 * 32;
-  r.smem = static_cast<size_t>(r.stages) * r.stage_bytes + gate;
+  r.threads = ring_threads(a.H);
+  r.stages =
+      static_cast<int>(std::min<size_t>(kRingMaxStages, ring_smem(r.threads) / r.stage_bytes));
+  r.smem = static_cast<size_t>(r.stages) * r.stage_bytes;
   return r;
 }
 
@@ -668,10 +860,10 @@ __global__ void __launch_bounds__(kReduceCols* kReduceSlices)
   if (grad_gate != nullptr) *reinterpret_cast<float4*>(grad_gate + col) = times(post);
 }
 
-// CTAs of the backward kernels: one per SM for the ring, about 1024 threads per SM
-// for the direct one.
+// CTAs of the backward kernels: all resident.
 int backward_grid(int T, int H, int num_sms) {
-  if (H >= kRingMinH && H <= kRingMaxH) return std::min(T, num_sms);
+  if (H >= kRingMinH && H <= kRingMaxH)
+    return std::min(T, num_sms * ring_ctas_per_sm(ring_threads(H)));
   const Shape s = shape_of(H);
   return std::min((T + s.per_cta - 1) / s.per_cta, num_sms * std::max(1, 1024 / s.threads));
 }
@@ -685,6 +877,7 @@ int residual_norm_partial_rows(int T, int H) {
 namespace {
 
 typedef void (*BackwardKernel)(const ResidualNormBackwardArgs, int);
+typedef void (*ForwardRingKernel)(const ResidualNormArgs, int, int, uint32_t*);
 typedef void (*RingKernel)(const ResidualNormBackwardArgs, int, int, uint32_t*);
 
 BackwardKernel backward_kernel(int pieces, bool f32) {
@@ -694,7 +887,29 @@ BackwardKernel backward_kernel(int pieces, bool f32) {
   }
 }
 
+template <int kRows>
+ForwardRingKernel forward_ring_kernel(int threads, bool f32) {
+  if (threads <= 640)
+    return f32 ? residual_norm_ring_kernel<true, 640, kRows>
+               : residual_norm_ring_kernel<false, 640, kRows>;
+  if (threads <= 896)
+    return f32 ? residual_norm_ring_kernel<true, 896, kRows>
+               : residual_norm_ring_kernel<false, 896, kRows>;
+  return f32 ? residual_norm_ring_kernel<true, 1024, kRows>
+             : residual_norm_ring_kernel<false, 1024, kRows>;
+}
+
+ForwardRingKernel forward_ring_kernel(int rows, int threads, bool f32) {
+  return rows == 2 ? forward_ring_kernel<2>(threads, f32) : forward_ring_kernel<1>(threads, f32);
+}
+
 RingKernel ring_kernel(int threads, bool f32) {
+  if (threads <= 288)
+    return f32 ? residual_norm_backward_ring_kernel<true, 288>
+               : residual_norm_backward_ring_kernel<false, 288>;
+  if (threads <= 448)
+    return f32 ? residual_norm_backward_ring_kernel<true, 448>
+               : residual_norm_backward_ring_kernel<false, 448>;
   if (threads <= 640)
     return f32 ? residual_norm_backward_ring_kernel<true, 640>
                : residual_norm_backward_ring_kernel<false, 640>;
@@ -713,17 +928,31 @@ cudaError_t setup_residual_norm(const DeviceInfo&) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          2 * 16384 * static_cast<int>(sizeof(float)));
     if (e != cudaSuccess) return e;
-    for (int threads : {640, 896, 1024})
+    for (int rows : {1, 2})
+      for (int threads : {640, 896, 1024})
+        if ((e = cudaFuncSetAttribute(forward_ring_kernel(rows, threads, f32),
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(kRingSmem))) != cudaSuccess)
+          return e;
+    for (int threads : {288, 448, 640, 896, 1024})
       if ((e = cudaFuncSetAttribute(ring_kernel(threads, f32),
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(kRingSmem))) != cudaSuccess)
+                                    static_cast<int>(ring_smem(threads)))) != cudaSuccess)
         return e;
   }
   return cudaSuccess;
 }
 
-cudaError_t launch_residual_norm(const ResidualNormArgs& a, const DeviceInfo&,
+cudaError_t launch_residual_norm(const ResidualNormArgs& a, const DeviceInfo& dev,
                                  cudaStream_t stream) {
+  int rows = 2;
+  RingPlan ring = ring_plan(a, rows, dev.num_sms);
+  if (ring.stages == 1) ring = ring_plan(a, rows = 1, dev.num_sms);
+  if (ring.stages != 0)
+    return launch_dependent(forward_ring_kernel(rows, ring.threads, a.residual_f32),
+                            dim3(std::min((a.T + rows - 1) / rows, dev.num_sms)),
+                            dim3(ring.threads), ring.smem, stream, a, ring.stages,
+                            ring.stage_bytes, dev.err_word);
   const Shape s = shape_of(a.H);
   const dim3 grid((a.T + s.per_cta - 1) / s.per_cta);
   void (*k)(const ResidualNormArgs, int) =

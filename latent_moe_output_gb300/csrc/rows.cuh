@@ -40,6 +40,51 @@ __device__ __forceinline__ uint4 pack8(const float (&a)[8]) {
                     pack_bf16x2(a[6], a[7]));
 }
 
+// Two FP32 values in a register pair: one packed instruction does both, with the
+// same rounding as the scalar one.
+typedef unsigned long long f32x2;
+
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float v) { return pair(v, v); }
+__device__ __forceinline__ void split(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ float sum2(f32x2 v) {
+  float lo, hi;
+  split(v, lo, hi);
+  return lo + hi;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, f32x2 (&a)[4]) {
+  a[0] = pair(bf16_lo(v.x), bf16_hi(v.x));
+  a[1] = pair(bf16_lo(v.y), bf16_hi(v.y));
+  a[2] = pair(bf16_lo(v.z), bf16_hi(v.z));
+  a[3] = pair(bf16_lo(v.w), bf16_hi(v.w));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(f32x2 v) {
+  float lo, hi;
+  split(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ uint4 pack8(const f32x2 (&a)[4]) {
+  return make_uint4(pack_bf16x2(a[0]), pack_bf16x2(a[1]), pack_bf16x2(a[2]), pack_bf16x2(a[3]));
+}
+
 // One kernel launch as a programmatic dependent of the work before it on the
 // stream: the kernel may start early and must call pdl_wait() before it reads
 // or writes memory.
