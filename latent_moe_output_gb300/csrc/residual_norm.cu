@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kMaxThreads)
 // The gradient for 1024 < H <= 8192: one CTA per SM walks over token rows, one
 // 8-element piece of the row per thread. The rows (up to five arrays) come through
 // a ring of stages with bulk copies that run ahead of the arithmetic; a stage is
-// refilled once all threads are past the row's second barrier.
+// refilled once all threads are past the next row's barrier.
 constexpr int kRingMinH = 1032, kRingMaxH = 8192;
 constexpr int kRingMaxStages = 6;
 constexpr int kRingMinWaves = 4;  // forward: rows per SM
@@ -414,38 +414,41 @@ constexpr size_t ring_smem(int threads) {
 }
 constexpr int ring_threads(int H) { return (H / 8 + 31) / 32 * 32; }
 
-// Sums of one, two or four values over the CTA with one barrier: halving exchanges
-// leave a lane with a part of one value, one partial per warp goes to shared memory,
-// and each warp adds the warps' partials again. `red` is [kValues][32].
+// Sums of 1, 2, 4 or 8 values over the CTA with one barrier: halving exchanges leave
+// a lane with a part of one value, one partial per warp goes to shared memory, and
+// each warp adds the warps' partials again. `red` is [kValues][32], zero where there
+// is no warp; consecutive calls use different ones.
 template <int kValues>
-__device__ __forceinline__ void cta_sum(float (&v)[kValues], float (*red)[32], int warps) {
+__device__ __forceinline__ void cta_sum(float (&v)[kValues], float (*red)[32]) {
   constexpr int kLanes = 32 / kValues;  // lanes per value
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float c = v[0];
-  if constexpr (kValues == 4) {
-    const bool up16 = lane & 16, up8 = lane & 8;
-    const float a = (up16 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up16 ? v[0] : v[2], 16);
-    const float b = (up16 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, up16 ? v[1] : v[3], 16);
-    c = (up8 ? b : a) + __shfl_xor_sync(0xffffffffu, up8 ? a : b, 8);
-  } else if constexpr (kValues == 2) {
-    const bool up16 = lane & 16;
-    c = (up16 ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up16 ? v[0] : v[1], 16);
+  float w[kValues];
+#pragma unroll
+  for (int i = 0; i < kValues; ++i) w[i] = v[i];
+#pragma unroll
+  for (int n = kValues / 2, o = 16; n > 0; n /= 2, o /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      w[i] = (up ? w[n + i] : w[i]) + __shfl_xor_sync(0xffffffffu, up ? w[i] : w[n + i], o);
   }
+  float c = w[0];
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
   const int which = lane / kLanes, at = (lane % kLanes) * kValues;
   if (lane % kLanes == 0) red[which][warp] = c;
   __syncthreads();
-  float p[kValues];  // kValues partials of this lane's value
-  if constexpr (kValues == 4)
-    *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(&red[which][at]);
-  else if constexpr (kValues == 2)
-    *reinterpret_cast<float2*>(p) = *reinterpret_cast<const float2*>(&red[which][at]);
-  else
-    p[0] = red[0][at];
   c = 0.f;
+  if constexpr (kValues >= 4) {
 #pragma unroll
-  for (int i = 0; i < kValues; ++i) c += at + i < warps ? p[i] : 0.f;
+    for (int i = 0; i < kValues; i += 4) {
+      const float4 p = *reinterpret_cast<const float4*>(&red[which][at + i]);
+      c += (p.x + p.y) + (p.z + p.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kValues; ++i) c += red[which][at + i];
+  }
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
 #pragma unroll
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int abort_flag;
   volatile int* abort_v = &abort_flag;
   const int lane = threadIdx.x;  // piece of the row
-  const int H = a.H, warps = blockDim.x >> 5;
+  const int H = a.H;
   const uint32_t h2 = static_cast<uint32_t>(H) * 2, hr = kF32 ? h2 * 2 : h2;
   const bool has_post = a.post != nullptr, full_gate = a.gate_kind == kGateFull;
   const uint32_t at_x = kRows * h2, at_g = at_x + kRows * hr;  // arrays of a stage: y, x, gate
@@ -500,6 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_flag = 0;
     mbar_fence_init();
   }
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(red) / 4); i += blockDim.x)
+    (&red[0][0][0])[i] = 0.f;
   pdl_launch_dependents();
   pdl_wait();
   __syncthreads();
@@ -559,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sum[r] = sum2(q);
     }
     if (has_post) {
-      cta_sum<kRows>(sum, red[0], warps);
+      cta_sum<kRows>(sum, red[0]);
 #pragma unroll
       for (int r = 0; r < kRows; ++r) factor[r] *= 1.0f / sqrtf(sum[r] * inv_h + a.eps);
     }
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sum[r] = sum2(q);
     }
     // Also without a second norm: after this barrier all threads are done with the stage.
-    cta_sum<kRows>(sum, red[1], warps);
+    cta_sum<kRows>(sum, red[1]);
     if (threadIdx.x == 0 && ok && t + static_cast<int64_t>(stages) * step < a.T)
       fetch(t + stages * step, s);
     if (a.next != nullptr) {
@@ -616,11 +621,11 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
                                        int stage_bytes, uint32_t* err) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full_bar[kRingMaxStages];
-  __shared__ __align__(16) float red[2][4][32];
+  __shared__ __align__(16) float red[2][8][32];
   __shared__ int abort_flag;
   volatile int* abort_v = &abort_flag;
   const int lane = threadIdx.x;  // piece of the row
-  const int H = a.H, warps = blockDim.x >> 5;
+  const int H = a.H;
   const uint32_t h2 = static_cast<uint32_t>(H) * 2, hr = kF32 ? h2 * 2 : h2;
   const bool has_dv = a.grad_residual_out != nullptr, has_next = a.next != nullptr;
   const bool has_post = a.post != nullptr, full_gate = a.gate_kind == kGateFull;
@@ -632,6 +637,8 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
     abort_flag = 0;
     mbar_fence_init();
   }
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(red) / 4); i += blockDim.x)
+    (&red[0][0][0])[i] = 0.f;
   pdl_launch_dependents();
   pdl_wait();
   __syncthreads();
@@ -670,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
   }
   const float inv_h = 1.0f / static_cast<float>(H);
   const f32x2 scale = both(a.scale);
-  int s = 0;
+  int s = 0, turn = 0, last = -1;  // last: the row before
   uint32_t parity = 0;
   bool ok = true;
   for (int t = blockIdx.x; t < a.T; t += step) {
@@ -678,37 +685,59 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
     const float gt =
         a.gate_kind == kGateToken ? __ldg(static_cast<const float*>(a.gate) + t) : 1.f;
     if (ok) ok = mbar_wait(smem_u32(&full_bar[s]), parity, err, abort_v);
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};  // y y, v v, a v
-    uint4 y_raw = make_uint4(0, 0, 0, 0);
+    // With w = gp * gate: y y, v v, a v, then the terms of mean(b yh), which is linear
+    // in d: dv w y, a w y, v w y. One reduction per row instead of two.
+    float sum[8] = {};
     if (on) {
-      f32x2 f[4], q = both(0.f);
-      y_raw = *reinterpret_cast<const uint4*>(st + lane * 16);
-      unpack8(y_raw, f);
+      f32x2 y[4], v[4], q[6];
+      lds8(st, lane, y);
+      lds_res8<kF32>(st + at_v, lane, v);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q = fma2(f[i], f[i], q);
-      sum[0] = sum2(q);
+      for (int i = 0; i < 6; ++i) q[i] = both(0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[0] = fma2(y[i], y[i], q[0]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], gp[i]);
+      if (full_gate) {
+        f32x2 g[4];
+        lds8(st + at_g, lane, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], g[i]);
+      }
       if (has_next) {
-        f32x2 z[4], av = both(0.f);
-        q = both(0.f);
-        lds_res8<kF32>(st + at_v, lane, f);
+        f32x2 z[4];
         lds8(st + at_z, lane, z);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          q = fma2(f[i], f[i], q);
-          av = fma2(mul2(z[i], gn[i]), f[i], av);
+          z[i] = mul2(z[i], gn[i]);
+          q[1] = fma2(v[i], v[i], q[1]);
+          q[2] = fma2(z[i], v[i], q[2]);
+          q[4] = fma2(z[i], y[i], q[4]);
+          q[5] = fma2(v[i], y[i], q[5]);
         }
-        sum[1] = sum2(q);
-        sum[2] = sum2(av);
       }
+      if (has_dv) {
+        lds_res8<kF32>(st + at_d, lane, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[3] = fma2(v[i], y[i], q[3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 6; ++i) sum[i] = sum2(q[i]);
     }
-    cta_sum<4>(sum, red[0], warps);
-    const float r1 = has_post ? 1.0f / sqrtf(sum[0] * inv_h + a.eps) : 1.f;
-
-    const size_t base = static_cast<size_t>(t) * H + col;
-    f32x2 d[4];
-    float by[1] = {0.f};  // r1 d gp y (times a full gate): a token gate's gradient
+    cta_sum<8>(sum, red[turn]);
+    turn ^= 1;
+    // All threads are done with the previous row's stage.
+    if (threadIdx.x == 0 && ok && last >= 0 && last + static_cast<int64_t>(stages) * step < a.T)
+      fetch(last + stages * step, s == 0 ? stages - 1 : s - 1);
+    last = t;
+    const float r1 = has_post ? rsqrtf(fmaf(sum[0], inv_h, a.eps)) : 1.f;
+    const float r2 = has_next ? rsqrtf(fmaf(sum[1], inv_h, a.eps)) : 0.f;
+    const float k2 = -(sum[2] * inv_h * r2 * r2 * r2);                    // d = dv + r2 a + k2 v
+    const float by = r1 * fmaf(k2, sum[5], fmaf(r2, sum[4], sum[3]));  // sum of b yh, gt apart
+    if (a.gate_kind == kGateToken && threadIdx.x == 0) static_cast<float*>(a.grad_gate)[t] = by;
     if (on) {
-      f32x2 f[4];
+      const size_t base = static_cast<size_t>(t) * H + col;
+      f32x2 d[4], f[4], z[4];
       if (has_dv) {
         lds_res8<kF32>(st + at_d, lane, d);
       } else {
@@ -716,10 +745,7 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
         for (int i = 0; i < 4; ++i) d[i] = both(0.f);
       }
       if (has_next) {
-        // d = dv + r2 a - v (r2^2 mean(a vh)), with a = dz gn
-        const float r2 = 1.0f / sqrtf(sum[1] * inv_h + a.eps);
-        const f32x2 c = both(r2), k = both(-(sum[2] * inv_h * r2 * r2 * r2));
-        f32x2 z[4];
+        const f32x2 c = both(r2), k = both(k2);
         lds_res8<kF32>(st + at_v, lane, f);
         lds8(st + at_z, lane, z);
 #pragma unroll
@@ -729,46 +755,35 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
           acc_n[i] = fma2(z[i], f[i], acc_n[i]);
         }
       }
-      f32x2 g[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) g[i] = mul2(scale, d[i]);
-      store_res8<kF32>(a.grad_residual, base, g);
-      unpack8(y_raw, f);
-      const f32x2 c = both(r1), cg = both(gt);
-      f32x2 q = both(0.f);
-      if (full_gate) lds8(st + at_g, lane, g);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x2 dr = mul2(d[i], c);
-        d[i] = mul2(dr, gp[i]);  // r1 d gp; times the gate below
-        if (full_gate) {
-          acc_p[i] = fma2(mul2(dr, g[i]), f[i], acc_p[i]);
-          const f32x2 u = mul2(d[i], f[i]);  // d u
-          d[i] = mul2(d[i], g[i]);
-          g[i] = u;
-        } else {
-          acc_p[i] = fma2(mul2(dr, cg), f[i], acc_p[i]);
-        }
-        q = fma2(d[i], f[i], q);
-      }
-      if (full_gate)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_gate) + base) = pack8(g);
-      by[0] = sum2(q);
-    }
-    cta_sum<1>(by, red[1], warps);
-    // All threads are done with the stage.
-    if (threadIdx.x == 0 && ok && t + static_cast<int64_t>(stages) * step < a.T)
-      fetch(t + stages * step, s);
-    if (a.gate_kind == kGateToken && threadIdx.x == 0) static_cast<float*>(a.grad_gate)[t] = by[0];
-    if (on) {
+      for (int i = 0; i < 4; ++i) z[i] = mul2(scale, d[i]);
+      store_res8<kF32>(a.grad_residual, base, z);
       // dy = gt (r1 b - y r1^2 mean(b yh)) with b = d gate gp
-      const f32x2 k = both(has_post ? -(by[0] * inv_h * r1 * r1 * gt) : 0.f), cg = both(gt);
-      f32x2 f[4];
-      unpack8(y_raw, f);
+      const f32x2 c = both(r1 * gt);
+      const f32x2 k = both(has_post ? -(by * inv_h * r1 * r1 * gt) : 0.f);
+      lds8(st, lane, f);
+      if (full_gate) {
+        lds8(st + at_g, lane, z);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        d[i] = mul2(d[i], cg);
-        if (has_post) d[i] = fma2(k, f[i], d[i]);
+        for (int i = 0; i < 4; ++i) {
+          d[i] = mul2(d[i], c);
+          const f32x2 g = z[i], e = mul2(d[i], gp[i]);
+          z[i] = mul2(e, f[i]);  // d u
+          acc_p[i] = fma2(mul2(d[i], g), f[i], acc_p[i]);
+          d[i] = mul2(e, g);
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_gate) + base) = pack8(z);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          d[i] = mul2(d[i], c);
+          acc_p[i] = fma2(d[i], f[i], acc_p[i]);
+          d[i] = mul2(d[i], gp[i]);
+        }
+      }
+      if (has_post) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = fma2(k, f[i], d[i]);
       }
       *reinterpret_cast<uint4*>(a.grad_block + base) = pack8(d);
     }
