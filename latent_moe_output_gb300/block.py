@@ -13,11 +13,12 @@ ordered by the caller, as for any torch operation.
 
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple, Optional
 
 import torch
 
-from .binding import _check, _stream_handle, load_library
+from .binding import LatentTailError, _stream_handle, load_library
 
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 _GATE_NONE, _GATE_TOKEN, _GATE_CHANNEL, _GATE_FULL = range(4)
@@ -32,30 +33,47 @@ class Dispatched(NamedTuple):
     position: torch.Tensor        # [T, K] int32: row of each choice, -1 - row without an expert
 
 
+# A call on small tensors takes a few microseconds on the GPU, so its checks read
+# each property once and the stream comes as a plain handle, without a Stream object.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_entry_points = {}
+
+
 def _ptr(t, name, dtype, shape, index):
     """Device address of ``t`` after checking it; 0 for None."""
     if t is None:
         return 0
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index \
+                and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.get_device() != index:
-        raise ValueError(f"{name} must be on CUDA device {index}" if index >= 0 else
-                         f"{name} must be on a CUDA device")
+        raise ValueError(f"{name} must be on CUDA device {index}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _index(t, name, ndim) -> int:
-    """CUDA device index of the tensor that fixes a call's shapes."""
+def _shape(t, name, ndim):
+    """Shape of a tensor that fixes a call's sizes."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != ndim:
-        raise ValueError(f"{name}: expected {ndim} dimensions, got {t.dim()}")
+    shape = t.shape
+    if len(shape) != ndim:
+        raise ValueError(f"{name}: expected {ndim} dimensions, got {len(shape)}")
+    return shape
+
+
+def _index(t, name) -> int:
+    """CUDA device index of the tensor that fixes a call's device."""
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{name} must be on a CUDA device")
@@ -73,12 +91,18 @@ def _empty(shape, dtype, index, stream):
 
 def _call(name, index, stream, *args):
     """Run one C entry point with ``index`` as the current device."""
-    if torch.cuda.current_device() != index:
+    if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(index):
             return _call(name, index, stream, *args)
-    _check(getattr(load_library(), name)(*args, _stream_handle(stream)), name)
+    fn = _entry_points.get(name)
+    if fn is None:
+        fn = _entry_points[name] = getattr(load_library(), name)
+    status = fn(*args, _raw_stream(index) if stream is None else _stream_handle(stream))
+    if status:
+        raise LatentTailError(status, name)
 
 
+@functools.lru_cache(maxsize=256)
 def dispatch_workspace_size(T: int, K: int, E: int) -> int:
     return int(load_library().latent_tail_dispatch_workspace_size(T, K, E))
 
@@ -88,12 +112,11 @@ def dispatch(x, expert_ids, E: int, rows=None, offsets=None, order=None, positio
     """Sort the choices ``expert_ids`` [T, K] (int32; anything outside [0, E) is a
     choice without an expert) by expert and copy the rows of ``x`` [T, L] to their
     places. ``x`` None sorts alone. See latent_tail_dispatch."""
-    i = _index(expert_ids, "expert_ids", 2)
-    T, K = expert_ids.shape
+    T, K = _shape(expert_ids, "expert_ids", 2)
+    i = _index(expert_ids, "expert_ids")
     L = 0
     if x is not None:
-        _index(x, "x", 2)
-        L = x.shape[1]
+        L = _shape(x, "x", 2)[1]
         if rows is None:
             rows = _empty((T * K, L), _BF16, i, stream)
     elif rows is not None:
@@ -104,10 +127,12 @@ def dispatch(x, expert_ids, E: int, rows=None, offsets=None, order=None, positio
         order = _empty((T * K,), _I32, i, stream)
     if position is None:
         position = _empty((T, K), _I32, i, stream)
+    ws = ws_bytes = 0
     need = dispatch_workspace_size(T, K, E)
-    if need and workspace is None:
-        workspace = _empty((need,), _U8, i, stream)
-    ws, ws_bytes = _workspace(workspace, i)
+    if need:
+        if workspace is None:
+            workspace = _empty((need,), _U8, i, stream)
+        ws, ws_bytes = _workspace(workspace, i)
     _call("latent_tail_dispatch", i, stream,
           _ptr(x, "x", _BF16, (T, L), i), _ptr(expert_ids, "expert_ids", _I32, (T, K), i),
           _ptr(rows, "rows", _BF16, (T * K, L), i), _ptr(offsets, "offsets", _I32, (E + 1,), i),
@@ -117,8 +142,6 @@ def dispatch(x, expert_ids, E: int, rows=None, offsets=None, order=None, positio
 
 
 def _workspace(workspace, index):
-    if workspace is None:
-        return 0, 0
     nbytes = workspace.numel() * workspace.element_size()
     return _ptr(workspace, "workspace", workspace.dtype, workspace.shape, index), nbytes
 
@@ -126,10 +149,9 @@ def _workspace(workspace, index):
 def combine(rows, position, weights=None, out=None, stream=None):
     """out[t] = sum over the routed choices k of weights[t, k] * rows[position[t, k]]
     (weights None: 1, the gradient of ``dispatch``'s copy). See latent_tail_combine."""
-    i = _index(position, "position", 2)
-    T, K = position.shape
-    _index(rows, "rows", 2)
-    L = rows.shape[1]
+    T, K = _shape(position, "position", 2)
+    i = _index(position, "position")
+    L = _shape(rows, "rows", 2)[1]
     if out is None:
         out = _empty((T, L), _BF16, i, stream)
     _call("latent_tail_combine", i, stream, _ptr(rows, "rows", _BF16, (T * K, L), i),
@@ -142,10 +164,9 @@ def combine_backward(grad_out, rows, position, weights=None, grad_rows=None, gra
                      stream=None):
     """(grad_rows, grad_weights) of ``combine``. ``rows`` None: only grad_rows, with
     None for grad_weights. See latent_tail_combine_backward."""
-    i = _index(position, "position", 2)
-    T, K = position.shape
-    _index(grad_out, "grad_out", 2)
-    L = grad_out.shape[1]
+    T, K = _shape(position, "position", 2)
+    i = _index(position, "position")
+    L = _shape(grad_out, "grad_out", 2)[1]
     if grad_rows is None:
         grad_rows = _empty((T * K, L), _BF16, i, stream)
     if grad_weights is None and rows is not None:
@@ -165,12 +186,10 @@ def expert_matvec4(x, packed, scales, offsets=None, out=None, stream=None):
     x [N, C] bf16, packed [E, M, C/2] uint8 (even c in the low four bits), scales
     [E, M, C/G] bf16 with G = 32, 64 or 128. See latent_tail_expert_matvec4 and
     ``quantize4``."""
-    i = _index(x, "x", 2)
-    N, C = x.shape
-    _index(packed, "packed", 3)
-    _index(scales, "scales", 3)
-    E, M = packed.shape[0], packed.shape[1]
-    groups = scales.shape[2]
+    N, C = _shape(x, "x", 2)
+    i = _index(x, "x")
+    E, M, _ = _shape(packed, "packed", 3)
+    groups = _shape(scales, "scales", 3)[2]
     if groups == 0 or C % groups != 0:
         raise ValueError(f"scales: {groups} groups do not divide {C} columns")
     if out is None:
@@ -227,8 +246,8 @@ def residual_norm(block, residual, post_weight, next_weight, eps: float, gate=No
     block [T, H] bf16, residual [T, H] bf16 or fp32, weights [H] fp32 or None (that
     norm is left out; next_out is then None), gate None, [T, 1] fp32, [H] fp32 or
     [T, H] bf16. residual_out may be residual itself. See latent_tail_residual_norm."""
-    i = _index(block, "block", 2)
-    T, H = block.shape
+    T, H = _shape(block, "block", 2)
+    i = _index(block, "block")
     kind, gate_dtype, gate_shape = _gate_kind(gate, T, H)
     f32 = _residual_type(residual, "residual")
     if residual_out is None:
@@ -245,6 +264,7 @@ def residual_norm(block, residual, post_weight, next_weight, eps: float, gate=No
     return residual_out, next_out
 
 
+@functools.lru_cache(maxsize=256)
 def residual_norm_backward_workspace_size(T: int, H: int) -> int:
     return int(load_library().latent_tail_residual_norm_backward_workspace_size(T, H))
 
@@ -256,8 +276,8 @@ def residual_norm_backward(grad_residual_out, grad_next, block, residual_out, po
     ``residual_norm`` (None for what was not given), from the gradients of its outputs
     (either may be None) and its stored residual_out. See
     latent_tail_residual_norm_backward."""
-    i = _index(block, "block", 2)
-    T, H = block.shape
+    T, H = _shape(block, "block", 2)
+    i = _index(block, "block")
     kind, gate_dtype, gate_shape = _gate_kind(gate, T, H)
     f32 = _residual_type(residual_out, "residual_out")
     rdt = residual_out.dtype
