@@ -55,90 +55,116 @@ __global__ void __launch_bounds__(kThreads)
   reinterpret_cast<uint4*>(out)[static_cast<size_t>(t) * nch + c] = pack8(acc);
 }
 
-// A group of `tpt` threads (a power of two, 8 to 256) per token; each thread owns
-// every tpt-th 16-byte piece of the token's row.
-__global__ void __launch_bounds__(kThreads)
+// A group of kTpt threads per token; each thread owns every kTpt-th 16-byte piece of
+// the token's row. Lane j of the group holds choice k0 + j. The rows are requested
+// first, the gradients of the rows (which do not need them) written meanwhile, the
+// products with the rows summed last; three CTAs per SM overlap the three steps (four
+// measured the same).
+template <int kTpt>
+__global__ void __launch_bounds__(kThreads, 3)
     combine_backward_kernel(const uint16_t* __restrict__ grad_out,
                             const uint16_t* __restrict__ rows,
                             const int32_t* __restrict__ position,
                             const float* __restrict__ weights, uint16_t* __restrict__ grad_rows,
-                            float* __restrict__ grad_weights, int T, int K, int nch, int tpt) {
+                            float* __restrict__ grad_weights, int T, int K, int nch) {
+  constexpr int kSpan = kTpt < 32 ? kTpt : 32;  // lanes of one token in a warp
   __shared__ float s_dot[kThreads / 32][kAhead];
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & (tpt - 1);
-  const int t = blockIdx.x * (kThreads / tpt) + threadIdx.x / tpt;
+  const int lane = threadIdx.x % kTpt, wlane = threadIdx.x & 31, first = wlane & ~(kSpan - 1);
+  const int t = blockIdx.x * (kThreads / kTpt) + threadIdx.x / kTpt;
   const bool live = t < T;
   const int n = T * K;
   const size_t at = static_cast<size_t>(t) * K;
   const uint4* g4 = reinterpret_cast<const uint4*>(grad_out) + static_cast<size_t>(t) * nch;
   const uint4* r4 = reinterpret_cast<const uint4*>(rows);
   uint4* d4 = reinterpret_cast<uint4*>(grad_rows);
+  const bool dots = grad_weights != nullptr;
   for (int k0 = 0; k0 < K; k0 += kAhead) {
-    int place[kAhead];  // row of grad_rows, or -1
-    float w[kAhead];
-    bool on[kAhead];
-    float dot[kAhead] = {};
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int k = k0 + j;
-      const bool have = live && k < K;
-      const int p = have ? position[at + k] : -1;
-      const int row = p >= 0 ? p : ~p;
-      on[j] = have && p >= 0 && p < n;
-      place[j] = have && row < n ? row : -1;
-      w[j] = !on[j] ? 0.f : weights != nullptr ? weights[at + k] : 1.f;
+    int mine = n;  // position of choice k0 + j in lane j; n: none
+    float my_w = 0.f;
+    const int j0 = wlane - first;
+    if (live && j0 < kAhead && k0 + j0 < K) {
+      mine = position[at + k0 + j0];
+      if (mine >= 0 && mine < n) my_w = weights != nullptr ? weights[at + k0 + j0] : 1.f;
     }
-    if (live) {
-      for (int c = lane; c < nch; c += tpt) {
-        const uint4 gv = ld_stream_v4(g4 + c);
-        uint4 v[kAhead];
+    float dot[kAhead] = {};
+    const int chunks = (nch + kTpt - 1) / kTpt;
+    for (int i = 0; i < chunks; ++i) {
+      const int c = lane + i * kTpt;
+      const bool have = live && c < nch;
+      uint4 v[kAhead], gv = make_uint4(0, 0, 0, 0);
+      if (have) gv = ld_stream_v4(g4 + c);
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-          v[j] = on[j] && grad_weights != nullptr
-                     ? ld_stream_v4(r4 + static_cast<size_t>(place[j]) * nch + c)
-                     : make_uint4(0, 0, 0, 0);
-        float g[8];
-        unpack8(gv, g);
+      for (int j = 0; j < kAhead; ++j) {
+        const int p = __shfl_sync(0xffffffffu, mine, first + j);
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (have && dots && p >= 0 && p < n) v[j] = ld_stream_v4(r4 + static_cast<size_t>(p) * nch + c);
+      }
+      f32x2 g[4];
+      unpack8(gv, g);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int p = __shfl_sync(0xffffffffu, mine, first + j);
+        const f32x2 w = both(__shfl_sync(0xffffffffu, my_w, first + j));
+        const int row = p >= 0 ? p : ~p;
+        f32x2 d[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) d[q] = mul2(w, g[q]);
+        // A choice without an expert gets zeros even where grad_out is not finite.
+        if (have && row < n)
+          d4[static_cast<size_t>(row) * nch + c] = p >= 0 ? pack8(d) : make_uint4(0, 0, 0, 0);
+      }
+      if (dots) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-          if (place[j] < 0) continue;
-          float a[8];
-          if (on[j]) {
-            unpack8(v[j], a);
+          f32x2 a[4], q = both(0.f);
+          unpack8(v[j], a);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], a[i], dot[j]);
-          }
-          // A choice without an expert gets zeros even where grad_out is not finite.
-#pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] = on[j] ? w[j] * g[i] : 0.f;
-          d4[static_cast<size_t>(place[j]) * nch + c] = pack8(a);
+          for (int u = 0; u < 4; ++u) q = fma2(g[u], a[u], q);
+          const int p = __shfl_sync(0xffffffffu, mine, first + j);
+          if (p >= 0 && p < n) dot[j] += sum2(q);  // (zeros times an infinity are not added)
         }
       }
     }
-    if (grad_weights == nullptr) continue;
-    const int span = tpt < 32 ? tpt : 32;
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      for (int o = span / 2; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-    if (tpt > 32) {  // the warps of a token add up in warp order
-      const int warp = threadIdx.x >> 5;
-      __syncthreads();
-      if ((threadIdx.x & 31) == 0)
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) s_dot[warp][j] = dot[j];
-      __syncthreads();
-      const int j = lane;
-      if (live && j < kAhead && k0 + j < K) {
-        const int w0 = threadIdx.x / tpt * (tpt / 32);
-        float sum = 0.f;
-        for (int i = 0; i < tpt / 32; ++i) sum += s_dot[w0 + i][j];
-        grad_weights[at + k0 + j] = sum;
-      }
-    } else if (live && lane == 0) {
+    if (!dots) continue;
+    if constexpr (kTpt < 32) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j)
-        if (k0 + j < K) grad_weights[at + k0 + j] = dot[j];
+#pragma unroll
+        for (int o = kSpan / 2; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+      if (live && lane == 0)
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (k0 + j < K) grad_weights[at + k0 + j] = dot[j];
+    } else {
+      // Halving exchanges leave lanes 4 j .. 4 j + 3 with parts of dot[j].
+#pragma unroll
+      for (int m = kAhead / 2, o = 16; m > 0; m /= 2, o /= 2) {
+        const bool up = wlane & o;
+#pragma unroll
+        for (int j = 0; j < m; ++j)
+          dot[j] = (up ? dot[m + j] : dot[j]) +
+                   __shfl_xor_sync(0xffffffffu, up ? dot[j] : dot[m + j], o);
+      }
+      float sum = dot[0];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      const int j = wlane >> 2;
+      if constexpr (kTpt == 32) {
+        if (live && (wlane & 3) == 0 && k0 + j < K) grad_weights[at + k0 + j] = sum;
+      } else {  // the warps of a token add up in warp order
+        const int warp = threadIdx.x >> 5;
+        if (k0 > 0) __syncthreads();
+        if ((wlane & 3) == 0) s_dot[warp][j] = sum;
+        __syncthreads();
+        if (live && lane < kAhead && k0 + lane < K) {
+          sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < kTpt / 32; ++i) sum += s_dot[threadIdx.x / kTpt * (kTpt / 32) + i][lane];
+          grad_weights[at + k0 + lane] = sum;
+        }
+      }
     }
   }
 }
@@ -159,10 +185,16 @@ cudaError_t launch_combine_backward(const CombineBackwardArgs& a, const DeviceIn
   const int nch = a.L / 8;
   int tpt = 8;
   while (tpt < nch && tpt < kThreads) tpt *= 2;
+  auto* k = tpt == 8     ? combine_backward_kernel<8>
+            : tpt == 16  ? combine_backward_kernel<16>
+            : tpt == 32  ? combine_backward_kernel<32>
+            : tpt == 64  ? combine_backward_kernel<64>
+            : tpt == 128 ? combine_backward_kernel<128>
+                         : combine_backward_kernel<256>;
   const int per_cta = kThreads / tpt;
-  return launch_dependent(combine_backward_kernel, dim3((a.T + per_cta - 1) / per_cta),
-                          dim3(kThreads), 0, stream, a.grad_out, a.rows, a.position, a.weights,
-                          a.grad_rows, a.grad_weights, a.T, a.K, nch, tpt);
+  return launch_dependent(k, dim3((a.T + per_cta - 1) / per_cta), dim3(kThreads), 0, stream,
+                          a.grad_out, a.rows, a.position, a.weights, a.grad_rows, a.grad_weights,
+                          a.T, a.K, nch);
 }
 
 }  // namespace lt
