@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(kMaxThreads)
 }
 
 // ------------------------------------------------------------ ring kernel
-// The gradient for 1024 < H <= 8192: one CTA per SM walks over token rows, one
-// 8-element piece of the row per thread. The rows (up to five arrays) come through
+// The gradient for 1024 < H <= 8192: one to three CTAs per SM walk over token rows, one
+// or two 8-element pieces of the row per thread. The rows (up to five arrays) come through
 // a ring of stages with bulk copies that run ahead of the arithmetic; a stage is
 // refilled once all threads are past the next row's barrier.
 constexpr int kRingMinH = 1032, kRingMaxH = 8192;
@@ -409,10 +409,21 @@ constexpr int kForwardRingMinH = 4096;
 
 // Narrow rows have few threads: several CTAs then share an SM (72 registers each).
 constexpr int ring_ctas_per_sm(int threads) { return threads <= 288 ? 3 : threads <= 448 ? 2 : 1; }
-constexpr size_t ring_smem(int threads) {
-  return ring_ctas_per_sm(threads) == 1 ? kRingSmem : kRingSmem / ring_ctas_per_sm(threads) - 2048;
-}
 constexpr int ring_threads(int H) { return (H / 8 + 31) / 32 * 32; }
+
+// The gradient's ring: rows of more than 448 pieces take two per thread (half the
+// warps to synchronize and to reduce over, with twice the work each).
+constexpr int backward_ring_pieces(int H) { return H / 8 > 448 ? 2 : 1; }
+constexpr int backward_ring_threads(int H) {
+  const int per_thread = backward_ring_pieces(H);
+  return ((H / 8 + per_thread - 1) / per_thread + 31) / 32 * 32;
+}
+constexpr int backward_ring_ctas(int H) {
+  return backward_ring_pieces(H) == 2 ? 1 : ring_ctas_per_sm(ring_threads(H));
+}
+constexpr size_t backward_ring_smem(int H) {
+  return backward_ring_ctas(H) == 1 ? kRingSmem : kRingSmem / backward_ring_ctas(H) - 2048;
+}
 
 // Sums of 1, 2, 4 or 8 values over the CTA with one barrier: halving exchanges leave
 // a lane with a part of one value, one partial per warp goes to shared memory, and
@@ -615,8 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (*abort_v && threadIdx.x == 0) drain_ring(full_bar, stages);
 }
 
-template <bool kF32, int kThreads>
-__global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
+template <bool kF32, int kThreads, int kPieces>
+__global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(kThreads))
     residual_norm_backward_ring_kernel(const ResidualNormBackwardArgs a, int stages,
                                        int stage_bytes, uint32_t* err) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -624,7 +635,6 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
   __shared__ __align__(16) float red[2][8][32];
   __shared__ int abort_flag;
   volatile int* abort_v = &abort_flag;
-  const int lane = threadIdx.x;  // piece of the row
   const int H = a.H;
   const uint32_t h2 = static_cast<uint32_t>(H) * 2, hr = kF32 ? h2 * 2 : h2;
   const bool has_dv = a.grad_residual_out != nullptr, has_next = a.next != nullptr;
@@ -660,20 +670,26 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
     for (int s = 0; s < stages && static_cast<int>(blockIdx.x) + s * step < a.T; ++s)
       fetch(blockIdx.x + s * step, s);
 
-  const int col = lane * 8;
-  const bool on = col < H;
   // gp: post weight, times a channel gate; gn: next weight. acc_p sums
   // d * gate * yh (d * yh with a channel gate), acc_n dz * vh.
-  f32x2 gp[4], gn[4], acc_p[4], acc_n[4];
+  f32x2 gp[kPieces][4], gn[kPieces][4], acc_p[kPieces][4], acc_n[kPieces][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) gp[i] = both(1.f), gn[i] = acc_p[i] = acc_n[i] = both(0.f);
-  if (on && has_post) load8(a.post + col, gp);
-  if (on && has_next) load8(a.next + col, gn);
-  if (on && a.gate_kind == kGateChannel) {
-    f32x2 g[4];
-    load8(static_cast<const float*>(a.gate) + col, g);
+  for (int e = 0; e < kPieces; ++e) {
+    const int col = (threadIdx.x + e * blockDim.x) * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) gp[i] = mul2(gp[i], g[i]);
+    for (int i = 0; i < 4; ++i) {
+      gp[e][i] = both(1.f);
+      gn[e][i] = acc_p[e][i] = acc_n[e][i] = both(0.f);
+    }
+    if (col >= H) continue;
+    if (has_post) load8(a.post + col, gp[e]);
+    if (has_next) load8(a.next + col, gn[e]);
+    if (a.gate_kind == kGateChannel) {
+      f32x2 g[4];
+      load8(static_cast<const float*>(a.gate) + col, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) gp[e][i] = mul2(gp[e][i], g[i]);
+    }
   }
   const float inv_h = 1.0f / static_cast<float>(H);
   const f32x2 scale = both(a.scale);
@@ -688,16 +704,20 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
     // With w = gp * gate: y y, v v, a v, then the terms of mean(b yh), which is linear
     // in d: dv w y, a w y, v w y. One reduction per row instead of two.
     float sum[8] = {};
-    if (on) {
-      f32x2 y[4], v[4], q[6];
+    f32x2 q[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) q[i] = both(0.f);
+#pragma unroll
+    for (int e = 0; e < kPieces; ++e) {
+      const int lane = threadIdx.x + e * blockDim.x;  // piece of the row
+      if (lane * 8 >= H) continue;
+      f32x2 y[4], v[4];
       lds8(st, lane, y);
       lds_res8<kF32>(st + at_v, lane, v);
 #pragma unroll
-      for (int i = 0; i < 6; ++i) q[i] = both(0.f);
-#pragma unroll
       for (int i = 0; i < 4; ++i) q[0] = fma2(y[i], y[i], q[0]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], gp[i]);
+      for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], gp[e][i]);
       if (full_gate) {
         f32x2 g[4];
         lds8(st + at_g, lane, g);
@@ -709,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
         lds8(st + at_z, lane, z);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          z[i] = mul2(z[i], gn[i]);
+          z[i] = mul2(z[i], gn[e][i]);
           q[1] = fma2(v[i], v[i], q[1]);
           q[2] = fma2(z[i], v[i], q[2]);
           q[4] = fma2(z[i], y[i], q[4]);
@@ -721,9 +741,9 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
 #pragma unroll
         for (int i = 0; i < 4; ++i) q[3] = fma2(v[i], y[i], q[3]);
       }
-#pragma unroll
-      for (int i = 0; i < 6; ++i) sum[i] = sum2(q[i]);
     }
+#pragma unroll
+    for (int i = 0; i < 6; ++i) sum[i] = sum2(q[i]);
     cta_sum<8>(sum, red[turn]);
     turn ^= 1;
     // All threads are done with the previous row's stage.
@@ -735,8 +755,11 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
     const float k2 = -(sum[2] * inv_h * r2 * r2 * r2);                    // d = dv + r2 a + k2 v
     const float by = r1 * fmaf(k2, sum[5], fmaf(r2, sum[4], sum[3]));  // sum of b yh, gt apart
     if (a.gate_kind == kGateToken && threadIdx.x == 0) static_cast<float*>(a.grad_gate)[t] = by;
-    if (on) {
-      const size_t base = static_cast<size_t>(t) * H + col;
+#pragma unroll
+    for (int e = 0; e < kPieces; ++e) {
+      const int lane = threadIdx.x + e * blockDim.x;
+      if (lane * 8 >= H) continue;
+      const size_t base = static_cast<size_t>(t) * H + lane * 8;
       f32x2 d[4], f[4], z[4];
       if (has_dv) {
         lds_res8<kF32>(st + at_d, lane, d);
@@ -751,8 +774,8 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           z[i] = mul2(z[i], c);
-          d[i] = fma2(z[i], gn[i], fma2(k, f[i], d[i]));
-          acc_n[i] = fma2(z[i], f[i], acc_n[i]);
+          d[i] = fma2(z[i], gn[e][i], fma2(k, f[i], d[i]));
+          acc_n[e][i] = fma2(z[i], f[i], acc_n[e][i]);
         }
       }
 #pragma unroll
@@ -767,18 +790,18 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           d[i] = mul2(d[i], c);
-          const f32x2 g = z[i], e = mul2(d[i], gp[i]);
-          z[i] = mul2(e, f[i]);  // d u
-          acc_p[i] = fma2(mul2(d[i], g), f[i], acc_p[i]);
-          d[i] = mul2(e, g);
+          const f32x2 g = z[i], b = mul2(d[i], gp[e][i]);
+          z[i] = mul2(b, f[i]);  // d u
+          acc_p[e][i] = fma2(mul2(d[i], g), f[i], acc_p[e][i]);
+          d[i] = mul2(b, g);
         }
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_gate) + base) = pack8(z);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           d[i] = mul2(d[i], c);
-          acc_p[i] = fma2(d[i], f[i], acc_p[i]);
-          d[i] = mul2(d[i], gp[i]);
+          acc_p[e][i] = fma2(d[i], f[i], acc_p[e][i]);
+          d[i] = mul2(d[i], gp[e][i]);
         }
       }
       if (has_post) {
@@ -789,11 +812,14 @@ __global__ void __launch_bounds__(kThreads, ring_ctas_per_sm(kThreads))
     }
     if (++s == stages) s = 0, parity ^= 1;
   }
-  if (on) {
-    const size_t plane = static_cast<size_t>(gridDim.x) * H;
+  const size_t plane = static_cast<size_t>(gridDim.x) * H;
+#pragma unroll
+  for (int e = 0; e < kPieces; ++e) {
+    const int col = (threadIdx.x + e * blockDim.x) * 8;
+    if (col >= H) continue;
     const size_t at = static_cast<size_t>(blockIdx.x) * H + col;
-    if (has_post || a.gate_kind == kGateChannel) store8(a.partials + at, acc_p);
-    if (has_next) store8(a.partials + plane + at, acc_n);
+    if (has_post || a.gate_kind == kGateChannel) store8(a.partials + at, acc_p[e]);
+    if (has_next) store8(a.partials + plane + at, acc_n[e]);
   }
   if (*abort_v && threadIdx.x == 0) drain_ring(full_bar, stages);
 }
@@ -825,9 +851,9 @@ RingPlan ring_plan(const ResidualNormBackwardArgs& a) {
                     (a.grad_residual_out != nullptr ? hr : 0) +
                     (a.gate_kind == kGateFull ? h2 : 0);
   r.stage_bytes = (bytes + 127) / 128 * 128;
-  r.threads = ring_threads(a.H);
-  r.stages =
-      static_cast<int>(std::min<size_t>(kRingMaxStages, ring_smem(r.threads) / r.stage_bytes));
+  r.threads = backward_ring_threads(a.H);
+  r.stages = static_cast<int>(
+      std::min<size_t>(kRingMaxStages, backward_ring_smem(a.H) / r.stage_bytes));
   r.smem = static_cast<size_t>(r.stages) * r.stage_bytes;
   return r;
 }
@@ -878,7 +904,7 @@ __global__ void __launch_bounds__(kReduceCols* kReduceSlices)
 // CTAs of the backward kernels: all resident.
 int backward_grid(int T, int H, int num_sms) {
   if (H >= kRingMinH && H <= kRingMaxH)
-    return std::min(T, num_sms * ring_ctas_per_sm(ring_threads(H)));
+    return std::min(T, num_sms * backward_ring_ctas(H));
   const Shape s = shape_of(H);
   return std::min((T + s.per_cta - 1) / s.per_cta, num_sms * std::max(1, 1024 / s.threads));
 }
@@ -918,22 +944,17 @@ ForwardRingKernel forward_ring_kernel(int rows, int threads, bool f32) {
   return rows == 2 ? forward_ring_kernel<2>(threads, f32) : forward_ring_kernel<1>(threads, f32);
 }
 
-RingKernel ring_kernel(int threads, bool f32) {
-  if (threads <= 288)
-    return f32 ? residual_norm_backward_ring_kernel<true, 288>
-               : residual_norm_backward_ring_kernel<false, 288>;
-  if (threads <= 448)
-    return f32 ? residual_norm_backward_ring_kernel<true, 448>
-               : residual_norm_backward_ring_kernel<false, 448>;
-  if (threads <= 640)
-    return f32 ? residual_norm_backward_ring_kernel<true, 640>
-               : residual_norm_backward_ring_kernel<false, 640>;
-  if (threads <= 896)
-    return f32 ? residual_norm_backward_ring_kernel<true, 896>
-               : residual_norm_backward_ring_kernel<false, 896>;
-  return f32 ? residual_norm_backward_ring_kernel<true, 1024>
-             : residual_norm_backward_ring_kernel<false, 1024>;
+template <bool kF32>
+RingKernel ring_kernel(int H) {
+  const int threads = backward_ring_threads(H);
+  if (backward_ring_pieces(H) == 1)
+    return threads <= 288 ? residual_norm_backward_ring_kernel<kF32, 288, 1>
+                          : residual_norm_backward_ring_kernel<kF32, 448, 1>;
+  return threads <= 448 ? residual_norm_backward_ring_kernel<kF32, 448, 2>
+                        : residual_norm_backward_ring_kernel<kF32, 512, 2>;
 }
+
+RingKernel ring_kernel(int H, bool f32) { return f32 ? ring_kernel<true>(H) : ring_kernel<false>(H); }
 
 }  // namespace
 
@@ -949,10 +970,10 @@ cudaError_t setup_residual_norm(const DeviceInfo&) {
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       static_cast<int>(kRingSmem))) != cudaSuccess)
           return e;
-    for (int threads : {288, 448, 640, 896, 1024})
-      if ((e = cudaFuncSetAttribute(ring_kernel(threads, f32),
+    for (int H : {2304, 3584, 7168, 8192})  // one of each kernel
+      if ((e = cudaFuncSetAttribute(ring_kernel(H, f32),
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(ring_smem(threads)))) != cudaSuccess)
+                                    static_cast<int>(backward_ring_smem(H)))) != cudaSuccess)
         return e;
   }
   return cudaSuccess;
@@ -983,7 +1004,7 @@ cudaError_t launch_residual_norm_backward(const ResidualNormBackwardArgs& a,
   const RingPlan ring = ring_plan(a);
   cudaError_t e;
   if (ring.stages != 0) {
-    e = launch_dependent(ring_kernel(ring.threads, a.residual_f32), dim3(grid), dim3(ring.threads),
+    e = launch_dependent(ring_kernel(a.H, a.residual_f32), dim3(grid), dim3(ring.threads),
                          ring.smem, stream, a, ring.stages, ring.stage_bytes, dev.err_word);
   } else {
     const Shape s = shape_of(a.H);
