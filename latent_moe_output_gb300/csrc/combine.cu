@@ -58,10 +58,11 @@ __global__ void __launch_bounds__(kThreads)
 // A group of kTpt threads per token; each thread owns every kTpt-th 16-byte piece of
 // the token's row. Lane j of the group holds choice k0 + j. The rows are requested
 // first, the gradients of the rows (which do not need them) written meanwhile, the
-// products with the rows summed last; three CTAs per SM overlap the three steps (four
-// measured the same).
+// products with the rows summed last; four CTAs per SM overlap the three steps. At
+// T = 8192, K = 8, L = 2048: 85 us with streaming stores (the rows are not read again
+// here), 88 with plain ones, 92 with three CTAs per SM, 113 with two.
 template <int kTpt>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
     combine_backward_kernel(const uint16_t* __restrict__ grad_out,
                             const uint16_t* __restrict__ rows,
                             const int32_t* __restrict__ position,
@@ -113,7 +114,8 @@ __global__ void __launch_bounds__(kThreads, 3)
         for (int q = 0; q < 4; ++q) d[q] = mul2(w, g[q]);
         // A choice without an expert gets zeros even where grad_out is not finite.
         if (have && row < n)
-          d4[static_cast<size_t>(row) * nch + c] = p >= 0 ? pack8(d) : make_uint4(0, 0, 0, 0);
+          st_stream_v4(d4 + static_cast<size_t>(row) * nch + c,
+                       p >= 0 ? pack8(d) : make_uint4(0, 0, 0, 0));
       }
       if (dots) {
 #pragma unroll

@@ -43,14 +43,14 @@ constexpr int kMaxStages = 8;
 constexpr int kSmemPerSm = 204 * 1024;  // dynamic, without the experts' table
 constexpr int table_bytes(int E) { return (E + 1) * 2 * static_cast<int>(sizeof(int)); }
 
-template <int kSplit, int kTiles>
+template <int kSplit, int kTiles, int kM>
 struct Config {
-  static constexpr int kRows = 128 / kSplit;
-  static constexpr int kCtasPerSm = kTiles == 4 ? 1 : 2;  // registers: 96 at two
-  static constexpr int kWeightBytes = 128 * 128;
+  static constexpr int kRows = 64 * kM / kSplit;
+  static constexpr int kCtasPerSm = kTiles == 4 || kM == 4 ? 1 : 2;  // registers: 96 at two
+  static constexpr int kWeightBytes = kSplit * kRows * 128;
   static constexpr int kXBoxBytes = 8 * 128;  // 8 rows x 64 columns
   static constexpr int kXBytes = kSplit * kTiles * 4 * kXBoxBytes;
-  static constexpr int kScaleBytes = 128 * 16;  // eight scales per row and box
+  static constexpr int kScaleBytes = kSplit * kRows * 16;  // eight scales per row and box
   static constexpr int kStageBytes = kWeightBytes + kXBytes + kScaleBytes;
   static constexpr int kParts = 2 * kSplit;
   // Column parts 1.. of a tile's sums.
@@ -151,12 +151,12 @@ __device__ __forceinline__ Tile tile_at(int64_t tile, int mblocks, int rows_per_
   return t;
 }
 
-template <int kGroup, int kSplit, int kTiles>
-__global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
+template <int kGroup, int kSplit, int kTiles, int kM>
+__global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPerSm)
     matvec4_kernel(const __grid_constant__ CUtensorMap w_map,
                    const __grid_constant__ CUtensorMap x_map,
                    const __grid_constant__ CUtensorMap s_map, const Params p) {
-  using Cfg = Config<kSplit, kTiles>;
+  using Cfg = Config<kSplit, kTiles, kM>;
   constexpr int kPass = 8 * kTiles;
   constexpr int kScales = kBoxCols / kGroup;  // per row and box
   extern __shared__ uint8_t smem_raw[];
@@ -275,12 +275,12 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
       }
     }
   } else {
-    constexpr int kRowWarps = Cfg::kRows / 32;
+    constexpr int kRowWarps = Cfg::kRows / (16 * kM);
     constexpr int kHalf = kScales / 2;              // scales per row and half box
     constexpr int kWords = (kHalf + 1) / 2;
     const int part = warp / kRowWarps;              // column part of every stage
     const int box_in = part >> 1, half = part & 1;  // its box and half
-    const int mrow = warp % kRowWarps * 32;         // first weight row in the tile
+    const int mrow = warp % kRowWarps * 16 * kM;         // first weight row in the tile
     const int g = lane >> 2, c4 = lane & 3;
     // Column n of a fragment holds row (n >> 1) + 4 (n & 1) of the eight: lanes of
     // one quarter of the warp then read different halves of the swizzled rows.
@@ -292,15 +292,17 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
       const Tile t = tile_at(tile, mblocks, Cfg::kRows, kPass, s_first, s_unit, p.E);
       const int n_tiles = kTiles == 1 ? 1 : (t.rows + 7) / 8;
       const uint16_t* stile = p.scales + (static_cast<size_t>(t.e) * p.M + t.m0) * pitch;
-      int srow[4];  // weight rows mrow + g + 8 h
+      int srow[2 * kM];  // weight rows mrow + g + 8 h
 #pragma unroll
-      for (int h = 0; h < 4; ++h)  // (rows past the matrix are read from its last row)
+      for (int h = 0; h < 2 * kM; ++h)  // (rows past the matrix are read from its last row)
         srow[h] = min(p.M - 1 - t.m0, mrow + g + h * 8) * pitch;
-      float total[2][kTiles][4];
+      float total[kM][kTiles][4];
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n)
+      for (int m = 0; m < kM; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) total[0][n][j] = total[1][n][j] = 0.f;
+        for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) total[m][n][j] = 0.f;
 
       for (int i = 0; i < steps; ++i, ++it) {
         const uint32_t s = it % Cfg::kStages;
@@ -313,13 +315,13 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
         const uint32_t xa =
             st + Cfg::kWeightBytes + box_in * kTiles * 4 * Cfg::kXBoxBytes + xrow * 128;
         // Scales of half a box: kHalf per row, two per register.
-        uint32_t sc[4][kWords] = {};
+        uint32_t sc[2 * kM][kWords] = {};
         if (p.staged_scales) {
           const uint32_t sa = st + Cfg::kWeightBytes + Cfg::kXBytes +
                               (box_in * Cfg::kRows + mrow + g) * 16 +
                               ((box * kScales & 7) + half * kHalf) * 2;
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
+          for (int h = 0; h < 2 * kM; ++h) {
             if constexpr (kHalf == 4) {
               const uint2 v = lds64(sa + h * 128);
               sc[h][0] = v.x;
@@ -331,21 +333,21 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
         } else if (ok && runs > 0) {
           const int first = box * kScales + half * kHalf;
 #pragma unroll
-          for (int h = 0; h < 4; ++h)
+          for (int h = 0; h < 2 * kM; ++h)
 #pragma unroll
             for (int q = 0; q < kHalf; ++q)
               if (first + q < pitch)
                 sc[h][q >> 1] |= static_cast<uint32_t>(__ldg(stile + srow[h] + first + q))
                                  << (16 * (q & 1));
         }
-        float acc[2][kTiles][4];
+        float acc[kM][kTiles][4];
         auto run = [&](int j) {  // j: run in the half box, known at compile time
           constexpr int kRunsPerGroup = kGroup / 32;
           const bool opens = j % kRunsPerGroup == 0, closes = (j + 1) % kRunsPerGroup == 0;
           const int chunk = half * 4 + j;
-          uint32_t lo[2][4], hi[2][4];  // fragments: values 0, 1, 4, 5 and 2, 3, 6, 7
+          uint32_t lo[kM][4], hi[kM][4];  // fragments: values 0, 1, 4, 5 and 2, 3, 6, 7
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
+          for (int m = 0; m < kM; ++m) {
             const uint32_t at = wa + m * 16 * 128 + ((chunk ^ g) << 4);
             const uint32_t w0 = lds32(at), w1 = lds32(at + 8 * 128);
             lo[m][0] = weight_pair<false>(w0);
@@ -366,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
             const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410), b1 = __byte_perm(v.x, v.z, 0x7632);
             const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410), b3 = __byte_perm(v.y, v.w, 0x7632);
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
+            for (int m = 0; m < kM; ++m) {
               if (opens)
                 mma_bf16(acc[m][n], lo[m], b0, b1, zero);
               else
@@ -401,11 +403,11 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
 
       // The column parts of a row are added in order by part 0's warp.
       consumer_barrier();  // the last tile's sums have been read
-      constexpr int kPerWarp = 32 * 8 * kTiles;
+      constexpr int kPerWarp = 16 * kM * 8 * kTiles;
       if (part > 0) {
         float* dst = sums + ((part - 1) * kRowWarps + warp % kRowWarps) * kPerWarp + lane;
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < kM; ++m)
 #pragma unroll
           for (int n = 0; n < kTiles; ++n)
 #pragma unroll
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
       for (int q = 0; q < Cfg::kParts - 1; ++q) {
         const float* src = sums + (q * kRowWarps + warp) * kPerWarp + lane;
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < kM; ++m)
 #pragma unroll
           for (int n = 0; n < kTiles; ++n)
 #pragma unroll
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
       // Element (j, lane) of a fragment: weight row g + 8 (j >> 1), column
       // 2 c4 + (j & 1), i.e. row c4 + 4 (j & 1) of x.
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < kM; ++m)
 #pragma unroll
         for (int n = 0; n < kTiles; ++n)
 #pragma unroll
@@ -454,16 +456,17 @@ struct Variant {
   int rows, ctas_per_sm;
 };
 
-template <int kGroup, int kSplit, int kTiles>
+template <int kGroup, int kSplit, int kTiles, int kM = 2>
 Variant variant() {
-  return Variant{matvec4_kernel<kGroup, kSplit, kTiles>, Config<kSplit, kTiles>::kSmem,
-                 Config<kSplit, kTiles>::kRows, Config<kSplit, kTiles>::kCtasPerSm};
+  using Cfg = Config<kSplit, kTiles, kM>;
+  return Variant{matvec4_kernel<kGroup, kSplit, kTiles, kM>, Cfg::kSmem, Cfg::kRows,
+                 Cfg::kCtasPerSm};
 }
 
 template <int kGroup>
 Variant pick(int split, int tiles) {
   if (split > 1) return tiles == 1 ? variant<kGroup, 4, 1>() : variant<kGroup, 2, 2>();
-  return tiles == 1 ? variant<kGroup, 1, 1>()
+  return tiles == 1 ? variant<kGroup, 1, 1, 4>()
                     : tiles == 2 ? variant<kGroup, 1, 2>() : variant<kGroup, 1, 4>();
 }
 
