@@ -50,7 +50,13 @@ struct Config {
   static constexpr int kWeightBytes = kSplit * kRows * 128;
   static constexpr int kXBoxBytes = 8 * 128;  // 8 rows x 64 columns
   static constexpr int kXBytes = kSplit * kTiles * 4 * kXBoxBytes;
-  static constexpr int kScaleBytes = kSplit * kRows * 16;  // eight scales per row and box
+  // With one or two boxes per stage, 16 scales per row (32 bytes, a whole memory
+  // sector) come with the first stage that needs them and serve group / 16 boxes; the
+  // buffer belongs to a stage's slot, so it is free again no later than the slot is.
+  // Otherwise eight scales per row and box, every time.
+  static constexpr bool kPieces = kSplit <= 2;
+  static constexpr int kPieceBytes = kPieces ? 32 : 16;
+  static constexpr int kScaleBytes = (kPieces ? 1 : kSplit) * kRows * kPieceBytes;
   static constexpr int kStageBytes = kWeightBytes + kXBytes + kScaleBytes;
   static constexpr int kParts = 2 * kSplit;
   // Column parts 1.. of a tile's sums.
@@ -71,32 +77,6 @@ struct Params {
   uint32_t* err;
 };
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-
 // Two of the eight values of a word, in the low four bits of each half (kHigh
 // false) or the four bits above them: (q - 8) / 64 as two bf16 numbers, exact.
 template <bool kHigh>
@@ -112,8 +92,7 @@ __device__ __forceinline__ uint32_t weight_pair(uint32_t w) {
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1, const float (&c)[4]) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
@@ -165,8 +144,10 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
   volatile int* abort_v = &abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  float* sums = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) +
-                                         Cfg::kStages * Cfg::kStageBytes);
+  // (shared memory is read through pointers, not asm, so that the compiler may move
+  // the loads of one run of columns above the products of the last)
+  uint8_t* ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
+  float* sums = reinterpret_cast<float*>(ring_ptr + Cfg::kStages * Cfg::kStageBytes);
   int* s_first = reinterpret_cast<int*>(sums) + Cfg::kSumBytes / 4;  // first row of each expert
   int* s_unit = s_first + p.E + 1;                                   // passes before each expert
 
@@ -222,6 +203,8 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
   }
   __syncthreads();
 
+  constexpr int kStagesPerPiece = kGroup / 16 / kSplit > 1 ? kGroup / 16 / kSplit : 1;
+  constexpr int kScalesAt = Cfg::kWeightBytes + Cfg::kXBytes;  // in a stage
   const int mblocks = (p.M + Cfg::kRows - 1) / Cfg::kRows;
   const int64_t tiles = static_cast<int64_t>(s_unit[p.E]) * mblocks;
   const int boxes = (p.C + kBoxCols - 1) / kBoxCols;
@@ -230,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
   if (warp == kConsumers) {
     if (lane == 0) {
       uint32_t it = 0;  // stages issued
+      uint32_t pieces = 0;  // scale pieces issued (one box per stage)
       bool ok = true;
       for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
         const Tile t = tile_at(tile, mblocks, Cfg::kRows, kPass, s_first, s_unit, p.E);
@@ -241,13 +225,20 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
           const int live = min(kSplit, boxes - i * kSplit);
           const uint32_t bar = smem_u32(&full_bar[s]);
           const uint32_t st = ring + s * Cfg::kStageBytes;
-          mbar_arrive_expect_tx(bar, static_cast<uint32_t>(live) *
-                                         (Cfg::kRows * (p.staged_scales ? 144 : 128) +
-                                          n_tiles * 4 * Cfg::kXBoxBytes));
+          const bool piece = p.staged_scales && (!Cfg::kPieces || i % kStagesPerPiece == 0);
+          mbar_arrive_expect_tx(
+              bar, static_cast<uint32_t>(live) *
+                           (Cfg::kRows * 128 + n_tiles * 4 * Cfg::kXBoxBytes) +
+                       (piece ? (Cfg::kPieces ? 1 : live) * Cfg::kRows * Cfg::kPieceBytes : 0));
+          if (Cfg::kPieces && piece) {
+            tma_load_2d(ring + pieces % Cfg::kStages * Cfg::kStageBytes + kScalesAt, &s_map, bar,
+                        i / kStagesPerPiece * 32, t.e * p.M + t.m0);
+            ++pieces;
+          }
           for (int j = 0; j < live; ++j) {
             const int c0 = (i * kSplit + j) * kBoxCols;
             tma_load_2d(st + j * Cfg::kRows * 128, &w_map, bar, c0 / 2, t.e * p.M + t.m0);
-            if (p.staged_scales)  // whole 16-byte pieces, from the one that holds the box's first
+            if (!Cfg::kPieces && piece)  // from the piece that holds the box's first scale
               tma_load_2d(st + Cfg::kWeightBytes + Cfg::kXBytes + j * Cfg::kRows * 16, &s_map, bar,
                           (c0 / kGroup & ~7) * 2, t.e * p.M + t.m0);
             const uint32_t xs = st + Cfg::kWeightBytes + j * kTiles * 4 * Cfg::kXBoxBytes;
@@ -286,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
     // one quarter of the warp then read different halves of the swizzled rows.
     const int xrow = (g >> 1) + (g & 1) * 4;
     const int pitch = p.C / kGroup;  // scales per row
-    uint32_t it = 0;
+    uint32_t it = 0, pieces = 0;
     bool ok = true;
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
       const Tile t = tile_at(tile, mblocks, Cfg::kRows, kPass, s_first, s_unit, p.E);
@@ -310,24 +301,30 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
         const int box = i * kSplit + box_in;
         // Runs of 32 columns in this half box.
         const int runs = min(4, (p.C - box * kBoxCols) / 32 - half * 4);
-        const uint32_t st = ring + s * Cfg::kStageBytes;
-        const uint32_t wa = st + box_in * Cfg::kRows * 128 + (mrow + g) * 128 + c4 * 4;
-        const uint32_t xa =
+        const uint8_t* st = ring_ptr + s * Cfg::kStageBytes;
+        const uint8_t* wa = st + box_in * Cfg::kRows * 128 + (mrow + g) * 128 + c4 * 4;
+        const uint8_t* xa =
             st + Cfg::kWeightBytes + box_in * kTiles * 4 * Cfg::kXBoxBytes + xrow * 128;
         // Scales of half a box: kHalf per row, two per register.
         uint32_t sc[2 * kM][kWords] = {};
         if (p.staged_scales) {
-          const uint32_t sa = st + Cfg::kWeightBytes + Cfg::kXBytes +
-                              (box_in * Cfg::kRows + mrow + g) * 16 +
-                              ((box * kScales & 7) + half * kHalf) * 2;
+          if (Cfg::kPieces && i % kStagesPerPiece == 0) ++pieces;
+          const uint32_t slot = Cfg::kPieces ? (pieces - 1) % Cfg::kStages : s;
+          constexpr int kMask = Cfg::kPieceBytes / 2 - 1;  // scales in a piece
+          const uint8_t* sa = ring_ptr + slot * Cfg::kStageBytes + kScalesAt +
+                              ((Cfg::kPieces ? 0 : box_in * Cfg::kRows) + mrow + g) *
+                                  Cfg::kPieceBytes +
+                              ((box * kScales & kMask) + half * kHalf) * 2;
 #pragma unroll
           for (int h = 0; h < 2 * kM; ++h) {
             if constexpr (kHalf == 4) {
-              const uint2 v = lds64(sa + h * 128);
+              const uint2 v = *reinterpret_cast<const uint2*>(sa + h * 8 * Cfg::kPieceBytes);
               sc[h][0] = v.x;
               sc[h][1] = v.y;
             } else {
-              sc[h][0] = kHalf == 2 ? lds32(sa + h * 128) : lds16(sa + h * 128);
+              sc[h][0] = kHalf == 2
+                             ? *reinterpret_cast<const uint32_t*>(sa + h * 8 * Cfg::kPieceBytes)
+                             : *reinterpret_cast<const uint16_t*>(sa + h * 8 * Cfg::kPieceBytes);
             }
           }
         } else if (ok && runs > 0) {
@@ -348,8 +345,9 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
           uint32_t lo[kM][4], hi[kM][4];  // fragments: values 0, 1, 4, 5 and 2, 3, 6, 7
 #pragma unroll
           for (int m = 0; m < kM; ++m) {
-            const uint32_t at = wa + m * 16 * 128 + ((chunk ^ g) << 4);
-            const uint32_t w0 = lds32(at), w1 = lds32(at + 8 * 128);
+            const uint8_t* at = wa + m * 16 * 128 + ((chunk ^ g) << 4);
+            const uint32_t w0 = *reinterpret_cast<const uint32_t*>(at);
+            const uint32_t w1 = *reinterpret_cast<const uint32_t*>(at + 8 * 128);
             lo[m][0] = weight_pair<false>(w0);
             lo[m][1] = weight_pair<false>(w1);
             lo[m][2] = weight_pair<true>(w0);
@@ -363,8 +361,9 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
 #pragma unroll
           for (int n = 0; n < kTiles; ++n) {
             if (kTiles > 1 && n >= n_tiles) break;
-            const uint4 v = lds128(xa + (n * 4 + (chunk >> 1)) * Cfg::kXBoxBytes +
-                                   ((((chunk & 1) * 4 + c4) ^ xrow) << 4));
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                xa + (n * 4 + (chunk >> 1)) * Cfg::kXBoxBytes +
+                ((((chunk & 1) * 4 + c4) ^ xrow) << 4));
             const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410), b1 = __byte_perm(v.x, v.z, 0x7632);
             const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410), b3 = __byte_perm(v.y, v.w, 0x7632);
 #pragma unroll
@@ -453,21 +452,21 @@ typedef void (*Kernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, 
 struct Variant {
   Kernel kernel;
   size_t smem;
-  int rows, ctas_per_sm;
+  int rows, ctas_per_sm, piece_bytes;
 };
 
 template <int kGroup, int kSplit, int kTiles, int kM = 2>
 Variant variant() {
   using Cfg = Config<kSplit, kTiles, kM>;
   return Variant{matvec4_kernel<kGroup, kSplit, kTiles, kM>, Cfg::kSmem, Cfg::kRows,
-                 Cfg::kCtasPerSm};
+                 Cfg::kCtasPerSm, Cfg::kPieceBytes};
 }
 
 template <int kGroup>
 Variant pick(int split, int tiles) {
   if (split > 1) return tiles == 1 ? variant<kGroup, 4, 1>() : variant<kGroup, 2, 2>();
   return tiles == 1 ? variant<kGroup, 1, 1, 4>()
-                    : tiles == 2 ? variant<kGroup, 1, 2>() : variant<kGroup, 1, 4>();
+                    : tiles == 2 ? variant<kGroup, 1, 2, 4>() : variant<kGroup, 1, 4>();
 }
 
 Variant pick(int group, int split, int tiles) {
@@ -510,7 +509,7 @@ cudaError_t launch_matvec4(const Matvec4Args& a, const DeviceInfo& dev, cudaStre
     return cudaErrorInvalidValue;
   if (!staged)
     s_map = w_map;  // not used
-  else if (!make_map_u8(&s_map, a.scales, rows, pitch, 16, v.rows))
+  else if (!make_map_u8(&s_map, a.scales, rows, pitch, v.piece_bytes, v.rows))
     return cudaErrorInvalidValue;
   const int64_t most = (static_cast<int64_t>(matrices) + a.N / 8 + 1) *
                        ((a.M + v.rows - 1) / v.rows);
