@@ -21,8 +21,8 @@ namespace lt {
 namespace {
 
 constexpr int kMaxThreads = 512;
-constexpr int kReduceCols = 32;    // float4 columns per CTA of the column sum
-constexpr int kReduceSlices = 16;  // parts of the partial rows per CTA
+constexpr int kReduceCols = 16;    // float4 columns per CTA of the column sum
+constexpr int kReduceSlices = 32;  // parts of the partial rows per CTA
 
 struct Shape {
   int threads;  // per CTA
@@ -229,33 +229,26 @@ __global__ void __launch_bounds__(kMaxThreads, kPieces == 4 ? 1 : 2)
   }
 }
 
-// The gradient for rows that the ring kernel below does not take. Each CTA walks
-// over token rows and keeps the column sums of its threads' columns: in registers
-// for one piece per thread, else in shared memory. With a channel gate one sum,
-// S = sum_t d * yh, gives both dgp = gate * S and dgate = gp * S.
+// The gradient for rows wider than the ring kernel below takes (their column sums do
+// not fit in the registers of an SM). Each CTA walks over token rows and keeps the
+// column sums in shared memory. With a channel gate one sum, S = sum_t d * yh, gives
+// both dgp = gate * S and dgate = gp * S.
 template <int kPieces, bool kF32>
 __global__ void __launch_bounds__(kMaxThreads)
     residual_norm_backward_kernel(const ResidualNormBackwardArgs a, int tpr) {
-  extern __shared__ float s_acc[];  // kPieces > 1: [2][H]
+  extern __shared__ float s_acc[];  // [2][H]
   __shared__ float red[4][kMaxThreads / 32];
   pdl_launch_dependents();
   pdl_wait();
   const int row = threadIdx.x / tpr, lane = threadIdx.x - row * tpr, wpr = tpr >> 5;
   const int per_cta = blockDim.x / tpr;
   const float inv_h = 1.0f / static_cast<float>(a.H);
-  float acc[2][8] = {};
-  if constexpr (kPieces > 1)
-    for (int i = threadIdx.x; i < 2 * a.H; i += blockDim.x) s_acc[i] = 0.f;
-  if constexpr (kPieces > 1) __syncthreads();
+  for (int i = threadIdx.x; i < 2 * a.H; i += blockDim.x) s_acc[i] = 0.f;
+  __syncthreads();
   auto add = [&](int which, int q, const float (&v)[8]) {
-    if constexpr (kPieces == 1) {
+    float* p = s_acc + static_cast<size_t>(which) * a.H + (lane + q * tpr) * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[which][i] += v[i];
-    } else {
-      float* p = s_acc + static_cast<size_t>(which) * a.H + (lane + q * tpr) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] += v[i];
-    }
+    for (int i = 0; i < 8; ++i) p[i] += v[i];
   };
 
   for (int t0 = blockIdx.x * per_cta; t0 < a.T; t0 += gridDim.x * per_cta) {
@@ -371,29 +364,11 @@ __global__ void __launch_bounds__(kMaxThreads)
   const size_t plane = static_cast<size_t>(gridDim.x) * a.H;
   const size_t at = static_cast<size_t>(blockIdx.x) * a.H;
   const bool want[2] = {a.post != nullptr || a.gate_kind == kGateChannel, a.next != nullptr};
-  if constexpr (kPieces == 1) {  // the rows that the CTA worked on at once add up in order
-    __shared__ float s_rows[256 * 8];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (!want[s]) continue;
-      __syncthreads();
-      if (lane * 8 < a.H)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s_rows[row * a.H + lane * 8 + i] = acc[s][i];
-      __syncthreads();
-      for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
-        float o = 0.f;
-        for (int r = 0; r < per_cta; ++r) o += s_rows[r * a.H + c];
-        a.partials[s * plane + at + c] = o;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-      if (want[s])
-        for (int c = threadIdx.x; c < a.H; c += blockDim.x)
-          a.partials[s * plane + at + c] = s_acc[s * a.H + c];
-  }
+  for (int s = 0; s < 2; ++s)
+    if (want[s])
+      for (int c = threadIdx.x; c < a.H; c += blockDim.x)
+        a.partials[s * plane + at + c] = s_acc[s * a.H + c];
 }
 
 // ------------------------------------------------------------ ring kernel
@@ -401,14 +376,17 @@ __global__ void __launch_bounds__(kMaxThreads)
 // or two 8-element pieces of the row per thread. The rows (up to five arrays) come through
 // a ring of stages with bulk copies that run ahead of the arithmetic; a stage is
 // refilled once all threads are past the next row's barrier.
-constexpr int kRingMinH = 1032, kRingMaxH = 8192;
+constexpr int kNarrowMaxH = 512;  // up to here a warp takes a row of the gradient
+constexpr int kRingMinH = kNarrowMaxH + 8, kRingMaxH = 8192;
 constexpr int kRingMaxStages = 6;
 constexpr int kRingMinWaves = 4;  // forward: rows per SM
 constexpr size_t kRingSmem = 224 * 1024;  // one CTA per SM
 constexpr int kForwardRingMinH = 4096;
 
-// Narrow rows have few threads: several CTAs then share an SM (72 registers each).
-constexpr int ring_ctas_per_sm(int threads) { return threads <= 288 ? 3 : threads <= 448 ? 2 : 1; }
+// Rows of few pieces have few threads: several CTAs then share an SM.
+constexpr int ring_ctas_per_sm(int threads) {
+  return threads <= 128 ? 6 : threads <= 288 ? 3 : threads <= 448 ? 2 : 1;
+}
 constexpr int ring_threads(int H) { return (H / 8 + 31) / 32 * 32; }
 
 // The gradient's ring: rows of more than 448 pieces take two per thread (half the
@@ -480,6 +458,210 @@ __device__ __forceinline__ void lds_res8(const uint8_t* row, int lane, f32x2 (&a
     lds8(reinterpret_cast<const float*>(row), lane, a);
   else
     lds8(row, lane, a);
+}
+
+// ------------------------------------------------- arithmetic of the gradient
+// What a row of the gradient needs besides its elements.
+struct GradRow {
+  float r1, r2, k2, by, gt;
+};
+
+// Which inputs a call has. The kernels are built for calls with all of them (kAll:
+// without, kAllGated: with a gate per element), where the choices fold away, and for
+// the rest.
+struct GradHas {
+  bool post, next, dv, full_gate;
+};
+enum GradMode { kSome = 0, kAll = 1, kAllGated = 2 };
+
+template <int kMode>
+__device__ __forceinline__ GradHas grad_has(const ResidualNormBackwardArgs& a) {
+  if constexpr (kMode == kSome)
+    return GradHas{a.post != nullptr, a.next != nullptr, a.grad_residual_out != nullptr,
+                   a.gate_kind == kGateFull};
+  return GradHas{true, true, true, kMode == kAllGated};
+}
+
+int grad_mode(const ResidualNormBackwardArgs& a) {
+  if (a.post == nullptr || a.next == nullptr || a.grad_residual_out == nullptr) return kSome;
+  return a.gate_kind == kGateFull ? kAllGated : kAll;
+}
+
+// Sums over one 8-element piece. With w = gp * gate: y y, v v, a v (a = dz gn), then
+// the terms of mean(b yh), which is linear in d: dv w y, a w y, v w y. So one
+// reduction per row is enough. gp holds a channel gate already.
+__device__ __forceinline__ void grad_sums(f32x2 (&q)[6], const GradHas& has, const f32x2 (&y)[4],
+                                          const f32x2 (&v)[4], const f32x2 (&z)[4],
+                                          const f32x2 (&dv)[4], const f32x2 (&g)[4],
+                                          const f32x2 (&gp)[4], const f32x2 (&gn)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    q[0] = fma2(y[i], y[i], q[0]);
+    f32x2 wy = mul2(y[i], gp[i]);
+    if (has.full_gate) wy = mul2(wy, g[i]);
+    if (has.next) {
+      const f32x2 a = mul2(z[i], gn[i]);
+      q[1] = fma2(v[i], v[i], q[1]);
+      q[2] = fma2(a, v[i], q[2]);
+      q[4] = fma2(a, wy, q[4]);
+      q[5] = fma2(v[i], wy, q[5]);
+    }
+    if (has.dv) q[3] = fma2(dv[i], wy, q[3]);
+  }
+}
+
+// From the row's sums: d = dv + r2 a + k2 v, and by = r1 sum(d w y), a token gate apart.
+__device__ __forceinline__ GradRow grad_row(const float (&sum)[8], const GradHas& has,
+                                            float inv_h, float eps, float gt) {
+  GradRow r;
+  r.r1 = has.post ? rsqrtf(fmaf(sum[0], inv_h, eps)) : 1.f;
+  r.r2 = has.next ? rsqrtf(fmaf(sum[1], inv_h, eps)) : 0.f;
+  r.k2 = -(sum[2] * inv_h * r.r2 * r.r2 * r.r2);
+  r.by = r.r1 * fmaf(r.k2, sum[5], fmaf(r.r2, sum[4], sum[3]));
+  r.gt = gt;
+  return r;
+}
+
+// Gradients of one piece: dv becomes dy, z becomes dx, g becomes the gradient of a
+// full gate; acc_p += d gate yh (d yh with a channel gate), acc_n += dz vh.
+__device__ __forceinline__ void grad_piece(const GradRow& r, const GradHas& has, float scale,
+                                           float inv_h, const f32x2 (&y)[4], const f32x2 (&v)[4],
+                                           f32x2 (&z)[4], f32x2 (&dv)[4], f32x2 (&g)[4],
+                                           const f32x2 (&gp)[4], const f32x2 (&gn)[4],
+                                           f32x2 (&acc_p)[4], f32x2 (&acc_n)[4]) {
+  const f32x2 r2 = both(r.r2), k2 = both(r.k2), c = both(r.r1 * r.gt), s = both(scale);
+  // dy = gt (r1 b - y r1^2 mean(b yh)) with b = d gate gp
+  const f32x2 k = both(has.post ? -(r.by * inv_h * r.r1 * r.r1 * r.gt) : 0.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f32x2 d = dv[i];
+    if (has.next) {
+      const f32x2 zr = mul2(z[i], r2);
+      d = fma2(zr, gn[i], fma2(k2, v[i], d));
+      acc_n[i] = fma2(zr, v[i], acc_n[i]);
+    }
+    z[i] = mul2(s, d);
+    d = mul2(d, c);
+    if (has.full_gate) {
+      const f32x2 b = mul2(d, gp[i]);
+      acc_p[i] = fma2(mul2(d, g[i]), y[i], acc_p[i]);
+      d = mul2(b, g[i]);
+      g[i] = mul2(b, y[i]);  // d u
+    } else {
+      acc_p[i] = fma2(d, y[i], acc_p[i]);
+      d = mul2(d, gp[i]);
+    }
+    dv[i] = has.post ? fma2(k, y[i], d) : d;
+  }
+}
+
+// Weights of a piece for the two functions above; zeros the sums.
+__device__ __forceinline__ void grad_weights(const ResidualNormBackwardArgs& a, int col,
+                                             f32x2 (&gp)[4], f32x2 (&gn)[4], f32x2 (&acc_p)[4],
+                                             f32x2 (&acc_n)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    gp[i] = both(1.f);
+    gn[i] = acc_p[i] = acc_n[i] = both(0.f);
+  }
+  if (col >= a.H) return;
+  if (a.post != nullptr) load8(a.post + col, gp);
+  if (a.next != nullptr) load8(a.next + col, gn);
+  if (a.gate_kind == kGateChannel) {
+    f32x2 g[4];
+    load8(static_cast<const float*>(a.gate) + col, g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) gp[i] = mul2(gp[i], g[i]);
+  }
+}
+
+// ------------------------------------------------- gradient of narrow rows
+// H <= 512: one warp per token row, no barriers; the rows of a CTA's warps add up
+// through shared memory at the end.
+constexpr int kNarrowThreads = 256;
+
+template <bool kF32>
+__device__ __forceinline__ void ldg_res8(const void* base, size_t at, f32x2 (&a)[4]) {
+  if constexpr (kF32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    pairs_of(__ldg(p), __ldg(p + 1), a);
+  } else {
+    unpack8(ld_stream_v4(static_cast<const uint16_t*>(base) + at), a);
+  }
+}
+
+template <bool kF32, int kPieces, int kMode>
+__global__ void __launch_bounds__(kNarrowThreads, kPieces == 1 ? 2 : 1)
+    residual_norm_backward_narrow_kernel(const ResidualNormBackwardArgs a) {
+  __shared__ __align__(16) float s_sum[kNarrowThreads / 32][kNarrowMaxH];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const GradHas has = grad_has<kMode>(a);
+  const float inv_h = 1.0f / static_cast<float>(a.H);
+  f32x2 gp[kPieces][4], gn[kPieces][4], acc_p[kPieces][4], acc_n[kPieces][4];
+#pragma unroll
+  for (int e = 0; e < kPieces; ++e)
+    grad_weights(a, (lane + e * 32) * 8, gp[e], gn[e], acc_p[e], acc_n[e]);
+  const int step = gridDim.x * (kNarrowThreads / 32);
+  for (int t = blockIdx.x * (kNarrowThreads / 32) + warp; t < a.T; t += step) {
+    const float gt =
+        a.gate_kind == kGateToken ? __ldg(static_cast<const float*>(a.gate) + t) : 1.f;
+    f32x2 y[kPieces][4], v[kPieces][4], z[kPieces][4], d[kPieces][4], g[kPieces][4], q[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) q[i] = both(0.f);
+#pragma unroll
+    for (int e = 0; e < kPieces; ++e) {
+      const int col = (lane + e * 32) * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        y[e][i] = v[e][i] = z[e][i] = d[e][i] = g[e][i] = both(0.f);
+      if (col >= a.H) continue;
+      const size_t at = static_cast<size_t>(t) * a.H + col;
+      unpack8(ld_stream_v4(a.block + at), y[e]);
+      ldg_res8<kF32>(a.residual_out, at, v[e]);
+      if (has.next) unpack8(ld_stream_v4(a.grad_next + at), z[e]);
+      if (has.dv) ldg_res8<kF32>(a.grad_residual_out, at, d[e]);
+      if (has.full_gate) unpack8(ld_stream_v4(static_cast<const uint16_t*>(a.gate) + at), g[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < kPieces; ++e) grad_sums(q, has, y[e], v[e], z[e], d[e], g[e], gp[e], gn[e]);
+    float sum[8] = {};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) sum[i] = warp_sum_f(sum2(q[i]));
+    const GradRow r = grad_row(sum, has, inv_h, a.eps, gt);
+    if (a.gate_kind == kGateToken && lane == 0) static_cast<float*>(a.grad_gate)[t] = r.by;
+#pragma unroll
+    for (int e = 0; e < kPieces; ++e) {
+      const int col = (lane + e * 32) * 8;
+      if (col >= a.H) continue;
+      const size_t at = static_cast<size_t>(t) * a.H + col;
+      grad_piece(r, has, a.scale, inv_h, y[e], v[e], z[e], d[e], g[e], gp[e], gn[e], acc_p[e],
+                 acc_n[e]);
+      store_res8<kF32>(a.grad_residual, at, z[e]);
+      if (has.full_gate)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_gate) + at) = pack8(g[e]);
+      *reinterpret_cast<uint4*>(a.grad_block + at) = pack8(d[e]);
+    }
+  }
+  const size_t plane = static_cast<size_t>(gridDim.x) * a.H;
+  float* out = a.partials + static_cast<size_t>(blockIdx.x) * a.H;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    if (p == 0 ? !has.post && a.gate_kind != kGateChannel : !has.next) continue;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kPieces; ++e)
+      if ((lane + e * 32) * 8 < a.H)
+        store8(&s_sum[warp][(lane + e * 32) * 8], p == 0 ? acc_p[e] : acc_n[e]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.H; c += kNarrowThreads) {
+      float o = 0.f;
+#pragma unroll
+      for (int w = 0; w < kNarrowThreads / 32; ++w) o += s_sum[w][c];
+      out[p * plane + c] = o;
+    }
+  }
 }
 
 // After a wait that ran out: lets copies in flight land before the CTA exits.
@@ -626,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (*abort_v && threadIdx.x == 0) drain_ring(full_bar, stages);
 }
 
-template <bool kF32, int kThreads, int kPieces>
+template <bool kF32, int kThreads, int kPieces, int kMode>
 __global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(kThreads))
     residual_norm_backward_ring_kernel(const ResidualNormBackwardArgs a, int stages,
                                        int stage_bytes, uint32_t* err) {
@@ -637,8 +819,8 @@ __global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(
   volatile int* abort_v = &abort_flag;
   const int H = a.H;
   const uint32_t h2 = static_cast<uint32_t>(H) * 2, hr = kF32 ? h2 * 2 : h2;
-  const bool has_dv = a.grad_residual_out != nullptr, has_next = a.next != nullptr;
-  const bool has_post = a.post != nullptr, full_gate = a.gate_kind == kGateFull;
+  const GradHas has = grad_has<kMode>(a);
+  const bool has_post = has.post, has_next = has.next, has_dv = has.dv, full_gate = has.full_gate;
   // Arrays of a stage: y, v, dz, dv, gate.
   const uint32_t at_v = h2, at_z = at_v + hr, at_d = at_z + (has_next ? h2 : 0),
                  at_g = at_d + (has_dv ? hr : 0);
@@ -670,29 +852,11 @@ __global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(
     for (int s = 0; s < stages && static_cast<int>(blockIdx.x) + s * step < a.T; ++s)
       fetch(blockIdx.x + s * step, s);
 
-  // gp: post weight, times a channel gate; gn: next weight. acc_p sums
-  // d * gate * yh (d * yh with a channel gate), acc_n dz * vh.
   f32x2 gp[kPieces][4], gn[kPieces][4], acc_p[kPieces][4], acc_n[kPieces][4];
 #pragma unroll
-  for (int e = 0; e < kPieces; ++e) {
-    const int col = (threadIdx.x + e * blockDim.x) * 8;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      gp[e][i] = both(1.f);
-      gn[e][i] = acc_p[e][i] = acc_n[e][i] = both(0.f);
-    }
-    if (col >= H) continue;
-    if (has_post) load8(a.post + col, gp[e]);
-    if (has_next) load8(a.next + col, gn[e]);
-    if (a.gate_kind == kGateChannel) {
-      f32x2 g[4];
-      load8(static_cast<const float*>(a.gate) + col, g);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) gp[e][i] = mul2(gp[e][i], g[i]);
-    }
-  }
+  for (int e = 0; e < kPieces; ++e)
+    grad_weights(a, (threadIdx.x + e * blockDim.x) * 8, gp[e], gn[e], acc_p[e], acc_n[e]);
   const float inv_h = 1.0f / static_cast<float>(H);
-  const f32x2 scale = both(a.scale);
   int s = 0, turn = 0, last = -1;  // last: the row before
   uint32_t parity = 0;
   bool ok = true;
@@ -701,46 +865,27 @@ __global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(
     const float gt =
         a.gate_kind == kGateToken ? __ldg(static_cast<const float*>(a.gate) + t) : 1.f;
     if (ok) ok = mbar_wait(smem_u32(&full_bar[s]), parity, err, abort_v);
-    // With w = gp * gate: y y, v v, a v, then the terms of mean(b yh), which is linear
-    // in d: dv w y, a w y, v w y. One reduction per row instead of two.
     float sum[8] = {};
     f32x2 q[6];
 #pragma unroll
     for (int i = 0; i < 6; ++i) q[i] = both(0.f);
+    auto load = [&](int lane, f32x2 (&y)[4], f32x2 (&v)[4], f32x2 (&z)[4], f32x2 (&d)[4],
+                    f32x2 (&g)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[i] = d[i] = g[i] = both(0.f);
+      lds8(st, lane, y);
+      lds_res8<kF32>(st + at_v, lane, v);
+      if (has_next) lds8(st + at_z, lane, z);
+      if (has_dv) lds_res8<kF32>(st + at_d, lane, d);
+      if (full_gate) lds8(st + at_g, lane, g);
+    };
 #pragma unroll
     for (int e = 0; e < kPieces; ++e) {
       const int lane = threadIdx.x + e * blockDim.x;  // piece of the row
       if (lane * 8 >= H) continue;
-      f32x2 y[4], v[4];
-      lds8(st, lane, y);
-      lds_res8<kF32>(st + at_v, lane, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[0] = fma2(y[i], y[i], q[0]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], gp[e][i]);
-      if (full_gate) {
-        f32x2 g[4];
-        lds8(st + at_g, lane, g);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], g[i]);
-      }
-      if (has_next) {
-        f32x2 z[4];
-        lds8(st + at_z, lane, z);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          z[i] = mul2(z[i], gn[e][i]);
-          q[1] = fma2(v[i], v[i], q[1]);
-          q[2] = fma2(z[i], v[i], q[2]);
-          q[4] = fma2(z[i], y[i], q[4]);
-          q[5] = fma2(v[i], y[i], q[5]);
-        }
-      }
-      if (has_dv) {
-        lds_res8<kF32>(st + at_d, lane, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[3] = fma2(v[i], y[i], q[3]);
-      }
+      f32x2 y[4], v[4], z[4], d[4], g[4];
+      load(lane, y, v, z, d, g);
+      grad_sums(q, has, y, v, z, d, g, gp[e], gn[e]);
     }
 #pragma unroll
     for (int i = 0; i < 6; ++i) sum[i] = sum2(q[i]);
@@ -750,64 +895,19 @@ __global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(
     if (threadIdx.x == 0 && ok && last >= 0 && last + static_cast<int64_t>(stages) * step < a.T)
       fetch(last + stages * step, s == 0 ? stages - 1 : s - 1);
     last = t;
-    const float r1 = has_post ? rsqrtf(fmaf(sum[0], inv_h, a.eps)) : 1.f;
-    const float r2 = has_next ? rsqrtf(fmaf(sum[1], inv_h, a.eps)) : 0.f;
-    const float k2 = -(sum[2] * inv_h * r2 * r2 * r2);                    // d = dv + r2 a + k2 v
-    const float by = r1 * fmaf(k2, sum[5], fmaf(r2, sum[4], sum[3]));  // sum of b yh, gt apart
-    if (a.gate_kind == kGateToken && threadIdx.x == 0) static_cast<float*>(a.grad_gate)[t] = by;
+    const GradRow r = grad_row(sum, has, inv_h, a.eps, gt);
+    if (a.gate_kind == kGateToken && threadIdx.x == 0) static_cast<float*>(a.grad_gate)[t] = r.by;
 #pragma unroll
     for (int e = 0; e < kPieces; ++e) {
       const int lane = threadIdx.x + e * blockDim.x;
       if (lane * 8 >= H) continue;
       const size_t base = static_cast<size_t>(t) * H + lane * 8;
-      f32x2 d[4], f[4], z[4];
-      if (has_dv) {
-        lds_res8<kF32>(st + at_d, lane, d);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = both(0.f);
-      }
-      if (has_next) {
-        const f32x2 c = both(r2), k = both(k2);
-        lds_res8<kF32>(st + at_v, lane, f);
-        lds8(st + at_z, lane, z);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          z[i] = mul2(z[i], c);
-          d[i] = fma2(z[i], gn[e][i], fma2(k, f[i], d[i]));
-          acc_n[e][i] = fma2(z[i], f[i], acc_n[e][i]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) z[i] = mul2(scale, d[i]);
+      f32x2 y[4], v[4], z[4], d[4], g[4];
+      load(lane, y, v, z, d, g);
+      grad_piece(r, has, a.scale, inv_h, y, v, z, d, g, gp[e], gn[e], acc_p[e], acc_n[e]);
       store_res8<kF32>(a.grad_residual, base, z);
-      // dy = gt (r1 b - y r1^2 mean(b yh)) with b = d gate gp
-      const f32x2 c = both(r1 * gt);
-      const f32x2 k = both(has_post ? -(by * inv_h * r1 * r1 * gt) : 0.f);
-      lds8(st, lane, f);
-      if (full_gate) {
-        lds8(st + at_g, lane, z);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          d[i] = mul2(d[i], c);
-          const f32x2 g = z[i], b = mul2(d[i], gp[e][i]);
-          z[i] = mul2(b, f[i]);  // d u
-          acc_p[e][i] = fma2(mul2(d[i], g), f[i], acc_p[e][i]);
-          d[i] = mul2(b, g);
-        }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_gate) + base) = pack8(z);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          d[i] = mul2(d[i], c);
-          acc_p[e][i] = fma2(d[i], f[i], acc_p[e][i]);
-          d[i] = mul2(d[i], gp[e][i]);
-        }
-      }
-      if (has_post) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = fma2(k, f[i], d[i]);
-      }
+      if (full_gate)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_gate) + base) = pack8(g);
       *reinterpret_cast<uint4*>(a.grad_block + base) = pack8(d);
     }
     if (++s == stages) s = 0, parity ^= 1;
@@ -858,8 +958,8 @@ RingPlan ring_plan(const ResidualNormBackwardArgs& a) {
   return r;
 }
 
-// Sums of the partial rows, in a fixed order: 16 slices of rows per CTA, then the
-// slices in order. Plane 0 gives the gradients of the post weight and of a channel
+// Sums of the partial rows, in a fixed order: 32 slices of rows per CTA, then a tree
+// over the slices. Plane 0 gives the gradients of the post weight and of a channel
 // gate, plane 1 that of the next weight.
 __global__ void __launch_bounds__(kReduceCols* kReduceSlices)
     column_sum_kernel(const float* __restrict__ partials, const float* __restrict__ post,
@@ -882,12 +982,16 @@ __global__ void __launch_bounds__(kReduceCols* kReduceSlices)
     }
   }
   s_part[slice][cx] = s;
-  __syncthreads();
-  if (slice != 0 || col >= H) return;
-  for (int i = 1; i < kReduceSlices; ++i) {
-    const float4 v = s_part[i][cx];
-    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+#pragma unroll
+  for (int n = kReduceSlices / 2; n > 0; n /= 2) {
+    __syncthreads();
+    if (slice < n) {
+      const float4 v = s_part[slice + n][cx];
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      s_part[slice][cx] = s;
+    }
   }
+  if (slice != 0 || col >= H) return;
   if (blockIdx.y == 1) {
     *reinterpret_cast<float4*>(grad_next + col) = s;
     return;
@@ -903,10 +1007,10 @@ __global__ void __launch_bounds__(kReduceCols* kReduceSlices)
 
 // CTAs of the backward kernels: all resident.
 int backward_grid(int T, int H, int num_sms) {
-  if (H >= kRingMinH && H <= kRingMaxH)
-    return std::min(T, num_sms * backward_ring_ctas(H));
-  const Shape s = shape_of(H);
-  return std::min((T + s.per_cta - 1) / s.per_cta, num_sms * std::max(1, 1024 / s.threads));
+  if (H > kRingMaxH) return std::min(T, num_sms);
+  if (H >= kRingMinH) return std::min(T, num_sms * backward_ring_ctas(H));
+  const int rows = kNarrowThreads / 32;
+  return std::min((T + rows - 1) / rows, 2 * num_sms);
 }
 
 }  // namespace
@@ -921,11 +1025,25 @@ typedef void (*BackwardKernel)(const ResidualNormBackwardArgs, int);
 typedef void (*ForwardRingKernel)(const ResidualNormArgs, int, int, uint32_t*);
 typedef void (*RingKernel)(const ResidualNormBackwardArgs, int, int, uint32_t*);
 
-BackwardKernel backward_kernel(int pieces, bool f32) {
-  switch (pieces) {
-    case 1: return f32 ? residual_norm_backward_kernel<1, true> : residual_norm_backward_kernel<1, false>;
-    default: return f32 ? residual_norm_backward_kernel<4, true> : residual_norm_backward_kernel<4, false>;
-  }
+BackwardKernel backward_kernel(bool f32) {  // H > kRingMaxH
+  return f32 ? residual_norm_backward_kernel<4, true> : residual_norm_backward_kernel<4, false>;
+}
+
+typedef void (*NarrowKernel)(const ResidualNormBackwardArgs);
+
+template <int kMode>
+NarrowKernel narrow_kernel(int H, bool f32) {
+  if (H <= 256)
+    return f32 ? residual_norm_backward_narrow_kernel<true, 1, kMode>
+               : residual_norm_backward_narrow_kernel<false, 1, kMode>;
+  return f32 ? residual_norm_backward_narrow_kernel<true, 2, kMode>
+             : residual_norm_backward_narrow_kernel<false, 2, kMode>;
+}
+
+NarrowKernel narrow_kernel(int H, bool f32, int mode) {
+  return mode == kSome  ? narrow_kernel<kSome>(H, f32)
+         : mode == kAll ? narrow_kernel<kAll>(H, f32)
+                        : narrow_kernel<kAllGated>(H, f32);
 }
 
 template <int kRows>
@@ -944,23 +1062,30 @@ ForwardRingKernel forward_ring_kernel(int rows, int threads, bool f32) {
   return rows == 2 ? forward_ring_kernel<2>(threads, f32) : forward_ring_kernel<1>(threads, f32);
 }
 
-template <bool kF32>
+template <bool kF32, int kMode>
 RingKernel ring_kernel(int H) {
   const int threads = backward_ring_threads(H);
+  if (threads <= 128) return residual_norm_backward_ring_kernel<kF32, 128, 1, kMode>;
   if (backward_ring_pieces(H) == 1)
-    return threads <= 288 ? residual_norm_backward_ring_kernel<kF32, 288, 1>
-                          : residual_norm_backward_ring_kernel<kF32, 448, 1>;
-  return threads <= 448 ? residual_norm_backward_ring_kernel<kF32, 448, 2>
-                        : residual_norm_backward_ring_kernel<kF32, 512, 2>;
+    return threads <= 288 ? residual_norm_backward_ring_kernel<kF32, 288, 1, kMode>
+                          : residual_norm_backward_ring_kernel<kF32, 448, 1, kMode>;
+  return threads <= 448 ? residual_norm_backward_ring_kernel<kF32, 448, 2, kMode>
+                        : residual_norm_backward_ring_kernel<kF32, 512, 2, kMode>;
 }
 
-RingKernel ring_kernel(int H, bool f32) { return f32 ? ring_kernel<true>(H) : ring_kernel<false>(H); }
+RingKernel ring_kernel(int H, bool f32, int mode) {
+  switch (mode) {
+    case kSome: return f32 ? ring_kernel<true, kSome>(H) : ring_kernel<false, kSome>(H);
+    case kAll: return f32 ? ring_kernel<true, kAll>(H) : ring_kernel<false, kAll>(H);
+    default: return f32 ? ring_kernel<true, kAllGated>(H) : ring_kernel<false, kAllGated>(H);
+  }
+}
 
 }  // namespace
 
 cudaError_t setup_residual_norm(const DeviceInfo&) {
   for (bool f32 : {false, true}) {
-    cudaError_t e = cudaFuncSetAttribute(backward_kernel(4, f32),
+    cudaError_t e = cudaFuncSetAttribute(backward_kernel(f32),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          2 * 16384 * static_cast<int>(sizeof(float)));
     if (e != cudaSuccess) return e;
@@ -970,11 +1095,12 @@ cudaError_t setup_residual_norm(const DeviceInfo&) {
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       static_cast<int>(kRingSmem))) != cudaSuccess)
           return e;
-    for (int H : {2304, 3584, 7168, 8192})  // one of each kernel
-      if ((e = cudaFuncSetAttribute(ring_kernel(H, f32),
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(backward_ring_smem(H)))) != cudaSuccess)
-        return e;
+    for (int H : {1024, 2304, 3584, 7168, 8192})  // one of each kernel
+      for (int mode : {kSome, kAll, kAllGated})
+        if ((e = cudaFuncSetAttribute(ring_kernel(H, f32, mode),
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(backward_ring_smem(H)))) != cudaSuccess)
+          return e;
   }
   return cudaSuccess;
 }
@@ -1004,13 +1130,15 @@ cudaError_t launch_residual_norm_backward(const ResidualNormBackwardArgs& a,
   const RingPlan ring = ring_plan(a);
   cudaError_t e;
   if (ring.stages != 0) {
-    e = launch_dependent(ring_kernel(a.H, a.residual_f32), dim3(grid), dim3(ring.threads),
+    e = launch_dependent(ring_kernel(a.H, a.residual_f32, grad_mode(a)), dim3(grid), dim3(ring.threads),
                          ring.smem, stream, a, ring.stages, ring.stage_bytes, dev.err_word);
+  } else if (a.H <= kNarrowMaxH) {
+    e = launch_dependent(narrow_kernel(a.H, a.residual_f32, grad_mode(a)), dim3(grid),
+                         dim3(kNarrowThreads), 0, stream, a);
   } else {
     const Shape s = shape_of(a.H);
-    const size_t smem = s.pieces == 1 ? 0 : 2 * static_cast<size_t>(a.H) * sizeof(float);
-    e = launch_dependent(backward_kernel(s.pieces, a.residual_f32), dim3(grid), dim3(s.threads),
-                         smem, stream, a, s.tpr);
+    e = launch_dependent(backward_kernel(a.residual_f32), dim3(grid), dim3(s.threads),
+                         2 * static_cast<size_t>(a.H) * sizeof(float), stream, a, s.tpr);
   }
   const bool channel = a.gate_kind == kGateChannel;
   if (e != cudaSuccess || (a.post == nullptr && a.next == nullptr && !channel)) return e;
