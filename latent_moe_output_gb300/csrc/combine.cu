@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads)
       for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[j], a[i], acc[i]);
     }
   }
-  reinterpret_cast<uint4*>(out)[static_cast<size_t>(t) * nch + c] = pack8(acc);
+  st_stream_v4(reinterpret_cast<uint4*>(out) + static_cast<size_t>(t) * nch + c, pack8(acc));
 }
 
 // A group of kTpt threads per token; each thread owns every kTpt-th 16-byte piece of

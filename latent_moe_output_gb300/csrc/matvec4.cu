@@ -161,7 +161,6 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
     tma_prefetch_map(&w_map);
     tma_prefetch_map(&x_map);
   }
-  pdl_launch_dependents();
   pdl_wait();
   if (p.offsets != nullptr) {
     for (int e = threadIdx.x; e <= p.E; e += kThreads)
@@ -438,6 +437,9 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
                   static_cast<uint16_t>(pack_bf16x2(64.f * total[m][n][j], 0.f) & 0xffffu);
           }
     }
+    // Not before: CTAs of the next kernel would take the places of this one's that are
+    // not resident yet (one matrix, one row: 6.3 against 5.7 us).
+    pdl_launch_dependents();
     // Rows that no expert owns.
     const int mvec = p.M / 8;
     uint4* o4 = reinterpret_cast<uint4*>(p.out);

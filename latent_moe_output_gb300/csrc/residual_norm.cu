@@ -522,36 +522,44 @@ __device__ __forceinline__ GradRow grad_row(const float (&sum)[8], const GradHas
   return r;
 }
 
-// Gradients of one piece: dv becomes dy, z becomes dx, g becomes the gradient of a
-// full gate; acc_p += d gate yh (d yh with a channel gate), acc_n += dz vh.
-__device__ __forceinline__ void grad_piece(const GradRow& r, const GradHas& has, float scale,
-                                           float inv_h, const f32x2 (&y)[4], const f32x2 (&v)[4],
-                                           f32x2 (&z)[4], f32x2 (&dv)[4], f32x2 (&g)[4],
-                                           const f32x2 (&gp)[4], const f32x2 (&gn)[4],
-                                           f32x2 (&acc_p)[4], f32x2 (&acc_n)[4]) {
-  const f32x2 r2 = both(r.r2), k2 = both(r.k2), c = both(r.r1 * r.gt), s = both(scale);
-  // dy = gt (r1 b - y r1^2 mean(b yh)) with b = d gate gp
+// One piece: dv becomes d, z becomes dx; acc_n += dz vh.
+__device__ __forceinline__ void grad_residual_piece(const GradRow& r, const GradHas& has,
+                                                    float scale, const f32x2 (&v)[4],
+                                                    f32x2 (&z)[4], f32x2 (&dv)[4],
+                                                    const f32x2 (&gn)[4], f32x2 (&acc_n)[4]) {
+  const f32x2 r2 = both(r.r2), k2 = both(r.k2), s = both(scale);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (has.next) {
+      const f32x2 zr = mul2(z[i], r2);
+      dv[i] = fma2(zr, gn[i], fma2(k2, v[i], dv[i]));
+      acc_n[i] = fma2(zr, v[i], acc_n[i]);
+    }
+    z[i] = mul2(s, dv[i]);
+  }
+}
+
+// One piece: d becomes dy, g the gradient of a full gate; acc_p += d gate yh (d yh
+// with a channel gate). dy = gt (r1 b - y r1^2 mean(b yh)) with b = d gate gp.
+__device__ __forceinline__ void grad_block_piece(const GradRow& r, const GradHas& has,
+                                                 float inv_h, const f32x2 (&y)[4],
+                                                 f32x2 (&d)[4], f32x2 (&g)[4],
+                                                 const f32x2 (&gp)[4], f32x2 (&acc_p)[4]) {
+  const f32x2 c = both(r.r1 * r.gt);
   const f32x2 k = both(has.post ? -(r.by * inv_h * r.r1 * r.r1 * r.gt) : 0.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f32x2 d = dv[i];
-    if (has.next) {
-      const f32x2 zr = mul2(z[i], r2);
-      d = fma2(zr, gn[i], fma2(k2, v[i], d));
-      acc_n[i] = fma2(zr, v[i], acc_n[i]);
-    }
-    z[i] = mul2(s, d);
-    d = mul2(d, c);
+    const f32x2 e = mul2(d[i], c);
     if (has.full_gate) {
-      const f32x2 b = mul2(d, gp[i]);
-      acc_p[i] = fma2(mul2(d, g[i]), y[i], acc_p[i]);
-      d = mul2(b, g[i]);
+      const f32x2 b = mul2(e, gp[i]);
+      acc_p[i] = fma2(mul2(e, g[i]), y[i], acc_p[i]);
+      d[i] = mul2(b, g[i]);
       g[i] = mul2(b, y[i]);  // d u
     } else {
-      acc_p[i] = fma2(d, y[i], acc_p[i]);
-      d = mul2(d, gp[i]);
+      acc_p[i] = fma2(e, y[i], acc_p[i]);
+      d[i] = mul2(e, gp[i]);
     }
-    dv[i] = has.post ? fma2(k, y[i], d) : d;
+    if (has.post) d[i] = fma2(k, y[i], d[i]);
   }
 }
 
@@ -594,7 +602,6 @@ template <bool kF32, int kPieces, int kMode>
 __global__ void __launch_bounds__(kNarrowThreads, kPieces == 1 ? 2 : 1)
     residual_norm_backward_narrow_kernel(const ResidualNormBackwardArgs a) {
   __shared__ __align__(16) float s_sum[kNarrowThreads / 32][kNarrowMaxH];
-  pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const GradHas has = grad_has<kMode>(a);
@@ -636,14 +643,15 @@ __global__ void __launch_bounds__(kNarrowThreads, kPieces == 1 ? 2 : 1)
       const int col = (lane + e * 32) * 8;
       if (col >= a.H) continue;
       const size_t at = static_cast<size_t>(t) * a.H + col;
-      grad_piece(r, has, a.scale, inv_h, y[e], v[e], z[e], d[e], g[e], gp[e], gn[e], acc_p[e],
-                 acc_n[e]);
+      grad_residual_piece(r, has, a.scale, v[e], z[e], d[e], gn[e], acc_n[e]);
       store_res8<kF32>(a.grad_residual, at, z[e]);
+      grad_block_piece(r, has, inv_h, y[e], d[e], g[e], gp[e], acc_p[e]);
       if (has.full_gate)
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_gate) + at) = pack8(g[e]);
       *reinterpret_cast<uint4*>(a.grad_block + at) = pack8(d[e]);
     }
   }
+  pdl_launch_dependents();
   const size_t plane = static_cast<size_t>(gridDim.x) * a.H;
   float* out = a.partials + static_cast<size_t>(blockIdx.x) * a.H;
 #pragma unroll
@@ -789,8 +797,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Also without a second norm: after this barrier all threads are done with the stage.
     cta_sum<kRows>(sum, red[1]);
-    if (threadIdx.x == 0 && ok && t + static_cast<int64_t>(stages) * step < a.T)
-      fetch(t + stages * step, s);
     if (a.next != nullptr) {
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
@@ -803,6 +809,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    // Refilled after the row's stores: asking for it right after the barrier measured
+    // 1-4 % slower.
+    if (threadIdx.x == 0 && ok && t + static_cast<int64_t>(stages) * step < a.T)
+      fetch(t + stages * step, s);
     if (++s == stages) s = 0, parity ^= 1;
   }
   if (*abort_v && threadIdx.x == 0) drain_ring(full_bar, stages);
@@ -831,7 +841,6 @@ __global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(
   }
   for (int i = threadIdx.x; i < static_cast<int>(sizeof(red) / 4); i += blockDim.x)
     (&red[0][0][0])[i] = 0.f;
-  pdl_launch_dependents();
   pdl_wait();
   __syncthreads();
 
@@ -869,22 +878,16 @@ __global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(
     f32x2 q[6];
 #pragma unroll
     for (int i = 0; i < 6; ++i) q[i] = both(0.f);
-    auto load = [&](int lane, f32x2 (&y)[4], f32x2 (&v)[4], f32x2 (&z)[4], f32x2 (&d)[4],
-                    f32x2 (&g)[4]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) z[i] = d[i] = g[i] = both(0.f);
-      lds8(st, lane, y);
-      lds_res8<kF32>(st + at_v, lane, v);
-      if (has_next) lds8(st + at_z, lane, z);
-      if (has_dv) lds_res8<kF32>(st + at_d, lane, d);
-      if (full_gate) lds8(st + at_g, lane, g);
-    };
 #pragma unroll
     for (int e = 0; e < kPieces; ++e) {
       const int lane = threadIdx.x + e * blockDim.x;  // piece of the row
       if (lane * 8 >= H) continue;
       f32x2 y[4], v[4], z[4], d[4], g[4];
-      load(lane, y, v, z, d, g);
+      lds8(st, lane, y);
+      lds_res8<kF32>(st + at_v, lane, v);
+      if (has_next) lds8(st + at_z, lane, z);
+      if (has_dv) lds_res8<kF32>(st + at_d, lane, d);
+      if (full_gate) lds8(st + at_g, lane, g);
       grad_sums(q, has, y, v, z, d, g, gp[e], gn[e]);
     }
 #pragma unroll
@@ -903,15 +906,27 @@ __global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(
       if (lane * 8 >= H) continue;
       const size_t base = static_cast<size_t>(t) * H + lane * 8;
       f32x2 y[4], v[4], z[4], d[4], g[4];
-      load(lane, y, v, z, d, g);
-      grad_piece(r, has, a.scale, inv_h, y, v, z, d, g, gp[e], gn[e], acc_p[e], acc_n[e]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[i] = d[i] = both(0.f);
+      if (has_dv) lds_res8<kF32>(st + at_d, lane, d);
+      if (has_next) {
+        lds_res8<kF32>(st + at_v, lane, v);
+        lds8(st + at_z, lane, z);
+      }
+      grad_residual_piece(r, has, a.scale, v, z, d, gn[e], acc_n[e]);
       store_res8<kF32>(a.grad_residual, base, z);
+      lds8(st, lane, y);
+      if (full_gate) lds8(st + at_g, lane, g);
+      grad_block_piece(r, has, inv_h, y, d, g, gp[e], acc_p[e]);
       if (full_gate)
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_gate) + base) = pack8(g);
       *reinterpret_cast<uint4*>(a.grad_block + base) = pack8(d);
     }
     if (++s == stages) s = 0, parity ^= 1;
   }
+  // Not before: CTAs of the next kernel would take the places of this one's that are
+  // not resident yet (measured: 52 against 38 us at T = 4614, H = 1224, FP32).
+  pdl_launch_dependents();
   const size_t plane = static_cast<size_t>(gridDim.x) * H;
 #pragma unroll
   for (int e = 0; e < kPieces; ++e) {
@@ -937,7 +952,9 @@ RingPlan ring_plan(const ResidualNormArgs& a, int rows, int num_sms) {
   const int bytes = h2 + (a.residual_f32 ? 2 * h2 : h2) + (a.gate_kind == kGateFull ? h2 : 0);
   r.stage_bytes = (rows * bytes + 127) / 128 * 128;
   r.threads = ring_threads(a.H);
-  r.stages = static_cast<int>(std::min<size_t>(kRingMaxStages, kRingSmem / r.stage_bytes));
+  // Two stages: more measured slower (T = 8192, H = 7168, channel gate: 75 against 82 us
+  // with three; without a gate the same).
+  r.stages = static_cast<int>(std::min<size_t>(2, kRingSmem / r.stage_bytes));
   r.smem = static_cast<size_t>(r.stages) * r.stage_bytes;
   return r;
 }
@@ -952,8 +969,12 @@ RingPlan ring_plan(const ResidualNormBackwardArgs& a) {
                     (a.gate_kind == kGateFull ? h2 : 0);
   r.stage_bytes = (bytes + 127) / 128 * 128;
   r.threads = backward_ring_threads(a.H);
-  r.stages = static_cast<int>(
-      std::min<size_t>(kRingMaxStages, backward_ring_smem(a.H) / r.stage_bytes));
+  // Two stages at least; more only while they leave 24 KB of the SM's shared memory to
+  // the L1 cache (T = 8192, H = 7168: 110 us with three stages, 121 with four, 154 with
+  // two).
+  const size_t smem = backward_ring_smem(a.H);
+  r.stages = static_cast<int>(std::min<size_t>(kRingMaxStages, smem * 25 / 28 / r.stage_bytes));
+  r.stages = std::max(r.stages, static_cast<int>(std::min<size_t>(2, smem / r.stage_bytes)));
   r.smem = static_cast<size_t>(r.stages) * r.stage_bytes;
   return r;
 }
@@ -967,7 +988,6 @@ __global__ void __launch_bounds__(kReduceCols* kReduceSlices)
                       float* __restrict__ grad_gate, float* __restrict__ grad_next,
                       int partial_rows, int H) {
   __shared__ float4 s_part[kReduceSlices][kReduceCols];
-  pdl_launch_dependents();
   pdl_wait();
   if (blockIdx.y == 0 ? grad_post == nullptr && grad_gate == nullptr : grad_next == nullptr) return;
   const int cx = threadIdx.x % kReduceCols, slice = threadIdx.x / kReduceCols;
@@ -981,6 +1001,7 @@ __global__ void __launch_bounds__(kReduceCols* kReduceSlices)
       s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
     }
   }
+  pdl_launch_dependents();
   s_part[slice][cx] = s;
 #pragma unroll
   for (int n = kReduceSlices / 2; n > 0; n /= 2) {
