@@ -89,6 +89,13 @@ def _empty(shape, dtype, index, stream):
         return torch.empty(shape, dtype=dtype, device=index)
 
 
+def _like(t, stream):
+    """An empty tensor like the contiguous ``t`` (half the host time of torch.empty)."""
+    if stream is None:
+        return torch.empty_like(t)
+    return _empty(t.shape, t.dtype, t.get_device(), stream)
+
+
 def _call(name, index, stream, *args):
     """Run one C entry point with ``index`` as the current device."""
     if torch._C._cuda_getDevice() != index:
@@ -281,22 +288,26 @@ def residual_norm_backward(grad_residual_out, grad_next, block, residual_out, po
     kind, gate_dtype, gate_shape = _gate_kind(gate, T, H)
     f32 = _residual_type(residual_out, "residual_out")
     rdt = residual_out.dtype
-    grad_block = _empty((T, H), _BF16, i, stream)
-    grad_residual = _empty((T, H), rdt, i, stream)
-    grad_post = None if post_weight is None else _empty((H,), _F32, i, stream)
-    grad_nextw = None if next_weight is None else _empty((H,), _F32, i, stream)
-    grad_gate = None if gate is None else _empty(gate_shape, gate_dtype, i, stream)
+    given = (_ptr(grad_residual_out, "grad_residual_out", rdt, (T, H), i),
+             _ptr(grad_next, "grad_next", _BF16, (T, H), i),
+             _ptr(block, "block", _BF16, (T, H), i),
+             _ptr(residual_out, "residual_out", rdt, (T, H), i),
+             _ptr(post_weight, "post_weight", _F32, (H,), i),
+             _ptr(gate, "gate", gate_dtype, gate_shape, i),
+             _ptr(next_weight, "next_weight", _F32, (H,), i))
+    grad_block, grad_residual = _like(block, stream), _like(residual_out, stream)
+    grad_post = None if post_weight is None else _like(post_weight, stream)
+    grad_gate = None if gate is None else _like(gate, stream)
+    grad_nextw = None if next_weight is None else _like(next_weight, stream)
     if workspace is None:
-        workspace = _empty((max(16, residual_norm_backward_workspace_size(T, H)),), _U8, i, stream)
-    ws, ws_bytes = _workspace(workspace, i)
-    _call("latent_tail_residual_norm_backward", i, stream,
-          _ptr(grad_residual_out, "grad_residual_out", rdt, (T, H), i),
-          _ptr(grad_next, "grad_next", _BF16, (T, H), i), _ptr(block, "block", _BF16, (T, H), i),
-          _ptr(residual_out, "residual_out", rdt, (T, H), i),
-          _ptr(post_weight, "post_weight", _F32, (H,), i),
-          _ptr(gate, "gate", gate_dtype, gate_shape, i),
-          _ptr(next_weight, "next_weight", _F32, (H,), i), _ptr(grad_block, "", _BF16, (T, H), i),
-          _ptr(grad_residual, "", rdt, (T, H), i), _ptr(grad_post, "", _F32, (H,), i),
-          _ptr(grad_gate, "", gate_dtype, gate_shape, i), _ptr(grad_nextw, "", _F32, (H,), i),
+        ws_bytes = max(16, residual_norm_backward_workspace_size(T, H))
+        workspace = _empty((ws_bytes,), _U8, i, stream)
+        ws = workspace.data_ptr()
+    else:
+        ws, ws_bytes = _workspace(workspace, i)
+    _call("latent_tail_residual_norm_backward", i, stream, *given, grad_block.data_ptr(),
+          grad_residual.data_ptr(), 0 if grad_post is None else grad_post.data_ptr(),
+          0 if grad_gate is None else grad_gate.data_ptr(),
+          0 if grad_nextw is None else grad_nextw.data_ptr(),
           T, H, kind, f32, residual_scale, eps, ws, ws_bytes)
     return grad_block, grad_residual, grad_post, grad_gate, grad_nextw
