@@ -24,10 +24,11 @@
 // One warp streams weights and x through a ring of stages with TMA: a stage holds
 // kSplit boxes of 256 columns (kRows x 128 bytes of weights, swizzled so that the
 // eight rows of a fragment lie in different banks, 8 * kTiles rows of x, the scales). The
-// eight other warps each own 32 weight rows and half of one box's columns (a
-// fragment of x then serves two of weights); the 2 * kSplit column parts are added
-// in order through shared memory at the end of a tile. kSplit = 4 gives enough tiles
-// to fill the GPU from one matrix.
+// eight other warps each own 32 weight rows (a fragment of x serves two of weights) and,
+// with one box per stage, all of its columns: no warp then waits for another one.
+// With several boxes a warp takes half of one, and the column parts are added in
+// order through shared memory at the end of a tile: that makes enough tiles to fill
+// the GPU from one matrix.
 #include "block_launch.h"
 #include "rows.cuh"
 
@@ -45,8 +46,12 @@ constexpr int table_bytes(int E) { return (E + 1) * 2 * static_cast<int>(sizeof(
 
 template <int kSplit, int kTiles, int kM>
 struct Config {
-  static constexpr int kRows = 64 * kM / kSplit;
-  static constexpr int kCtasPerSm = kTiles == 4 || kM == 4 ? 1 : 2;  // registers: 96 at two
+  // With one box per stage a warp takes all of its columns, else half of one box's.
+  static constexpr int kHalves = kSplit == 1 ? 1 : 2;
+  static constexpr int kParts = kSplit * kHalves;  // column parts of a stage
+  static constexpr int kRowWarps = kConsumers / kParts;
+  static constexpr int kRows = kRowWarps * 16 * kM;
+  static constexpr int kCtasPerSm = kTiles == 4 ? 1 : 2;  // registers: 96 at two
   static constexpr int kWeightBytes = kSplit * kRows * 128;
   static constexpr int kXBoxBytes = 8 * 128;  // 8 rows x 64 columns
   static constexpr int kXBytes = kSplit * kTiles * 4 * kXBoxBytes;
@@ -58,7 +63,6 @@ struct Config {
   static constexpr int kPieceBytes = kPieces ? 32 : 16;
   static constexpr int kScaleBytes = (kPieces ? 1 : kSplit) * kRows * kPieceBytes;
   static constexpr int kStageBytes = kWeightBytes + kXBytes + kScaleBytes;
-  static constexpr int kParts = 2 * kSplit;
   // Column parts 1.. of a tile's sums.
   static constexpr int kSumBytes = (kParts - 1) * kRows * 8 * kTiles * 4;
   static constexpr int kFit = (kSmemPerSm / kCtasPerSm - kSumBytes - 1024) / kStageBytes;
@@ -103,8 +107,8 @@ __device__ __forceinline__ void consumer_barrier() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
 }
 
-// Rows [row0, row0 + rows) of expert e against weight rows m0...
-struct Tile {
+// Rows [row0, row0 + rows) of expert e against weight rows from m0 on.
+struct __align__(16) Tile {
   int e, row0, rows, m0;
 };
 
@@ -140,6 +144,9 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
   constexpr int kScales = kBoxCols / kGroup;  // per row and box
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full_bar[Cfg::kStages], empty_bar[Cfg::kStages];
+  // The tile that begins with a stage, for the consumers: written before the stage's
+  // barrier is armed, read after its wait, rewritten no earlier than the stage's slot.
+  __shared__ Tile s_tile[Cfg::kStages];
   __shared__ int abort_flag;
   volatile int* abort_v = &abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -221,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
           const uint32_t s = it % Cfg::kStages;
           ok = mbar_wait(smem_u32(&empty_bar[s]), ((it / Cfg::kStages) & 1u) ^ 1u, p.err, abort_v);
           if (!ok) break;
+          if (i == 0) s_tile[s] = t;
           const int live = min(kSplit, boxes - i * kSplit);
           const uint32_t bar = smem_u32(&full_bar[s]);
           const uint32_t st = ring + s * Cfg::kStageBytes;
@@ -265,12 +273,13 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
       }
     }
   } else {
-    constexpr int kRowWarps = Cfg::kRows / (16 * kM);
-    constexpr int kHalf = kScales / 2;              // scales per row and half box
+    constexpr int kRowWarps = Cfg::kRowWarps;
+    constexpr int kRuns = 8 / Cfg::kHalves;         // runs of 32 columns per box and warp
+    constexpr int kHalf = kScales / Cfg::kHalves;   // scales per row, box and warp
     constexpr int kWords = (kHalf + 1) / 2;
     const int part = warp / kRowWarps;              // column part of every stage
-    const int box_in = part >> 1, half = part & 1;  // its box and half
-    const int mrow = warp % kRowWarps * 16 * kM;         // first weight row in the tile
+    const int box_in = part / Cfg::kHalves, half = part % Cfg::kHalves;  // its box and half
+    const int mrow = warp % kRowWarps * 16 * kM;    // first weight row in the tile
     const int g = lane >> 2, c4 = lane & 3;
     // Column n of a fragment holds row (n >> 1) + 4 (n & 1) of the eight: lanes of
     // one quarter of the warp then read different halves of the swizzled rows.
@@ -279,13 +288,11 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
     uint32_t it = 0, pieces = 0;
     bool ok = true;
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-      const Tile t = tile_at(tile, mblocks, Cfg::kRows, kPass, s_first, s_unit, p.E);
+      if (ok) ok = mbar_wait(smem_u32(&full_bar[it % Cfg::kStages]), (it / Cfg::kStages) & 1u,
+                             p.err, abort_v);
+      Tile t{};
+      if (ok) t = s_tile[it % Cfg::kStages];
       const int n_tiles = kTiles == 1 ? 1 : (t.rows + 7) / 8;
-      const uint16_t* stile = p.scales + (static_cast<size_t>(t.e) * p.M + t.m0) * pitch;
-      int srow[2 * kM];  // weight rows mrow + g + 8 h
-#pragma unroll
-      for (int h = 0; h < 2 * kM; ++h)  // (rows past the matrix are read from its last row)
-        srow[h] = min(p.M - 1 - t.m0, mrow + g + h * 8) * pitch;
       float total[kM][kTiles][4];
 #pragma unroll
       for (int m = 0; m < kM; ++m)
@@ -296,15 +303,15 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
 
       for (int i = 0; i < steps; ++i, ++it) {
         const uint32_t s = it % Cfg::kStages;
-        if (ok) ok = mbar_wait(smem_u32(&full_bar[s]), (it / Cfg::kStages) & 1u, p.err, abort_v);
+        if (ok && i > 0)
+          ok = mbar_wait(smem_u32(&full_bar[s]), (it / Cfg::kStages) & 1u, p.err, abort_v);
         const int box = i * kSplit + box_in;
-        // Runs of 32 columns in this half box.
-        const int runs = min(4, (p.C - box * kBoxCols) / 32 - half * 4);
+        const int runs = min(kRuns, (p.C - box * kBoxCols) / 32 - half * kRuns);
         const uint8_t* st = ring_ptr + s * Cfg::kStageBytes;
         const uint8_t* wa = st + box_in * Cfg::kRows * 128 + (mrow + g) * 128 + c4 * 4;
         const uint8_t* xa =
             st + Cfg::kWeightBytes + box_in * kTiles * 4 * Cfg::kXBoxBytes + xrow * 128;
-        // Scales of half a box: kHalf per row, two per register.
+        // This warp's scales of the box: kHalf per row, two per register.
         uint32_t sc[2 * kM][kWords] = {};
         if (p.staged_scales) {
           if (Cfg::kPieces && i % kStagesPerPiece == 0) ++pieces;
@@ -316,7 +323,14 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
                               ((box * kScales & kMask) + half * kHalf) * 2;
 #pragma unroll
           for (int h = 0; h < 2 * kM; ++h) {
-            if constexpr (kHalf == 4) {
+            if constexpr (kHalf == 8) {
+              const uint4 v = *reinterpret_cast<const uint4*>(
+                  sa + ((h >> 1) * 16 + (h & 1) * 8) * Cfg::kPieceBytes);
+              sc[h][0] = v.x;
+              sc[h][1] = v.y;
+              sc[h][2] = v.z;
+              sc[h][3] = v.w;
+            } else if constexpr (kHalf == 4) {
               const uint2 v = *reinterpret_cast<const uint2*>(sa + h * 8 * Cfg::kPieceBytes);
               sc[h][0] = v.x;
               sc[h][1] = v.y;
@@ -328,19 +342,22 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
           }
         } else if (ok && runs > 0) {
           const int first = box * kScales + half * kHalf;
+          const uint16_t* stile = p.scales + (static_cast<size_t>(t.e) * p.M + t.m0) * pitch;
 #pragma unroll
           for (int h = 0; h < 2 * kM; ++h)
 #pragma unroll
             for (int q = 0; q < kHalf; ++q)
-              if (first + q < pitch)
-                sc[h][q >> 1] |= static_cast<uint32_t>(__ldg(stile + srow[h] + first + q))
+              if (first + q < pitch) {  // (rows past the matrix are read from its last row)
+                const int row = min(p.M - 1 - t.m0, mrow + g + h * 8);
+                sc[h][q >> 1] |= static_cast<uint32_t>(__ldg(stile + row * pitch + first + q))
                                  << (16 * (q & 1));
+              }
         }
         float acc[kM][kTiles][4];
         auto run = [&](int j) {  // j: run in the half box, known at compile time
           constexpr int kRunsPerGroup = kGroup / 32;
           const bool opens = j % kRunsPerGroup == 0, closes = (j + 1) % kRunsPerGroup == 0;
-          const int chunk = half * 4 + j;
+          const int chunk = half * kRuns + j;
           uint32_t lo[kM][4], hi[kM][4];  // fragments: values 0, 1, 4, 5 and 2, 3, 6, 7
 #pragma unroll
           for (int m = 0; m < kM; ++m) {
@@ -385,42 +402,42 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
             }
           }
         };
-        if (ok && runs == 4) {
-          run(0);
-          run(1);
-          run(2);
-          run(3);
-        } else if (ok && runs > 0) {  // (whole groups: C is a multiple of the group)
-          run(0);
-          if (runs > 1) run(1);
-          if (runs > 2) run(2);
+        if (ok && runs == kRuns) {
+#pragma unroll
+          for (int j = 0; j < kRuns; ++j) run(j);
+        } else if (ok) {  // (whole groups: C is a multiple of the group)
+#pragma unroll
+          for (int j = 0; j < kRuns - 1; ++j)
+            if (j < runs) run(j);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&empty_bar[s]));
       }
 
-      // The column parts of a row are added in order by part 0's warp.
-      consumer_barrier();  // the last tile's sums have been read
-      constexpr int kPerWarp = 16 * kM * 8 * kTiles;
-      if (part > 0) {
-        float* dst = sums + ((part - 1) * kRowWarps + warp % kRowWarps) * kPerWarp + lane;
+      if constexpr (Cfg::kParts > 1) {
+        // The column parts of a row are added in order by part 0's warp.
+        consumer_barrier();  // the last tile's sums have been read
+        constexpr int kPerWarp = 16 * kM * 8 * kTiles;
+        if (part > 0) {
+          float* dst = sums + ((part - 1) * kRowWarps + warp % kRowWarps) * kPerWarp + lane;
 #pragma unroll
-        for (int m = 0; m < kM; ++m)
+          for (int m = 0; m < kM; ++m)
 #pragma unroll
-          for (int n = 0; n < kTiles; ++n)
+            for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dst[((m * kTiles + n) * 4 + j) * 32] = total[m][n][j];
-      }
-      consumer_barrier();
-      if (part > 0) continue;
-      for (int q = 0; q < Cfg::kParts - 1; ++q) {
-        const float* src = sums + (q * kRowWarps + warp) * kPerWarp + lane;
+              for (int j = 0; j < 4; ++j) dst[((m * kTiles + n) * 4 + j) * 32] = total[m][n][j];
+        }
+        consumer_barrier();
+        if (part > 0) continue;
+        for (int q = 0; q < Cfg::kParts - 1; ++q) {
+          const float* src = sums + (q * kRowWarps + warp) * kPerWarp + lane;
 #pragma unroll
-        for (int m = 0; m < kM; ++m)
+          for (int m = 0; m < kM; ++m)
 #pragma unroll
-          for (int n = 0; n < kTiles; ++n)
+            for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) total[m][n][j] += src[((m * kTiles + n) * 4 + j) * 32];
+              for (int j = 0; j < 4; ++j) total[m][n][j] += src[((m * kTiles + n) * 4 + j) * 32];
+        }
       }
       // Element (j, lane) of a fragment: weight row g + 8 (j >> 1), column
       // 2 c4 + (j & 1), i.e. row c4 + 4 (j & 1) of x.
@@ -467,8 +484,8 @@ Variant variant() {
 template <int kGroup>
 Variant pick(int split, int tiles) {
   if (split > 1) return tiles == 1 ? variant<kGroup, 4, 1>() : variant<kGroup, 2, 2>();
-  return tiles == 1 ? variant<kGroup, 1, 1, 4>()
-                    : tiles == 2 ? variant<kGroup, 1, 2, 4>() : variant<kGroup, 1, 4>();
+  return tiles == 1 ? variant<kGroup, 1, 1>()
+                    : tiles == 2 ? variant<kGroup, 1, 2>() : variant<kGroup, 1, 4>();
 }
 
 Variant pick(int group, int split, int tiles) {
@@ -498,7 +515,7 @@ cudaError_t launch_matvec4(const Matvec4Args& a, const DeviceInfo& dev, cudaStre
   const int64_t mean8 = a.E == 1 ? a.N : 4 * (static_cast<int64_t>(a.N) / matrices);
   int tiles = mean8 <= 8 ? 1 : mean8 <= 16 ? 2 : 4;
   const int64_t large = static_cast<int64_t>(matrices) * ((a.M + 127) / 128);
-  const int split = tiles <= 2 && large < 4 * dev.num_sms ? 2 : 1;
+  const int split = tiles <= 2 && large < dev.num_sms ? 2 : 1;
   const Variant v = pick(a.G, split, tiles);
   const uint64_t rows = static_cast<uint64_t>(a.E) * a.M;
   const uint64_t pitch = static_cast<uint64_t>(a.C / a.G) * 2;
