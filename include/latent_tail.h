@@ -339,8 +339,8 @@ LT_API lt_status latent_tail_combine_backward(const uint16_t* grad_out, const ui
  *   out[r,m] = sum_c x[r,c] * (q[e,m,c] - 8) * scales[e,m,c/G]
  * with q[e,m,c] the 4-bit value in byte packed[e,m,c/2] (low four bits: even c),
  * products and sums in FP32, rounded once to bf16. Meant for the few rows of
- * decode steps, where reading the weights bounds the call: each matrix with rows
- * is read once for up to 32 of them.
+ * decode steps, where reading the weights bounds the call: a matrix is read once
+ * for 8 of its rows (16 where experts have many), again (mostly from L2) for more.
  *   x [N, C] bf16, packed [E, M, C/2] bytes, scales [E, M, C/G] bf16,
  *   offsets [E+1] int32 (rows of expert e: offsets[e] .. offsets[e+1]-1, as
  *   latent_tail_dispatch writes it; rows from offsets[E] on give zeros) or NULL

@@ -5,9 +5,10 @@
 //            = sum_groups s[e,m,g] * ( sum_{c in g} x[r,c] * (q[e,m,c] - 8) )
 //
 // With the few rows per expert of a decode step the weights are read once and
-// used at most a few times, so their stream bounds the call, and after it the
-// unpacking: at the measured copy rate an SM receives 41 weights per clock at
-// G = 32 and has 64 lanes per clock for logic operations.
+// used at most a few times, so their stream bounds the call, and right after it the
+// instructions that unpack them: at the measured copy rate an SM receives 41 weights
+// per clock at G = 32, has 128 instruction lanes per clock, and spends about two
+// instructions per weight.
 // A 4-bit value masked out at bit 0 or 4 of a bf16 pattern is that integer times
 // 2^-133 (subnormals and the first binade are one linear range), so one masking and
 // one exact bf16 fused multiply-add per two weights give (q - 8) / 64: five logic
@@ -15,10 +16,10 @@
 // exact operands and FP32 accumulators: 16 weight rows x 16 columns against 8 rows
 // of x per instruction. These warp-level instructions take their operands from
 // registers, where the unpacked weights are; the tcgen05 ones would need them
-// written back to shared memory first, and at 8 to 32 rows the tensor rate does not
+// written back to shared memory first, and at 8 or 16 rows the tensor rate does not
 // matter. Scales multiply the FP32 group sums; the factor 64 is applied at the end.
 //
-// Layout of the work. A tile is kRows = 128 / kSplit weight rows of one expert,
+// Layout of the work. A tile is kRows = 32 to 256 weight rows of one expert,
 // against up to 8 * kTiles rows of x (a pass). The CTAs walk over the tiles of
 // the experts that have rows (found from the offsets at the start of the kernel).
 // One warp streams weights and x through a ring of stages with TMA: a stage holds
@@ -29,6 +30,13 @@
 // With several boxes a warp takes half of one, and the column parts are added in
 // order through shared memory at the end of a tile: that makes enough tiles to fill
 // the GPU from one matrix.
+//
+// Measured (GB300, launched back to back, weights of three calls in turn): 16 tokens
+// with 8 of 256 experts of 2048 x 2048, G = 32 (about 103 experts read, 240 MB):
+// 50 us = 4.8 TB/s, 71 % of the measured copy rate; 64 tokens: 94 us, 5.6 TB/s. The
+// stream alone, without the arithmetic, takes 40 and 81 us; per stage a warp issues for
+// 2500 cycles, waits for 700 and spends 250 between tiles. One token with one matrix
+// of 7168 x 2048, G = 128: 5.4 us (latency: 2 stages per tile).
 #include "block_launch.h"
 #include "rows.cuh"
 
@@ -51,7 +59,7 @@ struct Config {
   static constexpr int kParts = kSplit * kHalves;  // column parts of a stage
   static constexpr int kRowWarps = kConsumers / kParts;
   static constexpr int kRows = kRowWarps * 16 * kM;
-  static constexpr int kCtasPerSm = kTiles == 4 ? 1 : 2;  // registers: 96 at two
+  static constexpr int kCtasPerSm = 2;  // 96 registers
   static constexpr int kWeightBytes = kSplit * kRows * 128;
   static constexpr int kXBoxBytes = 8 * 128;  // 8 rows x 64 columns
   static constexpr int kXBytes = kSplit * kTiles * 4 * kXBoxBytes;
@@ -481,11 +489,14 @@ Variant variant() {
                  Cfg::kCtasPerSm, Cfg::kPieceBytes};
 }
 
+// split: 1 (whole boxes), 2 (two boxes per stage, 64 rows), 4 (the smallest tiles).
 template <int kGroup>
 Variant pick(int split, int tiles) {
-  if (split > 1) return tiles == 1 ? variant<kGroup, 4, 1>() : variant<kGroup, 2, 2>();
-  return tiles == 1 ? variant<kGroup, 1, 1>()
-                    : tiles == 2 ? variant<kGroup, 1, 2>() : variant<kGroup, 1, 4>();
+  if (tiles == 1)
+    return split == 1   ? variant<kGroup, 1, 1>()
+           : split == 2 ? variant<kGroup, 2, 1>()
+                        : variant<kGroup, 4, 1>();
+  return split == 1 ? variant<kGroup, 1, 2>() : variant<kGroup, 2, 2>();
 }
 
 Variant pick(int group, int split, int tiles) {
@@ -497,8 +508,8 @@ Variant pick(int group, int split, int tiles) {
 
 cudaError_t setup_matvec4(const DeviceInfo&) {
   for (int group : {32, 64, 128})
-    for (int split : {1, 2})
-      for (int tiles : {1, 2, 4}) {
+    for (int split : {1, 2, 4})
+      for (int tiles : {1, 2}) {
         const Variant v = pick(group, split, tiles);
         const cudaError_t e = cudaFuncSetAttribute(
             v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -509,13 +520,21 @@ cudaError_t setup_matvec4(const DeviceInfo&) {
 }
 
 cudaError_t launch_matvec4(const Matvec4Args& a, const DeviceInfo& dev, cudaStream_t stream) {
-  // Rows per pass: all of them with one matrix, else by the mean rows per expert
-  // (an expert with more takes several passes, which re-read its weights from L2).
+  // Tiles of 64 rows, of 32 where even those would leave a third of the SMs idle, as
+  // long as tiles of 256 would not fill the GPU for a few rounds. (T tokens with 8 of
+  // 256 experts of 2048 x 2048, us with tiles of 256 and of 64 rows: T = 3 20.3 and
+  // 18.3, T = 6 28.5 and 28.6, T = 12 42.4 and 45.3. One row against one matrix, 64 and
+  // 32 rows: 7168 x 2048 5.4 and 6.0, 2048 x 7168 11.8 and 9.5.)
   const int matrices = std::min(a.E, a.N);
-  const int64_t mean8 = a.E == 1 ? a.N : 4 * (static_cast<int64_t>(a.N) / matrices);
-  int tiles = mean8 <= 8 ? 1 : mean8 <= 16 ? 2 : 4;
-  const int64_t large = static_cast<int64_t>(matrices) * ((a.M + 127) / 128);
-  const int split = tiles <= 2 && large < dev.num_sms ? 2 : 1;
+  const int64_t tiles256 = static_cast<int64_t>(matrices) * ((a.M + 255) / 256);
+  const int64_t tiles64 = static_cast<int64_t>(matrices) * ((a.M + 63) / 64);
+  const bool narrow = 3 * tiles64 < 2 * dev.num_sms;
+  const int split = tiles256 > 3 * dev.num_sms ? 1 : narrow ? 4 : 2;
+  // Sixteen rows of x per pass instead of eight where an expert has more than twelve on
+  // average: passes after the first read the weights from L2, and the second fragment
+  // of x costs registers and a stage's space. (Mean rows 8: 42.5 us with eight and 46.2
+  // with sixteen, 64 experts; mean 16: 66.4 and 61.6. One matrix, 24 rows: 9.6 and 8.3.)
+  const int tiles = a.N / matrices > 12 && !narrow ? 2 : 1;
   const Variant v = pick(a.G, split, tiles);
   const uint64_t rows = static_cast<uint64_t>(a.E) * a.M;
   const uint64_t pitch = static_cast<uint64_t>(a.C / a.G) * 2;
