@@ -5,13 +5,18 @@
 //   row(i) = #{j : key(j) < key(i)} + #{j < i : key(j) == key(i)}.
 //
 // Up to kDispatchOneLaunch choices, one kernel with one CTA per choice counts
-// that definition directly over all ids (a few 16-byte loads per thread, from
-// L2) while its row is on its way, and copies the row: one launch, no workspace.
+// that definition directly over all ids (a few loads per thread, from L2) while its
+// row is on its way, and copies the row: one launch, no workspace (2.0 us at 128
+// choices, of which nothing but latency is left).
 // Above that the choices are cut into contiguous chunks, one CTA each: a first
-// kernel counts the experts of each chunk, a second sums the counts of the
-// chunks before its own (so every CTA knows where its choices of each expert
-// begin), ranks its own choices with warp-wide matches, and a third copies the
-// rows. No atomics decide an order: the places are the same from run to run.
+// kernel counts the experts of each chunk; a second sums the counts of the chunks
+// before its own (so every CTA knows where its choices of each expert begin), ranks
+// its own choices with warp-wide matches, and copies their rows, or leaves that to a
+// third kernel that reads each row of x once for all its places. Memory bounds the
+// copy: 131072 choices of 16384 tokens, L = 2048: 98.5 us for 604 MB, 6.1 TB/s, 90 % of
+// the measured copy rate, with 88 us for the copy and the rest for the sort. (Bringing x
+// into L2 during the sort did not help: the writes of the call before still drain
+// then.) No atomics decide an order: the places are the same from run to run.
 #include "block_launch.h"
 #include "rows.cuh"
 
@@ -24,6 +29,14 @@ constexpr int kSmallThreads = 256;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kCopyThreads = 256;
+// The ranking kernel copies its chunk's rows itself up to this size, above it a third
+// kernel does (measured with 8 choices of 256 experts, L = 2048, us with two and three
+// kernels: T = 512 8.2 and 11.3, 1024 11.5 and 13.0, 2048 18.0 and 18.7, 4096 32.3 and
+// 30.8), and for rows of less than a warp's 16-byte pieces up to kMaxNarrowRows choices
+// per chunk (8 choices, L = 72: T = 605 5.9 and 7.1, 4000 8.3 and 7.2).
+constexpr size_t kMaxFusedBytes = size_t(80) << 20;
+constexpr int kMaxNarrowRows = 128;
+constexpr int kMaxChunkRows = 4096;  // choices per chunk that the ranking kernel copies itself
 
 __device__ __forceinline__ int choice_key(int id, int E) {
   return static_cast<unsigned>(id) < static_cast<unsigned>(E) ? id : E;
@@ -108,12 +121,14 @@ __global__ void __launch_bounds__(kSortThreads)
 __global__ void __launch_bounds__(kSortThreads)
     dispatch_rank_kernel(const int32_t* __restrict__ ids, const uint16_t* __restrict__ counts,
                          int32_t* __restrict__ offsets, int32_t* __restrict__ order,
-                         int32_t* __restrict__ position, int n, int E, int per_chunk,
-                         int stride) {
+                         int32_t* __restrict__ position, int n, int E, int per_chunk, int stride,
+                         const uint16_t* __restrict__ x, uint16_t* __restrict__ rows, int K,
+                         int nch) {
   extern __shared__ uint32_t smem[];
   uint32_t* s_before = smem;           // [stride] choices of the expert in earlier chunks
   uint32_t* s_total = smem + stride;   // [stride] choices of the expert in all chunks
   uint16_t* s_warp = reinterpret_cast<uint16_t*>(smem + 2 * stride);  // [warps][stride]
+  int32_t* s_place = reinterpret_cast<int32_t*>(s_warp + kSortWarps * stride);  // with nch != 0
   __shared__ uint32_t s_scan[kSortWarps];
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -140,10 +155,11 @@ __global__ void __launch_bounds__(kSortThreads)
         if (earlier) bef[j] += c;
       }
     }
+    // (element j of all vectors side by side, so that a warp's atomics meet 32 banks)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (tot[j]) atomicAdd(&s_total[vec * 8 + j], tot[j]);
-      if (bef[j]) atomicAdd(&s_before[vec * 8 + j], bef[j]);
+      if (tot[j]) atomicAdd(&s_total[j * nvec + vec], tot[j]);
+      if (bef[j]) atomicAdd(&s_before[j * nvec + vec], bef[j]);
     }
   }
   // Each warp counts its own contiguous part of the chunk.
@@ -163,7 +179,8 @@ __global__ void __launch_bounds__(kSortThreads)
 
   // First place of every expert: an exclusive sum over the experts (at most one
   // per thread); the choices without an expert begin after the last one.
-  const uint32_t own = tid < E ? s_total[tid] : 0;
+  auto at = [&](int e) { return (e & 7) * nvec + (e >> 3); };
+  const uint32_t own = tid < E ? s_total[at(tid)] : 0;
   uint32_t incl = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -185,11 +202,11 @@ __global__ void __launch_bounds__(kSortThreads)
   const uint32_t first = incl - own + (warp > 0 ? s_scan[warp - 1] : 0);
   const uint32_t routed = s_scan[kSortWarps - 1];
   if (tid < E) {
-    s_before[tid] += first;
+    s_before[at(tid)] += first;
     if (blockIdx.x == 0) offsets[tid] = static_cast<int32_t>(first);
   }
   if (tid == 0) {
-    s_before[E] += routed;
+    s_before[at(E)] += routed;
     if (blockIdx.x == 0) offsets[E] = static_cast<int32_t>(routed);
   }
   for (int e = tid; e <= E; e += kSortThreads) {  // exclusive sum over the warps
@@ -210,14 +227,28 @@ __global__ void __launch_bounds__(kSortThreads)
     const uint32_t before = key >= 0 ? mine[key] : 0;
     __syncwarp();
     if (key >= 0) {
-      const int row = static_cast<int>(s_before[key] + before +
+      const int row = static_cast<int>(s_before[at(key)] + before +
                                        __popc(peers & ((1u << lane) - 1)));
       order[row] = i;
       position[i] = key < E ? row : ~row;
+      if (nch != 0) s_place[i - lo] = key < E ? row : ~row;
       if (lane == __ffs(peers) - 1)
         mine[key] = static_cast<uint16_t>(before + __popc(peers));
     }
     __syncwarp();
+  }
+  if (nch == 0) return;
+  // The chunk's rows, one choice per warp at a time (x comes from L2 after the first).
+  __syncthreads();
+  const uint4* x4 = reinterpret_cast<const uint4*>(x);
+  uint4* r4 = reinterpret_cast<uint4*>(rows);
+  for (int i = lo + warp; i < hi; i += kSortWarps) {
+    const int p = s_place[i - lo];
+    const uint4* src = x4 + static_cast<size_t>(i / K) * nch;
+    uint4* dst = r4 + static_cast<size_t>(p >= 0 ? p : ~p) * nch;
+#pragma unroll 4
+    for (int c = lane; c < nch; c += 32)
+      st_stream_v4(dst + c, p >= 0 ? src[c] : make_uint4(0, 0, 0, 0));
   }
 }
 
@@ -239,7 +270,8 @@ __global__ void __launch_bounds__(kCopyThreads)
   for (int k = 0; k < K; ++k) {
     const int p = pos[k];
     const int row = p >= 0 ? p : ~p;
-    if (row < n) dst[static_cast<size_t>(row) * nch] = p >= 0 ? v : make_uint4(0, 0, 0, 0);
+    if (row < n)
+      st_stream_v4(dst + static_cast<size_t>(row) * nch, p >= 0 ? v : make_uint4(0, 0, 0, 0));
   }
 }
 
@@ -251,7 +283,8 @@ size_t rank_smem(int stride) {
 
 cudaError_t setup_dispatch(const DeviceInfo&) {
   return cudaFuncSetAttribute(dispatch_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(rank_smem(dispatch_counts_stride(kMaxExperts))));
+                              static_cast<int>(rank_smem(dispatch_counts_stride(kMaxExperts)) +
+                                               kMaxChunkRows * sizeof(int32_t)));
 }
 
 cudaError_t launch_dispatch(const DispatchArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
@@ -267,10 +300,14 @@ cudaError_t launch_dispatch(const DispatchArgs& a, const DeviceInfo& dev, cudaSt
                                    stride * sizeof(uint32_t), stream, a.ids, a.counts, n, a.E,
                                    per_chunk, stride);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(dispatch_rank_kernel, dim3(chunks), dim3(kSortThreads), rank_smem(stride),
-                       stream, a.ids, static_cast<const uint16_t*>(a.counts), a.offsets, a.order,
-                       a.position, n, a.E, per_chunk, stride);
-  if (e != cudaSuccess || nch == 0) return e;
+  const bool fused = nch != 0 && per_chunk <= kMaxChunkRows &&
+                     (nch >= 32 || per_chunk <= kMaxNarrowRows) &&
+                     static_cast<size_t>(n) * a.L * 2 <= kMaxFusedBytes;
+  e = launch_dependent(dispatch_rank_kernel, dim3(chunks), dim3(kSortThreads),
+                       rank_smem(stride) + (fused ? per_chunk * sizeof(int32_t) : 0), stream,
+                       a.ids, static_cast<const uint16_t*>(a.counts), a.offsets, a.order,
+                       a.position, n, a.E, per_chunk, stride, a.x, a.rows, a.K, fused ? nch : 0);
+  if (e != cudaSuccess || nch == 0 || fused) return e;
   const int64_t pieces = static_cast<int64_t>(a.T) * nch;
   return launch_dependent(dispatch_copy_kernel,
                           dim3(static_cast<unsigned>((pieces + kCopyThreads - 1) / kCopyThreads)),
