@@ -227,6 +227,8 @@ def _gate_kind(gate, T, H):
     """Kind, dtype and shape of a gate: None, [T, 1] or [H] fp32, [T, H] bf16."""
     if gate is None:
         return _GATE_NONE, None, None
+    if not isinstance(gate, torch.Tensor):
+        raise TypeError("gate must be a torch.Tensor")
     if gate.dim() == 1:
         return _GATE_CHANNEL, _F32, (H,)
     if gate.dim() == 2 and gate.shape[1] == 1:

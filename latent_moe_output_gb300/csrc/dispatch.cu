@@ -28,6 +28,8 @@ namespace {
 constexpr int kSmallThreads = 256;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxChunk = 65535;
+static_assert(static_cast<int64_t>(kDispatchMaxChunks) * kMaxChunk >= kMaxSlots, "16-bit counts");
 constexpr int kCopyThreads = 256;
 // The ranking kernel copies its chunk's rows itself up to this size, above it a third
 // kernel does (measured with 8 choices of 256 experts, L = 2048, us with two and three
@@ -294,7 +296,9 @@ cudaError_t launch_dispatch(const DispatchArgs& a, const DeviceInfo& dev, cudaSt
     return launch_dependent(dispatch_small_kernel, dim3(n), dim3(kSmallThreads), 0, stream, a.x,
                             a.ids, a.rows, a.offsets, a.order, a.position, n, a.K, a.E, nch);
   const int stride = dispatch_counts_stride(a.E);
-  const int chunks = std::min(dev.num_sms, kDispatchMaxChunks);
+  // One chunk per SM, more where a chunk would not fit its 16-bit counts.
+  const int chunks = std::min(kDispatchMaxChunks,
+                              std::max(dev.num_sms, (n + kMaxChunk - 1) / kMaxChunk));
   const int per_chunk = (n + chunks - 1) / chunks;
   cudaError_t e = launch_dependent(dispatch_count_kernel, dim3(chunks), dim3(kSortThreads),
                                    stride * sizeof(uint32_t), stream, a.ids, a.counts, n, a.E,

@@ -636,6 +636,8 @@ def test_refusals():
         (ValueError, lambda: lt.combine(d.rows, d.position, torch.ones(2, 4, device="cuda"))),
         (TypeError, lambda: lt.residual_norm(x, x.double(), None, None, EPS)),
         (ValueError, lambda: lt.residual_norm(x, x, torch.ones(32, device="cuda"), None, EPS)),
+        (TypeError, lambda: lt.residual_norm(x, x, None, None, EPS, gate=0.5)),
+        (TypeError, lambda: lt.residual_norm(x, x, None, None, EPS, gate=x[:, :1])),  # bf16 [T, 1]
     ]
     for kind, call in bad:
         with pytest.raises(kind):
@@ -665,3 +667,135 @@ def test_refusals():
             call()
         assert err.value.status == status
     latent_tail_check()
+
+
+# ------------------------------------------------ every kernel choice and its edges
+@pytest.mark.parametrize("N,M,C,G", [
+    (3, 8192, 256, 32),     # 64-row tiles; a row of scales shorter than a scale piece
+    (5, 6600, 96, 32),      # ... scales read outside the ring
+    (40, 7168, 320, 64),    # sixteen rows per pass, two and a half passes
+    (13, 13000, 1056, 32),  # sixteen per pass, a last tile of eight rows
+    (9, 40000, 128, 128),   # more tiles of 64 rows than CTAs
+    (2, 200, 2816, 128),    # the smallest tiles, steps without all of their boxes
+    (1, 131072, 512, 64),   # 256-row tiles of one matrix
+])
+def test_matvec4_dense_tile_choices(N, M, C, G):
+    g = gen(N + M + C)
+    packed, scales = weights4(1, M, C, G, g)
+    check_matvec4(randn(N, C, g=g), packed, scales, None)
+
+
+@pytest.mark.parametrize("T,K,E,M,C,G,drop", [
+    (64, 8, 64, 2048, 256, 32, 0.1), (64, 8, 64, 2056, 96, 32, 0.0), (90, 8, 64, 1992, 1152, 128, 0.3),
+    (300, 8, 70, 2000, 288, 32, 0.0), (128, 8, 64, 2048, 640, 64, 0.0), (33, 1, 256, 1024, 2048, 32, 0.0),
+    (700, 2, 128, 1000, 64, 32, 0.1)])
+def test_matvec4_experts_tile_choices(T, K, E, M, C, G, drop):
+    g = gen(T + M)
+    d = lt.dispatch(randn(T, C, g=g), choices(T, K, E, seed=T + E, drop=drop, skew=0.5), E)
+    packed, scales = weights4(E, M, C, G, g)
+    out = check_matvec4(d.rows, packed, scales, d.offsets)
+    assert (out[int(d.offsets[-1]):] == 0).all()
+
+
+RING = [(700, 4104), (613, 7168), (1300, 5128), (650, 8192)]
+
+
+@pytest.mark.parametrize("gate", ["none", "token", "channel", "full"])
+@pytest.mark.parametrize("residual", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,H", RING)
+def test_residual_norm_rows_through_the_ring(T, H, residual, gate):
+    c = norm_case(T, H, gate, residual, seed=T + H)
+    check_norm(c)
+    v, z = lt.residual_norm(c["block"], c["residual"], c["post"], c["nxt"], EPS, gate=c["gate"],
+                            residual_scale=0.5)
+    r = c["residual"].clone()
+    v2, z2 = lt.residual_norm(c["block"], r, c["post"], c["nxt"], EPS, gate=c["gate"],
+                              residual_scale=0.5, residual_out=r)
+    assert torch.equal(v2, v) and torch.equal(z2, z)
+
+
+@pytest.mark.parametrize("post,nxt", [(True, False), (False, True), (False, False)])
+def test_residual_norm_ring_without_one_of_the_norms(post, nxt):
+    check_norm(norm_case(611, 4800, "full", "bf16", seed=3, post=post, nxt=nxt))
+
+
+@pytest.mark.parametrize("gate", ["none", "token", "channel", "full"])
+@pytest.mark.parametrize("residual", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,H", [(700, 7168), (331, 8192), (1000, 520), (900, 1024), (1500, 2304),
+                                 (800, 3584), (2000, 512)])
+def test_residual_norm_backward_ring_depths(T, H, residual, gate):
+    check_backward(norm_case(T, H, gate, residual, seed=T + H), seed=T * H)
+
+
+def test_norm_rows_do_not_depend_on_the_other_rows():
+    """Rows of a call through the ring have the same bits in a call of another length
+    (a call of fewer rows than SMs takes another kernel, whose sums have another order)."""
+    c = norm_case(1300, 4104, "channel", "bf16", seed=17)
+    args = lambda n: (c["block"][:n].contiguous(), c["residual"][:n].contiguous(),  # noqa: E731
+                      c["post"], c["nxt"], EPS)
+    a = lt.residual_norm(*args(1300), gate=c["gate"])
+    b = lt.residual_norm(*args(701), gate=c["gate"])
+    for x, y in zip(a, b):
+        assert torch.equal(x[:701], y)
+
+
+@pytest.mark.parametrize("T,K,E,L", [(260, 8, 300, 2048), (2100, 1, 9, 8), (1200, 8, 64, 1024),
+                                     (5200, 8, 64, 1024), (3000, 8, 40, 264), (300, 7, 1024, 4096)])
+def test_dispatch_in_two_and_three_kernels(T, K, E, L):
+    ids = choices(T, K, E, seed=T, drop=0.15)
+    x = randn(T, L, g=gen(T + L))
+    rows = torch.full((T * K, L), float("nan"), dtype=torch.bfloat16, device="cuda")
+    got = lt.dispatch(x, ids, E, rows=rows)
+    order, position, offsets = br.dispatch(ids, E)
+    assert torch.equal(got.offsets.cpu(), offsets)
+    assert torch.equal(got.order.cpu(), order)
+    assert torch.equal(got.position.cpu(), position)
+    want = x.cpu()[(order // K).long()]
+    want[int(offsets[-1]):] = 0
+    assert torch.equal(got.rows.cpu().view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("L", [8, 64, 72, 128, 136, 256, 264, 512, 520, 1024, 1032, 2048, 2056])
+def test_combine_gradient_group_sizes(L):
+    """One width on each side of every thread-group size."""
+    T, K, E = 67, 9, 12
+    g = gen(L)
+    d = lt.dispatch(None, choices(T, K, E, seed=L, drop=0.2), E)
+    rows, go = randn(T * K, L, g=g), randn(T, L, g=g)
+    w = torch.rand(T, K, generator=g, device="cuda")
+    grad_rows, gw = lt.combine_backward(go, rows, d.position, w)
+    rr, rw, wmag = br.combine_backward(go, rows, d.position, w)
+    br.assert_within(grad_rows, rr, br.bf16_bound(rr, br.U32 * rr.abs()), "grad_rows")
+    br.assert_within(gw, rw, br.CHAIN * br.U32 * wmag, "grad_weights")
+
+
+@pytest.mark.parametrize("one_key", [True, False])
+def test_dispatch_of_the_most_choices(one_key):
+    """2^24 choices: chunks of more than 16-bit counts allow with one per SM."""
+    T, K, E = 1 << 21, 8, 5
+    if one_key:
+        ids = torch.full((T, K), 3, dtype=torch.int32, device="cuda")
+        ids[7, 2] = 0
+        ids[-1, -1] = -1
+    else:
+        ids = torch.randint(-1, E, (T, K), generator=gen(1), device="cuda", dtype=torch.int32)
+    d = lt.dispatch(None, ids, E)
+    flat = ids.reshape(-1).long()
+    key = torch.where((flat >= 0) & (flat < E), flat, torch.full_like(flat, E))
+    order = torch.argsort(key, stable=True)
+    assert torch.equal(d.order.long(), order)
+    bounds = torch.searchsorted(key[order], torch.arange(E + 1, device="cuda"))
+    assert torch.equal(d.offsets.long(), bounds)
+    at = torch.arange(T * K, device="cuda")
+    want = torch.empty_like(at)
+    want[order] = torch.where(at < bounds[-1], at, -1 - at)
+    assert torch.equal(d.position.reshape(-1).long(), want)
+
+
+@pytest.mark.parametrize("post,nxt", [(True, False), (False, True), (False, False)])
+@pytest.mark.parametrize("gate", ["token", "full"])
+@pytest.mark.parametrize("T,H", [(5, 264), (9, 488), (7, 7168), (3, 8200), (700, 1448)])
+def test_residual_norm_backward_gates_without_one_of_the_norms(T, H, gate, post, nxt):
+    check_backward(norm_case(T, H, gate, "fp32", seed=H, post=post, nxt=nxt), seed=H)
+    check_backward(norm_case(T, H, gate, "bf16", seed=H, post=post, nxt=nxt), seed=H + 1,
+                   grad_v=not nxt)
