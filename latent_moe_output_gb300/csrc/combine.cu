@@ -5,7 +5,10 @@
 //   grad_rows[position[t,k]] = w[t,k] * grad_out[t]
 //   grad_w[t,k] = <grad_out[t], rows[position[t,k]]>
 //
-// Both read and write every row once, so memory bounds them.
+// Both read and write every row once, so memory bounds them. Measured at K = 8,
+// L = 2048 (GB300, calls back to back): 8192 tokens with a quarter of the choices not
+// routed 38.1 us = 6.2 TB/s, 91 % of the measured copy rate; the gradient of 8192 tokens
+// 86 us = 6.6 TB/s, 97 %; 16 tokens 2.1 us.
 #include "block_launch.h"
 #include "rows.cuh"
 

@@ -799,3 +799,24 @@ def test_residual_norm_backward_gates_without_one_of_the_norms(T, H, gate, post,
     check_backward(norm_case(T, H, gate, "fp32", seed=H, post=post, nxt=nxt), seed=H)
     check_backward(norm_case(T, H, gate, "bf16", seed=H, post=post, nxt=nxt), seed=H + 1,
                    grad_v=not nxt)
+
+
+@pytest.mark.parametrize("gate", ["none", "token", "channel", "full"])
+@pytest.mark.parametrize("residual", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,H", [(80, 8200), (160, 9152), (301, 12296), (153, 16384)])
+def test_wide_rows_shared_by_two_ctas(T, H, residual, gate):
+    c = norm_case(T, H, gate, residual, seed=T + H)
+    check_norm(c)
+    check_backward(c, seed=T * H)
+    r = c["residual"].clone()
+    v, z = lt.residual_norm(c["block"], c["residual"], c["post"], c["nxt"], EPS, gate=c["gate"])
+    v2, z2 = lt.residual_norm(c["block"], r, c["post"], c["nxt"], EPS, gate=c["gate"],
+                              residual_out=r)
+    assert torch.equal(v2, v) and torch.equal(z2, z)
+
+
+@pytest.mark.parametrize("post,nxt", [(True, False), (False, True), (False, False)])
+def test_wide_rows_without_one_of_the_norms(post, nxt):
+    c = norm_case(170, 10008, "channel", "bf16", seed=3, post=post, nxt=nxt)
+    check_norm(c, scale=1.0)
+    check_backward(c, seed=4, scale=1.0)
