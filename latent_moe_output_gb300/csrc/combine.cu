@@ -7,8 +7,8 @@
 //
 // Both read and write every row once, so memory bounds them. Measured at K = 8,
 // L = 2048 (GB300, calls back to back): 8192 tokens with a quarter of the choices not
-// routed 38.1 us = 6.2 TB/s, 91 % of the measured copy rate; the gradient of 8192 tokens
-// 86 us = 6.6 TB/s, 97 %; 16 tokens 2.1 us.
+// routed 37.1 us = 6.3 TB/s, 93 % of the measured copy rate; the gradient of 8192 tokens
+// 86 us = 6.6 TB/s, 97 %; 16 tokens 1.9 us.
 #include "block_launch.h"
 #include "rows.cuh"
 
@@ -17,15 +17,18 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kAhead = 8;  // rows requested before the first is used
+// Threads of the forward kernel: T = 8192, a quarter not routed, 37.1 us with 128, 38.1
+// with 256, 40.4 with 512; T = 16 1.9, 2.1 and 2.5.
+constexpr int kForwardThreads = 128;
 
 // One thread per 16-byte piece of out.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kForwardThreads)
     combine_kernel(const uint16_t* __restrict__ rows, const int32_t* __restrict__ position,
                    const float* __restrict__ weights, uint16_t* __restrict__ out, int T, int K,
                    int nch) {
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kThreads;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * kForwardThreads;
   const int t0 = static_cast<int>(base / nch);
   const int rem = static_cast<int>(base - static_cast<int64_t>(t0) * nch) + threadIdx.x;
   const int t = t0 + rem / nch, c = rem % nch;
@@ -180,8 +183,9 @@ cudaError_t launch_combine(const CombineArgs& a, const DeviceInfo&, cudaStream_t
   const int nch = a.L / 8;
   const int64_t pieces = static_cast<int64_t>(a.T) * nch;
   return launch_dependent(combine_kernel,
-                          dim3(static_cast<unsigned>((pieces + kThreads - 1) / kThreads)),
-                          dim3(kThreads), 0, stream, a.rows, a.position, a.weights, a.out, a.T,
+                          dim3(static_cast<unsigned>((pieces + kForwardThreads - 1) /
+                                                     kForwardThreads)),
+                          dim3(kForwardThreads), 0, stream, a.rows, a.position, a.weights, a.out, a.T,
                           a.K, nch);
 }
 
