@@ -247,6 +247,7 @@ constexpr int kRingMaxStages = 6;
 constexpr int kRingMinRowsPerSm = 1;
 constexpr size_t kRingSmem = 224 * 1024;  // one CTA per SM
 constexpr int kForwardRingMinH = 4096;
+constexpr int kForwardRingBytes = 112 * 1024;
 
 // Rows of few pieces have few threads: several CTAs then share an SM.
 constexpr int ring_ctas_per_sm(int threads) {
@@ -257,6 +258,10 @@ constexpr int ring_cluster(int H) { return H > kRingMaxH ? 2 : 1; }
 constexpr int ring_width(int H) { return ring_cluster(H) == 1 ? H : (H / 8 + 1) / 2 * 8; }
 
 constexpr int ring_threads(int H) { return (H / 8 + 31) / 32 * 32; }
+// The forward ring: one piece per thread up to 1024 threads, else two.
+constexpr int forward_ring_threads(int H) {
+  return H <= kRingMaxH ? ring_threads(H) : (H / 8 + 63) / 64 * 32;
+}
 
 // The gradient's ring: rows of more than 448 pieces take two per thread (half the
 // warps to synchronize and to reduce over, with twice the work each).
@@ -576,8 +581,8 @@ __device__ __noinline__ void drain_ring(uint64_t* full_bar, int stages) {
 
 // The forward pass for many rows: like the gradient's ring kernel below, kRows
 // token rows at a time (adjacent in memory: one copy per array), which share the
-// two barriers.
-template <bool kF32, int kThreads, int kRows>
+// two barriers, kPieces 8-element pieces of each per thread.
+template <bool kF32, int kThreads, int kRows, int kPieces>
 __global__ void __launch_bounds__(kThreads, 1)
     residual_norm_ring_kernel(const ResidualNormArgs a, int stages, int stage_bytes,
                               uint32_t* err) {
@@ -586,7 +591,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(16) float red[2][kRows][32];
   __shared__ int abort_flag;
   volatile int* abort_v = &abort_flag;
-  const int lane = threadIdx.x;  // piece of the row
   const int H = a.H;
   const uint32_t h2 = static_cast<uint32_t>(H) * 2, hr = kF32 ? h2 * 2 : h2;
   const bool has_post = a.post != nullptr, full_gate = a.gate_kind == kGateFull;
@@ -620,18 +624,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t < a.T) fetch(static_cast<int>(t), s);
     }
 
-  const int col = lane * 8;
-  const bool on = col < H;
-  f32x2 gp[4], gn[4];  // post weight (times a channel gate), next weight
+  // Post weight (times a channel gate), next weight. With two pieces and more than 640
+  // threads the next weight is loaded for each row instead of held (T = 3500: H = 16384
+  // 74 us, 83 when held, with spills; H = 11520 54.7 and 58.5).
+  constexpr bool kHoldNext = kPieces == 1 || kThreads <= 640;
+  f32x2 gp[kPieces][4], gn[kPieces][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) gp[i] = both(1.f), gn[i] = both(0.f);
-  if (on && has_post) load8(a.post + col, gp);
-  if (on && a.next != nullptr) load8(a.next + col, gn);
-  if (on && a.gate_kind == kGateChannel) {
-    f32x2 g[4];
-    load8(static_cast<const float*>(a.gate) + col, g);
+  for (int e = 0; e < kPieces; ++e) {
+    const int col = (threadIdx.x + e * blockDim.x) * 8;
+    const bool on = col < H;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) gp[i] = mul2(gp[i], g[i]);
+    for (int i = 0; i < 4; ++i) gp[e][i] = both(1.f), gn[e][i] = both(0.f);
+    if (on && has_post) load8(a.post + col, gp[e]);
+    if (kHoldNext && on && a.next != nullptr) load8(a.next + col, gn[e]);
+    if (on && a.gate_kind == kGateChannel) {
+      f32x2 g[4];
+      load8(static_cast<const float*>(a.gate) + col, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) gp[e][i] = mul2(gp[e][i], g[i]);
+    }
   }
   const float inv_h = 1.0f / static_cast<float>(H);
   const f32x2 scale = both(a.scale);
@@ -642,18 +653,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint8_t* st = smem + static_cast<size_t>(s) * stage_bytes;
     if (ok) ok = mbar_wait(smem_u32(&full_bar[s]), parity, err, abort_v);
     float sum[kRows], factor[kRows];  // of y: r1 and a token gate
-    uint4 y_raw[kRows];
+    uint4 y_raw[kRows][kPieces];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      y_raw[r] = make_uint4(0, 0, 0, 0);
-      if (on && t + r < a.T) y_raw[r] = *reinterpret_cast<const uint4*>(st + r * h2 + lane * 16);
       factor[r] = a.gate_kind == kGateToken && t + r < a.T
                       ? __ldg(static_cast<const float*>(a.gate) + t + r)
                       : 1.f;
-      f32x2 f[4], q = both(0.f);
-      unpack8(y_raw[r], f);
+      f32x2 q = both(0.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q = fma2(f[i], f[i], q);
+      for (int e = 0; e < kPieces; ++e) {
+        const int lane = threadIdx.x + e * blockDim.x;  // piece of the row
+        f32x2 f[4];
+        y_raw[r][e] = make_uint4(0, 0, 0, 0);
+        if (lane * 8 < H && t + r < a.T)
+          y_raw[r][e] = *reinterpret_cast<const uint4*>(st + r * h2 + lane * 16);
+        unpack8(y_raw[r][e], f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q = fma2(f[i], f[i], q);
+      }
       sum[r] = sum2(q);
     }
     if (has_post) {
@@ -662,17 +679,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int r = 0; r < kRows; ++r) factor[r] *= 1.0f / sqrtf(sum[r] * inv_h + a.eps);
     }
-    f32x2 v[kRows][4];
+    f32x2 v[kRows][kPieces][4];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       f32x2 q = both(0.f);
-      if (on && t + r < a.T) {
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e) {
+        const int lane = threadIdx.x + e * blockDim.x, col = lane * 8;
+        if (col >= H || t + r >= a.T) continue;
         f32x2 f[4];
         const f32x2 c = both(factor[r]);
-        unpack8(y_raw[r], f);
-        lds_res8<kF32>(st + at_x + r * hr, lane, v[r]);
+        unpack8(y_raw[r][e], f);
+        lds_res8<kF32>(st + at_x + r * hr, lane, v[r][e]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = mul2(mul2(f[i], c), gp[i]);
+        for (int i = 0; i < 4; ++i) f[i] = mul2(mul2(f[i], c), gp[e][i]);
         if (full_gate) {
           f32x2 g[4];
           lds8(st + at_g + r * h2, lane, g);
@@ -681,10 +701,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          v[r][i] = fma2(scale, v[r][i], f[i]);
-          q = fma2(v[r][i], v[r][i], q);
+          v[r][e][i] = fma2(scale, v[r][e][i], f[i]);
+          q = fma2(v[r][e][i], v[r][e][i], q);
         }
-        store_res8<kF32>(a.residual_out, static_cast<size_t>(t + r) * H + col, v[r]);
+        store_res8<kF32>(a.residual_out, static_cast<size_t>(t + r) * H + col, v[r][e]);
       }
       sum[r] = sum2(q);
     }
@@ -695,10 +715,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
         const f32x2 r2 = both(1.0f / sqrtf(sum[r] * inv_h + a.eps));
-        if (on && t + r < a.T) {
-          f32x2 o[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = mul2(mul2(v[r][i], r2), gn[i]);
+        for (int e = 0; e < kPieces; ++e) {
+          const int col = (threadIdx.x + e * blockDim.x) * 8;
+          if (col >= H || t + r >= a.T) continue;
+          f32x2 o[4];
+          if constexpr (!kHoldNext) load8(a.next + col, gn[e]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = mul2(mul2(v[r][e][i], r2), gn[e][i]);
           *reinterpret_cast<uint4*>(a.next_out + static_cast<size_t>(t + r) * H + col) = pack8(o);
         }
       }
@@ -848,14 +872,16 @@ struct RingPlan {
 // The forward ring; stages == 0 when the direct kernel takes the call.
 RingPlan ring_plan(const ResidualNormArgs& a, int rows, int num_sms) {
   RingPlan r;
-  if (a.H < kForwardRingMinH || a.H > kRingMaxH || a.T < kRingMinRowsPerSm * num_sms) return r;
+  if (a.H < kForwardRingMinH || a.T < kRingMinRowsPerSm * num_sms) return r;
   const int h2 = a.H * 2;
   const int bytes = h2 + (a.residual_f32 ? 2 * h2 : h2) + (a.gate_kind == kGateFull ? h2 : 0);
   r.stage_bytes = (rows * bytes + 127) / 128 * 128;
-  r.threads = ring_threads(a.H);
-  // Two stages: more measured slower (T = 8192, H = 7168, channel gate: 75 against 82 us
-  // with three; without a gate the same).
-  r.stages = static_cast<int>(std::min<size_t>(2, kRingSmem / r.stage_bytes));
+  r.threads = forward_ring_threads(a.H);
+  // Two stages, three while they stay within kForwardRingBytes (T = 8192, H = 7168,
+  // channel gate: 75 us with two and 82 with three; H = 4096 47 and 43; T = 4000, H =
+  // 10240 54 and 57; H = 9152 50 and 47).
+  r.stages = std::min(3, std::max(2, kForwardRingBytes / r.stage_bytes));
+  r.stages = static_cast<int>(std::min<size_t>(r.stages, kRingSmem / r.stage_bytes));
   r.smem = static_cast<size_t>(r.stages) * r.stage_bytes;
   return r;
 }
@@ -965,20 +991,22 @@ NarrowKernel narrow_kernel(int H, bool f32, int mode) {
                         : narrow_kernel<kAllGated>(H, f32);
 }
 
-template <int kRows>
+template <int kRows, int kPieces>
 ForwardRingKernel forward_ring_kernel(int threads, bool f32) {
   if (threads <= 640)
-    return f32 ? residual_norm_ring_kernel<true, 640, kRows>
-               : residual_norm_ring_kernel<false, 640, kRows>;
+    return f32 ? residual_norm_ring_kernel<true, 640, kRows, kPieces>
+               : residual_norm_ring_kernel<false, 640, kRows, kPieces>;
   if (threads <= 896)
-    return f32 ? residual_norm_ring_kernel<true, 896, kRows>
-               : residual_norm_ring_kernel<false, 896, kRows>;
-  return f32 ? residual_norm_ring_kernel<true, 1024, kRows>
-             : residual_norm_ring_kernel<false, 1024, kRows>;
+    return f32 ? residual_norm_ring_kernel<true, 896, kRows, kPieces>
+               : residual_norm_ring_kernel<false, 896, kRows, kPieces>;
+  return f32 ? residual_norm_ring_kernel<true, 1024, kRows, kPieces>
+             : residual_norm_ring_kernel<false, 1024, kRows, kPieces>;
 }
 
-ForwardRingKernel forward_ring_kernel(int rows, int threads, bool f32) {
-  return rows == 2 ? forward_ring_kernel<2>(threads, f32) : forward_ring_kernel<1>(threads, f32);
+ForwardRingKernel forward_ring_kernel(int H, int rows, int threads, bool f32) {
+  if (H > kRingMaxH) return forward_ring_kernel<1, 2>(threads, f32);
+  return rows == 2 ? forward_ring_kernel<2, 1>(threads, f32)
+                   : forward_ring_kernel<1, 1>(threads, f32);
 }
 
 // The direct forward kernel. Of four pieces per thread (H > 8192) two CTAs share an SM
@@ -1018,12 +1046,13 @@ RingKernel ring_kernel(int H, bool f32, int mode) {
 cudaError_t setup_residual_norm(const DeviceInfo&) {
   for (bool f32 : {false, true}) {
     cudaError_t e;
-    for (int rows : {1, 2})
-      for (int threads : {640, 896, 1024})
-        if ((e = cudaFuncSetAttribute(forward_ring_kernel(rows, threads, f32),
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(kRingSmem))) != cudaSuccess)
-          return e;
+    for (int H : {4096, 16384})
+      for (int rows : {1, 2})
+        for (int threads : {640, 896, 1024})
+          if ((e = cudaFuncSetAttribute(forward_ring_kernel(H, rows, threads, f32),
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(kRingSmem))) != cudaSuccess)
+            return e;
     for (int H : {1024, 2304, 3584, 7168, 8192, 14336, 16384})  // one of each kernel
       for (int mode : {kSome, kAll, kAllGated})
         if ((e = cudaFuncSetAttribute(ring_kernel(H, f32, mode),
@@ -1037,11 +1066,11 @@ cudaError_t setup_residual_norm(const DeviceInfo&) {
 
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, const DeviceInfo& dev,
                                  cudaStream_t stream) {
-  int rows = 2;
+  int rows = a.H <= kRingMaxH ? 2 : 1;
   RingPlan ring = ring_plan(a, rows, dev.num_sms);
-  if (ring.stages == 1) ring = ring_plan(a, rows = 1, dev.num_sms);
-  if (ring.stages != 0)
-    return launch_dependent(forward_ring_kernel(rows, ring.threads, a.residual_f32),
+  if (ring.stages == 1 && rows == 2) ring = ring_plan(a, rows = 1, dev.num_sms);
+  if (ring.stages >= 2)
+    return launch_dependent(forward_ring_kernel(a.H, rows, ring.threads, a.residual_f32),
                             dim3(std::min((a.T + rows - 1) / rows, dev.num_sms)),
                             dim3(ring.threads), ring.smem, stream, a, ring.stages,
                             ring.stage_bytes, dev.err_word);
