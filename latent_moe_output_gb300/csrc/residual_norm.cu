@@ -23,8 +23,11 @@ namespace lt {
 namespace {
 
 constexpr int kMaxThreads = 512;
-constexpr int kReduceCols = 16;    // float4 columns per CTA of the column sum
-constexpr int kReduceSlices = 32;  // parts of the partial rows per CTA
+// Column sum: threads per CTA, and the widest rows for 4 float4 columns per CTA instead
+// of 16 (T = 8192 / T = 1000, gradient in us with 4 and with 16: H = 1024 23.0 / 8.8 and
+// 26.0 / 11.8, H = 4000 72.6 / 17.0 and 73.1 / 18.2; H = 7168 at T = 4000 59.6 and 58.2).
+constexpr int kReduceThreads = 512;
+constexpr int kReduceNarrowH = 4096;
 
 struct Shape {
   int threads;  // per CTA
@@ -36,9 +39,11 @@ struct Shape {
 Shape shape_of(int H) {
   const int nch = H / 8;
   Shape s;
-  s.pieces = nch <= 256 ? 1 : nch <= 1024 ? 2 : 4;
+  // A warp takes a row of up to 64 pieces (T = 8192, H = 264: 6.3 us, 7.8 with two warps;
+  // H = 512: 7.9 and 9.2).
+  s.pieces = nch <= 32 ? 1 : nch <= 64 ? 2 : nch <= 256 ? 1 : nch <= 1024 ? 2 : 4;
   if (nch <= 128) {
-    s.tpr = nch <= 32 ? 32 : nch <= 64 ? 64 : 128;
+    s.tpr = nch <= 64 ? 32 : 128;
     s.threads = 256;
   } else {
     s.tpr = ((nch + s.pieces - 1) / s.pieces + 31) / 32 * 32;
@@ -246,8 +251,14 @@ constexpr int kRingMaxStages = 6;
 // kernel; T = 200: 4.1 and 4.6).
 constexpr int kRingMinRowsPerSm = 1;
 constexpr size_t kRingSmem = 224 * 1024;  // one CTA per SM
-constexpr int kForwardRingMinH = 4096;
-constexpr int kForwardRingBytes = 112 * 1024;
+// Narrower rows take a warp each (T = 8192, us direct and ring: H = 512 7.9 and 9.9, 520
+// 10.9 and 9.5, 1024 16.9 and 13.5, 2048 31.8 and 22.8, 3584 49.5 and 38.5).
+constexpr int kForwardRingMinH = 520;
+constexpr int kForwardRingBytes = 112 * 1024;  // per SM
+// Rings of few threads let the next kernel's CTAs in when they are done (T = 8192, H = 520
+// and 1024: 10.5 and 13.5 us, 12.4 and 14.4 when at once; wider rows the other way round,
+// H = 2560: 29.9 and 29.5).
+constexpr int kLateTriggerThreads = 288;
 
 // Rows of few pieces have few threads: several CTAs then share an SM.
 constexpr int ring_ctas_per_sm(int threads) {
@@ -261,6 +272,12 @@ constexpr int ring_threads(int H) { return (H / 8 + 31) / 32 * 32; }
 // The forward ring: one piece per thread up to 1024 threads, else two.
 constexpr int forward_ring_threads(int H) {
   return H <= kRingMaxH ? ring_threads(H) : (H / 8 + 63) / 64 * 32;
+}
+
+// CTAs per SM, within 72 registers per thread (8192 rows of H = 768: 10.9 us with eight
+// of 96 threads, 12.5 with six).
+constexpr int forward_ring_ctas(int threads) {
+  return threads <= 96 ? 8 : threads <= 128 ? 6 : threads <= 288 ? 3 : threads <= 448 ? 2 : 1;
 }
 
 // The gradient's ring: rows of more than 448 pieces take two per thread (half the
@@ -583,7 +600,7 @@ __device__ __noinline__ void drain_ring(uint64_t* full_bar, int stages) {
 // token rows at a time (adjacent in memory: one copy per array), which share the
 // two barriers, kPieces 8-element pieces of each per thread.
 template <bool kF32, int kThreads, int kRows, int kPieces>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, forward_ring_ctas(kThreads))
     residual_norm_ring_kernel(const ResidualNormArgs a, int stages, int stage_bytes,
                               uint32_t* err) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -602,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   for (int i = threadIdx.x; i < static_cast<int>(sizeof(red) / 4); i += blockDim.x)
     (&red[0][0][0])[i] = 0.f;
-  pdl_launch_dependents();
+  if constexpr (kThreads > kLateTriggerThreads) pdl_launch_dependents();
   pdl_wait();
   __syncthreads();
 
@@ -733,6 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fetch(t + stages * step, s);
     if (++s == stages) s = 0, parity ^= 1;
   }
+  if constexpr (kThreads <= kLateTriggerThreads) pdl_launch_dependents();
   if (*abort_v && threadIdx.x == 0) drain_ring(full_bar, stages);
 }
 
@@ -880,8 +898,10 @@ RingPlan ring_plan(const ResidualNormArgs& a, int rows, int num_sms) {
   // Two stages, three while they stay within kForwardRingBytes (T = 8192, H = 7168,
   // channel gate: 75 us with two and 82 with three; H = 4096 47 and 43; T = 4000, H =
   // 10240 54 and 57; H = 9152 50 and 47).
-  r.stages = std::min(3, std::max(2, kForwardRingBytes / r.stage_bytes));
-  r.stages = static_cast<int>(std::min<size_t>(r.stages, kRingSmem / r.stage_bytes));
+  const int ctas = forward_ring_ctas(r.threads);
+  const size_t smem = ctas == 1 ? kRingSmem : kRingSmem / ctas - 2048;
+  r.stages = std::min(3, std::max(2, kForwardRingBytes / ctas / r.stage_bytes));
+  r.stages = static_cast<int>(std::min<size_t>(r.stages, smem / r.stage_bytes));
   r.smem = static_cast<size_t>(r.stages) * r.stage_bytes;
   return r;
 }
@@ -897,24 +917,26 @@ RingPlan ring_plan(const ResidualNormBackwardArgs& a) {
                     (a.gate_kind == kGateFull ? h2 : 0);
   r.stage_bytes = (bytes + 127) / 128 * 128;
   r.threads = backward_ring_threads(width);
-  // Two stages at least; more only while they leave 24 KB of the SM's shared memory to
-  // the L1 cache (T = 8192, H = 7168: 110 us with three stages, 121 with four, 154 with
-  // two).
+  // Three stages where they fit; more only while they leave 24 KB of the SM's shared
+  // memory to the L1 cache (T = 8192, H = 7168: 110 us with three stages, 121 with four,
+  // 154 with two; T = 777, H = 5128, FP32, full gate: 23.1 with three, 26.3 with two).
   const size_t smem = backward_ring_smem(width);
   r.stages = static_cast<int>(std::min<size_t>(kRingMaxStages, smem * 25 / 28 / r.stage_bytes));
-  r.stages = std::max(r.stages, static_cast<int>(std::min<size_t>(2, smem / r.stage_bytes)));
+  r.stages = std::max(r.stages, static_cast<int>(std::min<size_t>(3, smem / r.stage_bytes)));
   r.smem = static_cast<size_t>(r.stages) * r.stage_bytes;
   return r;
 }
 
-// Sums of the partial rows, in a fixed order: 32 slices of rows per CTA, then a tree
-// over the slices. Plane 0 gives the gradients of the post weight and of a channel
+// Sums of the partial rows, in a fixed order: a CTA's threads take slices of the rows of
+// its columns, then a tree adds the slices. Plane 0 gives the gradients of the post weight and of a channel
 // gate, plane 1 that of the next weight.
-__global__ void __launch_bounds__(kReduceCols* kReduceSlices)
+template <int kReduceCols>
+__global__ void __launch_bounds__(kReduceThreads)
     column_sum_kernel(const float* __restrict__ partials, const float* __restrict__ post,
                       const float* __restrict__ gate, float* __restrict__ grad_post,
                       float* __restrict__ grad_gate, float* __restrict__ grad_next,
                       int partial_rows, int H) {
+  constexpr int kReduceSlices = kReduceThreads / kReduceCols;
   __shared__ float4 s_part[kReduceSlices][kReduceCols];
   pdl_wait();
   if (blockIdx.y == 0 ? grad_post == nullptr && grad_gate == nullptr : grad_next == nullptr) return;
@@ -993,6 +1015,20 @@ NarrowKernel narrow_kernel(int H, bool f32, int mode) {
 
 template <int kRows, int kPieces>
 ForwardRingKernel forward_ring_kernel(int threads, bool f32) {
+  if constexpr (kPieces == 1) {
+    if (threads <= 96)
+      return f32 ? residual_norm_ring_kernel<true, 96, kRows, kPieces>
+                 : residual_norm_ring_kernel<false, 96, kRows, kPieces>;
+    if (threads <= 128)
+      return f32 ? residual_norm_ring_kernel<true, 128, kRows, kPieces>
+                 : residual_norm_ring_kernel<false, 128, kRows, kPieces>;
+    if (threads <= 288)
+      return f32 ? residual_norm_ring_kernel<true, 288, kRows, kPieces>
+                 : residual_norm_ring_kernel<false, 288, kRows, kPieces>;
+    if (threads <= 448)
+      return f32 ? residual_norm_ring_kernel<true, 448, kRows, kPieces>
+                 : residual_norm_ring_kernel<false, 448, kRows, kPieces>;
+  }
   if (threads <= 640)
     return f32 ? residual_norm_ring_kernel<true, 640, kRows, kPieces>
                : residual_norm_ring_kernel<false, 640, kRows, kPieces>;
@@ -1048,7 +1084,7 @@ cudaError_t setup_residual_norm(const DeviceInfo&) {
     cudaError_t e;
     for (int H : {4096, 16384})
       for (int rows : {1, 2})
-        for (int threads : {640, 896, 1024})
+        for (int threads : {96, 128, 288, 448, 640, 896, 1024})
           if ((e = cudaFuncSetAttribute(forward_ring_kernel(H, rows, threads, f32),
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(kRingSmem))) != cudaSuccess)
@@ -1071,7 +1107,8 @@ cudaError_t launch_residual_norm(const ResidualNormArgs& a, const DeviceInfo& de
   if (ring.stages == 1 && rows == 2) ring = ring_plan(a, rows = 1, dev.num_sms);
   if (ring.stages >= 2)
     return launch_dependent(forward_ring_kernel(a.H, rows, ring.threads, a.residual_f32),
-                            dim3(std::min((a.T + rows - 1) / rows, dev.num_sms)),
+                            dim3(std::min((a.T + rows - 1) / rows,
+                                          dev.num_sms * forward_ring_ctas(ring.threads))),
                             dim3(ring.threads), ring.smem, stream, a, ring.stages,
                             ring.stage_bytes, dev.err_word);
   const Shape s = shape_of(a.H);
@@ -1096,9 +1133,9 @@ cudaError_t launch_residual_norm_backward(const ResidualNormBackwardArgs& a,
   }
   const bool channel = a.gate_kind == kGateChannel;
   if (e != cudaSuccess || (a.post == nullptr && a.next == nullptr && !channel)) return e;
-  const int cols = kReduceCols * 4;
-  return launch_dependent(column_sum_kernel, dim3((a.H + cols - 1) / cols, 2),
-                          dim3(kReduceCols * kReduceSlices), 0, stream,
+  const int cols = a.H <= kReduceNarrowH ? 4 : 16;
+  return launch_dependent(cols == 4 ? column_sum_kernel<4> : column_sum_kernel<16>,
+                          dim3((a.H / 4 + cols - 1) / cols, 2), dim3(kReduceThreads), 0, stream,
                           static_cast<const float*>(a.partials), a.post,
                           channel ? static_cast<const float*>(a.gate) : nullptr, a.grad_post,
                           channel ? static_cast<float*>(a.grad_gate) : nullptr,

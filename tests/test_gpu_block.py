@@ -820,3 +820,37 @@ def test_wide_rows_without_one_of_the_norms(post, nxt):
     c = norm_case(170, 10008, "channel", "bf16", seed=3, post=post, nxt=nxt)
     check_norm(c, scale=1.0)
     check_backward(c, seed=4, scale=1.0)
+
+
+@pytest.mark.parametrize("gate", ["none", "token", "channel", "full"])
+@pytest.mark.parametrize("residual", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,H", [(1030, 384), (1025, 512), (153, 520), (2500, 768), (305, 776),
+                                 (915, 1024), (457, 1032), (921, 2304), (305, 2312), (640, 3584),
+                                 (153, 3592), (611, 4096), (304, 5128), (305, 8192)])
+def test_residual_norm_more_rows_than_the_gpu_works_on(T, H, residual, gate):
+    check_norm(norm_case(T, H, gate, residual, seed=T + H))
+
+
+@pytest.mark.parametrize("H", [512, 520, 1448, 3584, 7168, 9152, 12296, 16384])
+def test_residual_norm_nan_and_in_place_with_many_rows(H):
+    T = 333
+    c = norm_case(T, H, "token", "bf16", seed=H)
+    r = c["residual"].clone()
+    v, z = lt.residual_norm(c["block"], r, c["post"], c["nxt"], EPS, gate=c["gate"])
+    v2, z2 = lt.residual_norm(c["block"], r, c["post"], c["nxt"], EPS, gate=c["gate"],
+                              residual_out=r)
+    assert v2 is r and torch.equal(v2, v) and torch.equal(z2, z)
+    c["block"][4, 3] = float("nan")
+    c["residual"][T - 1, H - 1] = float("inf")
+    v3, z3 = lt.residual_norm(c["block"], c["residual"], c["post"], c["nxt"], EPS, gate=c["gate"])
+    keep = [t for t in range(T) if t not in (4, T - 1)]
+    assert torch.isnan(v3[4]).all() and torch.isnan(z3[4]).all()
+    assert torch.equal(v3[keep], v[keep]) and torch.equal(z3[keep], z[keep])
+    assert torch.equal(v3[T - 1, :-1], v[T - 1, :-1]) and torch.isinf(v3[T - 1, -1])
+
+
+@pytest.mark.parametrize("T,H", [(1000, 520), (333, 1024), (2000, 2304), (777, 4096),
+                                 (311, 4104), (700, 5128)])
+def test_residual_norm_backward_sums_over_many_rows(T, H):
+    for residual, gate in (("fp32", "full"), ("bf16", "channel")):
+        check_backward(norm_case(T, H, gate, residual, seed=H), seed=T)
