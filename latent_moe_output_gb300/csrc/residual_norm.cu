@@ -41,7 +41,7 @@ Shape shape_of(int H) {
   Shape s;
   // A warp takes a row of up to 64 pieces (T = 8192, H = 264: 6.3 us, 7.8 with two warps;
   // H = 512: 7.9 and 9.2).
-  s.pieces = nch <= 32 ? 1 : nch <= 64 ? 2 : nch <= 256 ? 1 : nch <= 1024 ? 2 : 4;
+  s.pieces = nch <= 32 ? 1 : nch <= 64 ? 2 : nch <= 256 ? 1 : 2;
   if (nch <= 128) {
     s.tpr = nch <= 64 ? 32 : 128;
     s.threads = 256;
@@ -162,8 +162,8 @@ struct Raw<true> {
 // One row per group of `tpr` threads. A row's loads, two reductions and stores
 // follow one another, so several CTAs per SM keep the memory busy; rows are held
 // as they were loaded to keep the registers for that.
-template <int kPieces, bool kF32, int kCtas>
-__global__ void __launch_bounds__(kMaxThreads, kCtas)
+template <int kPieces, bool kF32>
+__global__ void __launch_bounds__(kMaxThreads, 2)
     residual_norm_kernel(const ResidualNormArgs a, int tpr) {
   __shared__ float red[2][kMaxThreads / 32];
   pdl_launch_dependents();
@@ -247,8 +247,11 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas)
 constexpr int kNarrowMaxH = 512;  // up to here a warp takes a row of the gradient
 constexpr int kRingMinH = kNarrowMaxH + 8, kRingMaxH = 8192;  // per CTA
 constexpr int kRingMaxStages = 6;
-// Forward: fewest token rows per SM (T = 456, H = 7168: 6.7 us, 8.2 with the direct
-// kernel; T = 200: 4.1 and 4.6).
+// Forward: fewest token rows per SM up to kRingMaxH (T = 456, H = 7168: 6.7 us, 8.2 with
+// the direct kernel; T = 200: 4.1 and 4.6; T = 100, H = 8192: 4.8 and 4.4). Wider rows
+// always take the ring (T = 100, H = 9152: 3.5 us, 5.1 with a direct kernel; T = 1, H =
+// 16384: 4.8 and 5.9), with a single stage if two do not fit (T = 1700, H = 16384, FP32,
+// full gate: 80 and 86).
 constexpr int kRingMinRowsPerSm = 1;
 constexpr size_t kRingSmem = 224 * 1024;  // one CTA per SM
 // Narrower rows take a warp each (T = 8192, us direct and ring: H = 512 7.9 and 9.9, 520
@@ -890,7 +893,7 @@ struct RingPlan {
 // The forward ring; stages == 0 when the direct kernel takes the call.
 RingPlan ring_plan(const ResidualNormArgs& a, int rows, int num_sms) {
   RingPlan r;
-  if (a.H < kForwardRingMinH || a.T < kRingMinRowsPerSm * num_sms) return r;
+  if (a.H < kForwardRingMinH || (a.H <= kRingMaxH && a.T < kRingMinRowsPerSm * num_sms)) return r;
   const int h2 = a.H * 2;
   const int bytes = h2 + (a.residual_f32 ? 2 * h2 : h2) + (a.gate_kind == kGateFull ? h2 : 0);
   r.stage_bytes = (rows * bytes + 127) / 128 * 128;
@@ -1045,14 +1048,9 @@ ForwardRingKernel forward_ring_kernel(int H, int rows, int threads, bool f32) {
                    : forward_ring_kernel<1, 1>(threads, f32);
 }
 
-// The direct forward kernel. Of four pieces per thread (H > 8192) two CTAs share an SM
-// up to 416 threads anyway; above, the registers are held to that (T = 3500, H = 16384:
-// 115 us, 132 with one CTA; at 9152 and 12288 it would cost 3 and 12 %).
 template <bool kF32>
 auto forward_kernel(const Shape& s) -> void (*)(const ResidualNormArgs, int) {
-  if (s.pieces == 1) return residual_norm_kernel<1, kF32, 2>;
-  if (s.pieces == 2) return residual_norm_kernel<2, kF32, 2>;
-  return s.threads <= 416 ? residual_norm_kernel<4, kF32, 1> : residual_norm_kernel<4, kF32, 2>;
+  return s.pieces == 1 ? residual_norm_kernel<1, kF32> : residual_norm_kernel<2, kF32>;
 }
 
 template <bool kF32, int kMode>
@@ -1105,7 +1103,7 @@ cudaError_t launch_residual_norm(const ResidualNormArgs& a, const DeviceInfo& de
   int rows = a.H <= kRingMaxH ? 2 : 1;
   RingPlan ring = ring_plan(a, rows, dev.num_sms);
   if (ring.stages == 1 && rows == 2) ring = ring_plan(a, rows = 1, dev.num_sms);
-  if (ring.stages >= 2)
+  if (ring.stages != 0)
     return launch_dependent(forward_ring_kernel(a.H, rows, ring.threads, a.residual_f32),
                             dim3(std::min((a.T + rows - 1) / rows,
                                           dev.num_sms * forward_ring_ctas(ring.threads))),
