@@ -854,3 +854,25 @@ def test_residual_norm_nan_and_in_place_with_many_rows(H):
 def test_residual_norm_backward_sums_over_many_rows(T, H):
     for residual, gate in (("fp32", "full"), ("bf16", "channel")):
         check_backward(norm_case(T, H, gate, residual, seed=H), seed=T)
+
+
+@pytest.mark.parametrize("T,K,L", [(3001, 1, 520), (400, 1, 4096), (701, 2, 1448), (16000, 2, 72),
+                                   (300, 2, 16384), (999, 3, 264), (2000, 3, 1448),
+                                   (640, 4, 4096), (1300, 4, 1032), (613, 5, 512)])
+@pytest.mark.parametrize("drop", [0.0, 0.4])
+def test_combine_and_gradient_of_few_choices(T, K, L, drop):
+    g = gen(T + K)
+    d = lt.dispatch(None, choices(T, K, 16, seed=T + L, drop=drop), 16)
+    rows, go = randn(T * K, L, g=g), randn(T, L, g=g)
+    w = torch.rand(T, K, generator=g, device="cuda")
+    for weights in (w, None):
+        out = lt.combine(rows, d.position, weights)
+        ref, mag = br.combine(rows, d.position, weights)
+        br.assert_within(out, ref, br.bf16_bound(ref, (K + 2) * br.U32 * mag), "combine")
+    grad_rows = torch.full_like(rows, float("nan"))
+    grad_rows, gw = lt.combine_backward(go, rows, d.position, w, grad_rows=grad_rows)
+    rr, rw, wmag = br.combine_backward(go, rows, d.position, w)
+    br.assert_within(grad_rows, rr, br.bf16_bound(rr, br.U32 * rr.abs()), "grad_rows")
+    br.assert_within(gw, rw, br.CHAIN * br.U32 * wmag, "grad_weights")
+    only, none = lt.combine_backward(go, None, d.position, w)
+    assert none is None and torch.equal(only, grad_rows)
