@@ -8,7 +8,7 @@
 // Both read and write every row once, so memory bounds them. Measured at K = 8,
 // L = 2048 (GB300, calls back to back): 8192 tokens with a quarter of the choices not
 // routed 37.1 us = 6.3 TB/s, 93 % of the measured copy rate; the gradient of 8192 tokens
-// 85 us = 6.7 TB/s, 99 %; 16 tokens 1.9 us.
+// 86 us = 6.6 TB/s, 97 %; 16 tokens 1.9 us.
 #include "block_launch.h"
 #include "rows.cuh"
 
@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(kForwardThreads)
     t[e] = t0 + rem / nch;
     c[e] = rem % nch;
   }
+  if (kPieces == 1 && t[0] >= T) return;
   for (int k0 = 0; k0 < K; k0 += kRowsAhead) {
     uint4 v[kPieces][kRowsAhead];
     float w[kPieces][kRowsAhead];
@@ -52,7 +53,7 @@ __global__ void __launch_bounds__(kForwardThreads)
       for (int j = 0; j < kRowsAhead; ++j) {
         const int k = k0 + j;
         const size_t at = static_cast<size_t>(t[e]) * K + k;
-        const int p = t[e] < T && k < K ? position[at] : -1;
+        const int p = (kPieces == 1 || t[e] < T) && k < K ? position[at] : -1;
         on[e][j] = p >= 0 && p < n;
         v[e][j] = on[e][j] ? ld_stream_v4(src + static_cast<size_t>(p) * nch + c[e])
                            : make_uint4(0, 0, 0, 0);
@@ -71,7 +72,7 @@ __global__ void __launch_bounds__(kForwardThreads)
   }
 #pragma unroll
   for (int e = 0; e < kPieces; ++e)
-    if (t[e] < T)
+    if (kPieces == 1 || t[e] < T)
       st_stream_v4(reinterpret_cast<uint4*>(out) + static_cast<size_t>(t[e]) * nch + c[e],
                    pack8(acc[e]));
 }
