@@ -599,9 +599,10 @@ __device__ __noinline__ void drain_ring(uint64_t* full_bar, int stages) {
     }
 }
 
-// The forward pass for many rows: like the gradient's ring kernel below, kRows
-// token rows at a time (adjacent in memory: one copy per array), which share the
-// two barriers, kPieces 8-element pieces of each per thread.
+// The forward pass for many rows and for rows wider than 8192, one to eight CTAs per SM:
+// like the gradient's ring kernel below, kRows token rows at a time (adjacent in memory:
+// one copy per array), which share the two barriers, kPieces 8-element pieces of each per
+// thread.
 template <bool kF32, int kThreads, int kRows, int kPieces>
 __global__ void __launch_bounds__(kThreads, forward_ring_ctas(kThreads))
     residual_norm_ring_kernel(const ResidualNormArgs a, int stages, int stage_bytes,
