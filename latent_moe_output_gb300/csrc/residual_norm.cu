@@ -932,8 +932,8 @@ RingPlan ring_plan(const ResidualNormBackwardArgs& a) {
 }
 
 // Sums of the partial rows, in a fixed order: a CTA's threads take slices of the rows of
-// its columns, then a tree adds the slices. Plane 0 gives the gradients of the post weight and of a channel
-// gate, plane 1 that of the next weight.
+// its columns, then a tree adds the slices. Plane 0 gives the gradients of the post weight
+// and of a channel gate, plane 1 that of the next weight.
 template <int kReduceCols>
 __global__ void __launch_bounds__(kReduceThreads)
     column_sum_kernel(const float* __restrict__ partials, const float* __restrict__ post,
