@@ -343,8 +343,11 @@ LT_API lt_status latent_tail_combine_backward(const uint16_t* grad_out, const ui
  * for 8 of its rows (16 where experts have many), again (mostly from L2) for more.
  *   x [N, C] bf16, packed [E, M, C/2] bytes, scales [E, M, C/G] bf16,
  *   offsets [E+1] int32 (rows of expert e: offsets[e] .. offsets[e+1]-1, as
- *   latent_tail_dispatch writes it; rows from offsets[E] on give zeros) or NULL
- *   with E == 1 (every row); out [N, M] bf16.
+ *   latent_tail_dispatch writes it, or a slice of it for some of the experts) or
+ *   NULL with E == 1 (every row); out [N, M] bf16, every row of which is written.
+ * Offsets are cut to [0, N] and to their running maximum, so that ones that run
+ * backwards give empty experts. Rows that no expert owns, before offsets[0] and
+ * from offsets[E] on, give zeros.
  * Limits: 0 <= N <= 2^24, 1 <= E <= 1024, 8 <= M <= 1048576 with M % 8 == 0,
  * G = 32, 64 or 128, C a multiple of G and at most 16384.
  */

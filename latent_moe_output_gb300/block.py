@@ -188,7 +188,8 @@ def combine_backward(grad_out, rows, position, weights=None, grad_rows=None, gra
 
 def expert_matvec4(x, packed, scales, offsets=None, out=None, stream=None):
     """out[r, m] = sum_c x[r, c] * (q[e, m, c] - 8) * scales[e, m, c // G] for the rows
-    r of expert e (``offsets`` of ``dispatch``; None with one matrix: every row).
+    r of expert e (``offsets`` of ``dispatch``, or a slice of them; None with one matrix:
+    every row); zeros for rows that no expert owns.
 
     x [N, C] bf16, packed [E, M, C/2] uint8 (even c in the low four bits), scales
     [E, M, C/G] bf16 with G = 32, 64 or 128. See latent_tail_expert_matvec4 and

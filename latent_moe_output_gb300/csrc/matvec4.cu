@@ -465,12 +465,16 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
     // Not before: CTAs of the next kernel would take the places of this one's that are
     // not resident yet (one matrix, one row: 6.3 against 5.7 us).
     pdl_launch_dependents();
-    // Rows that no expert owns.
+    // Rows that no expert owns: before the first offset and from the last one on (all
+    // rows where the offsets' running maximum leaves none).
     const int mvec = p.M / 8;
     uint4* o4 = reinterpret_cast<uint4*>(p.out);
-    for (int r = s_first[p.E] + blockIdx.x; r < p.N; r += gridDim.x)
+    const int before = s_first[0], end = s_first[p.E];
+    for (int i = blockIdx.x; i < before + p.N - end; i += gridDim.x) {
+      const int r = i < before ? i : end + (i - before);
       for (int c = threadIdx.x; c < mvec; c += kConsumers * 32)
         o4[static_cast<size_t>(r) * mvec + c] = make_uint4(0, 0, 0, 0);
+    }
   }
 }
 
