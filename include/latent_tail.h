@@ -356,6 +356,18 @@ LT_API lt_status latent_tail_expert_matvec4(const uint16_t* x, const uint8_t* pa
                                             uint16_t* out, int N, int E, int M, int C, int G,
                                             lt_stream stream);
 
+/*
+ * Diagnostic as latent_tail_selftest_wait_timeout, for the waits of
+ * latent_tail_expert_matvec4: the same call with waits of limit_us microseconds
+ * (1 .. 1000000), in which tiles from copied_tiles (>= 0) on are never copied to the
+ * SMs. Their waits expire; latent_tail_check reports LT_ERR_TIMEOUT. Elements of out
+ * are then either the call's result or untouched.
+ */
+LT_API lt_status latent_tail_selftest_expert_matvec4_timeout(
+    const uint16_t* x, const uint8_t* packed, const uint16_t* scales, const int32_t* offsets,
+    uint16_t* out, int N, int E, int M, int C, int G, int copied_tiles, unsigned int limit_us,
+    lt_stream stream);
+
 /* What the gate of latent_tail_residual_norm holds. */
 typedef enum lt_gate {
   LT_GATE_NONE = 0,    /* no gate (gate == NULL): 1                */

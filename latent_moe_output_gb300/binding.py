@@ -68,6 +68,9 @@ _SIGNATURES = {
                                      + [ctypes.c_void_p]),
     "latent_tail_expert_matvec4": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int] * 5
                                    + [ctypes.c_void_p]),
+    "latent_tail_selftest_expert_matvec4_timeout": (
+        ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int] * 6
+        + [ctypes.c_uint, ctypes.c_void_p]),
     "latent_tail_residual_norm": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int] * 4
                                   + [ctypes.c_float] * 2 + [ctypes.c_void_p]),
     "latent_tail_residual_norm_backward_workspace_size": (ctypes.c_size_t, [ctypes.c_int] * 2),

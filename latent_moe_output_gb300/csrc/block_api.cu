@@ -73,6 +73,37 @@ lt_status zero(void* p, size_t bytes, cudaStream_t s) {
   return p == nullptr ? LT_OK : launch_status(cudaMemsetAsync(p, 0, bytes, s));
 }
 
+// Limits of a self-test of expired waits.
+bool test_limits(int copied, unsigned int limit_us, RingLimits* ring) {
+  if (copied < 0 || limit_us < 1 || limit_us > 1000000) return false;
+  *ring = RingLimits{copied, static_cast<uint64_t>(limit_us) * 1000u};
+  return true;
+}
+
+lt_status expert_matvec4(const uint16_t* x, const uint8_t* packed, const uint16_t* scales,
+                         const int32_t* offsets, uint16_t* out, int N, int E, int M, int C, int G,
+                         const RingLimits& ring, lt_stream stream) {
+  if (N < 0 || N > (1 << 24) || E < 1 || E > kMaxExperts || M < 8 || M > (1 << 20))
+    return LT_ERR_INVALID_ARG;
+  if (G != 32 && G != 64 && G != 128) return LT_ERR_INVALID_ARG;
+  if (C < G || C > 16384) return LT_ERR_INVALID_ARG;
+  if (M % 8 != 0 || C % G != 0) return LT_ERR_ALIGNMENT;
+  if (offsets == nullptr && E != 1) return LT_ERR_INVALID_ARG;
+  if (N == 0) return LT_OK;
+  lt_status st = check_ptrs({x, packed, scales, out});
+  if (st != LT_OK) return st;
+  if ((st = check_optional({offsets})) != LT_OK) return st;
+  const size_t em = static_cast<size_t>(E) * M;
+  if (!disjoint({span(out, static_cast<size_t>(N) * M * 2)},
+                {span(x, static_cast<size_t>(N) * C * 2), span(packed, em * (C / 2)),
+                 span(scales, em * (C / G) * 2), span(offsets, static_cast<size_t>(E + 1) * 4)}))
+    return LT_ERR_INVALID_ARG;
+  const lt::DeviceInfo* dev = nullptr;
+  if ((st = current_device(&dev)) != LT_OK) return st;
+  const Matvec4Args a{x, packed, scales, offsets, out, N, E, M, C, G, ring};
+  return launch_status(launch_matvec4(a, *dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -164,25 +195,16 @@ LT_API lt_status latent_tail_expert_matvec4(const uint16_t* x, const uint8_t* pa
                                             const uint16_t* scales, const int32_t* offsets,
                                             uint16_t* out, int N, int E, int M, int C, int G,
                                             lt_stream stream) {
-  if (N < 0 || N > (1 << 24) || E < 1 || E > kMaxExperts || M < 8 || M > (1 << 20))
-    return LT_ERR_INVALID_ARG;
-  if (G != 32 && G != 64 && G != 128) return LT_ERR_INVALID_ARG;
-  if (C < G || C > 16384) return LT_ERR_INVALID_ARG;
-  if (M % 8 != 0 || C % G != 0) return LT_ERR_ALIGNMENT;
-  if (offsets == nullptr && E != 1) return LT_ERR_INVALID_ARG;
-  if (N == 0) return LT_OK;
-  lt_status st = check_ptrs({x, packed, scales, out});
-  if (st != LT_OK) return st;
-  if ((st = check_optional({offsets})) != LT_OK) return st;
-  const size_t em = static_cast<size_t>(E) * M;
-  if (!disjoint({span(out, static_cast<size_t>(N) * M * 2)},
-                {span(x, static_cast<size_t>(N) * C * 2), span(packed, em * (C / 2)),
-                 span(scales, em * (C / G) * 2), span(offsets, static_cast<size_t>(E + 1) * 4)}))
-    return LT_ERR_INVALID_ARG;
-  const lt::DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev)) != LT_OK) return st;
-  const Matvec4Args a{x, packed, scales, offsets, out, N, E, M, C, G};
-  return launch_status(launch_matvec4(a, *dev, reinterpret_cast<cudaStream_t>(stream)));
+  return expert_matvec4(x, packed, scales, offsets, out, N, E, M, C, G, RingLimits{}, stream);
+}
+
+LT_API lt_status latent_tail_selftest_expert_matvec4_timeout(
+    const uint16_t* x, const uint8_t* packed, const uint16_t* scales, const int32_t* offsets,
+    uint16_t* out, int N, int E, int M, int C, int G, int copied_tiles, unsigned int limit_us,
+    lt_stream stream) {
+  RingLimits ring;
+  if (!test_limits(copied_tiles, limit_us, &ring)) return LT_ERR_INVALID_ARG;
+  return expert_matvec4(x, packed, scales, offsets, out, N, E, M, C, G, ring, stream);
 }
 
 LT_API lt_status latent_tail_residual_norm(const uint16_t* block, const void* residual,

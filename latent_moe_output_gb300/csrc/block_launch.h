@@ -58,6 +58,14 @@ bool make_map_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t byt
 bool make_map_bf16_rows64(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                           uint32_t box_rows, uint32_t box_chunks);
 
+// Limits of a kernel's ring of copies: work (tiles, rows) from `copied` on is never
+// copied in, and a wait runs out after limit_ns. Calls leave nothing out; the self-tests
+// of expired waits do.
+struct RingLimits {
+  int64_t copied = INT64_MAX;
+  uint64_t limit_ns = kWaitLimitNs;
+};
+
 struct Matvec4Args {
   const uint16_t* x;       // [N,C]
   const uint8_t* packed;   // [E,M,C/2]
@@ -65,6 +73,7 @@ struct Matvec4Args {
   const int32_t* offsets;  // [E+1] or null (E == 1)
   uint16_t* out;           // [N,M]
   int N, E, M, C, G;
+  RingLimits ring;
 };
 
 enum GateKind { kGateNone = 0, kGateToken = 1, kGateChannel = 2, kGateFull = 3 };

@@ -8,6 +8,10 @@
 
 namespace lt {
 
+// Upper bound of any single device-side wait. Normal waits last microseconds;
+// when one expires the kernel records kErrWaitTimeout and winds down.
+constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s
+
 // Device error word bits (set with atomicOr by kernels, read by latent_tail_check).
 constexpr uint32_t kErrWaitTimeout = 1u;
 

@@ -87,6 +87,7 @@ struct Params {
   bool staged_scales;  // the scales come through the ring (their rows are whole 16-byte pieces)
   bool x_chunks;       // x has whole 64-column chunks: one copy brings a box's four
   uint32_t* err;
+  RingLimits ring;
 };
 
 // Two of the eight values of a word, in the low four bits of each half (kHigh
@@ -111,8 +112,18 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
         "f"(c[2]), "f"(c[3]));
 }
 
-__device__ __forceinline__ void consumer_barrier() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
+// Barrier of the consumer warps; whether `ok` held for all of their threads.
+__device__ __forceinline__ bool consumer_barrier(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(ok)), "n"(kConsumers * 32)
+      : "memory");
+  return all != 0;
 }
 
 // Rows [row0, row0 + rows) of expert e against weight rows from m0 on.
@@ -229,12 +240,14 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
       uint32_t it = 0;  // stages issued
       uint32_t pieces = 0;  // scale pieces issued (one box per stage)
       bool ok = true;
-      for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      const int64_t copied = min(tiles, p.ring.copied);
+      for (int64_t tile = blockIdx.x; ok && tile < copied; tile += gridDim.x) {
         const Tile t = tile_at(tile, mblocks, Cfg::kRows, kPass, s_first, s_unit, p.E);
         const int n_tiles = (t.rows + 7) / 8;
         for (int i = 0; i < steps; ++i, ++it) {
           const uint32_t s = it % Cfg::kStages;
-          ok = mbar_wait(smem_u32(&empty_bar[s]), ((it / Cfg::kStages) & 1u) ^ 1u, p.err, abort_v);
+          ok = mbar_wait(smem_u32(&empty_bar[s]), ((it / Cfg::kStages) & 1u) ^ 1u, p.err, abort_v,
+                         p.ring.limit_ns);
           if (!ok) break;
           if (i == 0) s_tile[s] = t;
           const int live = min(kSplit, boxes - i * kSplit);
@@ -270,13 +283,13 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
           }
         }
       }
-      if (!ok) {  // let copies already in flight land before the CTA exits
-        for (uint32_t i = it > Cfg::kStages ? it - Cfg::kStages : 0; i < it; ++i) {
-          const uint32_t bar = smem_u32(&full_bar[i % Cfg::kStages]);
-          const uint64_t t0 = global_timer_ns();
-          while (!mbar_try_wait(bar, (i / Cfg::kStages) & 1u) &&
-                 global_timer_ns() - t0 < kWaitLimitNs) {
-          }
+      // The copies in flight land before the warp leaves; the consumers wait for them too,
+      // but not after a wait that ran out.
+      for (uint32_t i = it > Cfg::kStages ? it - Cfg::kStages : 0; i < it; ++i) {
+        const uint32_t bar = smem_u32(&full_bar[i % Cfg::kStages]), parity = i / Cfg::kStages & 1u;
+        if (mbar_try_wait(bar, parity)) continue;
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kWaitLimitNs) {
         }
       }
     }
@@ -294,11 +307,17 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
     const int xrow = (g >> 1) + (g & 1) * 4;
     const int pitch = p.C / kGroup;  // scales per row
     uint32_t it = 0, pieces = 0;
+    // Whether all stages have come. A lane whose wait runs out waits no more and releases
+    // no stage, but takes part in the products, which are operations of whole warps; what
+    // they make of a stage that did not come is not stored.
     bool ok = true;
+    auto wait_full = [&](uint32_t s) {
+      return mbar_wait(smem_u32(&full_bar[s]), (it / Cfg::kStages) & 1u, p.err, abort_v,
+                       p.ring.limit_ns);
+    };
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-      if (ok) ok = mbar_wait(smem_u32(&full_bar[it % Cfg::kStages]), (it / Cfg::kStages) & 1u,
-                             p.err, abort_v);
-      Tile t{};
+      ok = __all_sync(0xffffffffu, ok && wait_full(it % Cfg::kStages));
+      Tile t{};  // (without rows: nothing is stored)
       if (ok) t = s_tile[it % Cfg::kStages];
       const int n_tiles = kTiles == 1 ? 1 : (t.rows + 7) / 8;
       float total[kM][kTiles][4];
@@ -311,8 +330,7 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
 
       for (int i = 0; i < steps; ++i, ++it) {
         const uint32_t s = it % Cfg::kStages;
-        if (ok && i > 0)
-          ok = mbar_wait(smem_u32(&full_bar[s]), (it / Cfg::kStages) & 1u, p.err, abort_v);
+        if (ok && i > 0) ok = wait_full(s);
         const int box = i * kSplit + box_in;
         const int runs = min(kRuns, (p.C - box * kBoxCols) / 32 - half * kRuns);
         const uint8_t* st = ring_ptr + s * Cfg::kStageBytes;
@@ -348,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
                              : *reinterpret_cast<const uint16_t*>(sa + h * 8 * Cfg::kPieceBytes);
             }
           }
-        } else if (ok && runs > 0) {
+        } else if (runs > 0) {
           const int first = box * kScales + half * kHalf;
           const uint16_t* stile = p.scales + (static_cast<size_t>(t.e) * p.M + t.m0) * pitch;
 #pragma unroll
@@ -410,21 +428,23 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
             }
           }
         };
-        if (ok && runs == kRuns) {
+        if (runs == kRuns) {
 #pragma unroll
           for (int j = 0; j < kRuns; ++j) run(j);
-        } else if (ok) {  // (whole groups: C is a multiple of the group)
+        } else {  // (whole groups: C is a multiple of the group)
 #pragma unroll
           for (int j = 0; j < kRuns - 1; ++j)
             if (j < runs) run(j);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&empty_bar[s]));
+        if (ok && lane == 0) mbar_arrive(smem_u32(&empty_bar[s]));
       }
 
+      // Whether every stage has arrived for all warps whose sums a result has.
+      if constexpr (Cfg::kParts == 1) ok = __all_sync(0xffffffffu, ok);
       if constexpr (Cfg::kParts > 1) {
         // The column parts of a row are added in order by part 0's warp.
-        consumer_barrier();  // the last tile's sums have been read
+        ok = consumer_barrier(ok);  // the last tile's sums have been read
         constexpr int kPerWarp = 16 * kM * 8 * kTiles;
         if (part > 0) {
           float* dst = sums + ((part - 1) * kRowWarps + warp % kRowWarps) * kPerWarp + lane;
@@ -435,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
 #pragma unroll
               for (int j = 0; j < 4; ++j) dst[((m * kTiles + n) * 4 + j) * 32] = total[m][n][j];
         }
-        consumer_barrier();
+        consumer_barrier(true);
         if (part > 0) continue;
         for (int q = 0; q < Cfg::kParts - 1; ++q) {
           const float* src = sums + (q * kRowWarps + warp) * kPerWarp + lane;
@@ -447,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPer
               for (int j = 0; j < 4; ++j) total[m][n][j] += src[((m * kTiles + n) * 4 + j) * 32];
         }
       }
+      if (!ok) continue;
       // Element (j, lane) of a fragment: weight row g + 8 (j >> 1), column
       // 2 c4 + (j & 1), i.e. row c4 + 4 (j & 1) of x.
 #pragma unroll
@@ -557,7 +578,7 @@ cudaError_t launch_matvec4(const Matvec4Args& a, const DeviceInfo& dev, cudaStre
                        ((a.M + v.rows - 1) / v.rows);
   const int grid = static_cast<int>(std::min<int64_t>(v.ctas_per_sm * dev.num_sms, most));
   const Params p{a.scales, a.offsets, a.out, a.N, a.E, a.M, a.C, staged, x_chunks,
-                 dev.err_word};
+                 dev.err_word, a.ring};
   return launch_dependent(v.kernel, dim3(grid), dim3(kThreads),
                           v.smem + table_bytes(a.E), stream, w_map, x_map,
                           s_map, p);

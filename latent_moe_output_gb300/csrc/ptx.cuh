@@ -11,10 +11,6 @@
 
 namespace lt {
 
-// Upper bound of any single device-side wait. Normal waits last microseconds;
-// when one expires the kernel records kErrWaitTimeout and winds down.
-constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s
-
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

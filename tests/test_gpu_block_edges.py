@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import latent_moe_output_gb300 as lt
-from latent_moe_output_gb300.binding import latent_tail_check
+from latent_moe_output_gb300.binding import LatentTailError, Status, latent_tail_check
 
 import block_reference as br
 import gpu_helpers as gh
@@ -48,3 +48,47 @@ def test_matvec4_zeros_every_row_that_no_expert_owns(N, offsets, E, M, C, G):
     ref, mag = br.matvec4(x, packed, scales, owned)
     br.assert_within(out, ref, br.bf16_bound(ref, (C + 2) * br.U32 * mag))
     assert (out[:int(owned[0])] == 0).all() and (out[int(owned[-1]):] == 0).all()
+
+
+# ------------------------------------------------------ waits that run out
+def timed_out(call):
+    """Runs a self-test whose waits expire."""
+    assert call() == Status.OK
+    with pytest.raises(LatentTailError) as e:
+        latent_tail_check()
+    assert e.value.status == Status.TIMEOUT
+    latent_tail_check()  # the error word was cleared
+
+
+@pytest.mark.parametrize("N,E,M,C,G", [
+    (1, 1, 7168, 2048, 128),  # two boxes per stage
+    (1, 1, 256, 7168, 64),    # four
+    (64, 64, 2048, 512, 32),  # one, 256-row tiles
+    (24, 1, 7168, 1024, 64),  # sixteen rows per pass
+])
+def test_matvec4_keeps_what_did_not_arrive_out_of_the_result(lib, N, E, M, C, G):
+    g = gen(N + M)
+    packed, scales = weights4(E, M, C, G, g)
+    x = randn(N, C, g=g)
+    offsets = None
+    if E > 1:
+        offsets = torch.arange(E + 1, device="cuda").clamp(max=N).to(torch.int32)
+    ref = lt.expert_matvec4(x, packed, scales, offsets)
+    stream = torch.cuda.current_stream().cuda_stream
+    for copied in (0, 1, 5):
+        out = torch.full_like(ref, float("nan"))
+        timed_out(lambda: lib.latent_tail_selftest_expert_matvec4_timeout(
+            x.data_ptr(), packed.data_ptr(), scales.data_ptr(),
+            0 if offsets is None else offsets.data_ptr(), out.data_ptr(), N, E, M, C, G, copied,
+            2000, stream))
+        came = ~torch.isnan(out)
+        assert torch.equal(out[came], ref[came])
+        assert not came.all() and (came.any() or copied == 0)
+    assert torch.equal(lt.expert_matvec4(x, packed, scales, offsets), ref)
+    latent_tail_check()
+
+
+def test_selftest_limits(lib):
+    call = lib.latent_tail_selftest_expert_matvec4_timeout
+    for copied, limit in ((-1, 2000), (0, 0), (0, 1000001)):
+        assert call(*[0x10000000] * 5, 1, 1, 8, 32, 32, copied, limit, None) == Status.INVALID_ARG
