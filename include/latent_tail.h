@@ -271,6 +271,9 @@ LT_API lt_status latent_tail_forward_host(const uint16_t* routed_host,
  * kernel indexes by (expert ids, positions, offsets) are bounds-checked on the
  * device: a value out of range never leads to an access out of range. Results
  * are the same bits from run to run.
+ * After a wait that expired (LT_ERR_TIMEOUT) outputs are incomplete: an element with a
+ * token index, of an in-place residual too, is the call's result or untouched; gradients
+ * summed over tokens lack tokens.
  */
 
 /*
@@ -429,6 +432,30 @@ LT_API lt_status latent_tail_residual_norm_backward(
     float* grad_post_weight, void* grad_gate, float* grad_next_weight, int T, int H,
     lt_gate gate_kind, lt_residual residual_type, float residual_scale, float eps,
     void* workspace, size_t workspace_bytes, lt_stream stream);
+
+/*
+ * Diagnostics as latent_tail_selftest_expert_matvec4_timeout, for the waits of
+ * latent_tail_residual_norm and its gradient: token rows from copied_rows (an even
+ * number >= 0) on are never copied to the SMs. Shapes whose kernel loads its rows
+ * directly (the forward call with fewer tokens than SMs and H <= 8192, or H < 520; the
+ * gradient with H <= 512) have no such waits and give the whole result. Elements of the
+ * outputs with a token index, an in-place residual among them, are then either the
+ * call's result or untouched; the sums over tokens are incomplete.
+ */
+LT_API lt_status latent_tail_selftest_residual_norm_timeout(
+    const uint16_t* block, const void* residual, const float* post_weight, const void* gate,
+    const float* next_weight, void* residual_out, uint16_t* next_out, int T, int H,
+    lt_gate gate_kind, lt_residual residual_type, float residual_scale, float eps,
+    int copied_rows, unsigned int limit_us, lt_stream stream);
+
+LT_API lt_status latent_tail_selftest_residual_norm_backward_timeout(
+    const void* grad_residual_out, const uint16_t* grad_next, const uint16_t* block,
+    const void* residual_out, const float* post_weight, const void* gate,
+    const float* next_weight, uint16_t* grad_block, void* grad_residual,
+    float* grad_post_weight, void* grad_gate, float* grad_next_weight, int T, int H,
+    lt_gate gate_kind, lt_residual residual_type, float residual_scale, float eps,
+    void* workspace, size_t workspace_bytes, int copied_rows, unsigned int limit_us,
+    lt_stream stream);
 
 /* Static, human-readable name of a status code. Never NULL. */
 LT_API const char* latent_tail_status_string(lt_status status);

@@ -78,6 +78,12 @@ _SIGNATURES = {
                                            + [ctypes.c_int] * 4 + [ctypes.c_float] * 2
                                            + [ctypes.c_void_p, ctypes.c_size_t,
                                               ctypes.c_void_p]),
+    "latent_tail_selftest_residual_norm_timeout": (
+        ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int] * 4 + [ctypes.c_float] * 2
+        + [ctypes.c_int, ctypes.c_uint, ctypes.c_void_p]),
+    "latent_tail_selftest_residual_norm_backward_timeout": (
+        ctypes.c_int, [ctypes.c_void_p] * 12 + [ctypes.c_int] * 4 + [ctypes.c_float] * 2
+        + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint, ctypes.c_void_p]),
     "latent_tail_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
 

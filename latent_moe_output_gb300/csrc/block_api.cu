@@ -104,6 +104,93 @@ lt_status expert_matvec4(const uint16_t* x, const uint8_t* packed, const uint16_
   return launch_status(launch_matvec4(a, *dev, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+lt_status residual_norm(const uint16_t* block, const void* residual, const float* post_weight,
+                        const void* gate, const float* next_weight, void* residual_out,
+                        uint16_t* next_out, int T, int H, lt_gate gate_kind,
+                        lt_residual residual_type, float residual_scale, float eps,
+                        const RingLimits& ring, lt_stream stream) {
+  lt_status st = check_norm(T, H, gate_kind, gate, residual_type, residual_scale, eps);
+  if (st != LT_OK) return st;
+  if (T == 0) return LT_OK;
+  if ((next_weight == nullptr) != (next_out == nullptr)) return LT_ERR_INVALID_ARG;
+  if ((st = check_ptrs({block, residual, residual_out})) != LT_OK) return st;
+  if (gate_kind != LT_GATE_NONE && (st = check_ptrs({gate})) != LT_OK) return st;
+  if ((st = check_optional({post_weight, next_weight, next_out})) != LT_OK) return st;
+  const size_t th = static_cast<size_t>(T) * H;
+  const size_t r_bytes = th * (residual_type == LT_RESIDUAL_FP32 ? 4 : 2);
+  const size_t h_bytes = static_cast<size_t>(H) * 4;
+  if (!disjoint({span(residual_out, r_bytes), span(next_out, th * 2)},
+                {span(block, th * 2), span(residual, r_bytes), span(post_weight, h_bytes),
+                 span(gate, gate_bytes(gate_kind, T, H)), span(next_weight, h_bytes)},
+                residual))
+    return LT_ERR_INVALID_ARG;
+  // (residual_out == residual is the only in-place form: next_out has its own range)
+  if (next_out != nullptr && static_cast<const void*>(next_out) == residual)
+    return LT_ERR_INVALID_ARG;
+  const lt::DeviceInfo* dev = nullptr;
+  if ((st = current_device(&dev)) != LT_OK) return st;
+  const ResidualNormArgs a{block, residual, post_weight, gate, next_weight, residual_out,
+                           next_out, T, H, gate_kind, residual_type == LT_RESIDUAL_FP32,
+                           residual_scale, eps, ring};
+  return launch_status(launch_residual_norm(a, *dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t backward_workspace(int T, int H) {
+  if (T <= 0 || T > (1 << 24) || check_width(H, 16384) != LT_OK) return 0;
+  return round256(2 * static_cast<size_t>(residual_norm_partial_rows(T, H)) * H * sizeof(float));
+}
+
+lt_status residual_norm_backward(
+    const void* grad_residual_out, const uint16_t* grad_next, const uint16_t* block,
+    const void* residual_out, const float* post_weight, const void* gate,
+    const float* next_weight, uint16_t* grad_block, void* grad_residual, float* grad_post_weight,
+    void* grad_gate, float* grad_next_weight, int T, int H, lt_gate gate_kind,
+    lt_residual residual_type, float residual_scale, float eps, void* workspace,
+    size_t workspace_bytes, const RingLimits& ring, lt_stream stream) {
+  lt_status st = check_norm(T, H, gate_kind, gate, residual_type, residual_scale, eps);
+  if (st != LT_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const size_t h_bytes = static_cast<size_t>(H) * 4;
+  const lt::DeviceInfo* dev = nullptr;
+  if (T == 0) {
+    if ((st = check_optional({grad_post_weight, grad_next_weight, grad_gate})) != LT_OK) return st;
+    if ((st = current_device(&dev)) != LT_OK) return st;
+    if ((st = zero(grad_post_weight, h_bytes, s)) != LT_OK) return st;
+    if ((st = zero(grad_next_weight, h_bytes, s)) != LT_OK) return st;
+    return gate_kind == LT_GATE_CHANNEL ? zero(grad_gate, h_bytes, s) : LT_OK;
+  }
+  if ((post_weight == nullptr) != (grad_post_weight == nullptr) ||
+      (next_weight == nullptr) != (grad_next_weight == nullptr) ||
+      (next_weight == nullptr) != (grad_next == nullptr) ||
+      (gate_kind == LT_GATE_NONE) != (grad_gate == nullptr) ||
+      (grad_residual_out == nullptr && grad_next == nullptr))
+    return LT_ERR_INVALID_ARG;
+  if ((st = check_ptrs({block, residual_out, grad_block, grad_residual})) != LT_OK) return st;
+  if (gate_kind != LT_GATE_NONE && (st = check_ptrs({gate})) != LT_OK) return st;
+  if ((st = check_optional({grad_residual_out, grad_next, post_weight, next_weight,
+                            grad_post_weight, grad_gate, grad_next_weight})) != LT_OK)
+    return st;
+  const size_t need = backward_workspace(T, H);
+  if (workspace == nullptr || workspace_bytes < need) return LT_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return LT_ERR_ALIGNMENT;
+  const size_t th = static_cast<size_t>(T) * H;
+  const size_t r_bytes = th * (residual_type == LT_RESIDUAL_FP32 ? 4 : 2);
+  const size_t g_bytes = gate_bytes(gate_kind, T, H);
+  if (!disjoint({span(grad_block, th * 2), span(grad_residual, r_bytes),
+                 span(grad_post_weight, h_bytes), span(grad_gate, g_bytes),
+                 span(grad_next_weight, h_bytes), span(workspace, need)},
+                {span(grad_residual_out, r_bytes), span(grad_next, th * 2), span(block, th * 2),
+                 span(residual_out, r_bytes), span(post_weight, h_bytes), span(gate, g_bytes),
+                 span(next_weight, h_bytes)}))
+    return LT_ERR_INVALID_ARG;
+  if ((st = current_device(&dev)) != LT_OK) return st;
+  const ResidualNormBackwardArgs a{
+      grad_residual_out, grad_next, block, residual_out, post_weight, gate, next_weight,
+      grad_block, grad_residual, grad_post_weight, grad_gate, grad_next_weight, T, H, gate_kind,
+      residual_type == LT_RESIDUAL_FP32, residual_scale, eps, static_cast<float*>(workspace), ring};
+  return launch_status(launch_residual_norm_backward(a, *dev, s));
+}
+
 }  // namespace
 
 extern "C" {
@@ -213,35 +300,23 @@ LT_API lt_status latent_tail_residual_norm(const uint16_t* block, const void* re
                                            uint16_t* next_out, int T, int H, lt_gate gate_kind,
                                            lt_residual residual_type, float residual_scale,
                                            float eps, lt_stream stream) {
-  lt_status st = check_norm(T, H, gate_kind, gate, residual_type, residual_scale, eps);
-  if (st != LT_OK) return st;
-  if (T == 0) return LT_OK;
-  if ((next_weight == nullptr) != (next_out == nullptr)) return LT_ERR_INVALID_ARG;
-  if ((st = check_ptrs({block, residual, residual_out})) != LT_OK) return st;
-  if (gate_kind != LT_GATE_NONE && (st = check_ptrs({gate})) != LT_OK) return st;
-  if ((st = check_optional({post_weight, next_weight, next_out})) != LT_OK) return st;
-  const size_t th = static_cast<size_t>(T) * H;
-  const size_t r_bytes = th * (residual_type == LT_RESIDUAL_FP32 ? 4 : 2);
-  const size_t h_bytes = static_cast<size_t>(H) * 4;
-  if (!disjoint({span(residual_out, r_bytes), span(next_out, th * 2)},
-                {span(block, th * 2), span(residual, r_bytes), span(post_weight, h_bytes),
-                 span(gate, gate_bytes(gate_kind, T, H)), span(next_weight, h_bytes)},
-                residual))
-    return LT_ERR_INVALID_ARG;
-  // (residual_out == residual is the only in-place form: next_out has its own range)
-  if (next_out != nullptr && static_cast<const void*>(next_out) == residual)
-    return LT_ERR_INVALID_ARG;
-  const lt::DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev)) != LT_OK) return st;
-  const ResidualNormArgs a{block, residual, post_weight, gate, next_weight, residual_out,
-                           next_out, T, H, gate_kind, residual_type == LT_RESIDUAL_FP32,
-                           residual_scale, eps};
-  return launch_status(launch_residual_norm(a, *dev, reinterpret_cast<cudaStream_t>(stream)));
+  return residual_norm(block, residual, post_weight, gate, next_weight, residual_out, next_out, T,
+                       H, gate_kind, residual_type, residual_scale, eps, RingLimits{}, stream);
+}
+
+LT_API lt_status latent_tail_selftest_residual_norm_timeout(
+    const uint16_t* block, const void* residual, const float* post_weight, const void* gate,
+    const float* next_weight, void* residual_out, uint16_t* next_out, int T, int H,
+    lt_gate gate_kind, lt_residual residual_type, float residual_scale, float eps,
+    int copied_rows, unsigned int limit_us, lt_stream stream) {
+  RingLimits ring;
+  if (!test_limits(copied_rows, limit_us, &ring)) return LT_ERR_INVALID_ARG;
+  return residual_norm(block, residual, post_weight, gate, next_weight, residual_out, next_out, T,
+                       H, gate_kind, residual_type, residual_scale, eps, ring, stream);
 }
 
 LT_API size_t latent_tail_residual_norm_backward_workspace_size(int T, int H) {
-  if (T <= 0 || T > (1 << 24) || check_width(H, 16384) != LT_OK) return 0;
-  return round256(2 * static_cast<size_t>(residual_norm_partial_rows(T, H)) * H * sizeof(float));
+  return backward_workspace(T, H);
 }
 
 LT_API lt_status latent_tail_residual_norm_backward(
@@ -251,48 +326,27 @@ LT_API lt_status latent_tail_residual_norm_backward(
     void* grad_gate, float* grad_next_weight, int T, int H, lt_gate gate_kind,
     lt_residual residual_type, float residual_scale, float eps, void* workspace,
     size_t workspace_bytes, lt_stream stream) {
-  lt_status st = check_norm(T, H, gate_kind, gate, residual_type, residual_scale, eps);
-  if (st != LT_OK) return st;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const size_t h_bytes = static_cast<size_t>(H) * 4;
-  const lt::DeviceInfo* dev = nullptr;
-  if (T == 0) {
-    if ((st = check_optional({grad_post_weight, grad_next_weight, grad_gate})) != LT_OK) return st;
-    if ((st = current_device(&dev)) != LT_OK) return st;
-    if ((st = zero(grad_post_weight, h_bytes, s)) != LT_OK) return st;
-    if ((st = zero(grad_next_weight, h_bytes, s)) != LT_OK) return st;
-    return gate_kind == LT_GATE_CHANNEL ? zero(grad_gate, h_bytes, s) : LT_OK;
-  }
-  if ((post_weight == nullptr) != (grad_post_weight == nullptr) ||
-      (next_weight == nullptr) != (grad_next_weight == nullptr) ||
-      (next_weight == nullptr) != (grad_next == nullptr) ||
-      (gate_kind == LT_GATE_NONE) != (grad_gate == nullptr) ||
-      (grad_residual_out == nullptr && grad_next == nullptr))
-    return LT_ERR_INVALID_ARG;
-  if ((st = check_ptrs({block, residual_out, grad_block, grad_residual})) != LT_OK) return st;
-  if (gate_kind != LT_GATE_NONE && (st = check_ptrs({gate})) != LT_OK) return st;
-  if ((st = check_optional({grad_residual_out, grad_next, post_weight, next_weight,
-                            grad_post_weight, grad_gate, grad_next_weight})) != LT_OK)
-    return st;
-  const size_t need = latent_tail_residual_norm_backward_workspace_size(T, H);
-  if (workspace == nullptr || workspace_bytes < need) return LT_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return LT_ERR_ALIGNMENT;
-  const size_t th = static_cast<size_t>(T) * H;
-  const size_t r_bytes = th * (residual_type == LT_RESIDUAL_FP32 ? 4 : 2);
-  const size_t g_bytes = gate_bytes(gate_kind, T, H);
-  if (!disjoint({span(grad_block, th * 2), span(grad_residual, r_bytes),
-                 span(grad_post_weight, h_bytes), span(grad_gate, g_bytes),
-                 span(grad_next_weight, h_bytes), span(workspace, need)},
-                {span(grad_residual_out, r_bytes), span(grad_next, th * 2), span(block, th * 2),
-                 span(residual_out, r_bytes), span(post_weight, h_bytes), span(gate, g_bytes),
-                 span(next_weight, h_bytes)}))
-    return LT_ERR_INVALID_ARG;
-  if ((st = current_device(&dev)) != LT_OK) return st;
-  const ResidualNormBackwardArgs a{
-      grad_residual_out, grad_next, block, residual_out, post_weight, gate, next_weight,
-      grad_block, grad_residual, grad_post_weight, grad_gate, grad_next_weight, T, H, gate_kind,
-      residual_type == LT_RESIDUAL_FP32, residual_scale, eps, static_cast<float*>(workspace)};
-  return launch_status(launch_residual_norm_backward(a, *dev, s));
+  return residual_norm_backward(grad_residual_out, grad_next, block, residual_out, post_weight,
+                                gate, next_weight, grad_block, grad_residual, grad_post_weight,
+                                grad_gate, grad_next_weight, T, H, gate_kind, residual_type,
+                                residual_scale, eps, workspace, workspace_bytes, RingLimits{},
+                                stream);
+}
+
+LT_API lt_status latent_tail_selftest_residual_norm_backward_timeout(
+    const void* grad_residual_out, const uint16_t* grad_next, const uint16_t* block,
+    const void* residual_out, const float* post_weight, const void* gate,
+    const float* next_weight, uint16_t* grad_block, void* grad_residual, float* grad_post_weight,
+    void* grad_gate, float* grad_next_weight, int T, int H, lt_gate gate_kind,
+    lt_residual residual_type, float residual_scale, float eps, void* workspace,
+    size_t workspace_bytes, int copied_rows, unsigned int limit_us, lt_stream stream) {
+  RingLimits ring;
+  if (!test_limits(copied_rows, limit_us, &ring)) return LT_ERR_INVALID_ARG;
+  return residual_norm_backward(grad_residual_out, grad_next, block, residual_out, post_weight,
+                                gate, next_weight, grad_block, grad_residual, grad_post_weight,
+                                grad_gate, grad_next_weight, T, H, gate_kind, residual_type,
+                                residual_scale, eps, workspace, workspace_bytes, ring,
+                                stream);
 }
 
 }  // extern "C"

@@ -90,6 +90,7 @@ struct ResidualNormArgs {
   int gate_kind;
   bool residual_f32;
   float scale, eps;
+  RingLimits ring;
 };
 
 struct ResidualNormBackwardArgs {
@@ -110,6 +111,7 @@ struct ResidualNormBackwardArgs {
   bool residual_f32;
   float scale, eps;
   float* partials;                // workspace: [2][rows][H]
+  RingLimits ring;
 };
 
 // SMs that a workspace size computed without a device allows for.

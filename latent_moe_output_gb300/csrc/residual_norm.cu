@@ -301,9 +301,13 @@ constexpr size_t backward_ring_smem(int H) {
 // halving exchanges leave a lane with a part of one value, one partial per warp goes to
 // shared memory (of both CTAs), and each warp adds the warps' partials again. `red` is
 // [kValues][32], zero where there is no warp; the CTAs of a cluster (of up to 16 warps
-// each) have half of it each. Consecutive calls use different ones.
+// each) have half of it each. Consecutive calls use different ones. With a CTA's abort flag:
+// returns whether no thread had given up on a wait at the barrier (read beside the
+// partials; after them it costs up to 7 % of a forward call).
 template <int kValues, int kCluster>
-__device__ __forceinline__ void cta_sum(float (&v)[kValues], float (*red)[32]) {
+__device__ __forceinline__ bool cta_sum(float (&v)[kValues], float (*red)[32],
+                                        volatile int* abort_v = nullptr) {
+  bool came = true;
   constexpr int kLanes = 32 / kValues;  // lanes per value
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float w[kValues];
@@ -323,6 +327,7 @@ __device__ __forceinline__ void cta_sum(float (&v)[kValues], float (*red)[32]) {
   if constexpr (kCluster == 1) {
     if (lane % kLanes == 0) red[which][warp] = c;
     __syncthreads();
+    if (abort_v != nullptr) came = !*abort_v;
   } else {
     const uint32_t rank = cluster_rank();
     if (lane % kLanes == 0) {
@@ -347,6 +352,7 @@ __device__ __forceinline__ void cta_sum(float (&v)[kValues], float (*red)[32]) {
   for (int o = kLanes / 2; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
 #pragma unroll
   for (int i = 0; i < kValues; ++i) v[i] = __shfl_sync(0xffffffffu, c, kLanes * i);
+  return came;
 }
 
 // The part of a row that a CTA of a cluster owns.
@@ -589,15 +595,21 @@ __global__ void __launch_bounds__(kNarrowThreads, kPieces == 1 ? 2 : 1)
   }
 }
 
-// After a wait that ran out: lets copies in flight land before the CTA exits.
-__device__ __noinline__ void drain_ring(uint64_t* full_bar, int stages) {
+// After a wait that ran out: lets copies in flight land before the CTA exits, for limit_ns
+// at most in all (a stage that nothing is on its way to keeps one parity open).
+__device__ __noinline__ void drain_ring(uint64_t* full_bar, int stages, uint64_t limit_ns) {
+  const uint64_t t0 = global_timer_ns();
   for (int i = 0; i < stages; ++i)
-    for (uint32_t q = 0; q < 2; ++q) {
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(smem_u32(&full_bar[i]), q) && global_timer_ns() - t0 < kWaitLimitNs) {
+    for (uint32_t q = 0; q < 2; ++q)
+      while (!mbar_try_wait(smem_u32(&full_bar[i]), q) && global_timer_ns() - t0 < limit_ns) {
       }
-    }
 }
+
+// After a wait that ran out, the ring kernels go on to the end of their rows for the
+// barriers alone: nothing is fetched, and no value is stored that a row which did not come
+// has entered. A thread learns of the others' waits with the row's sums: by the CTA's flag
+// in the forward kernel, by the number of threads that gave up, summed with the rest, in
+// the gradient's, whose CTAs may share rows.
 
 // The forward pass for many rows and for rows wider than 8192, one to eight CTAs per SM:
 // like the gradient's ring kernel below, kRows token rows at a time (adjacent in memory:
@@ -639,10 +651,11 @@ __global__ void __launch_bounds__(kThreads, forward_ring_ctas(kThreads))
     if (full_gate) bulk_load(st + at_g, static_cast<const uint16_t*>(a.gate) + base, n * h2, bar);
   };
   const int step = gridDim.x * kRows, begin = blockIdx.x * kRows;
+  const int64_t copied = min(static_cast<int64_t>(a.T), a.ring.copied);
   if (threadIdx.x == 0)
     for (int s = 0; s < stages; ++s) {
       const int64_t t = begin + static_cast<int64_t>(s) * step;
-      if (t < a.T) fetch(static_cast<int>(t), s);
+      if (t < copied) fetch(static_cast<int>(t), s);
     }
 
   // Post weight (times a channel gate), next weight. With two pieces and more than 640
@@ -672,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, forward_ring_ctas(kThreads))
   bool ok = true;
   for (int t = begin; t < a.T; t += step) {
     const uint8_t* st = smem + static_cast<size_t>(s) * stage_bytes;
-    if (ok) ok = mbar_wait(smem_u32(&full_bar[s]), parity, err, abort_v);
+    if (ok) ok = mbar_wait(smem_u32(&full_bar[s]), parity, err, abort_v, a.ring.limit_ns);
     float sum[kRows], factor[kRows];  // of y: r1 and a token gate
     uint4 y_raw[kRows][kPieces];
 #pragma unroll
@@ -695,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, forward_ring_ctas(kThreads))
       sum[r] = sum2(q);
     }
     if (has_post) {
-      cta_sum<kRows, 1>(sum, red[turn]);
+      if (!cta_sum<kRows, 1>(sum, red[turn], abort_v)) ok = false;
       turn ^= 1;
 #pragma unroll
       for (int r = 0; r < kRows; ++r) factor[r] *= 1.0f / sqrtf(sum[r] * inv_h + a.eps);
@@ -725,14 +738,14 @@ __global__ void __launch_bounds__(kThreads, forward_ring_ctas(kThreads))
           v[r][e][i] = fma2(scale, v[r][e][i], f[i]);
           q = fma2(v[r][e][i], v[r][e][i], q);
         }
-        store_res8<kF32>(a.residual_out, static_cast<size_t>(t + r) * H + col, v[r][e]);
+        if (ok) store_res8<kF32>(a.residual_out, static_cast<size_t>(t + r) * H + col, v[r][e]);
       }
       sum[r] = sum2(q);
     }
     // Also without a second norm: after this barrier all threads are done with the stage.
-    cta_sum<kRows, 1>(sum, red[turn]);
+    if (!cta_sum<kRows, 1>(sum, red[turn], abort_v)) ok = false;
     turn ^= 1;
-    if (a.next != nullptr) {
+    if (a.next != nullptr && ok) {
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
         const f32x2 r2 = both(1.0f / sqrtf(sum[r] * inv_h + a.eps));
@@ -750,12 +763,12 @@ __global__ void __launch_bounds__(kThreads, forward_ring_ctas(kThreads))
     }
     // Refilled after the row's stores: asking for it right after the barrier measured
     // 1-4 % slower.
-    if (threadIdx.x == 0 && ok && t + static_cast<int64_t>(stages) * step < a.T)
+    if (threadIdx.x == 0 && ok && t + static_cast<int64_t>(stages) * step < copied)
       fetch(t + stages * step, s);
     if (++s == stages) s = 0, parity ^= 1;
   }
   if constexpr (kThreads <= kLateTriggerThreads) pdl_launch_dependents();
-  if (*abort_v && threadIdx.x == 0) drain_ring(full_bar, stages);
+  if (threadIdx.x == 0 && !ok) drain_ring(full_bar, stages, a.ring.limit_ns);
 }
 
 template <bool kF32, int kThreads, int kPieces, int kMode, int kCluster>
@@ -802,8 +815,9 @@ __global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(
     if (full_gate) bulk_load(st + at_g, static_cast<const uint16_t*>(a.gate) + base, h2, bar);
   };
   const int step = gridDim.x / kCluster, begin = blockIdx.x / kCluster;
+  const int64_t copied = min(static_cast<int64_t>(a.T), a.ring.copied);
   if (threadIdx.x == 0)
-    for (int s = 0; s < stages && begin + s * step < a.T; ++s) fetch(begin + s * step, s);
+    for (int s = 0; s < stages && begin + s * step < copied; ++s) fetch(begin + s * step, s);
 
   f32x2 gp[kPieces][4], gn[kPieces][4], acc_p[kPieces][4], acc_n[kPieces][4];
 #pragma unroll
@@ -819,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(
     const uint8_t* st = smem + static_cast<size_t>(s) * stage_bytes;
     const float gt =
         a.gate_kind == kGateToken ? __ldg(static_cast<const float*>(a.gate) + t) : 1.f;
-    if (ok) ok = mbar_wait(smem_u32(&full_bar[s]), parity, err, abort_v);
+    if (ok) ok = mbar_wait(smem_u32(&full_bar[s]), parity, err, abort_v, a.ring.limit_ns);
     float sum[8] = {};
     f32x2 q[6];
 #pragma unroll
@@ -838,10 +852,13 @@ __global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(
     }
 #pragma unroll
     for (int i = 0; i < 6; ++i) sum[i] = sum2(q[i]);
+    sum[6] = ok ? 0.f : 1.f;  // threads that gave up, in both CTAs of a cluster
     cta_sum<8, kCluster>(sum, red[turn]);
     turn ^= 1;
+    ok = sum[6] == 0.f;
+    if (!ok) continue;
     // All threads are done with the previous row's stage.
-    if (threadIdx.x == 0 && ok && last >= 0 && last + static_cast<int64_t>(stages) * step < a.T)
+    if (threadIdx.x == 0 && last >= 0 && last + static_cast<int64_t>(stages) * step < copied)
       fetch(last + stages * step, s == 0 ? stages - 1 : s - 1);
     last = t;
     const GradRow r = grad_row(sum, has, inv_h, a.eps, gt);
@@ -883,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(
     if (has_post || a.gate_kind == kGateChannel) store8(a.partials + at, acc_p[e]);
     if (has_next) store8(a.partials + plane + at, acc_n[e]);
   }
-  if (*abort_v && threadIdx.x == 0) drain_ring(full_bar, stages);
+  if (threadIdx.x == 0 && !ok) drain_ring(full_bar, stages, a.ring.limit_ns);
 }
 
 struct RingPlan {

@@ -9,7 +9,7 @@ from latent_moe_output_gb300.binding import LatentTailError, Status, latent_tail
 
 import block_reference as br
 import gpu_helpers as gh
-from test_gpu_block import gen, randn, weights4
+from test_gpu_block import EPS, gen, norm_case, randn, weights4
 
 pytestmark = pytest.mark.gpu
 
@@ -88,7 +88,87 @@ def test_matvec4_keeps_what_did_not_arrive_out_of_the_result(lib, N, E, M, C, G)
     latent_tail_check()
 
 
+def ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def kinds(c):
+    """Gate kind and residual type as the C entry points take them."""
+    gate = c["gate"]
+    kind = 0 if gate is None else 2 if gate.dim() == 1 else 1 if gate.shape[1] == 1 else 3
+    return kind, int(c["residual"].dtype == torch.float32)
+
+
+def arrived(got, want, before):
+    """Which elements are the call's result; all others must be as they were."""
+    came = got == want
+    assert torch.equal(got[~came].nan_to_num(7.0), before[~came].nan_to_num(7.0))
+    return came
+
+
+@pytest.mark.parametrize("post,nxt", [(True, True), (False, True), (True, False)])
+@pytest.mark.parametrize("T,H,gate,residual", [
+    (2000, 520, "none", "bf16"), (1000, 1024, "channel", "fp32"), (700, 7168, "token", "bf16"),
+    (400, 8192, "full", "fp32"), (170, 9152, "channel", "bf16"), (160, 16384, "full", "fp32")])
+def test_residual_norm_leaves_rows_that_did_not_arrive_untouched(lib, T, H, gate, residual, post,
+                                                                 nxt):
+    c = norm_case(T, H, gate, residual, seed=T + H, post=post, nxt=nxt)
+    v, z = lt.residual_norm(c["block"], c["residual"], c["post"], c["nxt"], EPS, gate=c["gate"])
+    stream = torch.cuda.current_stream().cuda_stream
+    for copied in (0, 2, 154):
+        r = c["residual"].clone()  # in place
+        z2 = None if z is None else torch.full_like(z, float("nan"))
+        timed_out(lambda: lib.latent_tail_selftest_residual_norm_timeout(
+            ptr(c["block"]), ptr(r), ptr(c["post"]), ptr(c["gate"]), ptr(c["nxt"]), ptr(r),
+            ptr(z2), T, H, *kinds(c), 1.0, EPS, copied, 2000, stream))
+        came = arrived(r, v, c["residual"])
+        assert came[:copied].all() and not came[copied:].all(1).any()
+        if z is not None:
+            came = arrived(z2, z, torch.full_like(z, float("nan")))
+            assert came[:copied].all() and not came[copied:].any()
+    again = lt.residual_norm(c["block"], c["residual"], c["post"], c["nxt"], EPS, gate=c["gate"])
+    assert torch.equal(again[0], v)
+    latent_tail_check()
+
+
+@pytest.mark.parametrize("T,H,gate,residual", [
+    (1000, 520, "token", "bf16"), (2000, 1024, "channel", "fp32"), (700, 7168, "full", "bf16"),
+    (170, 9152, "token", "bf16"), (160, 16384, "full", "fp32")])
+def test_residual_norm_backward_leaves_rows_that_did_not_arrive_untouched(lib, T, H, gate,
+                                                                          residual):
+    c = norm_case(T, H, gate, residual, seed=T + H)
+    g = gen(T)
+    dv, dz = randn(T, H, g=g, dtype=c["residual"].dtype), randn(T, H, g=g)
+    want = lt.residual_norm_backward(dv, dz, c["block"], c["residual"], c["post"], c["nxt"], EPS,
+                                     gate=c["gate"])
+    ws = torch.empty(lt.residual_norm_backward_workspace_size(T, H), dtype=torch.uint8,
+                     device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    for copied in (0, 2, 60):
+        got = [torch.full_like(w, float("nan")) for w in want]
+        timed_out(lambda: lib.latent_tail_selftest_residual_norm_backward_timeout(
+            ptr(dv), ptr(dz), ptr(c["block"]), ptr(c["residual"]), ptr(c["post"]), ptr(c["gate"]),
+            ptr(c["nxt"]), ptr(got[0]), ptr(got[1]), ptr(got[2]), ptr(got[3]), ptr(got[4]), T, H,
+            *kinds(c), 1.0, EPS, ptr(ws), ws.numel(), copied, 2000, stream))
+        for name, a, b in zip(("block", "residual", "post", "gate"), got, want):
+            if name == "post" or a.dim() == 1:
+                assert torch.isfinite(a).all()  # sums over the rows that came
+                continue
+            came = arrived(a, b, torch.full_like(a, float("nan")))
+            assert came[:copied].all() and not came[copied:].any(), name
+    again = lt.residual_norm_backward(dv, dz, c["block"], c["residual"], c["post"], c["nxt"], EPS,
+                                      gate=c["gate"])
+    for a, b in zip(again, want):
+        assert torch.equal(a, b)
+    latent_tail_check()
+
+
 def test_selftest_limits(lib):
     call = lib.latent_tail_selftest_expert_matvec4_timeout
     for copied, limit in ((-1, 2000), (0, 0), (0, 1000001)):
         assert call(*[0x10000000] * 5, 1, 1, 8, 32, 32, copied, limit, None) == Status.INVALID_ARG
+    call = lib.latent_tail_selftest_residual_norm_timeout
+    assert call(*[0x10000000] * 7, 1, 8, 0, 0, 1.0, EPS, -1, 2000, None) == Status.INVALID_ARG
+    call = lib.latent_tail_selftest_residual_norm_backward_timeout
+    assert call(*[0x10000000] * 12, 1, 8, 0, 0, 1.0, EPS, 0x10000000, 64, 0, 0,
+                None) == Status.INVALID_ARG
