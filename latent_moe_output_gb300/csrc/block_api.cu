@@ -22,7 +22,7 @@ lt_status check_width(int L, int most) {
 }
 
 // No output may overlap an input or another output; null spans are skipped.
-// `exact_pair`: an output that may be exactly one input (same range).
+// `in_place`: an output may be exactly an input that begins here (same range).
 bool disjoint(std::initializer_list<Span> outs, std::initializer_list<Span> ins,
               const void* in_place = nullptr) {
   for (const Span* a = outs.begin(); a != outs.end(); ++a) {
@@ -119,10 +119,15 @@ lt_status residual_norm(const uint16_t* block, const void* residual, const float
   const size_t th = static_cast<size_t>(T) * H;
   const size_t r_bytes = th * (residual_type == LT_RESIDUAL_FP32 ? 4 : 2);
   const size_t h_bytes = static_cast<size_t>(H) * 4;
-  if (!disjoint({span(residual_out, r_bytes), span(next_out, th * 2)},
-                {span(block, th * 2), span(residual, r_bytes), span(post_weight, h_bytes),
-                 span(gate, gate_bytes(gate_kind, T, H)), span(next_weight, h_bytes)},
-                residual))
+  // In place: every element of block, residual and a full gate is read before the element
+  // of residual_out that it enters is written. The vectors are read for each row.
+  const Span gate_span = span(gate, gate_bytes(gate_kind, T, H));
+  const bool full = gate_kind == LT_GATE_FULL;
+  const auto outs = {span(residual_out, r_bytes), span(next_out, th * 2)};
+  if (!disjoint(outs, {span(block, th * 2), span(residual, r_bytes), full ? gate_span : Span{0, 0}},
+                residual) ||
+      !disjoint(outs, {span(post_weight, h_bytes), full ? Span{0, 0} : gate_span,
+                       span(next_weight, h_bytes)}))
     return LT_ERR_INVALID_ARG;
   // (residual_out == residual is the only in-place form: next_out has its own range)
   if (next_out != nullptr && static_cast<const void*>(next_out) == residual)
