@@ -28,10 +28,14 @@ __device__ uint32_t g_error_word;
 
 constexpr int kMaxDevices = 64;
 
+constexpr int kOperators = static_cast<int>(lt::Operator::kResidualNorm) + 1;
+
 struct DeviceSlot {
   bool initialized = false;
   lt_status status = LT_OK;
   lt::DeviceInfo info{};
+  bool set_up[kOperators] = {};
+  lt_status operator_status[kOperators] = {};
 };
 
 DeviceSlot g_devices[kMaxDevices];
@@ -79,12 +83,23 @@ lt_status init_device(int dev, DeviceSlot& slot) {
       return LT_ERR_CUDA;
     g_ptr_attr = reinterpret_cast<PointerGetAttributeFn>(fn);
   }
-  if (lt::setup_norm(d) != cudaSuccess || lt::setup_decode(d) != cudaSuccess ||
-      lt::setup_prefill(d) != cudaSuccess || lt::setup_gemv(d) != cudaSuccess ||
-      lt::setup_dispatch(d) != cudaSuccess || lt::setup_matvec4(d) != cudaSuccess ||
-      lt::setup_residual_norm(d) != cudaSuccess)
-    return LT_ERR_CUDA;
   return LT_OK;
+}
+
+cudaError_t set_up(lt::Operator op, const lt::DeviceInfo& d) {
+  cudaError_t e = cudaSuccess;
+  switch (op) {
+    case lt::Operator::kNone: break;
+    case lt::Operator::kTail:
+      if ((e = lt::setup_norm(d)) != cudaSuccess) return e;
+      if ((e = lt::setup_decode(d)) != cudaSuccess) return e;
+      if ((e = lt::setup_prefill(d)) != cudaSuccess) return e;
+      return lt::setup_gemv(d);
+    case lt::Operator::kDispatch: return lt::setup_dispatch(d);
+    case lt::Operator::kMatvec4: return lt::setup_matvec4(d);
+    case lt::Operator::kResidualNorm: return lt::setup_residual_norm(d);
+  }
+  return e;
 }
 
 // out may be exactly one of the P shared partials (in-place beta-add): every
@@ -171,7 +186,7 @@ lt_status forward_impl(const uint16_t* routed, const uint16_t* shared, const flo
   if (overlaps(so, ss) && !aliases_a_partial(out, shared, P, T, H)) return LT_ERR_INVALID_ARG;
 
   const lt::DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev)) != LT_OK) return st;
+  if ((st = current_device(&dev, lt::Operator::kTail)) != LT_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (routed_in_device_memory && T <= lt::kGemvMaxTokens &&
       lt::gemv_supported(T, L, c0, c1, *dev)) {  // the whole tail in one launch
@@ -204,7 +219,7 @@ lt_status forward_impl(const uint16_t* routed, const uint16_t* shared, const flo
 
 namespace lt {
 
-lt_status current_device(const DeviceInfo** out) {
+lt_status current_device(const DeviceInfo** out, Operator op) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return LT_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return LT_ERR_UNSUPPORTED;
@@ -215,7 +230,13 @@ lt_status current_device(const DeviceInfo** out) {
     slot.initialized = true;
   }
   *out = &slot.info;
-  return slot.status;
+  if (slot.status != LT_OK) return slot.status;
+  const int i = static_cast<int>(op);
+  if (!slot.set_up[i]) {
+    slot.operator_status[i] = launch_status(set_up(op, slot.info));
+    slot.set_up[i] = true;
+  }
+  return slot.operator_status[i];
 }
 
 bool make_map_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t bytes,
@@ -324,7 +345,7 @@ LT_API lt_status latent_tail_forward_host(const uint16_t* routed_host, const uin
   if (overlaps(so, span(shared_host, s_bytes)) && !aliases_a_partial(out_host, shared_host, P, T, H))
     return LT_ERR_INVALID_ARG;
   const lt::DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev)) != LT_OK) return st;
+  if ((st = current_device(&dev, lt::Operator::kTail)) != LT_OK) return st;
   void* rd = mapped_host_range(routed_host, r_bytes);
   void* sd = mapped_host_range(shared_host, s_bytes);
   void* od = mapped_host_range(out_host, o_bytes);
@@ -381,7 +402,7 @@ LT_API lt_status latent_tail_norm(const uint16_t* routed, const float* norm_weig
       overlaps(sy, span(norm_weight, norm_weight ? static_cast<size_t>(L) * 4 : 0)))
     return LT_ERR_INVALID_ARG;
   const lt::DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev)) != LT_OK) return st;
+  if ((st = current_device(&dev, lt::Operator::kTail)) != LT_OK) return st;
   const lt::NormArgs na{routed, norm_weight, latent, P, T, L, eps, nullptr, 0, false};
   return launch_status(lt::launch_norm(na, false, *dev, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -402,7 +423,7 @@ LT_API lt_status latent_tail_project_cols(const uint16_t* latent, const uint16_t
       !aliases_a_partial(out, shared, P, T, H))
     return LT_ERR_INVALID_ARG;
   const lt::DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev)) != LT_OK) return st;
+  if ((st = current_device(&dev, lt::Operator::kTail)) != LT_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (T <= lt::kGemvMaxTokens && lt::gemv_supported(T, L, col_start, col_end, *dev)) {
     const lt::GemvArgs ga{nullptr, nullptr, latent, shared, W, out, P, T, L, H,

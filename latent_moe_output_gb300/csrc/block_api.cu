@@ -99,7 +99,7 @@ lt_status expert_matvec4(const uint16_t* x, const uint8_t* packed, const uint16_
                  span(scales, em * (C / G) * 2), span(offsets, static_cast<size_t>(E + 1) * 4)}))
     return LT_ERR_INVALID_ARG;
   const lt::DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev)) != LT_OK) return st;
+  if ((st = current_device(&dev, Operator::kMatvec4)) != LT_OK) return st;
   const Matvec4Args a{x, packed, scales, offsets, out, N, E, M, C, G, ring};
   return launch_status(launch_matvec4(a, *dev, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -133,7 +133,7 @@ lt_status residual_norm(const uint16_t* block, const void* residual, const float
   if (next_out != nullptr && static_cast<const void*>(next_out) == residual)
     return LT_ERR_INVALID_ARG;
   const lt::DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev)) != LT_OK) return st;
+  if ((st = current_device(&dev, Operator::kResidualNorm)) != LT_OK) return st;
   const ResidualNormArgs a{block, residual, post_weight, gate, next_weight, residual_out,
                            next_out, T, H, gate_kind, residual_type == LT_RESIDUAL_FP32,
                            residual_scale, eps, ring};
@@ -159,7 +159,7 @@ lt_status residual_norm_backward(
   const lt::DeviceInfo* dev = nullptr;
   if (T == 0) {
     if ((st = check_optional({grad_post_weight, grad_next_weight, grad_gate})) != LT_OK) return st;
-    if ((st = current_device(&dev)) != LT_OK) return st;
+    if ((st = current_device(&dev, Operator::kResidualNorm)) != LT_OK) return st;
     if ((st = zero(grad_post_weight, h_bytes, s)) != LT_OK) return st;
     if ((st = zero(grad_next_weight, h_bytes, s)) != LT_OK) return st;
     return gate_kind == LT_GATE_CHANNEL ? zero(grad_gate, h_bytes, s) : LT_OK;
@@ -188,7 +188,7 @@ lt_status residual_norm_backward(
                  span(residual_out, r_bytes), span(post_weight, h_bytes), span(gate, g_bytes),
                  span(next_weight, h_bytes)}))
     return LT_ERR_INVALID_ARG;
-  if ((st = current_device(&dev)) != LT_OK) return st;
+  if ((st = current_device(&dev, Operator::kResidualNorm)) != LT_OK) return st;
   const ResidualNormBackwardArgs a{
       grad_residual_out, grad_next, block, residual_out, post_weight, gate, next_weight,
       grad_block, grad_residual, grad_post_weight, grad_gate, grad_next_weight, T, H, gate_kind,
@@ -219,7 +219,7 @@ LT_API lt_status latent_tail_dispatch(const uint16_t* x, const int32_t* expert_i
   if (T == 0) {
     if ((st = check_ptrs({offsets})) != LT_OK) return st;
     const lt::DeviceInfo* dev = nullptr;
-    if ((st = current_device(&dev)) != LT_OK) return st;
+    if ((st = current_device(&dev, Operator::kDispatch)) != LT_OK) return st;
     return zero(offsets, static_cast<size_t>(E + 1) * 4, s);
   }
   if (copy && (st = check_width(L, 16384)) != LT_OK) return st;
@@ -236,7 +236,7 @@ LT_API lt_status latent_tail_dispatch(const uint16_t* x, const int32_t* expert_i
                 {span(x, copy ? static_cast<size_t>(T) * L * 2 : 0), span(expert_ids, n * 4)}))
     return LT_ERR_INVALID_ARG;
   const lt::DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev)) != LT_OK) return st;
+  if ((st = current_device(&dev, Operator::kDispatch)) != LT_OK) return st;
   const DispatchArgs a{x, expert_ids, rows, offsets, order, position, T, K, E, L,
                        static_cast<uint16_t*>(workspace)};
   return launch_status(launch_dispatch(a, *dev, s));

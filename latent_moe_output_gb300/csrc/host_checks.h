@@ -11,8 +11,12 @@
 
 namespace lt {
 
-// Per-device state of the current device; set up on first use.
-lt_status current_device(const DeviceInfo** out);
+// Operators whose kernels have attributes to set on a device before their first launch.
+enum class Operator { kNone, kTail, kDispatch, kMatvec4, kResidualNorm };
+
+// Per-device state of the current device, set up on first use, with the kernels of `op`
+// (those of an operator alone, so that no other pays for them or fails with them).
+lt_status current_device(const DeviceInfo** out, Operator op = Operator::kNone);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -1,6 +1,10 @@
 """Edges of the operators around the tail on the GPU: rows that no expert owns,
 orders of summation, waits that expire."""
 
+import subprocess
+import sys
+from pathlib import Path
+
 import pytest
 import torch
 
@@ -172,3 +176,34 @@ def test_selftest_limits(lib):
     call = lib.latent_tail_selftest_residual_norm_backward_timeout
     assert call(*[0x10000000] * 12, 1, 8, 0, 0, 1.0, EPS, 0x10000000, 64, 0, 0,
                 None) == Status.INVALID_ARG
+
+
+# ----------------------------------------------------------- first calls
+FIRST_CALLS = """
+import torch
+import latent_moe_output_gb300 as lt
+bf16 = lambda *s: torch.ones(*s, dtype=torch.bfloat16, device="cuda")
+x, h, w = bf16(300, 256), bf16(300, 1024), torch.ones(1024, device="cuda")
+ids = (torch.arange(2400, device="cuda").reshape(300, 8) % 5).int()
+packed = torch.full((5, 64, 128), 0x99, dtype=torch.uint8, device="cuda")
+scales = bf16(5, 64, 8)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    d = lt.dispatch(x, ids, 5)
+    e = lt.expert_matvec4(d.rows, packed, scales, d.offsets)
+    c = lt.combine(e, d.position)
+    r, n = lt.residual_norm(h, h, w, w, 1e-6)
+    b = lt.residual_norm_backward(h, h, h, h, w, w, 1e-6)
+graph.replay()
+lt.latent_tail_check()
+assert (c == 8 * 256).all() and (r == 2).all() and ((n - 1).abs() < 1e-2).all()
+assert b[0].isfinite().all()
+"""
+
+
+def test_first_calls_can_be_captured():
+    """A process whose first calls of the operators, with their set-up, are in a capture."""
+    root = Path(__file__).resolve().parents[1]
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True,
+                       text=True)
+    assert r.returncode == 0, r.stderr
