@@ -31,16 +31,17 @@ class _Dispatch(torch.autograd.Function):
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, position, weights):
-        ctx.save_for_backward(rows, position, weights)
+        # Only the gradient of the weights reads the rows.
+        wanted = weights is not None and ctx.needs_input_grad[2]
+        ctx.save_for_backward(rows if wanted else None, position, weights)
         return _block.combine(rows, position, weights)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_out):
         rows, position, weights = ctx.saved_tensors
-        wanted = weights is not None and ctx.needs_input_grad[2]
-        grad_rows, grad_weights = _block.combine_backward(
-            grad_out.contiguous(), rows if wanted else None, position, weights)
+        grad_rows, grad_weights = _block.combine_backward(grad_out.contiguous(), rows, position,
+                                                          weights)
         return grad_rows, None, grad_weights
 
 

@@ -1,7 +1,11 @@
 """Host-side edges of the operators around the tail, on a machine without a GPU too."""
 
-import pytest
+import weakref
 
+import pytest
+import torch
+
+from latent_moe_output_gb300 import autograd as lta
 from latent_moe_output_gb300 import binding
 from latent_moe_output_gb300.binding import Status
 
@@ -28,3 +32,64 @@ def test_residual_out_on_a_vector_that_is_the_residual_too_is_refused(lib, T, H,
     st = lib.latent_tail_residual_norm(BLOCK, RES, p["post"], p["gate"], p["next"], RES, Z, T, H,
                                        2, rt, 1.0, 1e-6, None)
     assert st == Status.INVALID_ARG
+
+
+# ------------------------------------------------- what a backward pass keeps
+@pytest.fixture
+def calls(monkeypatch):
+    """The operators' calls by autograd, answered by torch operations on the CPU."""
+    from latent_moe_output_gb300 import block
+
+    seen = []
+
+    def combine(rows, position, weights=None):
+        seen.append("combine")
+        got = rows[position.long()]
+        return (got if weights is None else got * weights[..., None]).sum(1).to(rows.dtype)
+
+    def combine_backward(grad_out, rows, position, weights=None):
+        seen.append("combine_backward")
+        T, K = position.shape
+        grad_rows = torch.zeros(T * K, grad_out.shape[1], dtype=grad_out.dtype)
+        term = grad_out[:, None].expand(-1, K, -1)
+        grad_rows[position.reshape(-1).long()] = (
+            term if weights is None else term * weights[..., None]).reshape(T * K, -1).to(
+                grad_out.dtype)
+        return grad_rows, None if rows is None else (rows[position.long()] * term).sum(-1).float()
+
+    monkeypatch.setattr(block, "combine", combine)
+    monkeypatch.setattr(block, "combine_backward", combine_backward)
+    return seen
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+def test_combine_without_a_gradient_of_the_weights_lets_go_of_the_rows(calls, weighted):
+    """Only the gradient of the weights reads the rows: without it they may be written after
+    the call, and are not kept alive for the backward pass."""
+    rows = torch.randn(6, 8, dtype=torch.bfloat16)
+    position = torch.arange(6, dtype=torch.int32).reshape(3, 2)
+    weights = torch.full((3, 2), 0.5) if weighted else None
+    leaf = rows.clone().requires_grad_(True)
+    passed = leaf * 1
+    kept = weakref.ref(passed)
+    out = lta.combine_rows(passed, position, weights)
+    with torch.no_grad():
+        passed.mul_(2)
+    del passed
+    assert kept() is None
+    out.float().sum().backward()
+    assert torch.equal(leaf.grad, torch.full_like(rows, 0.5 if weighted else 1.0))
+    assert calls == ["combine", "combine_backward"]
+
+
+def test_combine_with_a_gradient_of_the_weights_keeps_the_rows(calls):
+    rows = torch.randn(6, 8, dtype=torch.bfloat16)
+    position = torch.arange(6, dtype=torch.int32).reshape(3, 2)
+    weights = torch.full((3, 2), 0.5, requires_grad=True)
+    changed = rows.clone()
+    lta.combine_rows(rows, position, weights).float().sum().backward()
+    assert torch.equal(weights.grad, rows[position.long()].sum(-1).float())
+    out = lta.combine_rows(changed, position, weights)
+    changed.mul_(2)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.float().sum().backward()
