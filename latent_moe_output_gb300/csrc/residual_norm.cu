@@ -297,6 +297,61 @@ constexpr size_t backward_ring_smem(int H) {
   return backward_ring_ctas(H) == 1 ? kRingSmem : kRingSmem / backward_ring_ctas(H) - 2048;
 }
 
+// Dynamic shared memory with which `ctas` CTAs of a ring kernel are resident on an SM:
+// 228 KB, of which a CTA also takes its static arrays and 1 KB of the system's.
+constexpr size_t kSmemOfSm = 228 * 1024;
+constexpr size_t kForwardStatic = 640, kBackwardStatic = 2176;
+constexpr size_t resident_smem(int ctas, size_t static_bytes) {
+  return kSmemOfSm / ctas - static_bytes - 1024;
+}
+
+// Stages of the forward ring: two, three while they stay within kForwardRingBytes (T =
+// 8192, H = 7168, channel gate: 75 us with two and 82 with three; H = 4096 47 and 43; T =
+// 4000, H = 10240 54 and 57; H = 9152 50 and 47).
+constexpr int forward_ring_stages(int H, int stage_bytes) {
+  const int ctas = forward_ring_ctas(forward_ring_threads(H));
+  const size_t smem = ctas == 1 ? kRingSmem : kRingSmem / ctas - 2048;
+  const int stages = std::min(3, std::max(2, kForwardRingBytes / ctas / stage_bytes));
+  return static_cast<int>(std::min<size_t>(stages, smem / stage_bytes));
+}
+
+// Stages of the gradient's ring: three where they fit; more only while they leave 24 KB of
+// the SM's shared memory to the L1 cache (T = 8192, H = 7168: 110 us with three stages, 121
+// with four, 154 with two; T = 777, H = 5128, FP32, full gate: 23.1 with three, 26.3 with
+// two); fewer where not all CTAs of the SM would be resident (T = 8192, FP32: H = 1000 30.3
+// us with two, 34.5 with three and a CTA that waits; H = 856, full gate, 30.9 and 35.4).
+constexpr int backward_ring_stages(int width, int stage_bytes) {
+  const size_t smem = backward_ring_smem(width);
+  int stages = static_cast<int>(std::min<size_t>(kRingMaxStages, smem * 25 / 28 / stage_bytes));
+  stages = std::max(stages, static_cast<int>(std::min<size_t>(3, smem / stage_bytes)));
+  return std::min(stages, static_cast<int>(
+                              resident_smem(backward_ring_ctas(width), kBackwardStatic) /
+                              stage_bytes));
+}
+
+// Whether the CTAs that calls of any width launch per SM are all resident: for FP32 (r = 2)
+// and bf16 rows of 1 to 3 (forward) and 2 to 5 arrays.
+constexpr bool rings_resident() {
+  for (int H = kRingMinH; H <= kRingMaxH; H += 8)
+    for (int halves = 2; halves <= 7; ++halves) {  // bytes of a row's arrays / 2 H
+      const int bytes = (halves * 2 * H + 127) / 128 * 128;
+      const int forward = forward_ring_ctas(forward_ring_threads(H));
+      const int backward = backward_ring_ctas(H);
+      if (backward_ring_stages(H, bytes) * bytes >
+          static_cast<int>(resident_smem(backward, kBackwardStatic)))
+        return false;
+      if (halves <= 4)
+        for (int rows = 1; rows <= 2; ++rows) {
+          const int stage = (rows * halves * 2 * H + 127) / 128 * 128;
+          if (forward_ring_stages(H, stage) * stage >
+              static_cast<int>(resident_smem(forward, kForwardStatic)))
+            return false;
+        }
+    }
+  return true;
+}
+static_assert(rings_resident(), "CTAs of a ring kernel that are launched together fit an SM");
+
 // Sums of 1, 2, 4 or 8 values over the CTA, or the cluster of two, with one barrier:
 // halving exchanges leave a lane with a part of one value, one partial per warp goes to
 // shared memory (of both CTAs), and each warp adds the warps' partials again. `red` is
@@ -623,6 +678,7 @@ __global__ void __launch_bounds__(kThreads, forward_ring_ctas(kThreads))
   __shared__ uint64_t full_bar[kRingMaxStages];
   __shared__ __align__(16) float red[2][kRows][32];
   __shared__ int abort_flag;
+  static_assert(sizeof(full_bar) + sizeof(red) + 16 <= kForwardStatic, "resident_smem");
   volatile int* abort_v = &abort_flag;
   const int H = a.H;
   const uint32_t h2 = static_cast<uint32_t>(H) * 2, hr = kF32 ? h2 * 2 : h2;
@@ -779,6 +835,7 @@ __global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(
   __shared__ uint64_t full_bar[kRingMaxStages];
   __shared__ __align__(16) float red[2][8][32];
   __shared__ int abort_flag;
+  static_assert(sizeof(full_bar) + sizeof(red) + 16 <= kBackwardStatic, "resident_smem");
   volatile int* abort_v = &abort_flag;
   static_assert(kCluster == 1 || kThreads <= 512, "half a plane of `red` per CTA");
   const int H = a.H;
@@ -916,13 +973,7 @@ RingPlan ring_plan(const ResidualNormArgs& a, int rows, int num_sms) {
   const int bytes = h2 + (a.residual_f32 ? 2 * h2 : h2) + (a.gate_kind == kGateFull ? h2 : 0);
   r.stage_bytes = (rows * bytes + 127) / 128 * 128;
   r.threads = forward_ring_threads(a.H);
-  // Two stages, three while they stay within kForwardRingBytes (T = 8192, H = 7168,
-  // channel gate: 75 us with two and 82 with three; H = 4096 47 and 43; T = 4000, H =
-  // 10240 54 and 57; H = 9152 50 and 47).
-  const int ctas = forward_ring_ctas(r.threads);
-  const size_t smem = ctas == 1 ? kRingSmem : kRingSmem / ctas - 2048;
-  r.stages = std::min(3, std::max(2, kForwardRingBytes / ctas / r.stage_bytes));
-  r.stages = static_cast<int>(std::min<size_t>(r.stages, smem / r.stage_bytes));
+  r.stages = forward_ring_stages(a.H, r.stage_bytes);
   r.smem = static_cast<size_t>(r.stages) * r.stage_bytes;
   return r;
 }
@@ -938,12 +989,7 @@ RingPlan ring_plan(const ResidualNormBackwardArgs& a) {
                     (a.gate_kind == kGateFull ? h2 : 0);
   r.stage_bytes = (bytes + 127) / 128 * 128;
   r.threads = backward_ring_threads(width);
-  // Three stages where they fit; more only while they leave 24 KB of the SM's shared
-  // memory to the L1 cache (T = 8192, H = 7168: 110 us with three stages, 121 with four,
-  // 154 with two; T = 777, H = 5128, FP32, full gate: 23.1 with three, 26.3 with two).
-  const size_t smem = backward_ring_smem(width);
-  r.stages = static_cast<int>(std::min<size_t>(kRingMaxStages, smem * 25 / 28 / r.stage_bytes));
-  r.stages = std::max(r.stages, static_cast<int>(std::min<size_t>(3, smem / r.stage_bytes)));
+  r.stages = backward_ring_stages(width, r.stage_bytes);
   r.smem = static_cast<size_t>(r.stages) * r.stage_bytes;
   return r;
 }

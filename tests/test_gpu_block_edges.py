@@ -13,7 +13,7 @@ from latent_moe_output_gb300.binding import LatentTailError, Status, latent_tail
 
 import block_reference as br
 import gpu_helpers as gh
-from test_gpu_block import EPS, gen, norm_case, randn, weights4
+from test_gpu_block import EPS, check_backward, gen, norm_case, randn, weights4
 
 pytestmark = pytest.mark.gpu
 
@@ -207,3 +207,10 @@ def test_first_calls_can_be_captured():
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True,
                        text=True)
     assert r.returncode == 0, r.stderr
+
+
+# -------------------------------------- widths whose ring had no room for its CTAs
+@pytest.mark.parametrize("T,H,gate", [(2000, 1000, "none"), (2000, 856, "full"),
+                                      (1000, 1000, "channel"), (913, 856, "full")])
+def test_residual_norm_backward_with_six_ctas_per_sm(T, H, gate):
+    check_backward(norm_case(T, H, gate, "fp32", seed=T + H), seed=H)
