@@ -34,6 +34,14 @@ def test_residual_out_on_a_vector_that_is_the_residual_too_is_refused(lib, T, H,
     assert st == Status.INVALID_ARG
 
 
+# ------------------------------------------------ partial sums of the gradient
+@pytest.mark.parametrize("H,per_sm", [(256, 2), (264, 1), (512, 1), (520, 6), (1024, 6), (7168, 1)])
+def test_residual_norm_backward_has_a_partial_row_per_resident_cta(lib, H, per_sm):
+    """... of the SMs that a size computed without a device allows for (304)."""
+    got = lib.latent_tail_residual_norm_backward_workspace_size(1 << 20, H)
+    assert got == 2 * 304 * per_sm * H * 4
+
+
 # ------------------------------------------------- what a backward pass keeps
 @pytest.fixture
 def calls(monkeypatch):
