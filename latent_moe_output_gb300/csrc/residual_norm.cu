@@ -315,6 +315,29 @@ constexpr int forward_ring_stages(int H, int stage_bytes) {
   return static_cast<int>(std::min<size_t>(stages, smem / stage_bytes));
 }
 
+// Bytes of `rows` token rows in the forward ring: two bytes per element and `halves`
+// (block 1, residual 1 or 2, a gate per element 1).
+constexpr int forward_stage_bytes(int H, int halves, int rows) {
+  return (rows * halves * 2 * H + 127) / 128 * 128;
+}
+// Token rows that the forward ring takes at a time: two, where two stages of them fit.
+constexpr int forward_ring_rows(int H, int halves) {
+  return H <= kRingMaxH && forward_ring_stages(H, forward_stage_bytes(H, halves, 2)) >= 2 ? 2 : 1;
+}
+// Up to kRingMaxH only FP32 rows with a gate per element are taken singly, and those in
+// CTAs of two sizes: no kernel is built for others.
+constexpr bool single_rows_as_built() {
+  for (int H = kForwardRingMinH; H <= kRingMaxH; H += 8)
+    for (int halves = 2; halves <= 4; ++halves) {
+      const int threads = forward_ring_threads(H);
+      if (forward_ring_rows(H, halves) == 1 &&
+          (halves != 4 || !((threads > 288 && threads <= 448) || threads > 896)))
+        return false;
+    }
+  return true;
+}
+static_assert(single_rows_as_built(), "forward_ring_kernel lacks a kernel");
+
 // Stages of the gradient's ring: three where they fit; more only while they leave 24 KB of
 // the SM's shared memory to the L1 cache (T = 8192, H = 7168: 110 us with three stages, 121
 // with four, 154 with two; T = 777, H = 5128, FP32, full gate: 23.1 with three, 26.3 with
@@ -342,7 +365,7 @@ constexpr bool rings_resident() {
         return false;
       if (halves <= 4)
         for (int rows = 1; rows <= 2; ++rows) {
-          const int stage = (rows * halves * 2 * H + 127) / 128 * 128;
+          const int stage = forward_stage_bytes(H, halves, rows);
           if (forward_ring_stages(H, stage) * stage >
               static_cast<int>(resident_smem(forward, kForwardStatic)))
             return false;
@@ -963,17 +986,17 @@ __global__ void __launch_bounds__(kThreads, kPieces == 2 ? 1 : ring_ctas_per_sm(
 }
 
 struct RingPlan {
-  int stages = 0, stage_bytes = 0, threads = 0;
+  int stages = 0, stage_bytes = 0, threads = 0, rows = 1;
   size_t smem = 0;
 };
 
 // The forward ring; stages == 0 when the direct kernel takes the call.
-RingPlan ring_plan(const ResidualNormArgs& a, int rows, int num_sms) {
+RingPlan ring_plan(const ResidualNormArgs& a, int num_sms) {
   RingPlan r;
   if (a.H < kForwardRingMinH || (a.H <= kRingMaxH && a.T < kRingMinRowsPerSm * num_sms)) return r;
-  const int h2 = a.H * 2;
-  const int bytes = h2 + (a.residual_f32 ? 2 * h2 : h2) + (a.gate_kind == kGateFull ? h2 : 0);
-  r.stage_bytes = (rows * bytes + 127) / 128 * 128;
+  const int halves = 1 + (a.residual_f32 ? 2 : 1) + (a.gate_kind == kGateFull ? 1 : 0);
+  r.rows = forward_ring_rows(a.H, halves);
+  r.stage_bytes = forward_stage_bytes(a.H, halves, r.rows);
   r.threads = forward_ring_threads(a.H);
   r.stages = forward_ring_stages(a.H, r.stage_bytes);
   r.smem = static_cast<size_t>(r.stages) * r.stage_bytes;
@@ -1111,8 +1134,9 @@ ForwardRingKernel forward_ring_kernel(int threads, bool f32) {
 
 ForwardRingKernel forward_ring_kernel(int H, int rows, int threads, bool f32) {
   if (H > kRingMaxH) return forward_ring_kernel<1, 2>(threads, f32);
-  return rows == 2 ? forward_ring_kernel<2, 1>(threads, f32)
-                   : forward_ring_kernel<1, 1>(threads, f32);
+  if (rows == 2) return forward_ring_kernel<2, 1>(threads, f32);
+  return threads <= 448 ? residual_norm_ring_kernel<true, 448, 1, 1>  // (single_rows_as_built)
+                        : residual_norm_ring_kernel<true, 1024, 1, 1>;
 }
 
 template <bool kF32>
@@ -1167,12 +1191,10 @@ cudaError_t setup_residual_norm(const DeviceInfo&) {
 
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, const DeviceInfo& dev,
                                  cudaStream_t stream) {
-  int rows = a.H <= kRingMaxH ? 2 : 1;
-  RingPlan ring = ring_plan(a, rows, dev.num_sms);
-  if (ring.stages == 1 && rows == 2) ring = ring_plan(a, rows = 1, dev.num_sms);
+  const RingPlan ring = ring_plan(a, dev.num_sms);
   if (ring.stages != 0)
-    return launch_dependent(forward_ring_kernel(a.H, rows, ring.threads, a.residual_f32),
-                            dim3(std::min((a.T + rows - 1) / rows,
+    return launch_dependent(forward_ring_kernel(a.H, ring.rows, ring.threads, a.residual_f32),
+                            dim3(std::min((a.T + ring.rows - 1) / ring.rows,
                                           dev.num_sms * forward_ring_ctas(ring.threads))),
                             dim3(ring.threads), ring.smem, stream, a, ring.stages,
                             ring.stage_bytes, dev.err_word);
