@@ -49,10 +49,11 @@ constexpr int kConsumers = 8;  // warps
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kBoxCols = 256;  // columns per box: 128 bytes of weights
 constexpr int kMaxStages = 8;
+constexpr int kM = 2;  // fragments of 16 weight rows per warp
 constexpr int kSmemPerSm = 204 * 1024;  // dynamic, without the experts' table
 constexpr int table_bytes(int E) { return (E + 1) * 2 * static_cast<int>(sizeof(int)); }
 
-template <int kSplit, int kTiles, int kM>
+template <int kSplit, int kTiles>
 struct Config {
   // With one box per stage a warp takes all of its columns, else half of one box's.
   static constexpr int kHalves = kSplit == 1 ? 1 : 2;
@@ -153,12 +154,12 @@ __device__ __forceinline__ Tile tile_at(int64_t tile, int mblocks, int rows_per_
   return t;
 }
 
-template <int kGroup, int kSplit, int kTiles, int kM>
-__global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles, kM>::kCtasPerSm)
+template <int kGroup, int kSplit, int kTiles>
+__global__ void __launch_bounds__(kThreads, Config<kSplit, kTiles>::kCtasPerSm)
     matvec4_kernel(const __grid_constant__ CUtensorMap w_map,
                    const __grid_constant__ CUtensorMap x_map,
                    const __grid_constant__ CUtensorMap s_map, const Params p) {
-  using Cfg = Config<kSplit, kTiles, kM>;
+  using Cfg = Config<kSplit, kTiles>;
   constexpr int kPass = 8 * kTiles;
   constexpr int kScales = kBoxCols / kGroup;  // per row and box
   extern __shared__ uint8_t smem_raw[];
@@ -507,10 +508,10 @@ struct Variant {
   int rows, ctas_per_sm, piece_bytes;
 };
 
-template <int kGroup, int kSplit, int kTiles, int kM = 2>
+template <int kGroup, int kSplit, int kTiles>
 Variant variant() {
-  using Cfg = Config<kSplit, kTiles, kM>;
-  return Variant{matvec4_kernel<kGroup, kSplit, kTiles, kM>, Cfg::kSmem, Cfg::kRows,
+  using Cfg = Config<kSplit, kTiles>;
+  return Variant{matvec4_kernel<kGroup, kSplit, kTiles>, Cfg::kSmem, Cfg::kRows,
                  Cfg::kCtasPerSm, Cfg::kPieceBytes};
 }
 
