@@ -214,3 +214,20 @@ def test_first_calls_can_be_captured():
                                       (1000, 1000, "channel"), (913, 856, "full")])
 def test_residual_norm_backward_with_six_ctas_per_sm(T, H, gate):
     check_backward(norm_case(T, H, gate, "fp32", seed=T + H), seed=H)
+
+
+# ------------------------------------------------------ orders of summation
+@pytest.mark.parametrize("N", [1, 8, 40, 64, 130])
+def test_matvec4_of_several_experts_across_tile_choices(N):
+    """With several experts the number of rows decides into how many column parts a sum is
+    cut, and so its order: the same row may differ in its last bits between calls of other
+    lengths, within the bound of any order. One call gives the same bits every time."""
+    E, M, C, G = 64, 2048, 1056, 32
+    g = gen(5)
+    packed, scales = weights4(E, M, C, G, g)
+    x = randn(130, C, g=g)[:N].contiguous()
+    offsets = (torch.arange(E + 1, device="cuda") * 3).clamp(max=N).to(torch.int32)
+    out = lt.expert_matvec4(x, packed, scales, offsets)
+    ref, mag = br.matvec4(x, packed, scales, offsets)
+    br.assert_within(out, ref, br.bf16_bound(ref, (C + 2) * br.U32 * mag))
+    assert torch.equal(out, lt.expert_matvec4(x, packed, scales, offsets))
