@@ -13,6 +13,13 @@ from torch.autograd.function import once_differentiable
 from . import block as _block
 
 
+def _dense(grad):
+    """A gradient as the operators take it. Autograd may pass a strided one, or a contiguous
+    view whose address is not a multiple of 16."""
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+
+
 class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, expert_ids, E):
@@ -25,7 +32,7 @@ class _Dispatch(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_rows, *_):
         (position,) = ctx.saved_tensors
-        return _block.combine(grad_rows.contiguous(), position), None, None
+        return _block.combine(_dense(grad_rows), position), None, None
 
 
 class _Combine(torch.autograd.Function):
@@ -40,8 +47,7 @@ class _Combine(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_out):
         rows, position, weights = ctx.saved_tensors
-        grad_rows, grad_weights = _block.combine_backward(grad_out.contiguous(), rows, position,
-                                                          weights)
+        grad_rows, grad_weights = _block.combine_backward(_dense(grad_out), rows, position, weights)
         return grad_rows, None, grad_weights
 
 
@@ -62,9 +68,9 @@ class _ResidualNorm(torch.autograd.Function):
         if grad_out is None and grad_next is None:
             return (None,) * 7
         if next_weight is not None:  # the next norm's output may have gone unused
-            grad_next = torch.zeros_like(block) if grad_next is None else grad_next.contiguous()
+            grad_next = torch.zeros_like(block) if grad_next is None else _dense(grad_next)
         if grad_out is not None:
-            grad_out = grad_out.contiguous()
+            grad_out = _dense(grad_out)
         g = _block.residual_norm_backward(grad_out, grad_next, block, out, post_weight,
                                           next_weight, ctx.eps, gate=gate,
                                           residual_scale=ctx.scale)

@@ -101,3 +101,53 @@ def test_combine_with_a_gradient_of_the_weights_keeps_the_rows(calls):
     changed.mul_(2)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         out.float().sum().backward()
+
+
+def test_gradients_at_any_offset_are_taken(calls, monkeypatch):
+    """Autograd may pass a contiguous view that is not 16-byte aligned, e.g. of the gradient
+    of flat tensors joined in one; the operators take aligned addresses alone."""
+    from latent_moe_output_gb300 import block
+
+    seen = []
+
+    def aligned(call):
+        def checked(*args, **kwargs):
+            for t in args:
+                if isinstance(t, torch.Tensor):
+                    assert t.is_contiguous() and t.data_ptr() % 16 == 0
+                    seen.append(t)
+            return call(*args, **kwargs)
+        return checked
+
+    def norm(b, r, post, nxt, eps, gate=None, residual_scale=1.0):
+        return b + r, (b + r) * 2
+
+    def norm_backward(dv, dz, b, out, post, nxt, eps, gate=None, residual_scale=1.0):
+        g = dv + 2 * dz
+        return g, g, None, None, torch.zeros_like(nxt)
+
+    def dispatch(x, ids, E):
+        n = ids.numel()
+        at = torch.arange(n, dtype=torch.int32)
+        return block.Dispatched(x.repeat_interleave(ids.shape[1], 0), at[:E], at,
+                                at.reshape(ids.shape))
+
+    monkeypatch.setattr(block, "combine_backward", aligned(block.combine_backward))
+    monkeypatch.setattr(block, "combine", aligned(block.combine))
+    monkeypatch.setattr(block, "residual_norm", norm)
+    monkeypatch.setattr(block, "residual_norm_backward", aligned(norm_backward))
+    monkeypatch.setattr(block, "dispatch", dispatch)
+
+    def flat(*tensors):  # a loss on one flat tensor with three values before the others
+        start = torch.zeros(3, dtype=torch.bfloat16)
+        joined = torch.cat([start] + [t.reshape(-1) for t in tensors])
+        return (joined * joined.detach()).float().sum()
+
+    new = lambda *s: torch.randn(*s, dtype=torch.bfloat16).requires_grad_(True)  # noqa: E731
+    rows, x, b = new(6, 8), new(3, 8), new(2, 8)
+    position = torch.arange(6, dtype=torch.int32).reshape(3, 2)
+    flat(lta.combine_rows(rows, position)).backward()
+    flat(lta.dispatch_rows(x, position, 4).rows).backward()
+    flat(*lta.residual_norm(b, torch.zeros(2, 8, dtype=torch.bfloat16), None, torch.ones(8),
+                            1e-6)).backward()
+    assert len(seen) >= 8 and all(t.grad is not None for t in (rows, x, b))

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import latent_moe_output_gb300 as lt
+from latent_moe_output_gb300 import autograd as lta
 from latent_moe_output_gb300.binding import LatentTailError, Status, latent_tail_check
 
 import block_reference as br
@@ -182,6 +183,7 @@ def test_selftest_limits(lib):
 FIRST_CALLS = """
 import torch
 import latent_moe_output_gb300 as lt
+from latent_moe_output_gb300 import autograd as lta
 bf16 = lambda *s: torch.ones(*s, dtype=torch.bfloat16, device="cuda")
 x, h, w = bf16(300, 256), bf16(300, 1024), torch.ones(1024, device="cuda")
 ids = (torch.arange(2400, device="cuda").reshape(300, 8) % 5).int()
@@ -231,3 +233,12 @@ def test_matvec4_of_several_experts_across_tile_choices(N):
     ref, mag = br.matvec4(x, packed, scales, offsets)
     br.assert_within(out, ref, br.bf16_bound(ref, (C + 2) * br.U32 * mag))
     assert torch.equal(out, lt.expert_matvec4(x, packed, scales, offsets))
+
+
+def test_autograd_takes_gradients_at_any_offset():
+    rows = randn(6, 8, g=gen(5)).requires_grad_(True)
+    position = torch.arange(6, dtype=torch.int32, device="cuda").reshape(3, 2)
+    joined = torch.cat([rows.new_zeros(3), lta.combine_rows(rows, position).reshape(-1)])
+    (joined * joined.detach()).float().sum().backward()
+    out = rows.detach().float().reshape(3, 2, 8).sum(1).to(torch.bfloat16)
+    assert torch.equal(rows.grad, out.repeat_interleave(2, 0))
