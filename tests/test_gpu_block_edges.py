@@ -235,6 +235,38 @@ def test_matvec4_of_several_experts_across_tile_choices(N):
     assert torch.equal(out, lt.expert_matvec4(x, packed, scales, offsets))
 
 
+# ----------------------------------------------------------- other streams
+def test_every_operator_on_another_stream():
+    """The outputs that a call allocates belong to the stream it is given."""
+    g = gen(3)
+    T, K, E, L, H = 600, 4, 9, 264, 1448
+    c = norm_case(T, H, "channel", "bf16", seed=4)
+    packed, scales = weights4(E, 72, 256, 64, g)
+    x, x4, ids = randn(T, L, g=g), randn(T, 256, g=g), torch.randint(
+        -1, E, (T, K), generator=g, device="cuda", dtype=torch.int32)
+    w, go = torch.rand(T, K, generator=g, device="cuda"), randn(T, L, g=g)
+
+    def calls(**on):
+        d = lt.dispatch(x, ids, E, **on)
+        e = lt.expert_matvec4(lt.dispatch(x4, ids, E, **on).rows, packed, scales, d.offsets, **on)
+        out = lt.combine(d.rows, d.position, w, **on)
+        back = lt.combine_backward(go, d.rows, d.position, w, **on)
+        norm = lt.residual_norm(c["block"], c["residual"], c["post"], c["nxt"], EPS,
+                                gate=c["gate"], **on)
+        grads = lt.residual_norm_backward(norm[0], norm[1], c["block"], norm[0], c["post"],
+                                          c["nxt"], EPS, gate=c["gate"], **on)
+        return [*d, e, out, *back, *norm, *grads]
+
+    want = calls()
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        got = calls(stream=stream)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    latent_tail_check()
+
+
 def test_autograd_takes_gradients_at_any_offset():
     rows = randn(6, 8, g=gen(5)).requires_grad_(True)
     position = torch.arange(6, dtype=torch.int32, device="cuda").reshape(3, 2)
