@@ -62,6 +62,15 @@ def _ptr(t, name, dtype, shape, index):
     raise ValueError(f"{name} must be contiguous")
 
 
+_INT_MAX = 2 ** 31 - 1  # ctypes cuts larger sizes off without a word
+
+
+def _size(n, name) -> int:
+    if n > _INT_MAX:
+        raise ValueError(f"{name}: sizes are at most {_INT_MAX}, got {n}")
+    return n
+
+
 def _shape(t, name, ndim):
     """Shape of a tensor that fixes a call's sizes."""
     if not isinstance(t, torch.Tensor):
@@ -69,6 +78,9 @@ def _shape(t, name, ndim):
     shape = t.shape
     if len(shape) != ndim:
         raise ValueError(f"{name}: expected {ndim} dimensions, got {len(shape)}")
+    for n in shape:
+        if n > _INT_MAX:
+            _size(n, name)
     return shape
 
 
@@ -120,6 +132,7 @@ def dispatch(x, expert_ids, E: int, rows=None, offsets=None, order=None, positio
     choice without an expert) by expert and copy the rows of ``x`` [T, L] to their
     places. ``x`` None sorts alone. See latent_tail_dispatch."""
     T, K = _shape(expert_ids, "expert_ids", 2)
+    _size(E, "E")
     i = _index(expert_ids, "expert_ids")
     L = 0
     if x is not None:
