@@ -3,9 +3,10 @@
     tokens -> dispatch -> experts (expert_matvec4) -> combine -> routed partial
            -> forward (the tail) -> residual_norm -> the next block
 
-Argument marshalling only, as in ``binding``: shapes are read from the tensors,
-every output can be passed in (a decode loop keeps its buffers) and is allocated
-with torch when it is not; a non-OK status raises ``LatentTailError``. Calls are
+Argument marshalling only, as in ``binding``: shapes are read from the tensors;
+outputs can be passed in (a decode loop keeps its buffers) and are allocated with
+torch when they are not, but for ``residual_norm_backward``, which allocates its
+gradients always; a non-OK status raises ``LatentTailError``. Calls are
 asynchronous on ``stream`` (default: torch's current stream). Tensors allocated
 here belong to that stream; a tensor of another stream must be kept alive and
 ordered by the caller, as for any torch operation.
@@ -201,8 +202,8 @@ def combine_backward(grad_out, rows, position, weights=None, grad_rows=None, gra
 
 def expert_matvec4(x, packed, scales, offsets=None, out=None, stream=None):
     """out[r, m] = sum_c x[r, c] * (q[e, m, c] - 8) * scales[e, m, c // G] for the rows
-    r of expert e (``offsets`` of ``dispatch``, or a slice of them; None with one matrix:
-    every row); zeros for rows that no expert owns.
+    r of expert e (``offsets`` of ``dispatch``, or of some of its experts, at a 16-byte
+    aligned address; None with one matrix: every row); zeros for rows that no expert owns.
 
     x [N, C] bf16, packed [E, M, C/2] uint8 (even c in the low four bits), scales
     [E, M, C/G] bf16 with G = 32, 64 or 128. See latent_tail_expert_matvec4 and
@@ -297,7 +298,8 @@ def residual_norm_backward(grad_residual_out, grad_next, block, residual_out, po
                            workspace=None, stream=None):
     """(grad_block, grad_residual, grad_post_weight, grad_gate, grad_next_weight) of
     ``residual_norm`` (None for what was not given), from the gradients of its outputs
-    (either may be None) and its stored residual_out. See
+    and its stored residual_out. grad_residual_out may be None (zero) where grad_next is
+    given; grad_next is given exactly when next_weight is. See
     latent_tail_residual_norm_backward."""
     T, H = _shape(block, "block", 2)
     i = _index(block, "block")

@@ -80,7 +80,9 @@ __global__ void __launch_bounds__(kForwardThreads)
 // Gradient: 16-byte pieces per thread in flight. With few choices per token one piece
 // leaves the memory idle (us with one row of eight slots used by K, and with two pieces
 // of K rows rounded up to 2 or 4: T = 16384, K = 1, L = 512 21.6 and 10.1; T = 2048, K = 2,
-// L = 4096 20.6 and 14.4; T = 8192, K = 3, L = 1448 42.9 and 31.0; four pieces spill).
+// L = 4096 20.6 and 14.4; T = 8192, K = 3, L = 1448 42.9 and 31.0). Within the 64
+// registers of four CTAs per SM the kernels of four slots spill 52-92 bytes, those of
+// eight 24-44; four pieces per thread spill 184 to 508.
 constexpr int pieces_ahead(int rows_ahead) { return rows_ahead == 8 ? 1 : 2; }
 
 // A group of kTpt threads per token; each thread owns every kTpt-th 16-byte piece of

@@ -5,10 +5,10 @@
 //            = sum_groups s[e,m,g] * ( sum_{c in g} x[r,c] * (q[e,m,c] - 8) )
 //
 // With the few rows per expert of a decode step the weights are read once and
-// used at most a few times, so their stream bounds the call, and right after it the
+// used at most a few times, so their stream bounds the call, and near it the
 // instructions that unpack them: at the measured copy rate an SM receives 41 weights
 // per clock at G = 32, has 128 instruction lanes per clock, and spends about two
-// instructions per weight.
+// instructions per weight (64 % of the lanes).
 // A 4-bit value masked out at bit 0 or 4 of a bf16 pattern is that integer times
 // 2^-133 (subnormals and the first binade are one linear range), so one masking and
 // one exact bf16 fused multiply-add per two weights give (q - 8) / 64: five logic
@@ -35,8 +35,11 @@
 // with 8 of 256 experts of 2048 x 2048, G = 32 (about 103 experts read, 240 MB):
 // 50 us = 4.8 TB/s, 71 % of the measured copy rate; 64 tokens: 94 us, 5.6 TB/s. The
 // stream alone, without the arithmetic, takes 40 and 81 us; per stage a warp issues for
-// 2500 cycles, waits for 700 and spends 250 between tiles. One token with one matrix
-// of 7168 x 2048, G = 128: 5.4 us (latency: 2 stages per tile).
+// 2500 cycles, waits for 700 and spends 250 between tiles. Which of them is the limit is
+// not known: 60 % of the issue slots are used, 26 % of the tensor pipe, 71 % of the copy
+// rate. One token with one matrix of 7168 x 2048, G = 128: 5.5 us, of which the weights'
+// bytes are 1.1: the weights are first asked for after the wait for the kernel before and
+// the experts' table, and a tile has two stages.
 #include "block_launch.h"
 #include "rows.cuh"
 

@@ -12,7 +12,7 @@
 //   dgp = sum_t d * gate * yh,  dgn = sum_t dz * vh
 //
 // Every element is read once and written once, so memory bounds both. Measured at
-// T = 8192, H = 7168, bf16 (GB300, calls back to back): forward 71 us = 6.6 TB/s, 97 % of
+// T = 8192, H = 7168, bf16 (GB300, calls back to back): forward 72 us = 6.6 TB/s, 97 % of
 // the measured copy rate; gradient 110 us = 6.4 TB/s, 94 %. One row alone: 3.6 us.
 #include "block_launch.h"
 #include "rows.cuh"
@@ -251,7 +251,7 @@ constexpr int kRingMaxStages = 6;
 // the direct kernel; T = 200: 4.1 and 4.6; T = 100, H = 8192: 4.8 and 4.4). Wider rows
 // always take the ring (T = 100, H = 9152: 3.5 us, 5.1 with a direct kernel; T = 1, H =
 // 16384: 4.8 and 5.9), with a single stage if two do not fit (T = 1700, H = 16384, FP32,
-// full gate: 80 and 86).
+// full gate: 82 and 86).
 constexpr int kRingMinRowsPerSm = 1;
 constexpr size_t kRingSmem = 224 * 1024;  // one CTA per SM
 // Narrower rows take a warp each (T = 8192, us direct and ring: H = 512 7.9 and 9.9, 520
