@@ -462,6 +462,129 @@ LT_API lt_status latent_tail_selftest_residual_norm_backward_timeout(
     void* workspace, size_t workspace_bytes, int copied_rows, unsigned int limit_us,
     lt_stream stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The experts in bf16, for prefill and training, with their gradients. Rows are
+ * sorted by expert as latent_tail_dispatch writes them:
+ *
+ *   latent_tail_dispatch -> latent_tail_expert_gated -> latent_tail_expert_matmul
+ *     -> latent_tail_combine
+ *
+ * and with one matrix (E == 1, offsets NULL) the same calls are a dense block, such
+ * as the shared expert. In all of them
+ *   offsets [E+1] int32 (rows of expert e: offsets[e] .. offsets[e+1]-1) or NULL with
+ *   E == 1 (every row). Offsets are cut to [0, N] and to their running maximum; rows
+ *   that no expert owns give zeros, and experts without rows zero gradients.
+ * Sums are FP32 on the tensor cores, results are rounded once to bf16; the order of a
+ * sum does not depend on the other rows of the call, so a row's result is the same in
+ * every call with the same sizes of matrices.
+ * Limits: 0 <= N <= 2^24, 1 <= E <= 1024, C, M and 2F multiples of 8 from 8 to 65536
+ * (F a multiple of 8).
+ * With N == 0 the gradients of weights are zeros.
+ */
+
+/* The activation a of a gated block. */
+typedef enum lt_activation {
+  LT_ACTIVATION_SILU = 0, /* g * sigmoid(g) */
+  LT_ACTIVATION_GELU = 1  /* the tanh form: g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+} lt_activation;
+
+/* How the projections of a gated block are kept for its backward pass. */
+typedef enum lt_saved {
+  LT_SAVED_NONE = 0, /* not kept */
+  LT_SAVED_BF16 = 1, /* saved [N, 2, F] bf16: gate, then up, of each row */
+  LT_SAVED_8BIT = 2  /* saved [N, 2, F] int8 with exponents [N, 2, ceil(F/16)], as
+                        latent_tail_quantize8 writes them for 2N rows of F columns */
+} lt_saved;
+
+/*
+ * Both projections of a gated feed-forward block, its activation and the product in one
+ * kernel: for row r of expert e
+ *   g = sum_c x[r,c] weights[e,f,c],  u = sum_c x[r,c] weights[e,F+f,c]
+ *   hidden[r,f] = bf16_rn(a(g) * u)
+ * and, where saved is given, g and u as saved_kind says (rounded from FP32).
+ *   x [N, C] bf16, weights [E, 2F, C] bf16; hidden [N, F] bf16, saved and
+ *   saved_exponents outputs by saved_kind (NULL where it has none).
+ */
+LT_API lt_status latent_tail_expert_gated(const uint16_t* x, const uint16_t* weights,
+                                          const int32_t* offsets, uint16_t* hidden, void* saved,
+                                          uint8_t* saved_exponents, int N, int E, int F, int C,
+                                          lt_activation activation, lt_saved saved_kind,
+                                          lt_stream stream);
+
+/*
+ * Bytes of device workspace latent_tail_expert_gated_backward needs: the gradient at both
+ * projections, [N, 2F] bf16. Returns 0 for N <= 0 or invalid shapes. Host-only.
+ */
+LT_API size_t latent_tail_expert_gated_backward_workspace_size(int N, int F);
+
+/*
+ * Gradient of latent_tail_expert_gated, from the projections g and u that it kept
+ * (saved_kind bf16 or 8 bits):
+ *   dg = grad_hidden * u * a'(g), du = grad_hidden * a(g)   (rounded to bf16: operands
+ *                                                             of the tensor cores)
+ *   grad_x[r,c]          = sum_f dg[r,f] weights[e,f,c] + du[r,f] weights[e,F+f,c]
+ *   grad_weights[e,f,c]  = sum over e's rows of dg[r,f] x[r,c], likewise F+f with du
+ *   hidden[r,f]          = bf16_rn(a(g) * u) once more, for the gradient of the product
+ *                          behind the block
+ *   Each output may be NULL (not wanted), not all three; weights is read for grad_x
+ *   alone, x for grad_weights alone, grad_hidden and the workspace for these two, and
+ *   each may be NULL where it is not read.
+ */
+LT_API lt_status latent_tail_expert_gated_backward(
+    const uint16_t* grad_hidden, const uint16_t* x, const uint16_t* weights, const void* saved,
+    const uint8_t* saved_exponents, const int32_t* offsets, uint16_t* grad_x,
+    uint16_t* grad_weights, uint16_t* hidden, int N, int E, int F, int C,
+    lt_activation activation, lt_saved saved_kind, void* workspace, size_t workspace_bytes,
+    lt_stream stream);
+
+/*
+ * Products of expert-sorted rows with bf16 weights: out[r,m] = sum_c x[r,c] weights[e,m,c]
+ * for row r of expert e.
+ *   x [N, C], weights [E, M, C], out [N, M], all bf16.
+ */
+LT_API lt_status latent_tail_expert_matmul(const uint16_t* x, const uint16_t* weights,
+                                           const int32_t* offsets, uint16_t* out, int N, int E,
+                                           int M, int C, lt_stream stream);
+
+/*
+ * Gradient of latent_tail_expert_matmul:
+ *   grad_x[r,c]         = sum_m grad_out[r,m] weights[e,m,c]
+ *   grad_weights[e,m,c] = sum over e's rows of grad_out[r,m] x[r,c]
+ *   Each output may be NULL (not wanted), not both; weights is read for grad_x alone, x
+ *   for grad_weights alone, and each may be NULL where it is not read.
+ */
+LT_API lt_status latent_tail_expert_matmul_backward(const uint16_t* grad_out, const uint16_t* x,
+                                                    const uint16_t* weights,
+                                                    const int32_t* offsets, uint16_t* grad_x,
+                                                    uint16_t* grad_weights, int N, int E, int M,
+                                                    int C, lt_stream stream);
+
+/*
+ * Activations in 8 bits: per row and 16 columns (fewer behind the last multiple of 16) a
+ * power of two 2^(e-127), e >= 1 the least for which the largest magnitude rounds to at
+ * most 127 of it, and the values' integers:
+ *   values[t,c]    = round(x[t,c] / 2^(e-127))      (to nearest even)
+ *   exponents[t,g] = e, 0 for a group of zeros, 255 for one that holds an infinity or a
+ *                    NaN (its values are 0)
+ * so that a value is off by at most 1/127 of its group's largest magnitude (half a unit;
+ * the largest magnitude is at least 63.5 units). Groups below 2^-126 * 63.5 round to that
+ * power of two.
+ *   x [T, C] bf16; values [T, C], exponents [T, ceil(C/16)].
+ * Limits: 0 <= T <= 2^24, C a multiple of 8 from 8 to 65536.
+ */
+LT_API lt_status latent_tail_quantize8(const uint16_t* x, int8_t* values, uint8_t* exponents,
+                                       int T, int C, lt_stream stream);
+
+/*
+ * out[t,c] = values[t,c] * 2^(exponents[t,g]-127) in bf16, which holds it exactly (values
+ * of -128, which latent_tail_quantize8 does not write, too); zeros for exponent 0 and NaNs
+ * for 255. Products past bf16's range, which latent_tail_quantize8 does not write either,
+ * give infinities.
+ */
+LT_API lt_status latent_tail_dequantize8(const int8_t* values, const uint8_t* exponents,
+                                         uint16_t* out, int T, int C, lt_stream stream);
+
 /* Static, human-readable name of a status code. Never NULL. */
 LT_API const char* latent_tail_status_string(lt_status status);
 

@@ -6,7 +6,8 @@
 The computation runs in the CUDA library built from ``csrc/`` and exposed
 through the C ABI in ``include/latent_tail.h``; ``binding`` is the thin ctypes
 layer over it, and ``block`` the same for the operators around the tail (expert
-dispatch and combine, 4-bit expert products, fused residual norms). Importing this package does not load the library; the first
+dispatch and combine, 4-bit expert products, fused residual norms) and ``experts`` for
+the bf16 experts with their gradients and for activations in 8 bits. Importing this package does not load the library; the first
 call does, and fails loudly if it was not built.
 """
 
@@ -38,4 +39,14 @@ from .block import (  # noqa: F401
     residual_norm,
     residual_norm_backward,
     residual_norm_backward_workspace_size,
+)
+from .experts import (  # noqa: F401
+    Checkpoint8,
+    dequantize8,
+    expert_gated,
+    expert_gated_backward,
+    expert_gated_backward_workspace_size,
+    expert_matmul,
+    expert_matmul_backward,
+    quantize8,
 )

@@ -28,7 +28,7 @@ __device__ uint32_t g_error_word;
 
 constexpr int kMaxDevices = 64;
 
-constexpr int kOperators = static_cast<int>(lt::Operator::kResidualNorm) + 1;
+constexpr int kOperators = static_cast<int>(lt::Operator::kExperts) + 1;
 
 struct DeviceSlot {
   bool initialized = false;
@@ -98,6 +98,7 @@ cudaError_t set_up(lt::Operator op, const lt::DeviceInfo& d) {
     case lt::Operator::kDispatch: return lt::setup_dispatch(d);
     case lt::Operator::kMatvec4: return lt::setup_matvec4(d);
     case lt::Operator::kResidualNorm: return lt::setup_residual_norm(d);
+    case lt::Operator::kExperts: return lt::setup_experts(d);
   }
   return e;
 }
@@ -265,6 +266,25 @@ bool make_map_bf16_rows64(CUtensorMap* map, const void* base, uint64_t rows, uin
       g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
                box, estrides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool make_map_bf16_nd(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box) {
+  if (g_encode == nullptr || rank < 2 || rank > 5) return false;
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5], e[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    e[i] = 1;
+    if (i > 0) s[i - 1] = strides[i - 1];
+  }
+  const CUresult r =
+      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+               const_cast<void*>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

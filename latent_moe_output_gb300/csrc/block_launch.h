@@ -58,6 +58,11 @@ bool make_map_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t byt
 bool make_map_bf16_rows64(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                           uint32_t box_rows, uint32_t box_chunks);
 
+// Map of a bf16 array of `rank` dimensions (innermost first; strides in bytes from the
+// second on) with 128-byte swizzle; box[0] is 64. Returns false if the driver rejects it.
+bool make_map_bf16_nd(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box);
+
 // Limits of a kernel's ring of copies: work (tiles, rows) from `copied` on is never
 // copied in, and a wait runs out after limit_ns. Calls leave nothing out; the self-tests
 // of expired waits do.
@@ -114,6 +119,62 @@ struct ResidualNormBackwardArgs {
   RingLimits ring;
 };
 
+enum Activation { kActSilu = 0, kActGelu = 1 };
+enum SavedKind { kSavedNone = 0, kSavedBf16 = 1, kSaved8 = 2 };
+
+struct ExpertGatedArgs {
+  const uint16_t* x;        // [N,C]
+  const uint16_t* weights;  // [E,2F,C], gate rows first
+  const int32_t* offsets;   // [E+1] or null (E == 1)
+  uint16_t* hidden;         // [N,F]
+  void* saved;              // [N,2,F] bf16 or 8 bits, or null
+  uint8_t* exponents;       // [N,2,ceil(F/16)] or null
+  int N, E, F, C;
+  int act, saved_kind;
+  RingLimits ring;
+};
+
+// out = x times each expert's [M,K] weights (or [K,M] ones, transposed).
+struct ExpertRowsArgs {
+  const uint16_t* x;        // [N,K]
+  const uint16_t* weights;  // [E,M,K]; transposed: [E,K,M]
+  const int32_t* offsets;
+  uint16_t* out;            // [N,M]
+  int N, E, M, K;
+  bool transposed;
+  RingLimits ring;
+};
+
+// grad_weights[e] = grad^T x over the rows of expert e.
+struct ExpertWeightsArgs {
+  const uint16_t* grad;     // [N,M]
+  const uint16_t* x;        // [N,C]
+  const int32_t* offsets;
+  uint16_t* grad_weights;   // [E,M,C]
+  int N, E, M, C;
+  RingLimits ring;
+};
+
+// The gradient at both projections, and the product again, from what was kept of them.
+struct GatedGradArgs {
+  const uint16_t* grad_hidden;  // [N,F]
+  const void* saved;            // [N,2,F]
+  const uint8_t* exponents;     // [N,2,ceil(F/16)] or null
+  const int32_t* offsets;
+  uint16_t* grad_pre;           // [N,2F] or null (not wanted)
+  uint16_t* hidden;             // [N,F] or null
+  int N, E, F;
+  int act, saved_kind;
+};
+
+struct Quantize8Args {
+  const uint16_t* x;   // [T,C] (quantize8)
+  int8_t* values;      // [T,C]
+  uint8_t* exponents;  // [T,ceil(C/16)]
+  uint16_t* out;       // [T,C] (dequantize8)
+  int T, C;
+};
+
 // SMs that a workspace size computed without a device allows for.
 constexpr int kMaxSms = 304;
 // Rows of partial sums that a call of T tokens of width H may write (bounds the
@@ -130,8 +191,19 @@ cudaError_t launch_residual_norm(const ResidualNormArgs& a, const DeviceInfo& de
 cudaError_t launch_residual_norm_backward(const ResidualNormBackwardArgs& a,
                                           const DeviceInfo& dev, cudaStream_t stream);
 
+cudaError_t launch_expert_gated(const ExpertGatedArgs& a, const DeviceInfo& dev,
+                                cudaStream_t stream);
+cudaError_t launch_expert_rows(const ExpertRowsArgs& a, const DeviceInfo& dev,
+                               cudaStream_t stream);
+cudaError_t launch_expert_weights(const ExpertWeightsArgs& a, const DeviceInfo& dev,
+                                  cudaStream_t stream);
+cudaError_t launch_gated_grad(const GatedGradArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_quantize8(const Quantize8Args& a, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_dequantize8(const Quantize8Args& a, const DeviceInfo& dev, cudaStream_t stream);
+
 cudaError_t setup_dispatch(const DeviceInfo& dev);
 cudaError_t setup_matvec4(const DeviceInfo& dev);
 cudaError_t setup_residual_norm(const DeviceInfo& dev);
+cudaError_t setup_experts(const DeviceInfo& dev);
 
 }  // namespace lt

@@ -1,0 +1,714 @@
+// Products of expert-sorted rows with bf16 weights on the tensor cores, and their
+// gradients (with r a row of expert e, W_e its weights):
+//   kGated    h[r,f]   = a(sum_c x[r,c] W_e[f,c]) * sum_c x[r,c] W_e[F+f,c]
+//   kRows     y[r,m]   = sum_k x[r,k] W_e[m,k]
+//   kRowsT    dx[r,c]  = sum_m dy[r,m] W_e[m,c]
+//   kWeights  dW_e[m,c] = sum_r dy[r,m] x[r,c]
+//
+// The row counts of experts are ragged, those of weights are not. So the weights are
+// the MMA's M side, always 256 rows over a pair of CTAs (tcgen05 cta_group::2: each CTA
+// loads its own 128 weight rows and half of the other operand), and the rows of an
+// expert its N side, which an instruction takes in any multiple of 16 up to 256: an
+// expert of n rows computes about n + 8 of them, where tiles of 256 (128) rows on the M
+// side would compute n + 128 (n + 64) on average. An expert's rows are cut into the
+// fewest tiles of at most 256, all of one size.
+//
+// kGated: the gate and the up row of a feature have to meet. A 5-D tensor map brings
+// them into the tile in turns of eight (gate 0..7, up 0..7, gate 8..15, ...): rows of the
+// accumulator are lanes of TMEM, so a lane finds the other projection of its feature
+// eight lanes away, and one shuffle per two columns gives each lane both values of one
+// (feature, row).
+//
+// kWeights: both operands run along M and N in memory (MN-major descriptors), and the
+// sum runs over the rows. An expert whose count is not a multiple of 16 ends inside an
+// MMA's 16 rows; what follows them are other experts' rows, of which one NaN would spoil
+// the sum even against zeros. A warp of each CTA overwrites those rows of both operands
+// with zeros in shared memory before the MMA reads them.
+//
+// Persistent, warp-specialized, one CTA per SM, 7 warps:
+//   warp 0      producer: this CTA's operand boxes of a 64-deep block into a stage ring
+//   warp 1      TMEM allocation; in the even CTA the MMA issuer
+//   warps 2..5  epilogue; two accumulators, so the next tile's MMAs run meanwhile. The
+//               lanes of TMEM are columns of the result: 32 rows at a time are turned
+//               over in shared memory and leave in 16-byte pieces of whole row parts
+//   warp 6      kWeights: the zeros above; else zeros in the rows that no expert owns
+// Sums are FP32; results are rounded once.
+#include "experts.cuh"
+
+#include <algorithm>
+
+namespace lt {
+namespace {
+
+enum Form { kGated, kRows, kRowsT, kWeights };
+
+constexpr int kTileRows = 256;      // MMA N: rows of an expert (kWeights: columns)
+constexpr int kBlockK = 64;
+constexpr uint32_t kOperandBytes = 128 * kBlockK * 2;
+constexpr uint32_t kStageBytes = 2 * kOperandBytes;
+constexpr int kMaxStages = 6;
+constexpr int kThreads = 224;
+constexpr uint32_t kTmemCols = 512;  // two accumulators
+constexpr int kChunk = 32;           // rows turned over at a time
+constexpr int kRowBoxes = 4;         // boxes of 32 rows that hold a CTA's half of a tile
+
+// Shared memory of one chunk. kRows: 32 rows of 128 bf16; the pad spreads them over banks.
+constexpr int kPlainStride = 272;
+// kGated: 32 rows of 64 products, and of 2 x 64 kept projections in bf16, or in 8 bits
+// with 2 x 4 exponents. Strides of 8 (mod 32) words keep the two rows that a warp writes
+// at once in different banks.
+constexpr int kHiddenStride = 160;
+constexpr int kKeptStride = 160;   // per projection
+constexpr int kByteStride = 80;    // per projection
+constexpr int kKeptAt = kChunk * kHiddenStride;
+constexpr int kExponentsAt = kKeptAt + kChunk * 2 * kByteStride;
+
+constexpr int turn_bytes(Form form, int saved_kind) {
+  return form == kWeights ? 0
+         : form != kGated ? kChunk * kPlainStride
+         : saved_kind == kSavedNone ? kKeptAt
+         : saved_kind == kSavedBf16 ? kKeptAt + kChunk * 2 * kKeptStride
+                                    : kExponentsAt + kChunk * 8;
+}
+
+struct Params {
+  const int32_t* offsets;
+  uint16_t* out;         // kGated: products [N,F]; kRows, kRowsT: [N,M]; kWeights: [E,M,C]
+  void* saved;           // kGated: kept projections [N,2,F], bf16 or 8 bits, or null
+  uint8_t* exponents;    // [N,2,groups]
+  int N, E;
+  int M;                 // kGated: F; kRows, kRowsT: columns of out; kWeights: its rows
+  int K;                 // depth of a sum (kWeights: columns of out)
+  int mblocks, cblocks;
+  int saved_kind;
+  int stages, turn;
+  uint32_t* err;
+  RingLimits ring;
+};
+
+struct Tile {
+  int e, row0, rows, m0, c0;
+};
+
+__device__ __forceinline__ int passes(int n) { return (n + kTileRows - 1) / kTileRows; }
+
+// Tiles in order: the features of one pass over an expert's rows, then the next pass.
+// `e` moves forward only.
+template <Form kForm>
+__device__ __forceinline__ Tile tile_at(const Params& p, int tile, int& e, const int* s_first,
+                                        const int* s_unit) {
+  Tile t;
+  if constexpr (kForm == kWeights) {
+    const int per = p.mblocks * p.cblocks;
+    t.e = tile / per;
+    const int in = tile - t.e * per;
+    t.row0 = s_first[t.e];
+    t.rows = s_first[t.e + 1] - t.row0;
+    t.m0 = in / p.cblocks * 256;
+    t.c0 = in % p.cblocks * kTileRows;
+  } else {
+    const int unit = tile / p.mblocks;
+    while (s_unit[e + 1] <= unit) ++e;
+    const int n = s_first[e + 1] - s_first[e], i = unit - s_unit[e], k = passes(n);
+    const int size = ((n + k - 1) / k + 15) & ~15;
+    t.e = e;
+    t.row0 = s_first[e] + i * size;
+    t.rows = min(size, n - i * size);
+    t.m0 = (tile - unit * p.mblocks) * (kForm == kGated ? 128 : 256);
+    t.c0 = 0;
+  }
+  return t;
+}
+
+__device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+  return true;
+}
+
+__device__ __forceinline__ void epilogue_barrier() {
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+
+template <Form kForm, int kAct>
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_kernel(const __grid_constant__ CUtensorMap a_map,
+                  const __grid_constant__ CUtensorMap b_map, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full_bar[kMaxStages];   // even CTA: both CTAs' stage landed
+  __shared__ uint64_t empty_bar[kMaxStages];  // stage consumed by the pair's MMAs
+  __shared__ uint64_t tail_bar[kMaxStages];   // kWeights: this CTA's last block landed
+  __shared__ uint64_t fixed_bar[kMaxStages];  // even CTA: both CTAs' zeros are in place
+  __shared__ uint64_t accf_bar[2];            // accumulator ready (both CTAs)
+  __shared__ uint64_t acce_bar[2];            // even CTA: accumulator drained by both
+  __shared__ uint64_t drain_bar;              // even CTA: MMAs before an abort are done
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  volatile int* abort_v = &abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int pair = static_cast<int>(blockIdx.x) >> 1;
+  const int n_pairs = static_cast<int>(gridDim.x) >> 1;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t ring = (raw + 1023u) & ~1023u;
+  const int stages = p.stages;
+  uint8_t* turn_ptr = smem_raw + (ring - raw) + static_cast<uint32_t>(stages) * kStageBytes;
+  int* s_first = reinterpret_cast<int*>(turn_ptr + 2 * p.turn);
+  int* s_unit = s_first + p.E + 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+      mbar_init(smem_u32(&tail_bar[s]), 1);
+      mbar_init(smem_u32(&fixed_bar[s]), 2);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&accf_bar[a]), 1);
+      mbar_init(smem_u32(&acce_bar[a]), 2 * 4);  // one arrival per epilogue warp of the pair
+    }
+    mbar_init(smem_u32(&drain_bar), 1);
+    abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_map(&a_map);
+    tma_prefetch_map(&b_map);
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(&tmem_slot), kTmemCols);
+  pdl_wait();
+  load_experts(p.offsets, p.N, p.E, s_first, s_unit, [](int n) { return passes(n); });
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  const int tiles = kForm == kWeights ? p.E * p.mblocks * p.cblocks : s_unit[p.E] * p.mblocks;
+  // Blocks of a tile's sum, and whether the last one of kWeights needs zeros.
+  auto blocks_of = [&](const Tile& t) {
+    return ((kForm == kWeights ? t.rows : p.K) + kBlockK - 1) / kBlockK;
+  };
+  auto needs_zeros = [&](const Tile& t) { return kForm == kWeights && (t.rows & 15) != 0; };
+  // Rows of an MMA's N side.
+  auto width_of = [&](const Tile& t) {
+    return kForm == kWeights ? kTileRows : (t.rows + 15) & ~15;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- producer (this CTA's halves) ----------------
+      int e = 0, s = 0;
+      uint32_t round = 0, tails = 0, tail_phase = 0;
+      int issued = 0;
+      const int copied = static_cast<int>(min(static_cast<int64_t>(tiles), p.ring.copied));
+      bool alive = true;
+      for (int tile = pair; alive && tile < copied; tile += n_pairs) {
+        const Tile t = tile_at<kForm>(p, tile, e, s_first, s_unit);
+        const int nkb = blocks_of(t);
+        const int half = width_of(t) / 2;
+        const int row0 = t.row0 + rank * half;
+        const int boxes = kForm == kWeights ? kRowBoxes : (half + 31) / 32;
+        const uint32_t bytes = kOperandBytes + static_cast<uint32_t>(boxes) * 4096u;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait_cluster(smem_u32(&empty_bar[s]), (round & 1u) ^ 1u, p.err, abort_v,
+                                 p.ring.limit_ns)) {
+            alive = false;
+            break;
+          }
+          const uint32_t a = ring + static_cast<uint32_t>(s) * kStageBytes, b = a + kOperandBytes;
+          if (kForm == kWeights && kb == nkb - 1 && needs_zeros(t)) {
+            // Completes on this CTA's own barrier, for the warp that puts the zeros in.
+            const uint32_t bar = smem_u32(&tail_bar[s]);
+            if (rank == 0) mbar_arrive(smem_u32(&full_bar[s]));
+            mbar_arrive_expect_tx(bar, kStageBytes);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              tma_load_2d(a + 8192u * j, &a_map, bar, t.m0 + rank * 128 + 64 * j,
+                          t.row0 + kb * kBlockK);
+              tma_load_2d(b + 8192u * j, &b_map, bar, t.c0 + rank * 128 + 64 * j,
+                          t.row0 + kb * kBlockK);
+            }
+            tails |= 1u << s;
+            tail_phase ^= 1u << s;
+          } else {
+            const uint32_t bar = map_to_rank(smem_u32(&full_bar[s]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), 2 * bytes);
+            if constexpr (kForm == kGated) {
+              tma_load_5d_pair(a, &a_map, bar, kb * kBlockK, 0, 0, (t.m0 + rank * 64) / 8, t.e);
+            } else if constexpr (kForm == kRows) {
+              tma_load_3d_pair(a, &a_map, bar, kb * kBlockK, t.m0 + rank * 128, t.e);
+            } else if constexpr (kForm == kRowsT) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                tma_load_3d_pair(a + 8192u * j, &a_map, bar, t.m0 + rank * 128 + 64 * j,
+                                 kb * kBlockK, t.e);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                tma_load_2d_pair(a + 8192u * j, &a_map, bar, t.m0 + rank * 128 + 64 * j,
+                                 t.row0 + kb * kBlockK);
+                tma_load_2d_pair(b + 8192u * j, &b_map, bar, t.c0 + rank * 128 + 64 * j,
+                                 t.row0 + kb * kBlockK);
+              }
+            }
+            if constexpr (kForm != kWeights) {
+              for (int j = 0; j < boxes; ++j)
+                tma_load_2d_pair(b + 4096u * j, &b_map, bar, kb * kBlockK, row0 + 32 * j);
+            }
+          }
+          ++issued;
+          if (++s == stages) {
+            s = 0;
+            ++round;
+          }
+        }
+      }
+      if (*abort_v) {  // copies in flight land before the CTA's shared memory goes
+        if (rank == 0)  // the even CTA's barriers count both CTAs' copies
+          for (int it = max(0, issued - stages); it < issued; ++it)
+            wait_drain(smem_u32(&full_bar[it % stages]), static_cast<uint32_t>(it / stages) & 1u);
+        for (int i = 0; i < stages; ++i)  // the last tail of each stage
+          if (tails >> i & 1u) wait_drain(smem_u32(&tail_bar[i]), (tail_phase >> i & 1u) ^ 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ---------------- pair MMA issuer ----------------
+      int e = 0, s = 0;
+      uint32_t round = 0, fixed_phase = 0, use = 0;
+      bool alive = true;
+      for (int tile = pair; alive && tile < tiles; tile += n_pairs) {
+        const Tile t = tile_at<kForm>(p, tile, e, s_first, s_unit);
+        const int nkb = blocks_of(t);
+        if (nkb == 0) continue;
+        const int acc = static_cast<int>(use & 1u);
+        if (!mbar_wait_cluster(smem_u32(&acce_bar[acc]), ((use >> 1) & 1u) ^ 1u, p.err, abort_v,
+                               p.ring.limit_ns))
+          break;
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(acc * kTileRows);
+        const uint32_t idesc = umma_idesc_bf16(256, width_of(t)) |
+                               (kForm == kRowsT || kForm == kWeights ? kUmmaTransposeA : 0u) |
+                               (kForm == kWeights ? kUmmaTransposeB : 0u);
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait_cluster(smem_u32(&full_bar[s]), round & 1u, p.err, abort_v,
+                                 p.ring.limit_ns)) {
+            alive = false;
+            break;
+          }
+          int steps = kBlockK / 16;
+          if (kForm == kWeights && kb == nkb - 1) {
+            steps = (t.rows - kb * kBlockK + 15) >> 4;
+            if (needs_zeros(t)) {
+              if (!mbar_wait_cluster(smem_u32(&fixed_bar[s]), fixed_phase >> s & 1u, p.err,
+                                     abort_v, p.ring.limit_ns)) {
+                alive = false;
+                break;
+              }
+              fixed_phase ^= 1u << s;
+            }
+          }
+          tc_fence_after();
+          const uint32_t a = ring + static_cast<uint32_t>(s) * kStageBytes, b = a + kOperandBytes;
+#pragma unroll
+          for (int k = 0; k < kBlockK / 16; ++k) {
+            if (k < steps)
+              umma_bf16_pair(
+                  d,
+                  kForm == kRowsT || kForm == kWeights ? umma_desc_sw128_mn(a + 2048u * k)
+                                                       : umma_desc_sw128(a + 32u * k),
+                  kForm == kWeights ? umma_desc_sw128_mn(b + 2048u * k)
+                                    : umma_desc_sw128(b + 32u * k),
+                  idesc, (kb | k) != 0 ? 1u : 0u);
+          }
+          umma_commit_pair(smem_u32(&empty_bar[s]), 0x3);
+          if (++s == stages) {
+            s = 0;
+            ++round;
+          }
+        }
+        umma_commit_pair(smem_u32(&accf_bar[acc]), 0x3);
+        ++use;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    if constexpr (kForm == kWeights) {
+      // ---------------- zeros behind an expert's last row ----------------
+      int e = 0, it = 0;
+      uint32_t phase = 0;
+      bool alive = true;
+      for (int tile = pair; alive && tile < tiles; tile += n_pairs) {
+        const Tile t = tile_at<kForm>(p, tile, e, s_first, s_unit);
+        it += blocks_of(t);
+        if (!needs_zeros(t)) continue;
+        const int s = (it - 1) % stages;
+        const int from = t.rows - (blocks_of(t) - 1) * kBlockK, to = (from + 15) & ~15;
+        alive = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tail_bar[s]), phase >> s & 1u, p.err,
+                                                  abort_v, p.ring.limit_ns));
+        if (!alive) break;
+        phase ^= 1u << s;
+        // Four 8 KB boxes of 64 rows of 128 bytes (the swizzle stays within a row).
+        uint8_t* st = smem_raw + (ring - raw) + static_cast<uint32_t>(s) * kStageBytes;
+        for (int i = lane; i < (to - from) * 32; i += 32) {
+          const int row = from + (i >> 5), box = (i >> 3) & 3, piece = i & 7;
+          *reinterpret_cast<uint4*>(st + box * 8192 + row * 128 + piece * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&fixed_bar[s]);
+          mbar_arrive_remote(map_to_rank(bar, 0));
+        }
+      }
+    } else {
+      // ---------------- rows that no expert owns ----------------
+      const int before = s_first[0], end = s_first[p.E];
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      for (int i = blockIdx.x; i < before + p.N - end; i += gridDim.x) {
+        const size_t r = static_cast<size_t>(i < before ? i : end + (i - before));
+        uint4* o = reinterpret_cast<uint4*>(p.out + r * p.M);
+        for (int c = lane; c < p.M / 8; c += 32) o[c] = zero;
+        if (kForm == kGated && p.saved_kind == kSavedBf16) {
+          uint4* k = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.saved) + r * 2 * p.M);
+          for (int c = lane; c < p.M / 4; c += 32) k[c] = zero;
+        } else if (kForm == kGated && p.saved_kind == kSaved8) {
+          uint4* k = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.saved) + r * 2 * p.M);
+          for (int c = lane; c < p.M / 8; c += 32) k[c] = zero;
+          const int groups = 2 * ((p.M + kGroup8 - 1) / kGroup8);
+          for (int c = lane; c < groups; c += 32) p.exponents[r * groups + c] = 0;
+        }
+      }
+    }
+  } else {
+    // ---------------- epilogue (warps 2..5) ----------------
+    const int q = warp & 3;  // the quarter of TMEM's lanes that this warp may access
+    const int tid = threadIdx.x - 64;
+    const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+    auto release_acc = [&](int a) {  // accumulator read: back to the MMA issuer
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t bar = smem_u32(&acce_bar[a]);
+        if (rank == 0)
+          mbar_arrive(bar);
+        else
+          mbar_arrive_remote(map_to_rank(bar, 0));
+      }
+    };
+    int e = 0, turn = 0;
+    uint32_t use = 0;
+    bool alive = true;
+    for (int tile = pair; alive && tile < tiles; tile += n_pairs) {
+      const Tile t = tile_at<kForm>(p, tile, e, s_first, s_unit);
+      const bool any = blocks_of(t) != 0;
+      const int acc = static_cast<int>(use & 1u);
+      const uint32_t dcol = tmem + lane_base + static_cast<uint32_t>(acc * kTileRows);
+      if (any) {
+        // Every warp's waits end alike: the flag that one sets ends the others' too.
+        alive = __all_sync(0xffffffffu,
+                           mbar_wait_cluster(smem_u32(&accf_bar[acc]), (use >> 1) & 1u, p.err,
+                                             abort_v, p.ring.limit_ns));
+        if constexpr (kForm != kWeights) {
+          uint32_t all;  // the warps turn rows over together
+          asm volatile(
+              "{\n\t.reg .pred p, q;\n\t"
+              "setp.ne.u32 p, %1, 0;\n\t"
+              "bar.red.and.pred q, 1, 128, p;\n\t"
+              "selp.u32 %0, 1, 0, q;\n\t}"
+              : "=r"(all)
+              : "r"(static_cast<uint32_t>(alive))
+              : "memory");
+          alive = all != 0;
+        }
+        if (!alive) break;
+        tc_fence_after();
+        ++use;
+      }
+      const int chunks = (width_of(t) + kChunk - 1) / kChunk;
+      if constexpr (kForm == kWeights) {
+        // Lanes are rows of dW_e, columns of TMEM its columns.
+        const int m = t.m0 + rank * 128 + q * 32 + lane;
+        uint16_t* dst = p.out + (static_cast<size_t>(t.e) * p.M + m) * p.K + t.c0;
+        for (int ch = 0; ch < chunks; ++ch) {
+          float v[32];
+          if (any) {
+            __syncwarp();
+            tmem_ld32(dcol + static_cast<uint32_t>(ch * kChunk), v);
+            if (ch == chunks - 1) release_acc(acc);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          }
+          if (m >= p.M) continue;
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            if (t.c0 + ch * kChunk + g * 8 < p.K)
+              *reinterpret_cast<uint4*>(dst + ch * kChunk + g * 8) =
+                  pack8(*reinterpret_cast<const float(*)[8]>(&v[g * 8]));
+        }
+      } else {
+        for (int ch = 0; ch < chunks; ++ch, ++turn) {
+          float v[32];
+          __syncwarp();
+          tmem_ld32(dcol + static_cast<uint32_t>(ch * kChunk), v);
+          if (ch == chunks - 1) release_acc(acc);
+          uint8_t* buf = turn_ptr + (turn & 1) * p.turn;
+          const int live = min(kChunk, t.rows - ch * kChunk);  // rows of the chunk
+          const size_t row = static_cast<size_t>(t.row0) + ch * kChunk;
+          if constexpr (kForm != kGated) {
+            uint8_t* at = buf + q * 64 + lane * 2;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              *reinterpret_cast<uint16_t*>(at + j * kPlainStride) =
+                  static_cast<uint16_t>(pack_bf16x2(v[j], 0.f));
+            epilogue_barrier();
+            // (the other buffer's turn ends at the next barrier)
+            const int m = t.m0 + rank * 128 + (tid & 15) * 8;
+            if (m < p.M) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = (tid >> 4) + i * 8;
+                if (r < live)
+                  *reinterpret_cast<uint4*>(p.out + (row + r) * p.M + m) =
+                      *reinterpret_cast<const uint4*>(buf + r * kPlainStride + (tid & 15) * 16);
+              }
+            }
+          } else {
+            // Lane: gate (half 0) or up (half 1) of feature `f` of this CTA's 64.
+            const int half = (lane >> 3) & 1;
+            const int f = q * 16 + ((lane >> 4) << 3) + (lane & 7);
+            if (p.saved_kind == kSavedBf16) {
+              uint8_t* at = buf + kKeptAt + half * kKeptStride + f * 2;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                *reinterpret_cast<uint16_t*>(at + j * 2 * kKeptStride) =
+                    static_cast<uint16_t>(pack_bf16x2(v[j], 0.f));
+            } else if (p.saved_kind == kSaved8) {
+              // A group is the 16 lanes of one projection; features past F are zeros.
+              uint8_t* at = buf + kKeptAt + half * kByteStride + f;
+              uint8_t* eat = buf + kExponentsAt + half * 4 + q;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                uint32_t top = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                const uint32_t ex = exponent8(top);
+                at[j * 2 * kByteStride] =
+                    static_cast<uint8_t>(quantize8(v[j], ex, scale8(ex)) & 0xFF);
+                if ((lane & 23) == 0) eat[j * 8] = static_cast<uint8_t>(ex);
+              }
+            }
+            uint8_t* at = buf + half * kHiddenStride + f * 2;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float other = __shfl_xor_sync(0xffffffffu, half ? v[2 * j] : v[2 * j + 1], 8);
+              const float g = half ? other : v[2 * j], u = half ? v[2 * j + 1] : other;
+              const float h = activation<kAct>(g) * u;
+              *reinterpret_cast<uint16_t*>(at + 2 * j * kHiddenStride) =
+                  static_cast<uint16_t>(pack_bf16x2(h, 0.f));
+            }
+            epilogue_barrier();
+            const int f0 = t.m0 + rank * 64;
+            {
+              const int c = (tid & 7) * 8;
+              if (f0 + c < p.M) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int r = (tid >> 3) + i * 16;
+                  if (r < live)
+                    *reinterpret_cast<uint4*>(p.out + (row + r) * p.M + f0 + c) =
+                        *reinterpret_cast<const uint4*>(buf + r * kHiddenStride + c * 2);
+                }
+              }
+            }
+            if (p.saved_kind == kSavedBf16) {
+              const int c = (tid & 7) * 8, h = (tid >> 3) & 1;
+              if (f0 + c < p.M) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int r = (tid >> 4) + i * 8;
+                  if (r < live)
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.saved) +
+                                              ((row + r) * 2 + h) * p.M + f0 + c) =
+                        *reinterpret_cast<const uint4*>(buf + kKeptAt +
+                                                        (r * 2 + h) * kKeptStride + c * 2);
+                }
+              }
+            } else if (p.saved_kind == kSaved8) {
+              const int c = (tid & 7) * 8, h = (tid >> 3) & 1;
+              if (f0 + c < p.M) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int r = (tid >> 4) + i * 8;
+                  if (r < live)
+                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.saved) +
+                                              ((row + r) * 2 + h) * p.M + f0 + c) =
+                        *reinterpret_cast<const uint2*>(buf + kKeptAt +
+                                                        (r * 2 + h) * kByteStride + c);
+                }
+              }
+              const int groups = (p.M + kGroup8 - 1) / kGroup8;
+              const int g0 = f0 / kGroup8 + (tid & 3);
+              if (g0 < groups) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int at2 = (tid >> 2) + i * 32, r = at2 >> 1, h2 = at2 & 1;
+                  if (r < live)
+                    p.exponents[((row + r) * 2 + h2) * groups + g0] =
+                        buf[kExponentsAt + r * 8 + h2 * 4 + (tid & 3)];
+                }
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+
+  // Neither CTA may leave while the pair's MMAs could still read its shared memory or
+  // write its TMEM, or while its peer could still signal it.
+  tc_fence_before();
+  __syncthreads();
+  pdl_launch_dependents();
+  if (warp == 1 && rank == 0 && *abort_v && lane == 0) {
+    // The MMAs issued before the abort: a commit behind them, waited for.
+    umma_commit_pair(smem_u32(&drain_bar), 0x1);
+    wait_drain(smem_u32(&drain_bar), 0);
+  }
+  __syncwarp();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+typedef void (*Kernel)(const CUtensorMap, const CUtensorMap, const Params);
+
+constexpr Kernel kKernels[] = {
+    expert_kernel<kGated, kActSilu>, expert_kernel<kGated, kActGelu>,
+    expert_kernel<kRows, kActSilu>, expert_kernel<kRowsT, kActSilu>,
+    expert_kernel<kWeights, kActSilu>};
+
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+cudaError_t launch(Kernel kernel, Form form, const CUtensorMap& a_map, const CUtensorMap& b_map,
+                   Params p, int64_t most_tiles, const DeviceInfo& dev, cudaStream_t stream) {
+  p.err = dev.err_word;
+  p.turn = turn_bytes(form, p.saved_kind);
+  // As many stages as fit beside the chunks, the experts' table and static shared memory.
+  const int rest = dev.max_smem_optin - 1024 - 1024 - 2 * p.turn - experts_table_bytes(p.E);
+  p.stages = std::min(kMaxStages, rest / static_cast<int>(kStageBytes));
+  const size_t smem = 1024 + static_cast<size_t>(p.stages) * kStageBytes + 2 * p.turn +
+                      experts_table_bytes(p.E);
+  const int pairs = static_cast<int>(std::min<int64_t>(dev.num_sms / 2, most_tiles));
+  return launch_dependent_clusters(2, kernel, dim3(2 * pairs), dim3(kThreads), smem, stream,
+                                   a_map, b_map, p);
+}
+
+// Most tiles of N rows and E experts in passes of 256 rows.
+int64_t most_row_tiles(int N, int E, int mblocks) {
+  return (static_cast<int64_t>(std::min(N, E)) + N / kTileRows) * mblocks;
+}
+
+// Rows [N, cols] in boxes of 64 columns.
+bool rows_map(CUtensorMap* map, const void* base, int N, int cols, int box_rows) {
+  return make_map_bf16_sw128(map, base, N, cols, box_rows);
+}
+
+// Matrices [E, rows, cols] in boxes of 64 columns of one matrix.
+bool matrices_map(CUtensorMap* map, const void* base, int E, int rows, int cols, int box_rows) {
+  const uint64_t c = cols, r = rows;
+  const uint64_t dims[] = {c, r, static_cast<uint64_t>(E)};
+  const uint64_t strides[] = {c * 2, r * c * 2};
+  const uint32_t box[] = {64, static_cast<uint32_t>(box_rows), 1};
+  return make_map_bf16_nd(map, base, 3, dims, strides, box);
+}
+
+}  // namespace
+
+cudaError_t setup_experts(const DeviceInfo& dev) {
+  for (Kernel k : kKernels) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
+        dev.max_smem_optin - 1024);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_expert_gated(const ExpertGatedArgs& a, const DeviceInfo& dev,
+                                cudaStream_t stream) {
+  Params p{};
+  p.offsets = a.offsets;
+  p.out = a.hidden;
+  p.saved = a.saved;
+  p.exponents = a.exponents;
+  p.N = a.N;
+  p.E = a.E;
+  p.M = a.F;
+  p.K = a.C;
+  p.mblocks = ceil_div(a.F, 128);
+  p.saved_kind = a.saved_kind;
+  p.ring = a.ring;
+  // Gate and up rows in turns of eight: columns, 8 rows, gate or up, eights of features,
+  // experts.
+  const uint64_t c = a.C, f = a.F;
+  const uint64_t dims[] = {c, 8, 2, f / 8, static_cast<uint64_t>(a.E)};
+  const uint64_t strides[] = {c * 2, f * c * 2, 8 * c * 2, 2 * f * c * 2};
+  const uint32_t box[] = {64, 8, 2, 8, 1};
+  CUtensorMap w_map, x_map;
+  if (!make_map_bf16_nd(&w_map, a.weights, 5, dims, strides, box) ||
+      !rows_map(&x_map, a.x, a.N, a.C, 32))
+    return cudaErrorInvalidValue;
+  return launch(kKernels[a.act == kActSilu ? 0 : 1], kGated, w_map, x_map, p,
+                most_row_tiles(a.N, a.E, p.mblocks), dev, stream);
+}
+
+cudaError_t launch_expert_rows(const ExpertRowsArgs& a, const DeviceInfo& dev,
+                               cudaStream_t stream) {
+  Params p{};
+  p.offsets = a.offsets;
+  p.out = a.out;
+  p.N = a.N;
+  p.E = a.E;
+  p.M = a.M;
+  p.K = a.K;
+  p.mblocks = ceil_div(a.M, 256);
+  p.ring = a.ring;
+  CUtensorMap w_map, x_map;
+  if (!(a.transposed ? matrices_map(&w_map, a.weights, a.E, a.K, a.M, 64)
+                     : matrices_map(&w_map, a.weights, a.E, a.M, a.K, 128)) ||
+      !rows_map(&x_map, a.x, a.N, a.K, 32))
+    return cudaErrorInvalidValue;
+  const Form form = a.transposed ? kRowsT : kRows;
+  return launch(kKernels[a.transposed ? 3 : 2], form, w_map, x_map, p,
+                most_row_tiles(a.N, a.E, p.mblocks), dev, stream);
+}
+
+cudaError_t launch_expert_weights(const ExpertWeightsArgs& a, const DeviceInfo& dev,
+                                  cudaStream_t stream) {
+  Params p{};
+  p.offsets = a.offsets;
+  p.out = a.grad_weights;
+  p.N = a.N;
+  p.E = a.E;
+  p.M = a.M;
+  p.K = a.C;
+  p.mblocks = ceil_div(a.M, 256);
+  p.cblocks = ceil_div(a.C, kTileRows);
+  p.ring = a.ring;
+  CUtensorMap g_map, x_map;
+  if (!rows_map(&g_map, a.grad, a.N, a.M, 64) || !rows_map(&x_map, a.x, a.N, a.C, 64))
+    return cudaErrorInvalidValue;
+  return launch(kKernels[4], kWeights, g_map, x_map, p,
+                static_cast<int64_t>(a.E) * p.mblocks * p.cblocks, dev, stream);
+}
+
+}  // namespace lt

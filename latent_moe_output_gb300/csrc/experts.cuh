@@ -1,0 +1,123 @@
+// Device helpers shared by the kernels of the bf16 experts: the table of the experts'
+// rows, the activation with its derivative, and the 8-bit form of kept activations.
+#pragma once
+
+#include "block_launch.h"
+#include "rows.cuh"
+
+namespace lt {
+
+// First row of each expert and the passes before it, from the caller's offsets: cut to
+// [0, N] and to their running maximum, so that ones that run backwards give empty
+// experts. Offsets that are null mean one matrix for all rows. Called by all threads;
+// `units` gives the passes of an expert of n rows. Ends with a block barrier.
+template <typename Units>
+__device__ __forceinline__ void load_experts(const int32_t* offsets, int N, int E, int* s_first,
+                                             int* s_unit, Units units) {
+  if (offsets != nullptr) {
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) s_first[e] = min(max(offsets[e], 0), N);
+  } else if (threadIdx.x == 0) {
+    s_first[0] = 0;
+    s_first[1] = N;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const int per = (E + 32) / 32;  // each lane takes a contiguous part
+    const int lo = min(E + 1, lane * per), hi = min(E + 1, lo + per);
+    int top = 0;
+    for (int e = lo; e < hi; ++e) top = max(top, s_first[e]);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, top, o);
+      if (lane >= o) top = max(top, up);
+    }
+    int run = __shfl_up_sync(0xffffffffu, top, 1);
+    if (lane == 0) run = 0;
+    for (int e = lo; e < hi; ++e) s_first[e] = run = max(run, s_first[e]);
+    __syncwarp();
+    int sum = 0;
+    for (int e = lo; e < hi && e < E; ++e) sum += units(s_first[e + 1] - s_first[e]);
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    run = incl - sum;
+    for (int e = lo; e < hi; ++e) {
+      s_unit[e] = run;
+      if (e < E) run += units(s_first[e + 1] - s_first[e]);
+    }
+  }
+  __syncthreads();
+}
+
+// Bytes of shared memory for s_first and s_unit.
+constexpr int experts_table_bytes(int E) { return ((E + 1) * 8 + 15) & ~15; }
+
+// ------------------------------------------------------------ activation
+// Both activations are g * sigmoid(s(g)): SiLU with s = g, the tanh form of GELU with
+// s = sqrt(8 / pi) (g + 0.044715 g^3), as 0.5 (1 + tanh(y)) = sigmoid(2 y). The cubic
+// takes g cut to +-32, where the sigmoid is 0 or 1 in FP32, so that it cannot overflow.
+__device__ __forceinline__ float sigmoid(float s) {
+  return __fdividef(1.f, 1.f + __expf(-s));
+}
+
+__device__ __forceinline__ float gelu_argument(float g) {
+  const float c = fminf(fmaxf(g, -32.f), 32.f);
+  return 1.59576912160573f * c * fmaf(0.044715f * c, c, 1.f);
+}
+
+template <int kAct>
+__device__ __forceinline__ float activation(float g) {
+  return g * sigmoid(kAct == kActSilu ? g : gelu_argument(g));
+}
+
+// The activation a and its derivative d at g.
+template <int kAct>
+__device__ __forceinline__ void activation_grad(float g, float& a, float& d) {
+  const float s = sigmoid(kAct == kActSilu ? g : gelu_argument(g));
+  a = g * s;
+  float slope = 1.f;
+  if (kAct != kActSilu) {
+    const float c = fminf(fmaxf(g, -32.f), 32.f);
+    slope = 1.59576912160573f * fmaf(3.f * 0.044715f * c, c, 1.f);
+  }
+  // s (1 - s) from the smaller of the two would keep more of the far tail, where the
+  // product with g is below the rounding of the sum in 32 bits all the same.
+  d = fmaf(a * (1.f - s), slope, s);
+}
+
+// ------------------------------------------------------------- 8-bit form
+// 16 consecutive values share a power of two 2^(e - 127): the least e >= 1 for which the
+// largest magnitude rounds to at most 127. An integer of 8 bits times a power of two is
+// exact in bf16, so reading back adds no second rounding. e = 0 stands for a group of
+// zeros, e = 255 for a group that holds an infinity or a NaN (read back as NaNs).
+constexpr int kGroup8 = 16;
+
+// `top`: the largest magnitude as bits (NaN sorts above infinity, and that above all).
+__device__ __forceinline__ uint32_t exponent8(uint32_t top) {
+  if (top >= 0x7F800000u) return 255u;
+  if (top == 0u) return 0u;
+  // 2^E <= top < 2^(E+1): in units of 2^(E-6) it rounds to 64 .. 127, or to 128 from
+  // 127.5 on, where the next unit is taken.
+  const int e = static_cast<int>(top >> 23) - 6 + ((top & 0x7FFFFFu) >= 0x7F0000u ? 1 : 0);
+  return static_cast<uint32_t>(max(e, 1));
+}
+
+// Factor from values to their integers; 0 for a group of zeros or one that is not finite.
+__device__ __forceinline__ float scale8(uint32_t e) {
+  return e == 0u || e == 255u ? 0.f : __uint_as_float((254u - e) << 23);
+}
+
+__device__ __forceinline__ int quantize8(float v, uint32_t e, float scale) {
+  return e == 255u ? 0 : __float2int_rn(v * scale);
+}
+
+// Factor from integers back to values; NaN where e = 255 (0 times it is NaN).
+__device__ __forceinline__ float unit8(uint32_t e) {
+  return e == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(e << 23);
+}
+
+}  // namespace lt

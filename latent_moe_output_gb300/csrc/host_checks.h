@@ -12,7 +12,7 @@
 namespace lt {
 
 // Operators whose kernels have attributes to set on a device before their first launch.
-enum class Operator { kNone, kTail, kDispatch, kMatvec4, kResidualNorm };
+enum class Operator { kNone, kTail, kDispatch, kMatvec4, kResidualNorm, kExperts };
 
 // Per-device state of the current device, set up on first use, with the kernels of `op`
 // (those of an operator alone, so that no other pays for them or fails with them).
