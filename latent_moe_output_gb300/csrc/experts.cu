@@ -50,7 +50,6 @@ constexpr int kMaxStages = 6;
 constexpr int kThreads = 224;
 constexpr uint32_t kTmemCols = 512;  // two accumulators
 constexpr int kChunk = 32;           // rows turned over at a time
-constexpr int kRowBoxes = 4;         // boxes of 32 rows that hold a CTA's half of a tile
 
 // Shared memory of one chunk. kRows: 32 rows of 128 bf16; the pad spreads them over banks.
 constexpr int kPlainStride = 272;
@@ -81,9 +80,20 @@ struct Params {
   int K;                 // depth of a sum (kWeights: columns of out)
   int mblocks, cblocks;
   int saved_kind;
+  // Whether one copy brings both 64-column boxes of an MN-major operand: where its width
+  // is a multiple of 64, so that a map may count the columns in such pieces.
+  bool whole_a, whole_b;
   int stages, turn;
   uint32_t* err;
   RingLimits ring;
+};
+
+// Maps of operand B. kWeights: the first alone. Else boxes of 128, 64 and 32 rows: a copy
+// costs the TMA unit more than its bytes (a half tile of 128 rows in one box instead of
+// four of 32: 350 -> 315 us for 8192 rows of 7168, F = 2048), so a half tile comes in one
+// box, or in two for 65 to 96 rows.
+struct Maps {
+  CUtensorMap map[3];
 };
 
 struct Tile {
@@ -134,7 +144,7 @@ __device__ __forceinline__ void epilogue_barrier() {
 template <Form kForm, int kAct>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_kernel(const __grid_constant__ CUtensorMap a_map,
-                  const __grid_constant__ CUtensorMap b_map, const Params p) {
+                  const __grid_constant__ Maps b_maps, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full_bar[kMaxStages];   // even CTA: both CTAs' stage landed
   __shared__ uint64_t empty_bar[kMaxStages];  // stage consumed by the pair's MMAs
@@ -173,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_flag = 0;
     mbar_fence_init();
     tma_prefetch_map(&a_map);
-    tma_prefetch_map(&b_map);
+    tma_prefetch_map(&b_maps.map[0]);
   }
   if (warp == 1) tmem_alloc_pair(smem_u32(&tmem_slot), kTmemCols);
   pdl_wait();
@@ -208,8 +218,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nkb = blocks_of(t);
         const int half = width_of(t) / 2;
         const int row0 = t.row0 + rank * half;
-        const int boxes = kForm == kWeights ? kRowBoxes : (half + 31) / 32;
-        const uint32_t bytes = kOperandBytes + static_cast<uint32_t>(boxes) * 4096u;
+        // Rows of the first box, and whether one of 32 rows follows.
+        const int box = half > 96 ? 128 : half > 32 ? 64 : 32;
+        const bool more = half > 64 && half <= 96;
+        const CUtensorMap* b_map = &b_maps.map[box == 128 ? 0 : box == 64 ? 1 : 2];
+        const uint32_t bytes =
+            kForm == kWeights ? kStageBytes
+                              : kOperandBytes + static_cast<uint32_t>(box + (more ? 32 : 0)) * 128u;
         for (int kb = 0; kb < nkb; ++kb) {
           if (!mbar_wait_cluster(smem_u32(&empty_bar[s]), (round & 1u) ^ 1u, p.err, abort_v,
                                  p.ring.limit_ns)) {
@@ -222,12 +237,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t bar = smem_u32(&tail_bar[s]);
             if (rank == 0) mbar_arrive(smem_u32(&full_bar[s]));
             mbar_arrive_expect_tx(bar, kStageBytes);
+            if (p.whole_a)
+              tma_load_3d(a, &a_map, bar, 0, t.row0 + kb * kBlockK, (t.m0 + rank * 128) / 64);
+            if (p.whole_b)
+              tma_load_3d(b, b_maps.map, bar, 0, t.row0 + kb * kBlockK, (t.c0 + rank * 128) / 64);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              tma_load_2d(a + 8192u * j, &a_map, bar, t.m0 + rank * 128 + 64 * j,
-                          t.row0 + kb * kBlockK);
-              tma_load_2d(b + 8192u * j, &b_map, bar, t.c0 + rank * 128 + 64 * j,
-                          t.row0 + kb * kBlockK);
+              if (!p.whole_a)
+                tma_load_2d(a + 8192u * j, &a_map, bar, t.m0 + rank * 128 + 64 * j,
+                            t.row0 + kb * kBlockK);
+              if (!p.whole_b)
+                tma_load_2d(b + 8192u * j, b_maps.map, bar, t.c0 + rank * 128 + 64 * j,
+                            t.row0 + kb * kBlockK);
             }
             tails |= 1u << s;
             tail_phase ^= 1u << s;
@@ -239,22 +260,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else if constexpr (kForm == kRows) {
               tma_load_3d_pair(a, &a_map, bar, kb * kBlockK, t.m0 + rank * 128, t.e);
             } else if constexpr (kForm == kRowsT) {
+              if (p.whole_a) {
+                tma_load_4d_pair(a, &a_map, bar, 0, kb * kBlockK, (t.m0 + rank * 128) / 64, t.e);
+              } else {
 #pragma unroll
-              for (int j = 0; j < 2; ++j)
-                tma_load_3d_pair(a + 8192u * j, &a_map, bar, t.m0 + rank * 128 + 64 * j,
-                                 kb * kBlockK, t.e);
+                for (int j = 0; j < 2; ++j)
+                  tma_load_3d_pair(a + 8192u * j, &a_map, bar, t.m0 + rank * 128 + 64 * j,
+                                   kb * kBlockK, t.e);
+              }
             } else {
+              if (p.whole_a)
+                tma_load_3d_pair(a, &a_map, bar, 0, t.row0 + kb * kBlockK,
+                                 (t.m0 + rank * 128) / 64);
+              if (p.whole_b)
+                tma_load_3d_pair(b, b_maps.map, bar, 0, t.row0 + kb * kBlockK,
+                                 (t.c0 + rank * 128) / 64);
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                tma_load_2d_pair(a + 8192u * j, &a_map, bar, t.m0 + rank * 128 + 64 * j,
-                                 t.row0 + kb * kBlockK);
-                tma_load_2d_pair(b + 8192u * j, &b_map, bar, t.c0 + rank * 128 + 64 * j,
-                                 t.row0 + kb * kBlockK);
+                if (!p.whole_a)
+                  tma_load_2d_pair(a + 8192u * j, &a_map, bar, t.m0 + rank * 128 + 64 * j,
+                                   t.row0 + kb * kBlockK);
+                if (!p.whole_b)
+                  tma_load_2d_pair(b + 8192u * j, b_maps.map, bar, t.c0 + rank * 128 + 64 * j,
+                                   t.row0 + kb * kBlockK);
               }
             }
             if constexpr (kForm != kWeights) {
-              for (int j = 0; j < boxes; ++j)
-                tma_load_2d_pair(b + 4096u * j, &b_map, bar, kb * kBlockK, row0 + 32 * j);
+              tma_load_2d_pair(b, b_map, bar, kb * kBlockK, row0);
+              if (more)
+                tma_load_2d_pair(b + 8192u, &b_maps.map[2], bar, kb * kBlockK, row0 + 64);
             }
           }
           ++issued;
@@ -589,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-typedef void (*Kernel)(const CUtensorMap, const CUtensorMap, const Params);
+typedef void (*Kernel)(const CUtensorMap, const Maps, const Params);
 
 constexpr Kernel kKernels[] = {
     expert_kernel<kGated, kActSilu>, expert_kernel<kGated, kActGelu>,
@@ -598,8 +632,8 @@ constexpr Kernel kKernels[] = {
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-cudaError_t launch(Kernel kernel, Form form, const CUtensorMap& a_map, const CUtensorMap& b_map,
-                   Params p, int64_t most_tiles, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch(Kernel kernel, Form form, const CUtensorMap& a_map, const Maps& b_maps, Params p,
+                   int64_t most_tiles, const DeviceInfo& dev, cudaStream_t stream) {
   p.err = dev.err_word;
   p.turn = turn_bytes(form, p.saved_kind);
   // As many stages as fit beside the chunks, the experts' table and static shared memory.
@@ -609,7 +643,7 @@ cudaError_t launch(Kernel kernel, Form form, const CUtensorMap& a_map, const CUt
                       experts_table_bytes(p.E);
   const int pairs = static_cast<int>(std::min<int64_t>(dev.num_sms / 2, most_tiles));
   return launch_dependent_clusters(2, kernel, dim3(2 * pairs), dim3(kThreads), smem, stream,
-                                   a_map, b_map, p);
+                                   a_map, b_maps, p);
 }
 
 // Most tiles of N rows and E experts in passes of 256 rows.
@@ -617,15 +651,30 @@ int64_t most_row_tiles(int N, int E, int mblocks) {
   return (static_cast<int64_t>(std::min(N, E)) + N / kTileRows) * mblocks;
 }
 
-// Rows [N, cols] in boxes of 64 columns.
-bool rows_map(CUtensorMap* map, const void* base, int N, int cols, int box_rows) {
-  return make_map_bf16_sw128(map, base, N, cols, box_rows);
+// Rows [N, cols] in boxes of 64 columns and 128, 64 or 32 rows.
+bool rows_maps(Maps* maps, const void* base, int N, int cols) {
+  return make_map_bf16_sw128(&maps->map[0], base, N, cols, 128) &&
+         make_map_bf16_sw128(&maps->map[1], base, N, cols, 64) &&
+         make_map_bf16_sw128(&maps->map[2], base, N, cols, 32);
+}
+
+// Rows [N, cols] as an MN-major operand: 64 rows of 64 columns, or of two pieces of 64.
+bool sums_map(CUtensorMap* map, const void* base, int N, int cols, bool whole) {
+  return whole ? make_map_bf16_rows64(map, base, N, cols, 64, 2)
+               : make_map_bf16_sw128(map, base, N, cols, 64);
 }
 
 // Matrices [E, rows, cols] in boxes of 64 columns of one matrix.
-bool matrices_map(CUtensorMap* map, const void* base, int E, int rows, int cols, int box_rows) {
-  const uint64_t c = cols, r = rows;
-  const uint64_t dims[] = {c, r, static_cast<uint64_t>(E)};
+bool matrices_map(CUtensorMap* map, const void* base, int E, int rows, int cols, int box_rows,
+                  bool whole) {
+  const uint64_t c = cols, r = rows, n = E;
+  if (whole) {
+    const uint64_t dims[] = {64, r, c / 64, n};
+    const uint64_t strides[] = {c * 2, 128, r * c * 2};
+    const uint32_t box[] = {64, static_cast<uint32_t>(box_rows), 2, 1};
+    return make_map_bf16_nd(map, base, 4, dims, strides, box);
+  }
+  const uint64_t dims[] = {c, r, n};
   const uint64_t strides[] = {c * 2, r * c * 2};
   const uint32_t box[] = {64, static_cast<uint32_t>(box_rows), 1};
   return make_map_bf16_nd(map, base, 3, dims, strides, box);
@@ -663,11 +712,12 @@ cudaError_t launch_expert_gated(const ExpertGatedArgs& a, const DeviceInfo& dev,
   const uint64_t dims[] = {c, 8, 2, f / 8, static_cast<uint64_t>(a.E)};
   const uint64_t strides[] = {c * 2, f * c * 2, 8 * c * 2, 2 * f * c * 2};
   const uint32_t box[] = {64, 8, 2, 8, 1};
-  CUtensorMap w_map, x_map;
+  CUtensorMap w_map;
+  Maps x_maps;
   if (!make_map_bf16_nd(&w_map, a.weights, 5, dims, strides, box) ||
-      !rows_map(&x_map, a.x, a.N, a.C, 32))
+      !rows_maps(&x_maps, a.x, a.N, a.C))
     return cudaErrorInvalidValue;
-  return launch(kKernels[a.act == kActSilu ? 0 : 1], kGated, w_map, x_map, p,
+  return launch(kKernels[a.act == kActSilu ? 0 : 1], kGated, w_map, x_maps, p,
                 most_row_tiles(a.N, a.E, p.mblocks), dev, stream);
 }
 
@@ -682,13 +732,15 @@ cudaError_t launch_expert_rows(const ExpertRowsArgs& a, const DeviceInfo& dev,
   p.K = a.K;
   p.mblocks = ceil_div(a.M, 256);
   p.ring = a.ring;
-  CUtensorMap w_map, x_map;
-  if (!(a.transposed ? matrices_map(&w_map, a.weights, a.E, a.K, a.M, 64)
-                     : matrices_map(&w_map, a.weights, a.E, a.M, a.K, 128)) ||
-      !rows_map(&x_map, a.x, a.N, a.K, 32))
+  p.whole_a = a.transposed && a.M % 64 == 0;
+  CUtensorMap w_map;
+  Maps x_maps;
+  if (!(a.transposed ? matrices_map(&w_map, a.weights, a.E, a.K, a.M, 64, p.whole_a)
+                     : matrices_map(&w_map, a.weights, a.E, a.M, a.K, 128, false)) ||
+      !rows_maps(&x_maps, a.x, a.N, a.K))
     return cudaErrorInvalidValue;
   const Form form = a.transposed ? kRowsT : kRows;
-  return launch(kKernels[a.transposed ? 3 : 2], form, w_map, x_map, p,
+  return launch(kKernels[a.transposed ? 3 : 2], form, w_map, x_maps, p,
                 most_row_tiles(a.N, a.E, p.mblocks), dev, stream);
 }
 
@@ -704,10 +756,14 @@ cudaError_t launch_expert_weights(const ExpertWeightsArgs& a, const DeviceInfo& 
   p.mblocks = ceil_div(a.M, 256);
   p.cblocks = ceil_div(a.C, kTileRows);
   p.ring = a.ring;
-  CUtensorMap g_map, x_map;
-  if (!rows_map(&g_map, a.grad, a.N, a.M, 64) || !rows_map(&x_map, a.x, a.N, a.C, 64))
+  p.whole_a = a.M % 64 == 0;
+  p.whole_b = a.C % 64 == 0;
+  CUtensorMap g_map;
+  Maps x_maps{};
+  if (!sums_map(&g_map, a.grad, a.N, a.M, p.whole_a) ||
+      !sums_map(&x_maps.map[0], a.x, a.N, a.C, p.whole_b))
     return cudaErrorInvalidValue;
-  return launch(kKernels[4], kWeights, g_map, x_map, p,
+  return launch(kKernels[4], kWeights, g_map, x_maps, p,
                 static_cast<int64_t>(a.E) * p.mblocks * p.cblocks, dev, stream);
 }
 
