@@ -26,7 +26,7 @@
 // with zeros in shared memory before the MMA reads them.
 //
 // Persistent, warp-specialized, one CTA per SM, 7 warps:
-//   warp 0      producer: this CTA's operand boxes of a 64-deep block into a stage ring
+//   warp 0      producer: this CTA's operand boxes of a 128-deep block into a stage ring
 //   warp 1      TMEM allocation; in the even CTA the MMA issuer
 //   warps 2..5  epilogue; two accumulators, so the next tile's MMAs run meanwhile. The
 //               lanes of TMEM are columns of the result: 32 rows at a time are turned
@@ -43,10 +43,16 @@ namespace {
 enum Form { kGated, kRows, kRowsT, kWeights };
 
 constexpr int kTileRows = 256;      // MMA N: rows of an expert (kWeights: columns)
-constexpr int kBlockK = 64;
-constexpr uint32_t kOperandBytes = 128 * kBlockK * 2;
+// Depth of a stage: two pieces of 64, the span of a 128-byte swizzled row. A copy costs
+// the TMA unit more than its bytes, so a stage is deep and each operand comes in one copy
+// of two pieces where its width is a multiple of 64 (8192 rows of 7168, 4096 columns:
+// 347 us with stages of 64 and rows in boxes of 32, 307 with one box, 278 with stages of
+// 128 in one copy per operand).
+constexpr int kBlockK = 128;
+constexpr uint32_t kPieceBytes = 128 * 128;  // 128 rows (or depths) of one piece
+constexpr uint32_t kOperandBytes = 2 * kPieceBytes;
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 3;
 constexpr int kThreads = 224;
 constexpr uint32_t kTmemCols = 512;  // two accumulators
 constexpr int kChunk = 32;           // rows turned over at a time
@@ -80,20 +86,17 @@ struct Params {
   int K;                 // depth of a sum (kWeights: columns of out)
   int mblocks, cblocks;
   int saved_kind;
-  // Whether one copy brings both 64-column boxes of an MN-major operand: where its width
-  // is a multiple of 64, so that a map may count the columns in such pieces.
+  // Whether one copy brings both 64-column pieces of an operand: where its width is a
+  // multiple of 64, so that a map may count the columns in pieces.
   bool whole_a, whole_b;
   int stages, turn;
   uint32_t* err;
   RingLimits ring;
 };
 
-// Maps of operand B. kWeights: the first alone. Else boxes of 128, 64 and 32 rows: a copy
-// costs the TMA unit more than its bytes (a half tile of 128 rows in one box instead of
-// four of 32: 350 -> 315 us for 8192 rows of 7168, F = 2048), so a half tile comes in one
-// box, or in two for 65 to 96 rows.
+// Maps of operand B. kWeights: the first alone. Else boxes of 32, 64, 96 and 128 rows.
 struct Maps {
-  CUtensorMap map[3];
+  CUtensorMap map[4];
 };
 
 struct Tile {
@@ -217,14 +220,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Tile t = tile_at<kForm>(p, tile, e, s_first, s_unit);
         const int nkb = blocks_of(t);
         const int half = width_of(t) / 2;
-        const int row0 = t.row0 + rank * half;
-        // Rows of the first box, and whether one of 32 rows follows.
-        const int box = half > 96 ? 128 : half > 32 ? 64 : 32;
-        const bool more = half > 64 && half <= 96;
-        const CUtensorMap* b_map = &b_maps.map[box == 128 ? 0 : box == 64 ? 1 : 2];
-        const uint32_t bytes =
-            kForm == kWeights ? kStageBytes
-                              : kOperandBytes + static_cast<uint32_t>(box + (more ? 32 : 0)) * 128u;
+        const int box = (half + 31) / 32;  // in 32 rows
+        const CUtensorMap* b_map = &b_maps.map[kForm == kWeights ? 0 : box - 1];
+        const uint32_t b_piece = kForm == kWeights ? kPieceBytes : box * 4096u;
+        const uint32_t bytes = kOperandBytes + 2 * b_piece;
         for (int kb = 0; kb < nkb; ++kb) {
           if (!mbar_wait_cluster(smem_u32(&empty_bar[s]), (round & 1u) ^ 1u, p.err, abort_v,
                                  p.ring.limit_ns)) {
@@ -232,63 +231,68 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t a = ring + static_cast<uint32_t>(s) * kStageBytes, b = a + kOperandBytes;
+          const int k0 = kb * kBlockK;
           if (kForm == kWeights && kb == nkb - 1 && needs_zeros(t)) {
             // Completes on this CTA's own barrier, for the warp that puts the zeros in.
             const uint32_t bar = smem_u32(&tail_bar[s]);
             if (rank == 0) mbar_arrive(smem_u32(&full_bar[s]));
             mbar_arrive_expect_tx(bar, kStageBytes);
-            if (p.whole_a)
-              tma_load_3d(a, &a_map, bar, 0, t.row0 + kb * kBlockK, (t.m0 + rank * 128) / 64);
-            if (p.whole_b)
-              tma_load_3d(b, b_maps.map, bar, 0, t.row0 + kb * kBlockK, (t.c0 + rank * 128) / 64);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (!p.whole_a)
-                tma_load_2d(a + 8192u * j, &a_map, bar, t.m0 + rank * 128 + 64 * j,
-                            t.row0 + kb * kBlockK);
-              if (!p.whole_b)
-                tma_load_2d(b + 8192u * j, b_maps.map, bar, t.c0 + rank * 128 + 64 * j,
-                            t.row0 + kb * kBlockK);
+            const int m = t.m0 + rank * 128, c = t.c0 + rank * 128, r = t.row0 + k0;
+            if (p.whole_a) {
+              tma_load_3d(a, &a_map, bar, 0, r, m / 64);
+            } else {
+              tma_load_2d(a, &a_map, bar, m, r);
+              tma_load_2d(a + kPieceBytes, &a_map, bar, m + 64, r);
+            }
+            if (p.whole_b) {
+              tma_load_3d(b, b_map, bar, 0, r, c / 64);
+            } else {
+              tma_load_2d(b, b_map, bar, c, r);
+              tma_load_2d(b + kPieceBytes, b_map, bar, c + 64, r);
             }
             tails |= 1u << s;
             tail_phase ^= 1u << s;
           } else {
             const uint32_t bar = map_to_rank(smem_u32(&full_bar[s]), 0);
             if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), 2 * bytes);
+            const int m = t.m0 + rank * (kForm == kGated ? 64 : 128);
             if constexpr (kForm == kGated) {
-              tma_load_5d_pair(a, &a_map, bar, kb * kBlockK, 0, 0, (t.m0 + rank * 64) / 8, t.e);
+              const int eight = t.e * (p.M / 4) + m / 8;  // eights of rows, all experts'
+              if (p.whole_a) {
+                tma_load_5d_pair(a, &a_map, bar, 0, 0, 0, eight, k0 / 64);
+              } else {
+                tma_load_4d_pair(a, &a_map, bar, k0, 0, 0, eight);
+                tma_load_4d_pair(a + kPieceBytes, &a_map, bar, k0 + 64, 0, 0, eight);
+              }
             } else if constexpr (kForm == kRows) {
-              tma_load_3d_pair(a, &a_map, bar, kb * kBlockK, t.m0 + rank * 128, t.e);
+              if (p.whole_a) {
+                tma_load_4d_pair(a, &a_map, bar, 0, m, k0 / 64, t.e);
+              } else {
+                tma_load_3d_pair(a, &a_map, bar, k0, m, t.e);
+                tma_load_3d_pair(a + kPieceBytes, &a_map, bar, k0 + 64, m, t.e);
+              }
             } else if constexpr (kForm == kRowsT) {
               if (p.whole_a) {
-                tma_load_4d_pair(a, &a_map, bar, 0, kb * kBlockK, (t.m0 + rank * 128) / 64, t.e);
+                tma_load_4d_pair(a, &a_map, bar, 0, k0, m / 64, t.e);
               } else {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  tma_load_3d_pair(a + 8192u * j, &a_map, bar, t.m0 + rank * 128 + 64 * j,
-                                   kb * kBlockK, t.e);
+                tma_load_3d_pair(a, &a_map, bar, m, k0, t.e);
+                tma_load_3d_pair(a + kPieceBytes, &a_map, bar, m + 64, k0, t.e);
               }
             } else {
-              if (p.whole_a)
-                tma_load_3d_pair(a, &a_map, bar, 0, t.row0 + kb * kBlockK,
-                                 (t.m0 + rank * 128) / 64);
-              if (p.whole_b)
-                tma_load_3d_pair(b, b_maps.map, bar, 0, t.row0 + kb * kBlockK,
-                                 (t.c0 + rank * 128) / 64);
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                if (!p.whole_a)
-                  tma_load_2d_pair(a + 8192u * j, &a_map, bar, t.m0 + rank * 128 + 64 * j,
-                                   t.row0 + kb * kBlockK);
-                if (!p.whole_b)
-                  tma_load_2d_pair(b + 8192u * j, b_maps.map, bar, t.c0 + rank * 128 + 64 * j,
-                                   t.row0 + kb * kBlockK);
+              if (p.whole_a) {
+                tma_load_3d_pair(a, &a_map, bar, 0, t.row0 + k0, m / 64);
+              } else {
+                tma_load_2d_pair(a, &a_map, bar, m, t.row0 + k0);
+                tma_load_2d_pair(a + kPieceBytes, &a_map, bar, m + 64, t.row0 + k0);
               }
             }
-            if constexpr (kForm != kWeights) {
-              tma_load_2d_pair(b, b_map, bar, kb * kBlockK, row0);
-              if (more)
-                tma_load_2d_pair(b + 8192u, &b_maps.map[2], bar, kb * kBlockK, row0 + 64);
+            // (kWeights: columns c of the rows from r on; else rows r, columns from k0 on)
+            const int c = t.c0 + rank * 128, r = t.row0 + (kForm == kWeights ? k0 : rank * half);
+            if (p.whole_b) {
+              tma_load_3d_pair(b, b_map, bar, 0, r, (kForm == kWeights ? c : k0) / 64);
+            } else {
+              tma_load_2d_pair(b, b_map, bar, kForm == kWeights ? c : k0, r);
+              tma_load_2d_pair(b + b_piece, b_map, bar, (kForm == kWeights ? c : k0) + 64, r);
             }
           }
           ++issued;
@@ -326,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idesc = umma_idesc_bf16(256, width_of(t)) |
                                (kForm == kRowsT || kForm == kWeights ? kUmmaTransposeA : 0u) |
                                (kForm == kWeights ? kUmmaTransposeB : 0u);
+        const uint32_t b_piece = static_cast<uint32_t>((width_of(t) / 2 + 31) / 32) * 4096u;
         for (int kb = 0; kb < nkb; ++kb) {
           if (!mbar_wait_cluster(smem_u32(&full_bar[s]), round & 1u, p.err, abort_v,
                                  p.ring.limit_ns)) {
@@ -333,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           int steps = kBlockK / 16;
-          if (kForm == kWeights && kb == nkb - 1) {
-            steps = (t.rows - kb * kBlockK + 15) >> 4;
+          if (kb == nkb - 1) {
+            steps = ((kForm == kWeights ? t.rows : p.K) - kb * kBlockK + 15) >> 4;
             if (needs_zeros(t)) {
               if (!mbar_wait_cluster(smem_u32(&fixed_bar[s]), fixed_phase >> s & 1u, p.err,
                                      abort_v, p.ring.limit_ns)) {
@@ -351,10 +356,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k < steps)
               umma_bf16_pair(
                   d,
-                  kForm == kRowsT || kForm == kWeights ? umma_desc_sw128_mn(a + 2048u * k)
-                                                       : umma_desc_sw128(a + 32u * k),
-                  kForm == kWeights ? umma_desc_sw128_mn(b + 2048u * k)
-                                    : umma_desc_sw128(b + 32u * k),
+                  kForm == kRowsT || kForm == kWeights
+                      ? umma_desc_sw128_mn(a + 2048u * k, kPieceBytes)
+                      : umma_desc_sw128(a + 32u * (k & 3) + kPieceBytes * (k >> 2)),
+                  kForm == kWeights ? umma_desc_sw128_mn(b + 2048u * k, kPieceBytes)
+                                    : umma_desc_sw128(b + 32u * (k & 3) + b_piece * (k >> 2)),
                   idesc, (kb | k) != 0 ? 1u : 0u);
           }
           umma_commit_pair(smem_u32(&empty_bar[s]), 0x3);
@@ -384,11 +390,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                   abort_v, p.ring.limit_ns));
         if (!alive) break;
         phase ^= 1u << s;
-        // Four 8 KB boxes of 64 rows of 128 bytes (the swizzle stays within a row).
+        // Four boxes of 128 rows of 128 bytes (the swizzle stays within a row).
         uint8_t* st = smem_raw + (ring - raw) + static_cast<uint32_t>(s) * kStageBytes;
         for (int i = lane; i < (to - from) * 32; i += 32) {
           const int row = from + (i >> 5), box = (i >> 3) & 3, piece = i & 7;
-          *reinterpret_cast<uint4*>(st + box * 8192 + row * 128 + piece * 16) =
+          *reinterpret_cast<uint4*>(st + box * kPieceBytes + row * 128 + piece * 16) =
               make_uint4(0, 0, 0, 0);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -522,12 +528,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint16_t*>(at + j * 2 * kKeptStride) =
                     static_cast<uint16_t>(pack_bf16x2(v[j], 0.f));
             } else if (p.saved_kind == kSaved8) {
-              // A group is the 16 lanes of one projection; features past F are zeros.
+              // A group is the 16 lanes of one projection. Behind the last feature the tile
+              // holds other rows' values; F is a multiple of 8, so half a group.
+              const bool past = t.m0 + rank * 64 + f >= p.M;
               uint8_t* at = buf + kKeptAt + half * kByteStride + f;
               uint8_t* eat = buf + kExponentsAt + half * 4 + q;
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
-                uint32_t top = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+                uint32_t top = past ? 0u : __float_as_uint(v[j]) & 0x7FFFFFFFu;
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
@@ -651,33 +659,55 @@ int64_t most_row_tiles(int N, int E, int mblocks) {
   return (static_cast<int64_t>(std::min(N, E)) + N / kTileRows) * mblocks;
 }
 
-// Rows [N, cols] in boxes of 64 columns and 128, 64 or 32 rows.
+// Whether one copy may bring two 64-column pieces of `cols` columns.
+bool whole(int cols) { return cols % 64 == 0; }
+
+// Rows [N, cols] in boxes of 32, 64, 96 and 128 rows.
 bool rows_maps(Maps* maps, const void* base, int N, int cols) {
-  return make_map_bf16_sw128(&maps->map[0], base, N, cols, 128) &&
-         make_map_bf16_sw128(&maps->map[1], base, N, cols, 64) &&
-         make_map_bf16_sw128(&maps->map[2], base, N, cols, 32);
+  for (int i = 0; i < 4; ++i)
+    if (!(whole(cols) ? make_map_bf16_rows64(&maps->map[i], base, N, cols, 32 * (i + 1), 2)
+                      : make_map_bf16_sw128(&maps->map[i], base, N, cols, 32 * (i + 1))))
+      return false;
+  return true;
 }
 
-// Rows [N, cols] as an MN-major operand: 64 rows of 64 columns, or of two pieces of 64.
-bool sums_map(CUtensorMap* map, const void* base, int N, int cols, bool whole) {
-  return whole ? make_map_bf16_rows64(map, base, N, cols, 64, 2)
-               : make_map_bf16_sw128(map, base, N, cols, 64);
+// Rows [N, cols] as an MN-major operand: 128 rows deep.
+bool sums_map(CUtensorMap* map, const void* base, int N, int cols) {
+  return whole(cols) ? make_map_bf16_rows64(map, base, N, cols, 128, 2)
+                     : make_map_bf16_sw128(map, base, N, cols, 128);
 }
 
-// Matrices [E, rows, cols] in boxes of 64 columns of one matrix.
-bool matrices_map(CUtensorMap* map, const void* base, int E, int rows, int cols, int box_rows,
-                  bool whole) {
+// Matrices [E, rows, cols] in boxes of 128 rows of one matrix.
+bool matrices_map(CUtensorMap* map, const void* base, int E, int rows, int cols) {
   const uint64_t c = cols, r = rows, n = E;
-  if (whole) {
+  if (whole(cols)) {
     const uint64_t dims[] = {64, r, c / 64, n};
     const uint64_t strides[] = {c * 2, 128, r * c * 2};
-    const uint32_t box[] = {64, static_cast<uint32_t>(box_rows), 2, 1};
+    const uint32_t box[] = {64, 128, 2, 1};
     return make_map_bf16_nd(map, base, 4, dims, strides, box);
   }
   const uint64_t dims[] = {c, r, n};
   const uint64_t strides[] = {c * 2, r * c * 2};
-  const uint32_t box[] = {64, static_cast<uint32_t>(box_rows), 1};
+  const uint32_t box[] = {64, 128, 1};
   return make_map_bf16_nd(map, base, 3, dims, strides, box);
+}
+
+// Gate and up rows in turns of eight: (pieces of) columns, 8 rows, gate or up, eights of
+// rows of all experts. The eights end F rows before the last row, so that the up rows
+// stay within the array; a tile's eights past an expert's F are other rows, whose results
+// are not stored.
+bool gated_map(CUtensorMap* map, const void* base, int E, int F, int C) {
+  const uint64_t c = C, f = F, eights = (2 * static_cast<uint64_t>(E) - 1) * f / 8;
+  if (whole(C)) {
+    const uint64_t dims[] = {64, 8, 2, eights, c / 64};
+    const uint64_t strides[] = {c * 2, f * c * 2, 8 * c * 2, 128};
+    const uint32_t box[] = {64, 8, 2, 8, 2};
+    return make_map_bf16_nd(map, base, 5, dims, strides, box);
+  }
+  const uint64_t dims[] = {c, 8, 2, eights};
+  const uint64_t strides[] = {c * 2, f * c * 2, 8 * c * 2};
+  const uint32_t box[] = {64, 8, 2, 8};
+  return make_map_bf16_nd(map, base, 4, dims, strides, box);
 }
 
 }  // namespace
@@ -706,16 +736,10 @@ cudaError_t launch_expert_gated(const ExpertGatedArgs& a, const DeviceInfo& dev,
   p.mblocks = ceil_div(a.F, 128);
   p.saved_kind = a.saved_kind;
   p.ring = a.ring;
-  // Gate and up rows in turns of eight: columns, 8 rows, gate or up, eights of features,
-  // experts.
-  const uint64_t c = a.C, f = a.F;
-  const uint64_t dims[] = {c, 8, 2, f / 8, static_cast<uint64_t>(a.E)};
-  const uint64_t strides[] = {c * 2, f * c * 2, 8 * c * 2, 2 * f * c * 2};
-  const uint32_t box[] = {64, 8, 2, 8, 1};
+  p.whole_a = p.whole_b = whole(a.C);
   CUtensorMap w_map;
   Maps x_maps;
-  if (!make_map_bf16_nd(&w_map, a.weights, 5, dims, strides, box) ||
-      !rows_maps(&x_maps, a.x, a.N, a.C))
+  if (!gated_map(&w_map, a.weights, a.E, a.F, a.C) || !rows_maps(&x_maps, a.x, a.N, a.C))
     return cudaErrorInvalidValue;
   return launch(kKernels[a.act == kActSilu ? 0 : 1], kGated, w_map, x_maps, p,
                 most_row_tiles(a.N, a.E, p.mblocks), dev, stream);
@@ -732,11 +756,12 @@ cudaError_t launch_expert_rows(const ExpertRowsArgs& a, const DeviceInfo& dev,
   p.K = a.K;
   p.mblocks = ceil_div(a.M, 256);
   p.ring = a.ring;
-  p.whole_a = a.transposed && a.M % 64 == 0;
+  p.whole_a = whole(a.transposed ? a.M : a.K);
+  p.whole_b = whole(a.K);
   CUtensorMap w_map;
   Maps x_maps;
-  if (!(a.transposed ? matrices_map(&w_map, a.weights, a.E, a.K, a.M, 64, p.whole_a)
-                     : matrices_map(&w_map, a.weights, a.E, a.M, a.K, 128, false)) ||
+  if (!(a.transposed ? matrices_map(&w_map, a.weights, a.E, a.K, a.M)
+                     : matrices_map(&w_map, a.weights, a.E, a.M, a.K)) ||
       !rows_maps(&x_maps, a.x, a.N, a.K))
     return cudaErrorInvalidValue;
   const Form form = a.transposed ? kRowsT : kRows;
@@ -756,12 +781,11 @@ cudaError_t launch_expert_weights(const ExpertWeightsArgs& a, const DeviceInfo& 
   p.mblocks = ceil_div(a.M, 256);
   p.cblocks = ceil_div(a.C, kTileRows);
   p.ring = a.ring;
-  p.whole_a = a.M % 64 == 0;
-  p.whole_b = a.C % 64 == 0;
+  p.whole_a = whole(a.M);
+  p.whole_b = whole(a.C);
   CUtensorMap g_map;
   Maps x_maps{};
-  if (!sums_map(&g_map, a.grad, a.N, a.M, p.whole_a) ||
-      !sums_map(&x_maps.map[0], a.x, a.N, a.C, p.whole_b))
+  if (!sums_map(&g_map, a.grad, a.N, a.M) || !sums_map(&x_maps.map[0], a.x, a.N, a.C))
     return cudaErrorInvalidValue;
   return launch(kKernels[4], kWeights, g_map, x_maps, p,
                 static_cast<int64_t>(a.E) * p.mblocks * p.cblocks, dev, stream);

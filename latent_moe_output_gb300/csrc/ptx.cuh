@@ -237,13 +237,13 @@ __device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t saddr) {
   return d;
 }
 
-// The same for an operand whose rows run along M or N (MN-major): boxes of 64 such
-// columns x 64 K rows, 128-byte swizzled, 8 K rows per 1024-byte atom, the next 64
-// columns 8 KB on. A step of 16 K rows moves `saddr` by 2048 bytes.
-__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t saddr) {
+// The same for an operand whose rows run along M or N (MN-major): pieces of 64 columns,
+// 128-byte swizzled, 8 K rows per 1024-byte atom, the next piece `piece` bytes on. A step
+// of 16 K rows moves `saddr` by 2048 bytes.
+__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t saddr, uint32_t piece) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);  // start address
-  d |= static_cast<uint64_t>(8192 >> 4) << 16;           // next 64 columns
+  d |= static_cast<uint64_t>(piece >> 4) << 16;          // next 64 columns
   d |= static_cast<uint64_t>(1024 >> 4) << 32;           // next 8 K rows
   d |= static_cast<uint64_t>(1) << 46;                   // descriptor version 1
   d |= static_cast<uint64_t>(2) << 61;                   // 128-byte swizzle
