@@ -569,7 +569,8 @@ LT_API lt_status latent_tail_expert_matmul_backward(const uint16_t* grad_out, co
  *                    NaN (its values are 0)
  * so that a value is off by at most 1/127 of its group's largest magnitude (half a unit;
  * the largest magnitude is at least 63.5 units). Groups below 2^-126 * 63.5 round to that
- * power of two.
+ * power of two. (Where the values are FP32, as in latent_tail_expert_gated, magnitudes
+ * below 2^-133 count as zeros.)
  *   x [T, C] bf16; values [T, C], exponents [T, ceil(C/16)].
  * Limits: 0 <= T <= 2^24, C a multiple of 8 from 8 to 65536.
  */

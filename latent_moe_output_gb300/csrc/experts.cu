@@ -25,13 +25,15 @@
 // the sum even against zeros. A warp of each CTA overwrites those rows of both operands
 // with zeros in shared memory before the MMA reads them.
 //
-// Persistent, warp-specialized, one CTA per SM, 7 warps:
+// Persistent, warp-specialized, one CTA per SM, 11 warps:
 //   warp 0      producer: this CTA's operand boxes of a 128-deep block into a stage ring
 //   warp 1      TMEM allocation; in the even CTA the MMA issuer
-//   warps 2..5  epilogue; two accumulators, so the next tile's MMAs run meanwhile. The
+//   warps 2..9  epilogue; two accumulators, so the next tile's MMAs run meanwhile. The
 //               lanes of TMEM are columns of the result: 32 rows at a time are turned
-//               over in shared memory and leave in 16-byte pieces of whole row parts
-//   warp 6      kWeights: the zeros above; else zeros in the rows that no expert owns
+//               over in shared memory and leave in 16-byte pieces of whole row parts.
+//               Two groups of four warps take every other 32 rows: one warp per scheduler
+//               waits for its own shuffles and reciprocals most of the time
+//   warp 10     kWeights: the zeros above; else zeros in the rows that no expert owns
 // Sums are FP32; results are rounded once.
 #include "experts.cuh"
 
@@ -53,7 +55,9 @@ constexpr uint32_t kPieceBytes = 128 * 128;  // 128 rows (or depths) of one piec
 constexpr uint32_t kOperandBytes = 2 * kPieceBytes;
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
 constexpr int kMaxStages = 3;
-constexpr int kThreads = 224;
+constexpr int kGroups = 2;           // of four epilogue warps
+constexpr int kSpareWarp = 2 + 4 * kGroups;
+constexpr int kThreads = 32 * (kSpareWarp + 1);
 constexpr uint32_t kTmemCols = 512;  // two accumulators
 constexpr int kChunk = 32;           // rows turned over at a time
 
@@ -68,8 +72,12 @@ constexpr int kByteStride = 80;    // per projection
 constexpr int kKeptAt = kChunk * kHiddenStride;
 constexpr int kExponentsAt = kKeptAt + kChunk * 2 * kByteStride;
 
+// kWeights: 32 rows of 32 bf16 for each warp.
+constexpr int kSumStride = 80;
+
+// Bytes for one group's chunk.
 constexpr int turn_bytes(Form form, int saved_kind) {
-  return form == kWeights ? 0
+  return form == kWeights ? 4 * 32 * kSumStride
          : form != kGated ? kChunk * kPlainStride
          : saved_kind == kSavedNone ? kKeptAt
          : saved_kind == kSavedBf16 ? kKeptAt + kChunk * 2 * kKeptStride
@@ -140,8 +148,8 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
   return true;
 }
 
-__device__ __forceinline__ void epilogue_barrier() {
-  asm volatile("bar.sync 1, 128;" ::: "memory");
+__device__ __forceinline__ void group_barrier(int group) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
 template <Form kForm, int kAct>
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ring = (raw + 1023u) & ~1023u;
   const int stages = p.stages;
   uint8_t* turn_ptr = smem_raw + (ring - raw) + static_cast<uint32_t>(stages) * kStageBytes;
-  int* s_first = reinterpret_cast<int*>(turn_ptr + 2 * p.turn);
+  int* s_first = reinterpret_cast<int*>(turn_ptr + kGroups * p.turn);
   int* s_unit = s_first + p.E + 1;
 
   if (threadIdx.x == 0) {
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&accf_bar[a]), 1);
-      mbar_init(smem_u32(&acce_bar[a]), 2 * 4);  // one arrival per epilogue warp of the pair
+      mbar_init(smem_u32(&acce_bar[a]), 2 * 4 * kGroups);  // one per epilogue warp of the pair
     }
     mbar_init(smem_u32(&drain_bar), 1);
     abort_flag = 0;
@@ -374,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 6) {
+  } else if (warp == kSpareWarp) {
     if constexpr (kForm == kWeights) {
       // ---------------- zeros behind an expert's last row ----------------
       int e = 0, it = 0;
@@ -424,9 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---------------- epilogue (warps 2..5) ----------------
+    // ---------------- epilogue (warps 2..9) ----------------
     const int q = warp & 3;  // the quarter of TMEM's lanes that this warp may access
-    const int tid = threadIdx.x - 64;
+    const int group = (warp - 2) >> 2;
+    const int tid = (threadIdx.x - 64) & 127;  // in the group
+    uint8_t* buf = turn_ptr + group * p.turn;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     auto release_acc = [&](int a) {  // accumulator read: back to the MMA issuer
       tc_fence_before();
@@ -439,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_remote(map_to_rank(bar, 0));
       }
     };
-    int e = 0, turn = 0;
+    int e = 0;
     uint32_t use = 0;
     bool alive = true;
     for (int tile = pair; alive && tile < tiles; tile += n_pairs) {
@@ -453,14 +463,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                            mbar_wait_cluster(smem_u32(&accf_bar[acc]), (use >> 1) & 1u, p.err,
                                              abort_v, p.ring.limit_ns));
         if constexpr (kForm != kWeights) {
-          uint32_t all;  // the warps turn rows over together
+          uint32_t all;  // a group's warps turn rows over together
           asm volatile(
               "{\n\t.reg .pred p, q;\n\t"
               "setp.ne.u32 p, %1, 0;\n\t"
-              "bar.red.and.pred q, 1, 128, p;\n\t"
+              "bar.red.and.pred q, %2, 128, p;\n\t"
               "selp.u32 %0, 1, 0, q;\n\t}"
               : "=r"(all)
-              : "r"(static_cast<uint32_t>(alive))
+              : "r"(static_cast<uint32_t>(alive)), "r"(1 + group)
               : "memory");
           alive = all != 0;
         }
@@ -470,33 +480,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int chunks = (width_of(t) + kChunk - 1) / kChunk;
       if constexpr (kForm == kWeights) {
-        // Lanes are rows of dW_e, columns of TMEM its columns.
-        const int m = t.m0 + rank * 128 + q * 32 + lane;
-        uint16_t* dst = p.out + (static_cast<size_t>(t.e) * p.M + m) * p.K + t.c0;
-        for (int ch = 0; ch < chunks; ++ch) {
+        // Lanes are rows of dW_e, columns of TMEM its columns. A lane's 64 bytes go through
+        // shared memory, so that a store is of 8 rows' 64 bytes and not of 32 rows' 16.
+        const int m0 = t.m0 + rank * 128 + q * 32;
+        uint16_t* dst = p.out + (static_cast<size_t>(t.e) * p.M + m0) * p.K + t.c0;
+        uint8_t* own = buf + q * 32 * kSumStride;
+        for (int ch = group; ch < chunks; ch += kGroups) {
           float v[32];
+          __syncwarp();  // the last chunk has been read
           if (any) {
-            __syncwarp();
             tmem_ld32(dcol + static_cast<uint32_t>(ch * kChunk), v);
-            if (ch == chunks - 1) release_acc(acc);
+            if (ch + kGroups >= chunks) release_acc(acc);
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
           }
-          if (m >= p.M) continue;
 #pragma unroll
           for (int g = 0; g < 4; ++g)
-            if (t.c0 + ch * kChunk + g * 8 < p.K)
-              *reinterpret_cast<uint4*>(dst + ch * kChunk + g * 8) =
-                  pack8(*reinterpret_cast<const float(*)[8]>(&v[g * 8]));
+            *reinterpret_cast<uint4*>(own + lane * kSumStride + g * 16) =
+                pack8(*reinterpret_cast<const float(*)[8]>(&v[g * 8]));
+          __syncwarp();
+          const int c = ch * kChunk + (lane & 3) * 8;
+          if (t.c0 + c < p.K) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = i * 8 + (lane >> 2);
+              if (m0 + r < p.M)
+                *reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * p.K + c) =
+                    *reinterpret_cast<const uint4*>(own + r * kSumStride + (lane & 3) * 16);
+            }
+          }
         }
       } else {
-        for (int ch = 0; ch < chunks; ++ch, ++turn) {
+        if (group >= chunks) release_acc(acc);
+        for (int ch = group; ch < chunks; ch += kGroups) {
           float v[32];
           __syncwarp();
           tmem_ld32(dcol + static_cast<uint32_t>(ch * kChunk), v);
-          if (ch == chunks - 1) release_acc(acc);
-          uint8_t* buf = turn_ptr + (turn & 1) * p.turn;
+          if (ch + kGroups >= chunks) release_acc(acc);
+          group_barrier(group);  // the last chunk has been read
           const int live = min(kChunk, t.rows - ch * kChunk);  // rows of the chunk
           const size_t row = static_cast<size_t>(t.row0) + ch * kChunk;
           if constexpr (kForm != kGated) {
@@ -505,8 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; ++j)
               *reinterpret_cast<uint16_t*>(at + j * kPlainStride) =
                   static_cast<uint16_t>(pack_bf16x2(v[j], 0.f));
-            epilogue_barrier();
-            // (the other buffer's turn ends at the next barrier)
+            group_barrier(group);
             const int m = t.m0 + rank * 128 + (tid & 15) * 8;
             if (m < p.M) {
 #pragma unroll
@@ -533,17 +554,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               const bool past = t.m0 + rank * 64 + f >= p.M;
               uint8_t* at = buf + kKeptAt + half * kByteStride + f;
               uint8_t* eat = buf + kExponentsAt + half * 4 + q;
+              // The exponent goes by the upper 16 bits of the largest magnitude: two
+              // columns' maxima in one word.
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                uint32_t top = past ? 0u : __float_as_uint(v[j]) & 0x7FFFFFFFu;
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                const uint32_t ex = exponent8(top);
-                at[j * 2 * kByteStride] =
-                    static_cast<uint8_t>(quantize8(v[j], ex, scale8(ex)) & 0xFF);
-                if ((lane & 23) == 0) eat[j * 8] = static_cast<uint8_t>(ex);
+              for (int j = 0; j < 32; j += 2) {
+                uint32_t top = past ? 0u
+                                    : __byte_perm(__float_as_uint(v[j]), __float_as_uint(v[j + 1]),
+                                                  0x7632) & 0x7FFF7FFFu;
+                top = __vmaxs2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = __vmaxs2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                top = __vmaxs2(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                top = __vmaxs2(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                const uint32_t e0 = exponent8(top & 0xFFFFu), e1 = exponent8(top >> 16);
+                at[j * 2 * kByteStride] = integer8(v[j], e0);
+                at[(j + 1) * 2 * kByteStride] = integer8(v[j + 1], e1);
+                if ((lane & 23) == 0) {
+                  eat[j * 8] = static_cast<uint8_t>(e0);
+                  eat[j * 8 + 8] = static_cast<uint8_t>(e1);
+                }
               }
             }
             uint8_t* at = buf + half * kHiddenStride + f * 2;
@@ -555,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint16_t*>(at + 2 * j * kHiddenStride) =
                   static_cast<uint16_t>(pack_bf16x2(h, 0.f));
             }
-            epilogue_barrier();
+            group_barrier(group);
             const int f0 = t.m0 + rank * 64;
             {
               const int c = (tid & 7) * 8;
@@ -645,9 +673,9 @@ cudaError_t launch(Kernel kernel, Form form, const CUtensorMap& a_map, const Map
   p.err = dev.err_word;
   p.turn = turn_bytes(form, p.saved_kind);
   // As many stages as fit beside the chunks, the experts' table and static shared memory.
-  const int rest = dev.max_smem_optin - 1024 - 1024 - 2 * p.turn - experts_table_bytes(p.E);
+  const int rest = dev.max_smem_optin - 1024 - 1024 - kGroups * p.turn - experts_table_bytes(p.E);
   p.stages = std::min(kMaxStages, rest / static_cast<int>(kStageBytes));
-  const size_t smem = 1024 + static_cast<size_t>(p.stages) * kStageBytes + 2 * p.turn +
+  const size_t smem = 1024 + static_cast<size_t>(p.stages) * kStageBytes + kGroups * p.turn +
                       experts_table_bytes(p.E);
   const int pairs = static_cast<int>(std::min<int64_t>(dev.num_sms / 2, most_tiles));
   return launch_dependent_clusters(2, kernel, dim3(2 * pairs), dim3(kThreads), smem, stream,

@@ -96,23 +96,27 @@ __device__ __forceinline__ void activation_grad(float g, float& a, float& d) {
 // zeros, e = 255 for a group that holds an infinity or a NaN (read back as NaNs).
 constexpr int kGroup8 = 16;
 
-// `top`: the largest magnitude as bits (NaN sorts above infinity, and that above all).
+// `top`: the upper 16 bits of the largest magnitude (as bf16 has them; NaN sorts above
+// infinity, and that above all). From 2^E up to 2^(E+1) it is 64 to 128 in units of
+// 2^(E-6); from 127.5 on, where it rounds to 128, the next unit is taken. That is where the
+// seven upper bits of the mantissa are ones, so adding one carries into the exponent.
 __device__ __forceinline__ uint32_t exponent8(uint32_t top) {
-  if (top >= 0x7F800000u) return 255u;
-  if (top == 0u) return 0u;
-  // 2^E <= top < 2^(E+1): in units of 2^(E-6) it rounds to 64 .. 127, or to 128 from
-  // 127.5 on, where the next unit is taken.
-  const int e = static_cast<int>(top >> 23) - 6 + ((top & 0x7FFFFFu) >= 0x7F0000u ? 1 : 0);
-  return static_cast<uint32_t>(max(e, 1));
+  const int e = max(static_cast<int>((top + 1u) >> 7) - 6, 1);
+  return top >= 0x7F80u ? 255u : top == 0u ? 0u : static_cast<uint32_t>(e);
 }
 
-// Factor from values to their integers; 0 for a group of zeros or one that is not finite.
+// Factor from values to their integers; 0 for a group that is not finite.
 __device__ __forceinline__ float scale8(uint32_t e) {
-  return e == 0u || e == 255u ? 0.f : __uint_as_float((254u - e) << 23);
+  return e == 255u ? 0.f : __uint_as_float((254u - e) << 23);
 }
 
-__device__ __forceinline__ int quantize8(float v, uint32_t e, float scale) {
-  return e == 255u ? 0 : __float2int_rn(v * scale);
+// Adding 1.5 * 2^23 rounds to an integer (to nearest even) and leaves it, in two's
+// complement, in the low bits.
+constexpr float kToInteger = 12582912.f;
+
+__device__ __forceinline__ uint8_t integer8(float v, uint32_t e) {
+  const uint32_t w = __float_as_uint(fmaf(v, scale8(e), kToInteger));
+  return static_cast<uint8_t>(e == 255u ? 0u : w & 0xFFu);
 }
 
 // Factor from integers back to values; NaN where e = 255 (0 times it is NaN).

@@ -17,10 +17,6 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// Adding 1.5 * 2^23 rounds to an integer (to nearest even) and leaves it, in two's
-// complement, in the low bits.
-constexpr float kToInteger = 12582912.f;
-
 // The integers of four values in one word.
 __device__ __forceinline__ uint32_t integers4(float a, float b, float c, float d, float scale) {
   const uint32_t w0 = __float_as_uint(fmaf(a, scale, kToInteger));
@@ -40,10 +36,12 @@ __device__ __forceinline__ void floats4(uint32_t w, float (&v)[4]) {
   v[3] = __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7443)) - 8388736.f;
 }
 
-__device__ __forceinline__ uint32_t top_of(const float (&v)[8], uint32_t top) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  return top;
+// Largest magnitudes of the even and of the odd values of eight, in one word.
+__device__ __forceinline__ uint32_t top_of(const uint4& v, uint32_t top) {
+  top = __vmaxs2(top, v.x & 0x7FFF7FFFu);
+  top = __vmaxs2(top, v.y & 0x7FFF7FFFu);
+  top = __vmaxs2(top, v.z & 0x7FFF7FFFu);
+  return __vmaxs2(top, v.w & 0x7FFF7FFFu);
 }
 
 // Group `i` of all rows: its first element and whether it has 16 columns (else 8).
@@ -73,7 +71,8 @@ __global__ void __launch_bounds__(kThreads) quantize8_kernel(const Quantize8Args
   float v[8], w[8];
   unpack8(lo, v);
   unpack8(hi, w);
-  const uint32_t e = exponent8(top_of(w, top_of(v, 0)));
+  const uint32_t top = top_of(hi, top_of(lo, 0u));
+  const uint32_t e = exponent8(max(top & 0xFFFFu, top >> 16));
   const float scale = scale8(e);
   uint4 q = make_uint4(integers4(v[0], v[1], v[2], v[3], scale),
                        integers4(v[4], v[5], v[6], v[7], scale),
