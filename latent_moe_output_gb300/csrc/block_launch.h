@@ -155,6 +155,9 @@ struct ExpertWeightsArgs {
   RingLimits ring;
 };
 
+// Whether experts_few.cu takes a call of N rows with E matrices of `blocks` times 32 rows.
+bool few_rows(const int32_t* offsets, int N, int E, int blocks, const DeviceInfo& dev);
+
 // The gradient at both projections, and the product again, from what was kept of them.
 struct GatedGradArgs {
   const uint16_t* grad_hidden;  // [N,F]
@@ -195,6 +198,8 @@ cudaError_t launch_expert_gated(const ExpertGatedArgs& a, const DeviceInfo& dev,
                                 cudaStream_t stream);
 cudaError_t launch_expert_rows(const ExpertRowsArgs& a, const DeviceInfo& dev,
                                cudaStream_t stream);
+cudaError_t launch_expert_gated_few(const ExpertGatedArgs& a, cudaStream_t stream);
+cudaError_t launch_expert_rows_few(const ExpertRowsArgs& a, cudaStream_t stream);
 cudaError_t launch_expert_weights(const ExpertWeightsArgs& a, const DeviceInfo& dev,
                                   cudaStream_t stream);
 cudaError_t launch_gated_grad(const GatedGradArgs& a, const DeviceInfo& dev, cudaStream_t stream);

@@ -8,8 +8,8 @@
 // The row counts of experts are ragged, those of weights are not. So the weights are
 // the MMA's M side, always 256 rows over a pair of CTAs (tcgen05 cta_group::2: each CTA
 // loads its own 128 weight rows and half of the other operand), and the rows of an
-// expert its N side, which an instruction takes in any multiple of 16 up to 256: an
-// expert of n rows computes about n + 8 of them, where tiles of 256 (128) rows on the M
+// expert its N side, which an instruction takes in any multiple of 32 up to 256: an
+// expert of n rows computes about n + 16 of them, where tiles of 256 (128) rows on the M
 // side would compute n + 128 (n + 64) on average. An expert's rows are cut into the
 // fewest tiles of at most 256, all of one size.
 //
@@ -53,8 +53,9 @@ constexpr int kTileRows = 256;      // MMA N: rows of an expert (kWeights: colum
 constexpr int kBlockK = 128;
 constexpr uint32_t kPieceBytes = 128 * 128;  // 128 rows (or depths) of one piece
 constexpr uint32_t kOperandBytes = 2 * kPieceBytes;
-constexpr uint32_t kStageBytes = 2 * kOperandBytes;
-constexpr int kMaxStages = 3;
+// Small tiles need less of operand B, and get more stages: a call of few tiles waits for
+// memory (16 rows of 7168, 4096 weight rows: 40 us with three stages, 31 with five).
+constexpr int kMaxStages = 5;
 constexpr int kGroups = 2;           // of four epilogue warps
 constexpr int kSpareWarp = 2 + 4 * kGroups;
 constexpr int kThreads = 32 * (kSpareWarp + 1);
@@ -93,11 +94,13 @@ struct Params {
   int M;                 // kGated: F; kRows, kRowsT: columns of out; kWeights: its rows
   int K;                 // depth of a sum (kWeights: columns of out)
   int mblocks, cblocks;
+  int tile_rows;         // most rows of a tile, at most kTileRows (kWeights: its columns)
+  int parts;             // pairs of a cluster, which share a tile's sum
   int saved_kind;
   // Whether one copy brings both 64-column pieces of an operand: where its width is a
   // multiple of 64, so that a map may count the columns in pieces.
   bool whole_a, whole_b;
-  int stages, turn;
+  int stages, stage_bytes, turn;
   uint32_t* err;
   RingLimits ring;
 };
@@ -111,7 +114,6 @@ struct Tile {
   int e, row0, rows, m0, c0;
 };
 
-__device__ __forceinline__ int passes(int n) { return (n + kTileRows - 1) / kTileRows; }
 
 // Tiles in order: the features of one pass over an expert's rows, then the next pass.
 // `e` moves forward only.
@@ -126,12 +128,13 @@ __device__ __forceinline__ Tile tile_at(const Params& p, int tile, int& e, const
     t.row0 = s_first[t.e];
     t.rows = s_first[t.e + 1] - t.row0;
     t.m0 = in / p.cblocks * 256;
-    t.c0 = in % p.cblocks * kTileRows;
+    t.c0 = in % p.cblocks * p.tile_rows;
   } else {
     const int unit = tile / p.mblocks;
     while (s_unit[e + 1] <= unit) ++e;
-    const int n = s_first[e + 1] - s_first[e], i = unit - s_unit[e], k = passes(n);
-    const int size = ((n + k - 1) / k + 15) & ~15;
+    const int n = s_first[e + 1] - s_first[e], i = unit - s_unit[e];
+    const int k = (n + p.tile_rows - 1) / p.tile_rows;
+    const int size = ((n + k - 1) / k + 31) & ~31;
     t.e = e;
     t.row0 = s_first[e] + i * size;
     t.rows = min(size, n - i * size);
@@ -166,16 +169,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t drain_bar;              // even CTA: MMAs before an abort are done
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
+  __shared__ int part_failed;  // a pair's sum did not come (first pair of a cluster)
   volatile int* abort_v = &abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_rank());
-  const int pair = static_cast<int>(blockIdx.x) >> 1;
-  const int n_pairs = static_cast<int>(gridDim.x) >> 1;
+  const int cta = static_cast<int>(cluster_rank());
+  const int rank = cta & 1, even = cta & ~1, part = cta >> 1;
+  const int cluster = static_cast<int>(blockIdx.x) / (2 * p.parts);
+  const int n_clusters = static_cast<int>(gridDim.x) / (2 * p.parts);
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
   const int stages = p.stages;
-  uint8_t* turn_ptr = smem_raw + (ring - raw) + static_cast<uint32_t>(stages) * kStageBytes;
+  uint8_t* turn_ptr = smem_raw + (ring - raw) + static_cast<uint32_t>(stages * p.stage_bytes);
   int* s_first = reinterpret_cast<int*>(turn_ptr + kGroups * p.turn);
   int* s_unit = s_first + p.E + 1;
 
@@ -192,30 +197,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&drain_bar), 1);
     abort_flag = 0;
+    part_failed = 0;
     mbar_fence_init();
     tma_prefetch_map(&a_map);
     tma_prefetch_map(&b_maps.map[0]);
   }
   if (warp == 1) tmem_alloc_pair(smem_u32(&tmem_slot), kTmemCols);
   pdl_wait();
-  load_experts(p.offsets, p.N, p.E, s_first, s_unit, [](int n) { return passes(n); });
+  load_experts(p.offsets, p.N, p.E, s_first, s_unit,
+               [&](int n) { return (n + p.tile_rows - 1) / p.tile_rows; });
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  const int tiles = kForm == kWeights ? p.E * p.mblocks * p.cblocks : s_unit[p.E] * p.mblocks;
+  int tiles = kForm == kWeights ? p.E * p.mblocks * p.cblocks : s_unit[p.E] * p.mblocks;
+  // Pairs that share a sum meet once: such a launch has a cluster for every tile.
+  if (p.parts > 1) tiles = min(tiles, n_clusters);
   // Blocks of a tile's sum, and whether the last one of kWeights needs zeros.
   auto blocks_of = [&](const Tile& t) {
     return ((kForm == kWeights ? t.rows : p.K) + kBlockK - 1) / kBlockK;
   };
+  // This pair's part of them.
+  auto first_block = [&](int nkb, int i) { return nkb * i / p.parts; };
   auto needs_zeros = [&](const Tile& t) { return kForm == kWeights && (t.rows & 15) != 0; };
   // Rows of an MMA's N side.
   auto width_of = [&](const Tile& t) {
-    return kForm == kWeights ? kTileRows : (t.rows + 15) & ~15;
+    return kForm == kWeights ? p.tile_rows : (t.rows + 31) & ~31;
   };
 
+  bool joined = false;  // whether this warp has met the others of the cluster for the sums
   if (warp == 0) {
     if (lane == 0) {
       // ---------------- producer (this CTA's halves) ----------------
@@ -224,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int issued = 0;
       const int copied = static_cast<int>(min(static_cast<int64_t>(tiles), p.ring.copied));
       bool alive = true;
-      for (int tile = pair; alive && tile < copied; tile += n_pairs) {
+      for (int tile = cluster; alive && tile < copied; tile += n_clusters) {
         const Tile t = tile_at<kForm>(p, tile, e, s_first, s_unit);
         const int nkb = blocks_of(t);
         const int half = width_of(t) / 2;
@@ -232,20 +244,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const CUtensorMap* b_map = &b_maps.map[kForm == kWeights ? 0 : box - 1];
         const uint32_t b_piece = kForm == kWeights ? kPieceBytes : box * 4096u;
         const uint32_t bytes = kOperandBytes + 2 * b_piece;
-        for (int kb = 0; kb < nkb; ++kb) {
+        for (int kb = first_block(nkb, part); kb < first_block(nkb, part + 1); ++kb) {
           if (!mbar_wait_cluster(smem_u32(&empty_bar[s]), (round & 1u) ^ 1u, p.err, abort_v,
                                  p.ring.limit_ns)) {
             alive = false;
             break;
           }
-          const uint32_t a = ring + static_cast<uint32_t>(s) * kStageBytes, b = a + kOperandBytes;
+          const uint32_t a = ring + static_cast<uint32_t>(s * p.stage_bytes), b = a + kOperandBytes;
           const int k0 = kb * kBlockK;
           if (kForm == kWeights && kb == nkb - 1 && needs_zeros(t)) {
             // Completes on this CTA's own barrier, for the warp that puts the zeros in.
             const uint32_t bar = smem_u32(&tail_bar[s]);
             if (rank == 0) mbar_arrive(smem_u32(&full_bar[s]));
-            mbar_arrive_expect_tx(bar, kStageBytes);
-            const int m = t.m0 + rank * 128, c = t.c0 + rank * 128, r = t.row0 + k0;
+            mbar_arrive_expect_tx(bar, 2 * kOperandBytes);
+            const int m = t.m0 + rank * 128, c = t.c0 + rank * half, r = t.row0 + k0;
             if (p.whole_a) {
               tma_load_3d(a, &a_map, bar, 0, r, m / 64);
             } else {
@@ -261,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tails |= 1u << s;
             tail_phase ^= 1u << s;
           } else {
-            const uint32_t bar = map_to_rank(smem_u32(&full_bar[s]), 0);
+            const uint32_t bar = map_to_rank(smem_u32(&full_bar[s]), even);
             if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), 2 * bytes);
             const int m = t.m0 + rank * (kForm == kGated ? 64 : 128);
             if constexpr (kForm == kGated) {
@@ -295,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             // (kWeights: columns c of the rows from r on; else rows r, columns from k0 on)
-            const int c = t.c0 + rank * 128, r = t.row0 + (kForm == kWeights ? k0 : rank * half);
+            const int c = t.c0 + rank * half, r = t.row0 + (kForm == kWeights ? k0 : rank * half);
             if (p.whole_b) {
               tma_load_3d_pair(b, b_map, bar, 0, r, (kForm == kWeights ? c : k0) / 64);
             } else {
@@ -325,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int e = 0, s = 0;
       uint32_t round = 0, fixed_phase = 0, use = 0;
       bool alive = true;
-      for (int tile = pair; alive && tile < tiles; tile += n_pairs) {
+      for (int tile = cluster; alive && tile < tiles; tile += n_clusters) {
         const Tile t = tile_at<kForm>(p, tile, e, s_first, s_unit);
         const int nkb = blocks_of(t);
         if (nkb == 0) continue;
@@ -339,7 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                (kForm == kRowsT || kForm == kWeights ? kUmmaTransposeA : 0u) |
                                (kForm == kWeights ? kUmmaTransposeB : 0u);
         const uint32_t b_piece = static_cast<uint32_t>((width_of(t) / 2 + 31) / 32) * 4096u;
-        for (int kb = 0; kb < nkb; ++kb) {
+        const int kb0 = first_block(nkb, part);
+        for (int kb = kb0; kb < first_block(nkb, part + 1); ++kb) {
           if (!mbar_wait_cluster(smem_u32(&full_bar[s]), round & 1u, p.err, abort_v,
                                  p.ring.limit_ns)) {
             alive = false;
@@ -358,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           tc_fence_after();
-          const uint32_t a = ring + static_cast<uint32_t>(s) * kStageBytes, b = a + kOperandBytes;
+          const uint32_t a = ring + static_cast<uint32_t>(s * p.stage_bytes), b = a + kOperandBytes;
 #pragma unroll
           for (int k = 0; k < kBlockK / 16; ++k) {
             if (k < steps)
@@ -369,15 +382,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                       : umma_desc_sw128(a + 32u * (k & 3) + kPieceBytes * (k >> 2)),
                   kForm == kWeights ? umma_desc_sw128_mn(b + 2048u * k, kPieceBytes)
                                     : umma_desc_sw128(b + 32u * (k & 3) + b_piece * (k >> 2)),
-                  idesc, (kb | k) != 0 ? 1u : 0u);
+                  idesc, kb != kb0 || k != 0 ? 1u : 0u);
           }
-          umma_commit_pair(smem_u32(&empty_bar[s]), 0x3);
+          umma_commit_pair(smem_u32(&empty_bar[s]), 0x3 << even);
           if (++s == stages) {
             s = 0;
             ++round;
           }
         }
-        umma_commit_pair(smem_u32(&accf_bar[acc]), 0x3);
+        umma_commit_pair(smem_u32(&accf_bar[acc]), 0x3 << even);
         ++use;
       }
     }
@@ -388,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int e = 0, it = 0;
       uint32_t phase = 0;
       bool alive = true;
-      for (int tile = pair; alive && tile < tiles; tile += n_pairs) {
+      for (int tile = cluster; alive && tile < tiles; tile += n_clusters) {
         const Tile t = tile_at<kForm>(p, tile, e, s_first, s_unit);
         it += blocks_of(t);
         if (!needs_zeros(t)) continue;
@@ -399,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!alive) break;
         phase ^= 1u << s;
         // Four boxes of 128 rows of 128 bytes (the swizzle stays within a row).
-        uint8_t* st = smem_raw + (ring - raw) + static_cast<uint32_t>(s) * kStageBytes;
+        uint8_t* st = smem_raw + (ring - raw) + static_cast<uint32_t>(s * p.stage_bytes);
         for (int i = lane; i < (to - from) * 32; i += 32) {
           const int row = from + (i >> 5), box = (i >> 3) & 3, piece = i & 7;
           *reinterpret_cast<uint4*>(st + box * kPieceBytes + row * 128 + piece * 16) =
@@ -409,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           const uint32_t bar = smem_u32(&fixed_bar[s]);
-          mbar_arrive_remote(map_to_rank(bar, 0));
+          mbar_arrive_remote(map_to_rank(bar, even));
         }
       }
     } else {
@@ -446,13 +459,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rank == 0)
           mbar_arrive(bar);
         else
-          mbar_arrive_remote(map_to_rank(bar, 0));
+          mbar_arrive_remote(map_to_rank(bar, even));
       }
     };
     int e = 0;
     uint32_t use = 0;
     bool alive = true;
-    for (int tile = pair; alive && tile < tiles; tile += n_pairs) {
+    for (int tile = cluster; alive && tile < tiles; tile += n_clusters) {
       const Tile t = tile_at<kForm>(p, tile, e, s_first, s_unit);
       const bool any = blocks_of(t) != 0;
       const int acc = static_cast<int>(use & 1u);
@@ -473,12 +486,38 @@ __global__ void __launch_bounds__(kThreads, 1)
               : "r"(static_cast<uint32_t>(alive)), "r"(1 + group)
               : "memory");
           alive = all != 0;
+          if (p.parts > 1) {
+            // All pairs' products are done, so the first pair's stages are free: the others
+            // put their sums there, [row][lane] for each pair and CTA.
+            __syncwarp();
+            cluster_sync();
+            const int nt = width_of(t);
+            if (part > 0 && alive) {
+              tc_fence_after();
+              const uint32_t to = map_to_rank(
+                  ring + (static_cast<uint32_t>(part - 1) * nt * 128 + q * 32 + lane) * 4, rank);
+              for (int ch = group; ch * kChunk < nt; ch += kGroups) {
+                float v[32];
+                __syncwarp();
+                tmem_ld32(dcol + static_cast<uint32_t>(ch * kChunk), v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  st_dsmem_f32(to + static_cast<uint32_t>(ch * kChunk + j) * 512, v[j]);
+              }
+            } else if (part > 0 && lane == 0) {
+              st_dsmem_u32(map_to_rank(smem_u32(&part_failed), rank), 1);
+            }
+            __syncwarp();
+            cluster_sync();
+            joined = true;
+            if (part > 0 || *const_cast<volatile int*>(&part_failed) != 0) break;
+          }
         }
         if (!alive) break;
         tc_fence_after();
         ++use;
       }
-      const int chunks = (width_of(t) + kChunk - 1) / kChunk;
+      const int chunks = width_of(t) / kChunk;
       if constexpr (kForm == kWeights) {
         // Lanes are rows of dW_e, columns of TMEM its columns. A lane's 64 bytes go through
         // shared memory, so that a store is of 8 rows' 64 bytes and not of 32 rows' 16.
@@ -518,6 +557,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           tmem_ld32(dcol + static_cast<uint32_t>(ch * kChunk), v);
           if (ch + kGroups >= chunks) release_acc(acc);
+          if (p.parts > 1) {  // the other pairs' sums, in their order
+            const int nt = width_of(t);
+            const float* from = reinterpret_cast<const float*>(smem_raw + (ring - raw)) +
+                                ch * kChunk * 128 + q * 32 + lane;
+            for (int i = 1; i < p.parts; ++i, from += nt * 128)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] += from[j * 128];
+          }
           group_barrier(group);  // the last chunk has been read
           const int live = min(kChunk, t.rows - ch * kChunk);  // rows of the chunk
           const size_t row = static_cast<size_t>(t.row0) + ch * kChunk;
@@ -641,6 +688,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if (kForm != kWeights && p.parts > 1 && !joined) {
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
+  }
   // Neither CTA may leave while the pair's MMAs could still read its shared memory or
   // write its TMEM, or while its peer could still signal it.
   tc_fence_before();
@@ -648,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   if (warp == 1 && rank == 0 && *abort_v && lane == 0) {
     // The MMAs issued before the abort: a commit behind them, waited for.
-    umma_commit_pair(smem_u32(&drain_bar), 0x1);
+    umma_commit_pair(smem_u32(&drain_bar), 0x1 << even);
     wait_drain(smem_u32(&drain_bar), 0);
   }
   __syncwarp();
@@ -667,24 +719,92 @@ constexpr Kernel kKernels[] = {
     expert_kernel<kWeights, kActSilu>};
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-cudaError_t launch(Kernel kernel, Form form, const CUtensorMap& a_map, const Maps& b_maps, Params p,
-                   int64_t most_tiles, const DeviceInfo& dev, cudaStream_t stream) {
-  p.err = dev.err_word;
-  p.turn = turn_bytes(form, p.saved_kind);
-  // As many stages as fit beside the chunks, the experts' table and static shared memory.
-  const int rest = dev.max_smem_optin - 1024 - 1024 - kGroups * p.turn - experts_table_bytes(p.E);
-  p.stages = std::min(kMaxStages, rest / static_cast<int>(kStageBytes));
-  const size_t smem = 1024 + static_cast<size_t>(p.stages) * kStageBytes + kGroups * p.turn +
-                      experts_table_bytes(p.E);
-  const int pairs = static_cast<int>(std::min<int64_t>(dev.num_sms / 2, most_tiles));
-  return launch_dependent_clusters(2, kernel, dim3(2 * pairs), dim3(kThreads), smem, stream,
-                                   a_map, b_maps, p);
+// Clusters of 2, 4 and 8 CTAs that are resident at once, by device (set_up has the lock).
+constexpr int kMaxDevices = 64;
+int g_clusters[kMaxDevices][3];
+
+int resident(const DeviceInfo& dev, int parts) {
+  return g_clusters[dev.device][parts == 1 ? 0 : parts == 2 ? 1 : 2];
 }
 
-// Most tiles of N rows and E experts in passes of 256 rows.
-int64_t most_row_tiles(int N, int E, int mblocks) {
-  return (static_cast<int64_t>(std::min(N, E)) + N / kTileRows) * mblocks;
+// How a call is cut: rows (kWeights: columns) of a tile and pairs that share a sum.
+struct Cut {
+  int tile_rows, parts;
+  int64_t tiles;  // at most
+};
+
+// Cycles of one tile: its blocks take the longer of the MMAs (four cycles a row) and of
+// what a CTA can take in (64 bytes a cycle; 700 cycles where little is in flight), and a
+// tile beyond that what it takes to begin and to end.
+int64_t tile_cycles(int blocks, int rows, int parts) {
+  const int half_boxes = (rows / 2 + 31) / 32;
+  const int64_t block = std::max({4 * rows, 512 + 128 * half_boxes, 700});
+  return ceil_div(blocks, parts) * block + 4000 + 8 * rows + (parts > 1 ? 3000 + 16 * rows : 0);
+}
+
+// `tiles(rows)` for tiles of at most `rows` rows. Whole waves count: as many tiles as pairs
+// are resident run at once. (777 rows of 2000 against 5128 weight columns: four tiles of 208
+// rows and 21 of columns take two waves of 76, seven of 112 two shorter ones.)
+template <typename Tiles>
+Cut cut(const DeviceInfo& dev, int blocks, int most_rows, int most_parts, Tiles tiles) {
+  Cut best{};
+  int64_t best_cycles = INT64_MAX;
+  for (int rows = std::min(kTileRows, most_rows); rows >= 64 || best_cycles == INT64_MAX;
+       rows -= 32)
+    for (int parts = 1; parts <= most_parts && parts <= blocks; parts *= 2) {
+      const int64_t n = tiles(rows), at_once = std::max(1, resident(dev, parts));
+      if (parts > 1 && (n > at_once || (parts - 1) * rows > 3 * 128)) continue;
+      const int64_t cycles = ceil_div(n, at_once) * tile_cycles(blocks, rows, parts);
+      if (cycles < best_cycles) {
+        best_cycles = cycles;
+        best = Cut{rows, parts, n};
+      }
+    }
+  return best;
+}
+
+// Most tiles of N rows and E experts in passes of `rows` rows.
+int64_t most_row_tiles(int N, int E, int mblocks, int rows) {
+  return (static_cast<int64_t>(std::min(N, E)) + N / rows) * mblocks;
+}
+
+Cut cut_rows(const DeviceInfo& dev, const int32_t* offsets, int N, int E, int mblocks, int K) {
+  const int all = (std::min(N, kTileRows) + 31) & ~31;
+  if (offsets == nullptr)  // tiles of one size, as the kernel cuts them
+    return cut(dev, ceil_div(K, kBlockK), all, 4, [&](int rows) {
+      return static_cast<int64_t>(ceil_div(N, rows)) * mblocks;
+    });
+  // The experts' counts are not known here: full tiles, and several pairs per sum where
+  // even the most tiles that there can be leave pairs idle.
+  Cut c{all, 1, most_row_tiles(N, E, mblocks, all)};
+  for (int parts = 2; parts <= 4 && parts <= ceil_div(K, kBlockK); parts *= 2)
+    if (c.tiles <= resident(dev, parts) && (parts - 1) * all <= 3 * 128) c.parts = parts;
+  return c;
+}
+
+cudaError_t launch(Kernel kernel, Form form, const CUtensorMap& a_map, const Maps& b_maps, Params p,
+                   const Cut& c, const DeviceInfo& dev, cudaStream_t stream) {
+  p.err = dev.err_word;
+  p.turn = turn_bytes(form, p.saved_kind);
+  p.tile_rows = c.tile_rows;
+  p.parts = c.parts;
+  const int half = form == kWeights ? 128 : (c.tile_rows / 2 + 31) / 32 * 32;
+  p.stage_bytes = kOperandBytes + half * 256;
+  // As many stages as fit beside the chunks, the experts' table and static shared memory.
+  const int rest = dev.max_smem_optin - 1024 - 1024 - kGroups * p.turn - experts_table_bytes(p.E);
+  p.stages = std::min(kMaxStages, rest / p.stage_bytes);
+  const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + kGroups * p.turn +
+                      experts_table_bytes(p.E);
+  // The other pairs' sums of a tile fit into the stages.
+  if ((c.parts - 1) * c.tile_rows * 512 > p.stages * p.stage_bytes) {
+    p.parts = 1;
+  }
+  const int clusters = static_cast<int>(
+      p.parts > 1 ? c.tiles : std::min<int64_t>(resident(dev, 1), c.tiles));
+  return launch_dependent_clusters(2 * p.parts, kernel, dim3(2 * p.parts * clusters),
+                                   dim3(kThreads), smem, stream, a_map, b_maps, p);
 }
 
 // Whether one copy may bring two 64-column pieces of `cols` columns.
@@ -700,9 +820,9 @@ bool rows_maps(Maps* maps, const void* base, int N, int cols) {
 }
 
 // Rows [N, cols] as an MN-major operand: 128 rows deep.
-bool sums_map(CUtensorMap* map, const void* base, int N, int cols) {
-  return whole(cols) ? make_map_bf16_rows64(map, base, N, cols, 128, 2)
-                     : make_map_bf16_sw128(map, base, N, cols, 128);
+bool sums_map(CUtensorMap* map, const void* base, int N, int cols, bool pieces) {
+  return pieces ? make_map_bf16_rows64(map, base, N, cols, 128, 2)
+                : make_map_bf16_sw128(map, base, N, cols, 128);
 }
 
 // Matrices [E, rows, cols] in boxes of 128 rows of one matrix.
@@ -747,11 +867,31 @@ cudaError_t setup_experts(const DeviceInfo& dev) {
         dev.max_smem_optin - 1024);
     if (e != cudaSuccess) return e;
   }
+  // (clusters of several pairs do not always fill every SM: the parts of the GPU that a
+  // cluster has to lie in do not all have a multiple of its size)
+  for (int i = 0; i < 3; ++i) {
+    const unsigned ctas = 2u << i;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms) / ctas * ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(dev.max_smem_optin) - 1024;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kKernels[2], &cfg);
+    if (e != cudaSuccess) return e;
+    g_clusters[dev.device][i] = std::min(n, dev.num_sms / static_cast<int>(ctas));
+  }
   return cudaSuccess;
 }
 
 cudaError_t launch_expert_gated(const ExpertGatedArgs& a, const DeviceInfo& dev,
                                 cudaStream_t stream) {
+  if (few_rows(a.offsets, a.N, a.E, ceil_div(a.F, 16), dev)) return launch_expert_gated_few(a, stream);
   Params p{};
   p.offsets = a.offsets;
   p.out = a.hidden;
@@ -770,11 +910,13 @@ cudaError_t launch_expert_gated(const ExpertGatedArgs& a, const DeviceInfo& dev,
   if (!gated_map(&w_map, a.weights, a.E, a.F, a.C) || !rows_maps(&x_maps, a.x, a.N, a.C))
     return cudaErrorInvalidValue;
   return launch(kKernels[a.act == kActSilu ? 0 : 1], kGated, w_map, x_maps, p,
-                most_row_tiles(a.N, a.E, p.mblocks), dev, stream);
+                cut_rows(dev, a.offsets, a.N, a.E, p.mblocks, a.C), dev, stream);
 }
 
 cudaError_t launch_expert_rows(const ExpertRowsArgs& a, const DeviceInfo& dev,
                                cudaStream_t stream) {
+  if (!a.transposed && few_rows(a.offsets, a.N, a.E, ceil_div(a.M, 32), dev))
+    return launch_expert_rows_few(a, stream);
   Params p{};
   p.offsets = a.offsets;
   p.out = a.out;
@@ -794,7 +936,7 @@ cudaError_t launch_expert_rows(const ExpertRowsArgs& a, const DeviceInfo& dev,
     return cudaErrorInvalidValue;
   const Form form = a.transposed ? kRowsT : kRows;
   return launch(kKernels[a.transposed ? 3 : 2], form, w_map, x_maps, p,
-                most_row_tiles(a.N, a.E, p.mblocks), dev, stream);
+                cut_rows(dev, a.offsets, a.N, a.E, p.mblocks, a.K), dev, stream);
 }
 
 cudaError_t launch_expert_weights(const ExpertWeightsArgs& a, const DeviceInfo& dev,
@@ -807,16 +949,19 @@ cudaError_t launch_expert_weights(const ExpertWeightsArgs& a, const DeviceInfo& 
   p.M = a.M;
   p.K = a.C;
   p.mblocks = ceil_div(a.M, 256);
-  p.cblocks = ceil_div(a.C, kTileRows);
+  const int mean = ceil_div(a.N, a.E);
+  const Cut c = cut(dev, ceil_div(mean, kBlockK), (a.C + 31) & ~31, 1, [&](int cols) {
+    return static_cast<int64_t>(a.E) * p.mblocks * ceil_div(a.C, cols);
+  });
+  p.cblocks = ceil_div(a.C, c.tile_rows);
   p.ring = a.ring;
   p.whole_a = whole(a.M);
-  p.whole_b = whole(a.C);
+  p.whole_b = whole(a.C) && c.tile_rows % 128 == 0;  // (a half begins at a whole piece)
   CUtensorMap g_map;
   Maps x_maps{};
-  if (!sums_map(&g_map, a.grad, a.N, a.M) || !sums_map(&x_maps.map[0], a.x, a.N, a.C))
+  if (!sums_map(&g_map, a.grad, a.N, a.M, p.whole_a) || !sums_map(&x_maps.map[0], a.x, a.N, a.C, p.whole_b))
     return cudaErrorInvalidValue;
-  return launch(kKernels[4], kWeights, g_map, x_maps, p,
-                static_cast<int64_t>(a.E) * p.mblocks * p.cblocks, dev, stream);
+  return launch(kKernels[4], kWeights, g_map, x_maps, p, c, dev, stream);
 }
 
 }  // namespace lt

@@ -76,6 +76,11 @@ SHAPES = [
     (1030, 2, 256, 128, (513, 517)), (90, 9, 40, 40, (10,) * 9),
     (3, 300, 16, 16, (0,) * 200 + (1, 0, 1) + (0,) * 96 + (1,)),
     (2000, 7, 264, 328, (5, 700, 0, 3, 1000, 64, 100)),
+    # sums shared by several pairs
+    (33, 1, 512, 2048, None), (128, 1, 264, 1032, None), (200, 1, 1000, 1096, None),
+    (60, 1, 4096, 512, None), (100, 4, 256, 1024, (10, 40, 0, 48)),
+    # columns of a weight gradient in narrower tiles
+    (300, 1, 1000, 2568, None), (130, 3, 520, 1600, (50, 0, 80)),
 ]
 IDS = [f"N{s[0]}E{s[1]}M{s[2]}C{s[3]}" for s in SHAPES]
 
