@@ -155,8 +155,10 @@ struct ExpertWeightsArgs {
   RingLimits ring;
 };
 
-// Whether experts_few.cu takes a call of N rows with E matrices of `blocks` times 32 rows.
-bool few_rows(const int32_t* offsets, int N, int E, int blocks, const DeviceInfo& dev);
+// Whether experts_few.cu takes a call of N rows of C columns with E matrices, whose result
+// has M columns.
+bool few_rows(const int32_t* offsets, int N, int E, int M, int C, bool gated,
+              const DeviceInfo& dev);
 
 // The gradient at both projections, and the product again, from what was kept of them.
 struct GatedGradArgs {

@@ -53,8 +53,8 @@ constexpr int kTileRows = 256;      // MMA N: rows of an expert (kWeights: colum
 constexpr int kBlockK = 128;
 constexpr uint32_t kPieceBytes = 128 * 128;  // 128 rows (or depths) of one piece
 constexpr uint32_t kOperandBytes = 2 * kPieceBytes;
-// Small tiles need less of operand B, and get more stages: a call of few tiles waits for
-// memory (16 rows of 7168, 4096 weight rows: 40 us with three stages, 31 with five).
+// (more than three, where tiles are small, measured the same; they hold the sums that pairs
+// share)
 constexpr int kMaxStages = 5;
 constexpr int kGroups = 2;           // of four epilogue warps
 constexpr int kSpareWarp = 2 + 4 * kGroups;
@@ -721,12 +721,14 @@ constexpr Kernel kKernels[] = {
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Clusters of 2, 4 and 8 CTAs that are resident at once, by device (set_up has the lock).
+// Clusters of one to four pairs that are resident at once, by device (its set-up has the
+// lock).
 constexpr int kMaxDevices = 64;
-int g_clusters[kMaxDevices][3];
+constexpr int kMaxParts = 4;
+int g_clusters[kMaxDevices][kMaxParts];
 
 int resident(const DeviceInfo& dev, int parts) {
-  return g_clusters[dev.device][parts == 1 ? 0 : parts == 2 ? 1 : 2];
+  return std::max(1, g_clusters[dev.device][parts - 1]);
 }
 
 // How a call is cut: rows (kWeights: columns) of a tile and pairs that share a sum.
@@ -735,28 +737,43 @@ struct Cut {
   int64_t tiles;  // at most
 };
 
-// Cycles of one tile: its blocks take the longer of the MMAs (four cycles a row) and of
-// what a CTA can take in (64 bytes a cycle; 700 cycles where little is in flight), and a
-// tile beyond that what it takes to begin and to end.
-int64_t tile_cycles(int blocks, int rows, int parts) {
+// Cycles of one tile: its blocks take the longest of the MMAs (four cycles a row), of what a
+// CTA can take in (64 bytes a cycle), and, where the weights come from memory and not from
+// L2 as for all tiles but the first of a pair, of 0.7 us per 32 KB, whatever the number of
+// stages in flight (measured with 1 to 64 tiles). A tile beyond that what it takes to begin
+// and to end, and to add another pair's sum (128 rows of 7168, 4096 weight rows, one to
+// three pairs: 40.5, 25.4 and 23.3 us; 200 rows of 712, 1448 weight rows: 9.4, 8.9, 10.5).
+int64_t tile_cycles(int blocks, int rows, int parts, bool first) {
   const int half_boxes = (rows / 2 + 31) / 32;
-  const int64_t block = std::max({4 * rows, 512 + 128 * half_boxes, 700});
-  return ceil_div(blocks, parts) * block + 4000 + 8 * rows + (parts > 1 ? 3000 + 16 * rows : 0);
+  const int64_t block = std::max({4 * rows, 512 + 128 * half_boxes, first ? 1300 : 700});
+  return ceil_div(blocks, parts) * block + 4000 + 8 * rows +
+         (parts - 1) * (1500 + 10 * rows);
+}
+
+// Bytes of a stage of tiles of `rows` rows.
+int stage_bytes(int rows) {
+  return static_cast<int>(kOperandBytes) + (rows / 2 + 31) / 32 * 8192;
+}
+
+// Whether the stages hold the sums of a tile's other pairs.
+bool sums_fit(int parts, int rows, int stages) {
+  return (parts - 1) * rows * 512 <= stages * stage_bytes(rows);
 }
 
 // `tiles(rows)` for tiles of at most `rows` rows. Whole waves count: as many tiles as pairs
-// are resident run at once. (777 rows of 2000 against 5128 weight columns: four tiles of 208
-// rows and 21 of columns take two waves of 76, seven of 112 two shorter ones.)
+// are resident run at once.
 template <typename Tiles>
 Cut cut(const DeviceInfo& dev, int blocks, int most_rows, int most_parts, Tiles tiles) {
   Cut best{};
   int64_t best_cycles = INT64_MAX;
   for (int rows = std::min(kTileRows, most_rows); rows >= 64 || best_cycles == INT64_MAX;
        rows -= 32)
-    for (int parts = 1; parts <= most_parts && parts <= blocks; parts *= 2) {
-      const int64_t n = tiles(rows), at_once = std::max(1, resident(dev, parts));
-      if (parts > 1 && (n > at_once || (parts - 1) * rows > 3 * 128)) continue;
-      const int64_t cycles = ceil_div(n, at_once) * tile_cycles(blocks, rows, parts);
+    for (int parts = 1; parts <= most_parts && parts <= blocks; ++parts) {
+      const int64_t n = tiles(rows), at_once = resident(dev, parts);
+      if (parts > 1 && (n > at_once || !sums_fit(parts, rows, std::min(kMaxStages, 196608 / stage_bytes(rows))))) continue;
+      const int64_t waves = ceil_div(n, at_once);
+      const int64_t cycles = tile_cycles(blocks, rows, parts, true) +
+                             (waves - 1) * tile_cycles(blocks, rows, parts, false);
       if (cycles < best_cycles) {
         best_cycles = cycles;
         best = Cut{rows, parts, n};
@@ -773,14 +790,14 @@ int64_t most_row_tiles(int N, int E, int mblocks, int rows) {
 Cut cut_rows(const DeviceInfo& dev, const int32_t* offsets, int N, int E, int mblocks, int K) {
   const int all = (std::min(N, kTileRows) + 31) & ~31;
   if (offsets == nullptr)  // tiles of one size, as the kernel cuts them
-    return cut(dev, ceil_div(K, kBlockK), all, 4, [&](int rows) {
+    return cut(dev, ceil_div(K, kBlockK), all, kMaxParts, [&](int rows) {
       return static_cast<int64_t>(ceil_div(N, rows)) * mblocks;
     });
   // The experts' counts are not known here: full tiles, and several pairs per sum where
   // even the most tiles that there can be leave pairs idle.
   Cut c{all, 1, most_row_tiles(N, E, mblocks, all)};
-  for (int parts = 2; parts <= 4 && parts <= ceil_div(K, kBlockK); parts *= 2)
-    if (c.tiles <= resident(dev, parts) && (parts - 1) * all <= 3 * 128) c.parts = parts;
+  for (int parts = 2; parts <= kMaxParts && parts <= ceil_div(K, kBlockK); ++parts)
+    if (c.tiles <= resident(dev, parts) && sums_fit(parts, all, std::min(kMaxStages, 196608 / stage_bytes(all)))) c.parts = parts;
   return c;
 }
 
@@ -790,17 +807,13 @@ cudaError_t launch(Kernel kernel, Form form, const CUtensorMap& a_map, const Map
   p.turn = turn_bytes(form, p.saved_kind);
   p.tile_rows = c.tile_rows;
   p.parts = c.parts;
-  const int half = form == kWeights ? 128 : (c.tile_rows / 2 + 31) / 32 * 32;
-  p.stage_bytes = kOperandBytes + half * 256;
+  p.stage_bytes = form == kWeights ? 2 * kOperandBytes : stage_bytes(c.tile_rows);
   // As many stages as fit beside the chunks, the experts' table and static shared memory.
   const int rest = dev.max_smem_optin - 1024 - 1024 - kGroups * p.turn - experts_table_bytes(p.E);
   p.stages = std::min(kMaxStages, rest / p.stage_bytes);
   const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + kGroups * p.turn +
                       experts_table_bytes(p.E);
-  // The other pairs' sums of a tile fit into the stages.
-  if ((c.parts - 1) * c.tile_rows * 512 > p.stages * p.stage_bytes) {
-    p.parts = 1;
-  }
+  if (!sums_fit(p.parts, p.tile_rows, p.stages)) p.parts = 1;  // (a wide table of experts)
   const int clusters = static_cast<int>(
       p.parts > 1 ? c.tiles : std::min<int64_t>(resident(dev, 1), c.tiles));
   return launch_dependent_clusters(2 * p.parts, kernel, dim3(2 * p.parts * clusters),
@@ -869,8 +882,8 @@ cudaError_t setup_experts(const DeviceInfo& dev) {
   }
   // (clusters of several pairs do not always fill every SM: the parts of the GPU that a
   // cluster has to lie in do not all have a multiple of its size)
-  for (int i = 0; i < 3; ++i) {
-    const unsigned ctas = 2u << i;
+  for (int i = 0; i < kMaxParts; ++i) {
+    const unsigned ctas = 2u * (i + 1);
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = ctas;
@@ -891,7 +904,7 @@ cudaError_t setup_experts(const DeviceInfo& dev) {
 
 cudaError_t launch_expert_gated(const ExpertGatedArgs& a, const DeviceInfo& dev,
                                 cudaStream_t stream) {
-  if (few_rows(a.offsets, a.N, a.E, ceil_div(a.F, 16), dev)) return launch_expert_gated_few(a, stream);
+  if (few_rows(a.offsets, a.N, a.E, a.F, a.C, true, dev)) return launch_expert_gated_few(a, stream);
   Params p{};
   p.offsets = a.offsets;
   p.out = a.hidden;
@@ -915,7 +928,7 @@ cudaError_t launch_expert_gated(const ExpertGatedArgs& a, const DeviceInfo& dev,
 
 cudaError_t launch_expert_rows(const ExpertRowsArgs& a, const DeviceInfo& dev,
                                cudaStream_t stream) {
-  if (!a.transposed && few_rows(a.offsets, a.N, a.E, ceil_div(a.M, 32), dev))
+  if (!a.transposed && few_rows(a.offsets, a.N, a.E, a.M, a.K, false, dev))
     return launch_expert_rows_few(a, stream);
   Params p{};
   p.offsets = a.offsets;
