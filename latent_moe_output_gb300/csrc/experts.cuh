@@ -7,13 +7,10 @@
 
 namespace lt {
 
-// First row of each expert and the passes before it, from the caller's offsets: cut to
-// [0, N] and to their running maximum, so that ones that run backwards give empty
-// experts. Offsets that are null mean one matrix for all rows. Called by all threads;
-// `units` gives the passes of an expert of n rows. Ends with a block barrier.
-template <typename Units>
-__device__ __forceinline__ void load_experts(const int32_t* offsets, int N, int E, int* s_first,
-                                             int* s_unit, Units units) {
+// First row of each expert, from the caller's offsets: cut to [0, N] and to their running
+// maximum, so that ones that run backwards give empty experts. Offsets that are null mean
+// one matrix for all rows. Called by all threads; ends with a block barrier.
+__device__ __forceinline__ void load_experts(const int32_t* offsets, int N, int E, int* s_first) {
   if (offsets != nullptr) {
     for (int e = threadIdx.x; e <= E; e += blockDim.x) s_first[e] = min(max(offsets[e], 0), N);
   } else if (threadIdx.x == 0) {
@@ -35,26 +32,70 @@ __device__ __forceinline__ void load_experts(const int32_t* offsets, int N, int 
     int run = __shfl_up_sync(0xffffffffu, top, 1);
     if (lane == 0) run = 0;
     for (int e = lo; e < hi; ++e) s_first[e] = run = max(run, s_first[e]);
-    __syncwarp();
+  }
+  __syncthreads();
+}
+
+// s_unit[i], i = 0 .. count: the sum of units(j) over j < i. Called by all threads; ends
+// with a block barrier.
+template <typename Units>
+__device__ __forceinline__ void sum_units(int count, int* s_unit, Units units) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const int per = (count + 32) / 32;
+    const int lo = min(count + 1, lane * per), hi = min(count + 1, lo + per);
     int sum = 0;
-    for (int e = lo; e < hi && e < E; ++e) sum += units(s_first[e + 1] - s_first[e]);
+    for (int i = lo; i < hi && i < count; ++i) sum += units(i);
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += up;
     }
-    run = incl - sum;
-    for (int e = lo; e < hi; ++e) {
-      s_unit[e] = run;
-      if (e < E) run += units(s_first[e + 1] - s_first[e]);
+    int run = incl - sum;
+    for (int i = lo; i < hi; ++i) {
+      s_unit[i] = run;
+      if (i < count) run += units(i);
     }
   }
   __syncthreads();
 }
 
-// Bytes of shared memory for s_first and s_unit.
-constexpr int experts_table_bytes(int E) { return ((E + 1) * 8 + 15) & ~15; }
+// Experts by class, 8 first, then 7 .. 1, and by number within a class; those of class 0
+// are left out. Returns how many there are. A warp places the experts of one class, so
+// blocks of at least eight warps; called by all threads, ends with a block barrier.
+constexpr int kClasses = 8;
+
+template <typename Class>
+__device__ __forceinline__ int order_experts(int E, int* s_order, Class class_of) {
+  __shared__ int s_count[kClasses];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int count = 0;
+  if (warp < kClasses) {
+    for (int e = lane; e - lane < E; e += 32)
+      count += __popc(__ballot_sync(0xffffffffu, e < E && class_of(e) == kClasses - warp));
+    if (lane == 0) s_count[warp] = count;
+  }
+  __syncthreads();
+  int at = 0, all = 0;
+  for (int i = 0; i < kClasses; ++i) {
+    if (i < warp) at += s_count[i];
+    all += s_count[i];
+  }
+  if (warp < kClasses && count != 0) {
+    for (int e = lane; e - lane < E; e += 32) {
+      const bool mine = e < E && class_of(e) == kClasses - warp;
+      const uint32_t who = __ballot_sync(0xffffffffu, mine);
+      if (mine) s_order[at + __popc(who & ((1u << lane) - 1u))] = e;
+      at += __popc(who);
+    }
+  }
+  __syncthreads();
+  return all;
+}
+
+// Bytes of shared memory for s_first, s_unit and s_order.
+constexpr int experts_table_bytes(int E) { return ((E + 1) * 12 + 15) & ~15; }
 
 // ------------------------------------------------------------ activation
 // Both activations are g * sigmoid(s(g)): SiLU with s = g, the tanh form of GELU with

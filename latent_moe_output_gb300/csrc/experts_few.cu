@@ -59,8 +59,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
   if (p.offsets != nullptr) {
     int* s_first = s_table;
     int* s_unit = s_first + p.E + 1;
-    load_experts(p.offsets, p.N, p.E, s_first, s_unit,
-                 [](int n) { return (n + kTokens - 1) / kTokens; });
+    load_experts(p.offsets, p.N, p.E, s_first);
+    sum_units(p.E, s_unit,
+              [&](int i) { return (s_first[i + 1] - s_first[i] + kTokens - 1) / kTokens; });
     before = s_first[0];
     end = s_first[p.E];
     units = s_unit[p.E];
