@@ -91,19 +91,13 @@ class DecodeBlock:
 
 
 def train_step(weights, x, expert_ids, expert_weights, shared, residual, residual_scale=1.0):
-    """The block with bf16 experts under autograd (the tail in torch operations: its
-    kernels have no backward pass). Returns (residual, next input)."""
+    """The block with bf16 experts, their projections kept in 8 bits, under autograd (the
+    tail in torch operations: its kernels have no backward pass). Returns (residual, next
+    input)."""
     w = weights
-    E, F2, L = w["up"].shape
-    d = lta.dispatch_rows(x, expert_ids, E)
-    parts = []
-    bounds = d.offsets.tolist()
-    for e in range(E):
-        rows = d.rows[bounds[e]:bounds[e + 1]]
-        gate, up = (rows @ w["up"][e].t()).chunk(2, dim=1)
-        parts.append((torch.nn.functional.silu(gate) * up) @ w["down"][e].t())
-    parts.append(d.rows[bounds[E]:])  # choices without an expert: zero rows
-    routed = lta.combine_rows(torch.cat(parts), d.position, expert_weights).float()
+    d = lta.dispatch_rows(x, expert_ids, w["up"].shape[0])
+    rows = lta.expert_ffn(d.rows, w["up"], w["down"], d.offsets)
+    routed = lta.combine_rows(rows, d.position, expert_weights).float()
     latent = routed * torch.rsqrt(routed.square().mean(-1, keepdim=True) + EPS) * w["latent_norm"]
     out = latent.to(torch.bfloat16) @ w["W"].t() + shared
     return lta.residual_norm(out, residual, w["post"], w["next"], EPS, gate=w["gate"],

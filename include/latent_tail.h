@@ -476,8 +476,8 @@ LT_API lt_status latent_tail_selftest_residual_norm_backward_timeout(
  *   E == 1 (every row). Offsets are cut to [0, N] and to their running maximum; rows
  *   that no expert owns give zeros, and experts without rows zero gradients.
  * Sums are FP32 on the tensor cores, results are rounded once to bf16; the order of a
- * sum does not depend on the other rows of the call, so a row's result is the same in
- * every call with the same sizes of matrices.
+ * sum, and with it the last bits of a result, depends on the sizes (N, E, F or M, C)
+ * alone, not on the offsets.
  * Limits: 0 <= N <= 2^24, 1 <= E <= 1024, C, M and 2F multiples of 8 from 8 to 65536
  * (F a multiple of 8).
  * With N == 0 the gradients of weights are zeros.
@@ -546,6 +546,17 @@ LT_API lt_status latent_tail_expert_gated_backward(
 LT_API lt_status latent_tail_expert_matmul(const uint16_t* x, const uint16_t* weights,
                                            const int32_t* offsets, uint16_t* out, int N, int E,
                                            int M, int C, lt_stream stream);
+
+/*
+ * Diagnostic as latent_tail_selftest_expert_matvec4_timeout, for the waits of
+ * latent_tail_expert_matmul: tiles from copied_tiles (>= 0) on, in the order in which the
+ * kernel takes them, are never copied to the SMs. Calls of few rows (up to 64, by the size
+ * of the weights) load their operands directly, have no such waits and give the whole
+ * result.
+ */
+LT_API lt_status latent_tail_selftest_expert_matmul_timeout(
+    const uint16_t* x, const uint16_t* weights, const int32_t* offsets, uint16_t* out, int N,
+    int E, int M, int C, int copied_tiles, unsigned int limit_us, lt_stream stream);
 
 /*
  * Gradient of latent_tail_expert_matmul:

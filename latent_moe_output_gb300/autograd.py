@@ -1,8 +1,9 @@
 """torch.autograd wrappers of the differentiable operators around the tail.
 
-``dispatch_rows``, ``combine_rows`` and ``residual_norm`` call the same kernels as
-``block`` forward and backward; gradients flow to x, rows, weights, block, residual,
-the norm weights and the gate. Second derivatives are not provided.
+``dispatch_rows``, ``combine_rows``, ``residual_norm`` and ``expert_ffn`` call the same
+kernels as ``block`` and ``experts`` forward and backward; gradients flow to x, rows,
+weights, block, residual, the norm weights and the gate. Second derivatives are not
+provided.
 """
 
 from __future__ import annotations
@@ -11,6 +12,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import block as _block
+from . import experts as _experts
 
 
 def _dense(grad):
@@ -76,6 +78,70 @@ class _ResidualNorm(torch.autograd.Function):
                                           residual_scale=ctx.scale)
         grad_block, grad_residual, grad_post, grad_gate, grad_nextw = g
         return grad_block, grad_residual, grad_post, grad_nextw, grad_gate, None, None
+
+
+_SAVE = ("bf16", "8bit", "all8bit")
+
+
+class _ExpertFFN(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, up, down, offsets, activation, save):
+        N, F = x.shape[0], up.shape[1] // 2
+        grads = any(ctx.needs_input_grad[:3])
+        kept = None
+        if grads:
+            kept = torch.empty(N, 2, F, dtype=torch.bfloat16, device=x.device) \
+                if save == "bf16" else _experts.Checkpoint8.empty(N, 2, F, device=x.device)
+        hidden = _experts.expert_gated(x, up, offsets, activation=activation, saved=kept)
+        out = _experts.expert_matmul(hidden, down, offsets)
+        if grads:
+            rows = None  # only the gradient of up reads them
+            if ctx.needs_input_grad[1]:
+                rows = _experts.quantize8(x) if save == "all8bit" else x
+            ctx.packed = isinstance(kept, tuple), isinstance(rows, tuple)
+            ctx.save_for_backward(up, down, offsets,
+                                  *(kept if ctx.packed[0] else (kept, None)),
+                                  *(rows if ctx.packed[1] else (rows, None)))
+            ctx.activation = activation
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out):
+        up, down, offsets, kept, kept8, rows, rows8 = ctx.saved_tensors
+        if ctx.packed[0]:
+            kept = _experts.Checkpoint8(kept, kept8)
+        grad_out = _dense(grad_out)
+        want_x, want_up, want_down = ctx.needs_input_grad[:3]
+        grad_x = grad_up = grad_down = None
+        if want_x or want_up:
+            grad_hidden, _ = _experts.expert_matmul_backward(grad_out, None, down, offsets)
+            x = None
+            if want_up:
+                x = _experts.dequantize8(_experts.Checkpoint8(rows, rows8)) if ctx.packed[1] \
+                    else rows
+            grad_x, grad_up, hidden = _experts.expert_gated_backward(
+                grad_hidden, x, up if want_x else None, kept, offsets,
+                activation=ctx.activation, hidden=None if want_down else False)
+        else:
+            _, _, hidden = _experts.expert_gated_backward(None, None, None, kept, offsets,
+                                                          activation=ctx.activation)
+        if want_down:
+            _, grad_down = _experts.expert_matmul_backward(grad_out, hidden, None, offsets)
+        return grad_x, grad_up, grad_down, None, None, None
+
+
+def expert_ffn(x, up, down, offsets=None, activation: str = "silu", save: str = "8bit"):
+    """A gated feed-forward block for rows sorted by expert (or, without ``offsets``, one
+    dense block): ``expert_matmul(expert_gated(x, up), down)`` with gradients for x [N, C],
+    up [E, 2F, C] and down [E, M, F].
+
+    ``save`` says what the backward pass reads: "bf16" keeps x and both projections in
+    bf16, "8bit" the projections in 8 bits, "all8bit" x too (per row 2C + 4F, 2C + 2.13F
+    and 1.06C + 2.13F bytes). The product of the block is computed again from them."""
+    if save not in _SAVE:
+        raise ValueError(f"save: expected one of {_SAVE}, got {save!r}")
+    return _ExpertFFN.apply(x, up, down, offsets, activation, save)
 
 
 def dispatch_rows(x, expert_ids, E: int) -> _block.Dispatched:

@@ -92,6 +92,9 @@ _SIGNATURES = {
                                           + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "latent_tail_expert_matmul": (ctypes.c_int, [ctypes.c_void_p] * 4 + [ctypes.c_int] * 4
                                   + [ctypes.c_void_p]),
+    "latent_tail_selftest_expert_matmul_timeout": (
+        ctypes.c_int, [ctypes.c_void_p] * 4 + [ctypes.c_int] * 5
+        + [ctypes.c_uint, ctypes.c_void_p]),
     "latent_tail_expert_matmul_backward": (ctypes.c_int, [ctypes.c_void_p] * 6
                                            + [ctypes.c_int] * 4 + [ctypes.c_void_p]),
     "latent_tail_quantize8": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_int] * 2

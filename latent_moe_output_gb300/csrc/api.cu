@@ -50,6 +50,19 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
 
+// Encodes a tensor map. A thread that has made no runtime call that needs a context (one of
+// an autograd engine's, say) has none bound, and the driver wants one: the runtime binds
+// the current device's when the device is set.
+template <typename... Args>
+CUresult encode(Args... args) {
+  const CUresult r = g_encode(args...);
+  int dev = -1;
+  if (r != CUDA_ERROR_INVALID_CONTEXT || cudaGetDevice(&dev) != cudaSuccess ||
+      cudaSetDevice(dev) != cudaSuccess)
+    return r;
+  return g_encode(args...);
+}
+
 lt_status init_device(int dev, DeviceSlot& slot) {
   int major = 0, minor = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
@@ -248,7 +261,7 @@ bool make_map_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t byt
   const cuuint32_t box[2] = {box_bytes, box_rows};
   const cuuint32_t estrides[2] = {1, 1};
   const CUresult r =
-      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+      encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
                estrides, CU_TENSOR_MAP_INTERLEAVE_NONE,
                box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -263,7 +276,7 @@ bool make_map_bf16_rows64(CUtensorMap* map, const void* base, uint64_t rows, uin
   const cuuint32_t box[3] = {64, box_rows, box_chunks};
   const cuuint32_t estrides[3] = {1, 1, 1};
   const CUresult r =
-      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+      encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
                box, estrides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
@@ -281,7 +294,7 @@ bool make_map_bf16_nd(CUtensorMap* map, const void* base, int rank, const uint64
     if (i > 0) s[i - 1] = strides[i - 1];
   }
   const CUresult r =
-      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+      encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
                const_cast<void*>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -296,7 +309,7 @@ bool make_map_bf16_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint
   const cuuint32_t box[2] = {64, box_rows};
   const cuuint32_t estrides[2] = {1, 1};
   const CUresult r =
-      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
+      encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
                box, estrides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;

@@ -433,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++round;
           }
         }
+        if (!alive) break;  // (a sum that is not whole is not handed on)
         umma_commit_pair(smem_u32(&accf_bar[acc]), 0x3 << even);
         ++use;
       }

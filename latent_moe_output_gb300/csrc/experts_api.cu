@@ -38,8 +38,6 @@ bool known(int act) { return act == LT_ACTIVATION_SILU || act == LT_ACTIVATION_G
 
 // Kept projections: their kind, and the arrays that it needs.
 lt_status check_saved(int kind, const void* saved, const void* exponents) {
-  if (kind != LT_SAVED_NONE && kind != LT_SAVED_BF16 && kind != LT_SAVED_8BIT)
-    return LT_ERR_INVALID_ARG;
   if ((kind == LT_SAVED_NONE) != (saved == nullptr)) return LT_ERR_INVALID_ARG;
   if ((kind == LT_SAVED_8BIT) != (exponents != nullptr)) return LT_ERR_INVALID_ARG;
   return check_optional({saved, exponents});
@@ -73,6 +71,23 @@ lt_status zero_weights(void* p, int E, int M, int C, lt_stream stream) {
                                        raw(stream)));
 }
 
+lt_status expert_matmul(const uint16_t* x, const uint16_t* weights, const int32_t* offsets,
+                        uint16_t* out, int N, int E, int M, int C, const RingLimits& ring,
+                        lt_stream stream) {
+  lt_status st = check_sizes(N, E, M, C, offsets);
+  if (st != LT_OK || N == 0) return st;
+  if ((st = check_ptrs({x, weights, out})) != LT_OK) return st;
+  if ((st = check_optional({offsets})) != LT_OK) return st;
+  if (!disjoint({span(out, bytes_of(N, M, 2))},
+                {span(x, bytes_of(N, C, 2)), span(weights, E * bytes_of(M, C, 2)),
+                 span(offsets, bytes_of(E + 1, 4, 1))}))
+    return LT_ERR_INVALID_ARG;
+  const lt::DeviceInfo* dev = nullptr;
+  if ((st = current_device(&dev, Operator::kExperts)) != LT_OK) return st;
+  const ExpertRowsArgs a{x, weights, offsets, out, N, E, M, C, false, ring};
+  return launch_status(launch_expert_rows(a, *dev, raw(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -85,8 +100,10 @@ LT_API lt_status latent_tail_expert_gated(const uint16_t* x, const uint16_t* wei
   lt_status st = check_sizes(N, E, F, C, offsets);
   if (st != LT_OK) return st;
   if (F > kMaxWidth / 2 || !known(activation)) return LT_ERR_INVALID_ARG;
-  if ((st = check_saved(saved_kind, saved, saved_exponents)) != LT_OK) return st;
+  if (saved_kind != LT_SAVED_NONE && saved_kind != LT_SAVED_BF16 && saved_kind != LT_SAVED_8BIT)
+    return LT_ERR_INVALID_ARG;
   if (N == 0) return LT_OK;
+  if ((st = check_saved(saved_kind, saved, saved_exponents)) != LT_OK) return st;
   if ((st = check_ptrs({x, weights, hidden})) != LT_OK) return st;
   if ((st = check_optional({offsets})) != LT_OK) return st;
   if (!disjoint({span(hidden, bytes_of(N, F, 2)), span(saved, saved_bytes(saved_kind, N, F)),
@@ -159,18 +176,15 @@ LT_API lt_status latent_tail_expert_gated_backward(
 LT_API lt_status latent_tail_expert_matmul(const uint16_t* x, const uint16_t* weights,
                                            const int32_t* offsets, uint16_t* out, int N, int E,
                                            int M, int C, lt_stream stream) {
-  lt_status st = check_sizes(N, E, M, C, offsets);
-  if (st != LT_OK || N == 0) return st;
-  if ((st = check_ptrs({x, weights, out})) != LT_OK) return st;
-  if ((st = check_optional({offsets})) != LT_OK) return st;
-  if (!disjoint({span(out, bytes_of(N, M, 2))},
-                {span(x, bytes_of(N, C, 2)), span(weights, E * bytes_of(M, C, 2)),
-                 span(offsets, bytes_of(E + 1, 4, 1))}))
-    return LT_ERR_INVALID_ARG;
-  const lt::DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev, Operator::kExperts)) != LT_OK) return st;
-  const ExpertRowsArgs a{x, weights, offsets, out, N, E, M, C, false, RingLimits{}};
-  return launch_status(launch_expert_rows(a, *dev, raw(stream)));
+  return expert_matmul(x, weights, offsets, out, N, E, M, C, RingLimits{}, stream);
+}
+
+LT_API lt_status latent_tail_selftest_expert_matmul_timeout(
+    const uint16_t* x, const uint16_t* weights, const int32_t* offsets, uint16_t* out, int N,
+    int E, int M, int C, int copied_tiles, unsigned int limit_us, lt_stream stream) {
+  if (copied_tiles < 0 || limit_us < 1 || limit_us > 1000000) return LT_ERR_INVALID_ARG;
+  const RingLimits ring{copied_tiles, static_cast<uint64_t>(limit_us) * 1000u};
+  return expert_matmul(x, weights, offsets, out, N, E, M, C, ring, stream);
 }
 
 LT_API lt_status latent_tail_expert_matmul_backward(const uint16_t* grad_out, const uint16_t* x,

@@ -49,6 +49,11 @@ def _activation(name) -> int:
             from None
 
 
+def _unwanted(grad, name, operand, operand_name):
+    if grad is not None and operand is None:
+        raise ValueError(f"{name} given without {operand_name}")
+
+
 def _saved(saved, N, F, i):
     """Kind and addresses of kept projections."""
     if saved is None:
@@ -122,9 +127,8 @@ def expert_gated_backward(grad_hidden, x, weights, saved, offsets=None, activati
     given = (_ptr(grad_hidden, "grad_hidden", _BF16, (N, F), i), _ptr(x, "x", _BF16, (N, C), i),
              _ptr(weights, "weights", _BF16, (E, 2 * F, C), i), values, exponents,
              _ptr(offsets, "offsets", _I32, (E + 1,), i))
-    for t, name, of in ((grad_x, "grad_x", weights), (grad_weights, "grad_weights", x)):
-        if of is None and t is not None:
-            raise ValueError(f"{name} given without {'weights' if t is grad_x else 'x'}")
+    _unwanted(grad_x, "grad_x", weights, "weights")
+    _unwanted(grad_weights, "grad_weights", x, "x")
     if weights is not None and grad_x is None:
         grad_x = _empty((N, C), _BF16, i, stream)
     if x is not None and grad_weights is None:
@@ -180,10 +184,8 @@ def expert_matmul_backward(grad_out, x, weights, offsets=None, grad_x=None, grad
     given = (_ptr(grad_out, "grad_out", _BF16, (N, M), i), _ptr(x, "x", _BF16, (N, C), i),
              _ptr(weights, "weights", _BF16, (E, M, C), i),
              _ptr(offsets, "offsets", _I32, (E + 1,), i))
-    if grad_x is not None and weights is None:
-        raise ValueError("grad_x given without weights")
-    if grad_weights is not None and x is None:
-        raise ValueError("grad_weights given without x")
+    _unwanted(grad_x, "grad_x", weights, "weights")
+    _unwanted(grad_weights, "grad_weights", x, "x")
     if weights is not None and grad_x is None:
         grad_x = _empty((N, C), _BF16, i, stream)
     if x is not None and grad_weights is None:
@@ -194,45 +196,44 @@ def expert_matmul_backward(grad_out, x, weights, offsets=None, grad_x=None, grad
     return grad_x, grad_weights
 
 
-def _flat(t, name):
-    """Rows and columns of a contiguous tensor of at least two dimensions."""
+def _rows(t, name):
+    """Rows and columns of a tensor of at least two dimensions."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() < 2:
-        raise ValueError(f"{name}: expected at least 2 dimensions, got {t.dim()}")
-    rows = 1
-    for n in t.shape[:-1]:
+    shape = t.shape
+    if len(shape) < 2:
+        raise ValueError(f"{name}: expected at least 2 dimensions, got {len(shape)}")
+    C = shape[-1]
+    rows = shape[0]
+    for n in shape[1:-1]:
         rows *= n
-    return _size(rows, name), _size(t.shape[-1], name)
+    return _size(rows, name), _size(C, name), shape
 
 
 def quantize8(x, out=None, stream=None) -> Checkpoint8:
     """``x`` [..., C] bf16 in 8 bits (``out``: buffers of an earlier call, or of
     ``Checkpoint8.empty``). See latent_tail_quantize8."""
-    T, C = _flat(x, "x")
+    T, C, shape = _rows(x, "x")
     i = _index(x, "x")
-    lead = tuple(x.shape[:-1])
+    eshape = shape[:-1] + (-(-C // GROUP8),)
     if out is None:
-        out = Checkpoint8(_empty(lead + (C,), _I8, i, stream),
-                          _empty(lead + (-(-C // GROUP8),), _U8, i, stream))
+        out = Checkpoint8(_empty(shape, _I8, i, stream), _empty(eshape, _U8, i, stream))
     values, exponents = out
-    _call("latent_tail_quantize8", i, stream, _ptr(x, "x", _BF16, lead + (C,), i),
-          _ptr(values, "out.values", _I8, lead + (C,), i),
-          _ptr(exponents, "out.exponents", _U8, lead + (-(-C // GROUP8),), i), T, C)
-    return Checkpoint8(values, exponents)
+    _call("latent_tail_quantize8", i, stream, _ptr(x, "x", _BF16, shape, i),
+          _ptr(values, "out.values", _I8, shape, i),
+          _ptr(exponents, "out.exponents", _U8, eshape, i), T, C)
+    return out if isinstance(out, Checkpoint8) else Checkpoint8(values, exponents)
 
 
 def dequantize8(checkpoint, out=None, stream=None):
     """The activations that ``checkpoint`` stands for, [..., C] bf16 (exact: an integer of
     8 bits times a power of two). See latent_tail_dequantize8."""
     values, exponents = checkpoint
-    T, C = _flat(values, "checkpoint.values")
+    T, C, shape = _rows(values, "checkpoint.values")
     i = _index(values, "checkpoint.values")
-    lead = tuple(values.shape[:-1])
     if out is None:
-        out = _empty(lead + (C,), _BF16, i, stream)
-    _call("latent_tail_dequantize8", i, stream,
-          _ptr(values, "checkpoint.values", _I8, lead + (C,), i),
-          _ptr(exponents, "checkpoint.exponents", _U8, lead + (-(-C // GROUP8),), i),
-          _ptr(out, "out", _BF16, lead + (C,), i), T, C)
+        out = _empty(shape, _BF16, i, stream)
+    _call("latent_tail_dequantize8", i, stream, _ptr(values, "checkpoint.values", _I8, shape, i),
+          _ptr(exponents, "checkpoint.exponents", _U8, shape[:-1] + (-(-C // GROUP8),), i),
+          _ptr(out, "out", _BF16, shape, i), T, C)
     return out

@@ -8,6 +8,11 @@ import torch
 GROUP = 16
 
 
+def power2(n):
+    """2^n in 64 bits, exactly (exp2 on the GPU may be off in its last bit)."""
+    return ((n.long() + 1023) << 52).view(torch.float64)
+
+
 def bounds(offsets, N, E):
     """Rows [a, b) of each expert: offsets cut to [0, N] and to their running maximum."""
     if offsets is None:
@@ -64,34 +69,32 @@ def act(g, name):
 
 
 def quantize8(v):
-    """(values, exponents) of ``v`` [..., C] (float64), group by group from the definition."""
+    """(values, exponents) of ``v`` [..., C] (float64) from the definition: the least e >= 1
+    for which the largest magnitude of the group rounds to at most 127 units."""
     C = v.shape[-1]
-    lead = v.shape[:-1]
-    groups = -(-C // GROUP)
-    q = torch.zeros(lead + (C,), dtype=torch.int8, device=v.device)
-    e8 = torch.zeros(lead + (groups,), dtype=torch.uint8, device=v.device)
-    for g in range(groups):
-        part = v[..., g * GROUP:(g + 1) * GROUP]
-        top = part.abs().amax(-1)
-        bad = ~torch.isfinite(part).all(-1)
-        top = torch.where(bad, torch.ones_like(top), top)
-        e = torch.full(top.shape, 1, dtype=torch.int64, device=v.device)
-        for _ in range(260):  # the least e >= 1 that holds the group
-            more = torch.round(top * 2.0 ** (127 - e).double()) > 127
-            if not more.any():
-                break
-            e = torch.where(more, e + 1, e)
-        n = torch.round(part * torch.exp2((127 - e).double())[..., None])
-        zero = (top == 0) | bad
-        q[..., g * GROUP:(g + 1) * GROUP] = torch.where(zero[..., None], torch.zeros_like(n),
-                                                        n).to(torch.int8)
-        e8[..., g] = torch.where(bad, 255, torch.where(top == 0, 0, e)).to(torch.uint8)
-    return q, e8
+    part = torch.nn.functional.pad(v, (0, -C % GROUP)).unflatten(-1, (-1, GROUP))
+    top = part.abs().amax(-1)
+    bad = ~torch.isfinite(part).all(-1)
+    top = torch.where(bad, torch.ones_like(top), top)
+
+    def fits(e):
+        return torch.round(top * power2(127 - e)) <= 127
+
+    e = (torch.frexp(top)[1] + 127 - 12).clamp(min=1).long()
+    assert not (fits(e - 1) & (e > 1) & (top > 0)).any()  # below the least
+    for _ in range(8):
+        e = torch.where(fits(e), e, e + 1)
+    assert fits(e).all()
+    zero = (top == 0) | bad
+    n = torch.round(part * power2(127 - e)[..., None])
+    q = torch.where(zero[..., None], torch.zeros_like(n), n).to(torch.int8)
+    e8 = torch.where(bad, 255, torch.where(top == 0, 0, e)).to(torch.uint8)
+    return q.flatten(-2)[..., :C].contiguous(), e8
 
 
 def dequantize8(values, exponents):
     """float64 values of an 8-bit checkpoint."""
-    e = exponents.double().repeat_interleave(GROUP, dim=-1)[..., :values.shape[-1]]
-    v = values.double() * torch.exp2(e - 127)
+    e = exponents.long().repeat_interleave(GROUP, dim=-1)[..., :values.shape[-1]]
+    v = values.double() * power2(e - 127)
     v = torch.where(e == 0, torch.zeros_like(v), v)
     return torch.where(e == 255, torch.full_like(v, math.nan), v)
