@@ -18,7 +18,8 @@ from typing import NamedTuple
 import torch
 
 from .binding import load_library
-from .block import (_BF16, _I32, _U8, _call, _empty, _index, _ptr, _shape, _size, _workspace)
+from .block import (_BF16, _I32, _INT_MAX, _U8, _call, _empty, _index, _ptr, _shape, _size,
+                    _workspace)
 
 _I8 = torch.int8
 _ACTIVATIONS = {"silu": 0, "gelu": 1}
@@ -197,25 +198,29 @@ def expert_matmul_backward(grad_out, x, weights, offsets=None, grad_x=None, grad
 
 
 def _rows(t, name):
-    """Rows and columns of a tensor of at least two dimensions."""
+    """Rows and columns of a tensor of at least two dimensions, its shape, and that of its
+    exponents."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     shape = t.shape
-    if len(shape) < 2:
+    if len(shape) == 2:
+        rows, C = shape
+    elif len(shape) > 2:
+        rows, C = 1, shape[-1]
+        for n in shape[:-1]:
+            rows *= n
+    else:
         raise ValueError(f"{name}: expected at least 2 dimensions, got {len(shape)}")
-    C = shape[-1]
-    rows = shape[0]
-    for n in shape[1:-1]:
-        rows *= n
-    return _size(rows, name), _size(C, name), shape
+    if rows > _INT_MAX or C > _INT_MAX:
+        _size(max(rows, C), name)
+    return rows, C, shape, (*shape[:-1], -(-C // GROUP8))
 
 
 def quantize8(x, out=None, stream=None) -> Checkpoint8:
     """``x`` [..., C] bf16 in 8 bits (``out``: buffers of an earlier call, or of
     ``Checkpoint8.empty``). See latent_tail_quantize8."""
-    T, C, shape = _rows(x, "x")
+    T, C, shape, eshape = _rows(x, "x")
     i = _index(x, "x")
-    eshape = shape[:-1] + (-(-C // GROUP8),)
     if out is None:
         out = Checkpoint8(_empty(shape, _I8, i, stream), _empty(eshape, _U8, i, stream))
     values, exponents = out
@@ -229,11 +234,11 @@ def dequantize8(checkpoint, out=None, stream=None):
     """The activations that ``checkpoint`` stands for, [..., C] bf16 (exact: an integer of
     8 bits times a power of two). See latent_tail_dequantize8."""
     values, exponents = checkpoint
-    T, C, shape = _rows(values, "checkpoint.values")
+    T, C, shape, eshape = _rows(values, "checkpoint.values")
     i = _index(values, "checkpoint.values")
     if out is None:
         out = _empty(shape, _BF16, i, stream)
     _call("latent_tail_dequantize8", i, stream, _ptr(values, "checkpoint.values", _I8, shape, i),
-          _ptr(exponents, "checkpoint.exponents", _U8, shape[:-1] + (-(-C // GROUP8),), i),
+          _ptr(exponents, "checkpoint.exponents", _U8, eshape, i),
           _ptr(out, "out", _BF16, shape, i), T, C)
     return out
