@@ -380,6 +380,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       int at = 0, s = 0;
       uint32_t round = 0, fixed_phase = 0, use = 0;
       bool alive = true;
+      // One thread issues all MMAs, and one of 256 x 256 x 16 takes 128 cycles: descriptors
+      // are kept ready, so that an issue is two additions (with descriptors put together for
+      // each, 160 cycles passed between two MMAs whatever their size).
+      constexpr bool kMajorA = kForm == kGated || kForm == kRows, kMajorB = kForm != kWeights;
+      const uint32_t a_base = kMajorA ? umma_desc_lo(ring) : umma_desc_lo(ring, kPieceBytes);
+      const uint32_t b_base = kMajorB ? umma_desc_lo(ring + kOperandBytes)
+                                      : umma_desc_lo(ring + kOperandBytes, kPieceBytes);
+      const uint32_t stage_step = static_cast<uint32_t>(p.stage_bytes) >> 4;
+      uint32_t a_lo = a_base, b_lo = b_base;
       for (Walk walk(cluster, n_clusters, tiles); alive && walk.more(); walk.next()) {
         const Tile t = tile_at<kForm>(p, walk.tile(), at, table);
         const int nkb = blocks_of(t);
@@ -393,17 +402,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idesc = umma_idesc_bf16(256, width_of(t)) |
                                (kForm == kRowsT || kForm == kWeights ? kUmmaTransposeA : 0u) |
                                (kForm == kWeights ? kUmmaTransposeB : 0u);
-        const uint32_t b_piece = static_cast<uint32_t>((width_of(t) / 2 + 31) / 32) * 4096u;
-        const int kb0 = first_block(nkb, part);
-        for (int kb = kb0; kb < first_block(nkb, part + 1); ++kb) {
+        // Sixteenths of the bytes between the pieces of a K-major operand B, and of a step.
+        const uint32_t b_piece = static_cast<uint32_t>((width_of(t) / 2 + 31) / 32) * 256u;
+        auto a_step = [](int k) {
+          return kMajorA ? 2u * (k & 3) + (kPieceBytes >> 4) * (k >> 2) : 128u * k;
+        };
+        auto b_step = [&](int k) { return kMajorB ? 2u * (k & 3) + b_piece * (k >> 2) : 128u * k; };
+        const int kb0 = first_block(nkb, part), kb1 = first_block(nkb, part + 1);
+        const int depth = kForm == kWeights ? t.rows : p.K;
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait_cluster(smem_u32(&full_bar[s]), round & 1u, p.err, abort_v,
                                  p.ring.limit_ns)) {
             alive = false;
             break;
           }
-          int steps = kBlockK / 16;
-          if (kb == nkb - 1) {
-            steps = ((kForm == kWeights ? t.rows : p.K) - kb * kBlockK + 15) >> 4;
+          const uint32_t first = kb != kb0 ? 1u : 0u;
+          if (depth - kb * kBlockK >= kBlockK) {
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kBlockK / 16; ++k)
+              umma_bf16_pair_lo(d, a_lo + a_step(k), b_lo + b_step(k), idesc, k == 0 ? first : 1u);
+          } else {  // the last block
             if (needs_zeros(t)) {
               if (!mbar_wait_cluster(smem_u32(&fixed_bar[s]), fixed_phase >> s & 1u, p.err,
                                      abort_v, p.ring.limit_ns)) {
@@ -412,25 +431,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               fixed_phase ^= 1u << s;
             }
-          }
-          tc_fence_after();
-          const uint32_t a = ring + static_cast<uint32_t>(s * p.stage_bytes), b = a + kOperandBytes;
-#pragma unroll
-          for (int k = 0; k < kBlockK / 16; ++k) {
-            if (k < steps)
-              umma_bf16_pair(
-                  d,
-                  kForm == kRowsT || kForm == kWeights
-                      ? umma_desc_sw128_mn(a + 2048u * k, kPieceBytes)
-                      : umma_desc_sw128(a + 32u * (k & 3) + kPieceBytes * (k >> 2)),
-                  kForm == kWeights ? umma_desc_sw128_mn(b + 2048u * k, kPieceBytes)
-                                    : umma_desc_sw128(b + 32u * (k & 3) + b_piece * (k >> 2)),
-                  idesc, kb != kb0 || k != 0 ? 1u : 0u);
+            tc_fence_after();
+            const int steps = (depth - kb * kBlockK + 15) >> 4;
+#pragma unroll 1
+            for (int k = 0; k < steps; ++k)
+              umma_bf16_pair_lo(d, a_lo + a_step(k), b_lo + b_step(k), idesc, k == 0 ? first : 1u);
           }
           umma_commit_pair(smem_u32(&empty_bar[s]), 0x3 << even);
+          a_lo += stage_step;
+          b_lo += stage_step;
           if (++s == stages) {
             s = 0;
             ++round;
+            a_lo = a_base;
+            b_lo = b_base;
           }
         }
         if (!alive) break;  // (a sum that is not whole is not handed on)

@@ -237,18 +237,16 @@ __device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t saddr) {
   return d;
 }
 
-// The same for an operand whose rows run along M or N (MN-major): pieces of 64 columns,
-// 128-byte swizzled, 8 K rows per 1024-byte atom, the next piece `piece` bytes on. A step
-// of 16 K rows moves `saddr` by 2048 bytes.
-__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t saddr, uint32_t piece) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);  // start address
-  d |= static_cast<uint64_t>(piece >> 4) << 16;          // next 64 columns
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;           // next 8 K rows
-  d |= static_cast<uint64_t>(1) << 46;                   // descriptor version 1
-  d |= static_cast<uint64_t>(2) << 61;                   // 128-byte swizzle
-  return d;
+// The two halves of such descriptors. The lower one has the address, so that an offset
+// within shared memory is an addition of its sixteenth; the upper one is the same for all
+// operands here: 8-row atoms 1024 bytes apart, version 1, 128-byte swizzle. For an operand
+// whose rows run along M or N (MN-major; pieces of 64 columns, 8 K rows per atom) `piece`
+// is the distance of the next 64 columns, and a step of 16 K rows 2048 bytes; for a K-major
+// one it is not used, and a step 32 bytes.
+__device__ __forceinline__ uint32_t umma_desc_lo(uint32_t saddr, uint32_t piece = 16) {
+  return ((saddr & 0x3FFFFu) >> 4) | (piece >> 4) << 16;
 }
+constexpr uint32_t kUmmaDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
 
 // Bits of an instruction descriptor for operands that are MN-major.
 constexpr uint32_t kUmmaTransposeA = 1u << 15;
@@ -298,6 +296,19 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a_desc,
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// umma_bf16_pair from the lower halves of both descriptors.
+__device__ __forceinline__ void umma_bf16_pair_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                                  uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kUmmaDescHi)
       : "memory");
 }
 
