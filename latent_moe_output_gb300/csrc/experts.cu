@@ -375,8 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      // ---------------- pair MMA issuer ----------------
+    if (rank == 0) {
+      // ---------------- pair MMA issuer (the whole warp, one lane issues) ----------------
       int at = 0, s = 0;
       uint32_t round = 0, fixed_phase = 0, use = 0;
       bool alive = true;
@@ -389,14 +389,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       : umma_desc_lo(ring + kOperandBytes, kPieceBytes);
       const uint32_t stage_step = static_cast<uint32_t>(p.stage_bytes) >> 4;
       uint32_t a_lo = a_base, b_lo = b_base;
+      auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu,
+                          mbar_wait_cluster(bar, parity, p.err, abort_v, p.ring.limit_ns));
+      };
       for (Walk walk(cluster, n_clusters, tiles); alive && walk.more(); walk.next()) {
         const Tile t = tile_at<kForm>(p, walk.tile(), at, table);
         const int nkb = blocks_of(t);
         if (nkb == 0) continue;
         const int acc = static_cast<int>(use & 1u);
-        if (!mbar_wait_cluster(smem_u32(&acce_bar[acc]), ((use >> 1) & 1u) ^ 1u, p.err, abort_v,
-                               p.ring.limit_ns))
-          break;
+        if (!wait_all(smem_u32(&acce_bar[acc]), ((use >> 1) & 1u) ^ 1u)) break;
         tc_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(acc * kTileRows);
         const uint32_t idesc = umma_idesc_bf16(256, width_of(t)) |
@@ -411,21 +413,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kb0 = first_block(nkb, part), kb1 = first_block(nkb, part + 1);
         const int depth = kForm == kWeights ? t.rows : p.K;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait_cluster(smem_u32(&full_bar[s]), round & 1u, p.err, abort_v,
-                                 p.ring.limit_ns)) {
+          if (!wait_all(smem_u32(&full_bar[s]), round & 1u)) {
             alive = false;
             break;
           }
           const uint32_t first = kb != kb0 ? 1u : 0u;
           if (depth - kb * kBlockK >= kBlockK) {
             tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kBlockK / 16; ++k)
-              umma_bf16_pair_lo(d, a_lo + a_step(k), b_lo + b_step(k), idesc, k == 0 ? first : 1u);
+              for (int k = 0; k < kBlockK / 16; ++k)
+                umma_bf16_pair_lo(d, a_lo + a_step(k), b_lo + b_step(k), idesc,
+                                  k == 0 ? first : 1u);
+              umma_commit_pair(smem_u32(&empty_bar[s]), 0x3 << even);
+            }
           } else {  // the last block
             if (needs_zeros(t)) {
-              if (!mbar_wait_cluster(smem_u32(&fixed_bar[s]), fixed_phase >> s & 1u, p.err,
-                                     abort_v, p.ring.limit_ns)) {
+              if (!wait_all(smem_u32(&fixed_bar[s]), fixed_phase >> s & 1u)) {
                 alive = false;
                 break;
               }
@@ -433,11 +437,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const int steps = (depth - kb * kBlockK + 15) >> 4;
+            if (elect_one()) {
 #pragma unroll 1
-            for (int k = 0; k < steps; ++k)
-              umma_bf16_pair_lo(d, a_lo + a_step(k), b_lo + b_step(k), idesc, k == 0 ? first : 1u);
+              for (int k = 0; k < steps; ++k)
+                umma_bf16_pair_lo(d, a_lo + a_step(k), b_lo + b_step(k), idesc,
+                                  k == 0 ? first : 1u);
+              umma_commit_pair(smem_u32(&empty_bar[s]), 0x3 << even);
+            }
           }
-          umma_commit_pair(smem_u32(&empty_bar[s]), 0x3 << even);
+          __syncwarp();
           a_lo += stage_step;
           b_lo += stage_step;
           if (++s == stages) {
@@ -448,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!alive) break;  // (a sum that is not whole is not handed on)
-        umma_commit_pair(smem_u32(&accf_bar[acc]), 0x3 << even);
+        if (elect_one()) umma_commit_pair(smem_u32(&accf_bar[acc]), 0x3 << even);
+        __syncwarp();
         ++use;
       }
     }
@@ -756,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   pdl_launch_dependents();
-  if (warp == 1 && rank == 0 && *abort_v && lane == 0) {
+  if (warp == 1 && rank == 0 && *abort_v && elect_one()) {
     // The MMAs issued before the abort: a commit behind them, waited for.
     umma_commit_pair(smem_u32(&drain_bar), 0x1 << even);
     wait_drain(smem_u32(&drain_bar), 0);
