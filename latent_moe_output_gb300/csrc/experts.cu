@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   bool joined = false;  // whether this warp has met the others of the cluster for the sums
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- producer (this CTA's halves) ----------------
+    {
+      // ---------------- producer (this CTA's halves; the whole warp, one lane issues) ------
       int at = 0, s = 0;
       uint32_t round = 0, tails = 0, tail_phase = 0;
       int issued = 0;
@@ -288,14 +288,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t b_piece = kForm == kWeights ? kPieceBytes : box * 4096u;
         const uint32_t bytes = kOperandBytes + 2 * b_piece;
         for (int kb = first_block(nkb, part); kb < first_block(nkb, part + 1); ++kb) {
-          if (!mbar_wait_cluster(smem_u32(&empty_bar[s]), (round & 1u) ^ 1u, p.err, abort_v,
-                                 p.ring.limit_ns)) {
-            alive = false;
-            break;
-          }
+          alive = __all_sync(0xffffffffu,
+                             mbar_wait_cluster(smem_u32(&empty_bar[s]), (round & 1u) ^ 1u, p.err,
+                                               abort_v, p.ring.limit_ns));
+          if (!alive) break;
           const uint32_t a = ring + static_cast<uint32_t>(s * p.stage_bytes), b = a + kOperandBytes;
           const int k0 = kb * kBlockK;
-          if (kForm == kWeights && kb == nkb - 1 && needs_zeros(t)) {
+          const bool tail = kForm == kWeights && kb == nkb - 1 && needs_zeros(t);
+          if (tail) {
+            tails |= 1u << s;
+            tail_phase ^= 1u << s;
+          }
+          const bool issue = elect_one();
+          if (issue && tail) {
             // Completes on this CTA's own barrier, for the warp that puts the zeros in.
             const uint32_t bar = smem_u32(&tail_bar[s]);
             if (rank == 0) mbar_arrive(smem_u32(&full_bar[s]));
@@ -313,9 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d(b, b_map, bar, c, r);
               tma_load_2d(b + kPieceBytes, b_map, bar, c + 64, r);
             }
-            tails |= 1u << s;
-            tail_phase ^= 1u << s;
-          } else {
+          } else if (issue) {
             const uint32_t bar = map_to_rank(smem_u32(&full_bar[s]), even);
             if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), 2 * bytes);
             const int m = t.m0 + rank * (kForm == kGated ? 64 : 128);
@@ -358,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d_pair(b + b_piece, b_map, bar, (kForm == kWeights ? c : k0) + 64, r);
             }
           }
+          __syncwarp();
           ++issued;
           if (++s == stages) {
             s = 0;
@@ -365,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (*abort_v) {  // copies in flight land before the CTA's shared memory goes
+      if (*abort_v && lane == 0) {  // copies in flight land before the CTA's shared memory goes
         if (rank == 0)  // the even CTA's barriers count both CTAs' copies
           for (int it = max(0, issued - stages); it < issued; ++it)
             wait_drain(smem_u32(&full_bar[it % stages]), static_cast<uint32_t>(it / stages) & 1u);
