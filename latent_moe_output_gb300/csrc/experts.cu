@@ -808,17 +808,16 @@ struct Cut {
   int64_t tiles;  // at most
 };
 
-// Cycles of one tile: its blocks take the longest of the MMAs (four cycles a row), of what a
-// CTA can take in (64 bytes a cycle), and, where the weights come from memory and not from
-// L2 as for all tiles but the first of a pair, of 0.7 us per 32 KB, whatever the number of
-// stages in flight (measured with 1 to 64 tiles). A tile beyond that what it takes to begin
-// and to end, and to add another pair's sum (128 rows of 7168, 4096 weight rows, one to
-// three pairs: 40.5, 25.4 and 23.3 us; 200 rows of 712, 1448 weight rows: 9.4, 8.9, 10.5).
-int64_t tile_cycles(int blocks, int rows, int parts, bool first) {
-  const int half_boxes = (rows / 2 + 31) / 32;
-  const int64_t block = std::max({4 * rows, 512 + 128 * half_boxes, first ? 1300 : 700});
-  return ceil_div(blocks, parts) * block + 4000 + 8 * rows +
-         (parts - 1) * (1500 + 10 * rows);
+// Cycles of one tile, and of meeting for a sum, fitted to calls of one to 64 tiles and one to
+// three waves (us measured: 1000 rows of 2048 against 2048 weight rows with tiles of 256,
+// 128 and 64 rows 16.6, 13.0 and 16.2; 128 rows of 7168, 2 x 2048 weight rows, one to three
+// pairs per sum 28.9, 22.7 and 21.5; 64 rows of them 23.3, 18.4 and 17.8). A block of 128
+// columns takes about its MMAs' time, four cycles a row, and no less than the weights need
+// to come in.
+int64_t tile_cycles(int blocks, int rows, int parts) {
+  const int64_t block = std::max<int64_t>(570, 240 + 21 * rows / 5);
+  return ceil_div(blocks, parts) * block + 1500 +
+         (parts > 1 ? 2500 + (parts - 1) * (2500 + 20 * rows) : 0);
 }
 
 // Bytes of a stage of tiles of `rows` rows.
@@ -843,8 +842,7 @@ Cut cut(const DeviceInfo& dev, int blocks, int most_rows, int most_parts, Tiles 
       const int64_t n = tiles(rows), at_once = resident(dev, parts);
       if (parts > 1 && (n > at_once || !sums_fit(parts, rows, std::min(kMaxStages, 196608 / stage_bytes(rows))))) continue;
       const int64_t waves = ceil_div(n, at_once);
-      const int64_t cycles = tile_cycles(blocks, rows, parts, true) +
-                             (waves - 1) * tile_cycles(blocks, rows, parts, false);
+      const int64_t cycles = waves * tile_cycles(blocks, rows, parts);
       if (cycles < best_cycles) {
         best_cycles = cycles;
         best = Cut{rows, parts, n};

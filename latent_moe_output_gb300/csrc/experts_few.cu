@@ -243,9 +243,9 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
 
 // One wave of CTAs for rows of several experts. With one matrix, 16 rows a pass, of which
 // all but the first read the weights from L2: the passes' time at 6.8 TB/s against that of
-// the tensor-core kernel, 3 us more to begin with and 0.35 us per 128 columns (both
-// measured, us: 58.7 MB of weights, 16, 32 and 64 rows 13, 21 and 37 against 24 to 25; 5.8
-// MB, 64 rows 7.7 against 10.3; 4.2 MB, 64 rows 6.6 against 9.4).
+// the tensor-core kernel, 1.5 us more to begin with and 0.2 us per 128 columns (both
+// measured, us: 58.7 MB of weights, 16 and 24 rows 13.5 and 20 against 16.7; 29 MB, 16 rows
+// 6.9 against 10.3; 4.2 MB, 64 rows 6.6 against 8.8).
 bool few_rows(const int32_t* offsets, int N, int E, int M, int C, bool gated,
               const DeviceInfo& dev) {
   const int64_t per = gated ? kRowsPerCta / 2 : kRowsPerCta;
@@ -253,7 +253,7 @@ bool few_rows(const int32_t* offsets, int N, int E, int M, int C, bool gated,
   if (offsets != nullptr) return N <= 16 && std::min(N, E) * blocks <= dev.num_sms;
   const double passes = (N + 15) / 16;
   const double bytes = (gated ? 4.0 : 2.0) * M * C;
-  return N <= 64 && passes * bytes / 6.8e6 <= 3.0 + 0.35 * ((C + 127) / 128);
+  return N <= 64 && passes * bytes / 6.8e6 <= 1.5 + 0.2 * ((C + 127) / 128);
 }
 
 cudaError_t launch_expert_gated_few(const ExpertGatedArgs& a, cudaStream_t stream) {
