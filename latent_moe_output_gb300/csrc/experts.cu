@@ -474,8 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool alive = true;
       for (Walk walk(cluster, n_clusters, tiles); alive && walk.more(); walk.next()) {
         const Tile t = tile_at<kForm>(p, walk.tile(), at, table);
-        it += blocks_of(t);
-        if (!needs_zeros(t)) continue;
+        const int nkb = blocks_of(t), end = first_block(nkb, part + 1);
+        it += end - first_block(nkb, part);
+        if (!needs_zeros(t) || end != nkb) continue;
         const int s = (it - 1) % stages;
         const int from = t.rows - (blocks_of(t) - 1) * kBlockK, to = (from + 15) & ~15;
         alive = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tail_bar[s]), phase >> s & 1u, p.err,
@@ -533,6 +534,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_remote(map_to_rank(bar, even));
       }
     };
+    // The other pairs' sums of 32 rows, in their order.
+    auto add_parts = [&](const Tile& t, int ch, float (&v)[32]) {
+      const int nt = width_of(t);
+      const float* from = reinterpret_cast<const float*>(smem_raw + (ring - raw)) +
+                          ch * kChunk * 128 + q * 32 + lane;
+      for (int i = 1; i < p.parts; ++i, from += nt * 128)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += from[j * 128];
+    };
     int at = 0;
     uint32_t use = 0;
     bool alive = true;
@@ -557,32 +567,32 @@ __global__ void __launch_bounds__(kThreads, 1)
               : "r"(static_cast<uint32_t>(alive)), "r"(1 + group)
               : "memory");
           alive = all != 0;
-          if (p.parts > 1) {
-            // All pairs' products are done, so the first pair's stages are free: the others
-            // put their sums there, [row][lane] for each pair and CTA.
-            __syncwarp();
-            cluster_sync();
-            const int nt = width_of(t);
-            if (part > 0 && alive) {
-              tc_fence_after();
-              const uint32_t to = map_to_rank(
-                  ring + (static_cast<uint32_t>(part - 1) * nt * 128 + q * 32 + lane) * 4, rank);
-              for (int ch = group; ch * kChunk < nt; ch += kGroups) {
-                float v[32];
-                __syncwarp();
-                tmem_ld32(dcol + static_cast<uint32_t>(ch * kChunk), v);
+        }
+        if (p.parts > 1) {
+          // All pairs' products are done, so the first pair's stages are free: the others
+          // put their sums there, [row][lane] for each pair and CTA.
+          __syncwarp();
+          cluster_sync();
+          const int nt = width_of(t);
+          if (part > 0 && alive) {
+            tc_fence_after();
+            const uint32_t to = map_to_rank(
+                ring + (static_cast<uint32_t>(part - 1) * nt * 128 + q * 32 + lane) * 4, rank);
+            for (int ch = group; ch * kChunk < nt; ch += kGroups) {
+              float v[32];
+              __syncwarp();
+              tmem_ld32(dcol + static_cast<uint32_t>(ch * kChunk), v);
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  st_dsmem_f32(to + static_cast<uint32_t>(ch * kChunk + j) * 512, v[j]);
-              }
-            } else if (part > 0 && lane == 0) {
-              st_dsmem_u32(map_to_rank(smem_u32(&part_failed), rank), 1);
+              for (int j = 0; j < 32; ++j)
+                st_dsmem_f32(to + static_cast<uint32_t>(ch * kChunk + j) * 512, v[j]);
             }
-            __syncwarp();
-            cluster_sync();
-            joined = true;
-            if (part > 0 || *const_cast<volatile int*>(&part_failed) != 0) break;
+          } else if (part > 0 && lane == 0) {
+            st_dsmem_u32(map_to_rank(smem_u32(&part_failed), rank), 1);
           }
+          __syncwarp();
+          cluster_sync();
+          joined = true;
+          if (part > 0 || *const_cast<volatile int*>(&part_failed) != 0) break;
         }
         if (!alive) break;
         tc_fence_after();
@@ -595,12 +605,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int m0 = t.m0 + rank * 128 + q * 32;
         uint16_t* dst = p.out + (static_cast<size_t>(t.e) * p.M + m0) * p.K + t.c0;
         uint8_t* own = buf + q * 32 * kSumStride;
+        if (any && group >= chunks) release_acc(acc);
         for (int ch = group; ch < chunks; ch += kGroups) {
           float v[32];
           __syncwarp();  // the last chunk has been read
           if (any) {
             tmem_ld32(dcol + static_cast<uint32_t>(ch * kChunk), v);
             if (ch + kGroups >= chunks) release_acc(acc);
+            if (p.parts > 1) add_parts(t, ch, v);
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
@@ -628,14 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           tmem_ld32(dcol + static_cast<uint32_t>(ch * kChunk), v);
           if (ch + kGroups >= chunks) release_acc(acc);
-          if (p.parts > 1) {  // the other pairs' sums, in their order
-            const int nt = width_of(t);
-            const float* from = reinterpret_cast<const float*>(smem_raw + (ring - raw)) +
-                                ch * kChunk * 128 + q * 32 + lane;
-            for (int i = 1; i < p.parts; ++i, from += nt * 128)
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] += from[j * 128];
-          }
+          if (p.parts > 1) add_parts(t, ch, v);
           group_barrier(group);  // the last chunk has been read
           const int live = min(kChunk, t.rows - ch * kChunk);  // rows of the chunk
           const size_t row = static_cast<size_t>(t.row0) + ch * kChunk;
@@ -759,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  if (kForm != kWeights && p.parts > 1 && !joined) {
+  if (p.parts > 1 && !joined) {
     __syncwarp();
     cluster_sync();
     cluster_sync();
@@ -1032,7 +1037,8 @@ cudaError_t launch_expert_weights(const ExpertWeightsArgs& a, const DeviceInfo& 
   p.K = a.C;
   p.mblocks = ceil_div(a.M, 256);
   const int mean = ceil_div(a.N, a.E);
-  const Cut c = cut(dev, ceil_div(mean, kBlockK), (a.C + 31) & ~31, 1, [&](int cols) {
+  const int most_parts = a.offsets == nullptr ? kMaxParts : 1;  // (of blocks known here)
+  const Cut c = cut(dev, ceil_div(mean, kBlockK), (a.C + 31) & ~31, most_parts, [&](int cols) {
     return static_cast<int64_t>(a.E) * p.mblocks * ceil_div(a.C, cols);
   });
   p.cblocks = ceil_div(a.C, c.tile_rows);

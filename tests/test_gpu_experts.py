@@ -79,6 +79,10 @@ SHAPES = [
     # sums shared by several pairs
     (33, 1, 512, 2048, None), (128, 1, 264, 1032, None), (200, 1, 1000, 1096, None),
     (60, 1, 4096, 512, None), (100, 4, 256, 1024, (10, 40, 0, 48)),
+    # sums over many rows of small matrices
+    (5000, 1, 264, 200, None), (1023, 1, 72, 1000, None), (700, 1, 128, 32, None),
+    # more tiles of one 32-row or 32-column chunk than two for each pair of CTAs
+    (1300, 260, 264, 24, (5,) * 260),
     # columns of a weight gradient in narrower tiles
     (300, 1, 1000, 2568, None), (130, 3, 520, 1600, (50, 0, 80)),
 ]
