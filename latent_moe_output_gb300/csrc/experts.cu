@@ -897,9 +897,10 @@ cudaError_t launch(Kernel kernel, Form form, const CUtensorMap& a_map, const Map
 // Whether one copy may bring two 64-column pieces of `cols` columns.
 bool whole(int cols) { return cols % 64 == 0; }
 
-// Rows [N, cols] in boxes of 32, 64, 96 and 128 rows.
-bool rows_maps(Maps* maps, const void* base, int N, int cols) {
-  for (int i = 0; i < 4; ++i)
+// Rows [N, cols] in boxes of 32, 64, 96 and 128 rows, as far as halves of tiles of
+// `tile_rows` rows need them.
+bool rows_maps(Maps* maps, const void* base, int N, int cols, int tile_rows) {
+  for (int i = 0; i < ceil_div(tile_rows / 2, 32); ++i)
     if (!(whole(cols) ? make_map_bf16_rows64(&maps->map[i], base, N, cols, 32 * (i + 1), 2)
                       : make_map_bf16_sw128(&maps->map[i], base, N, cols, 32 * (i + 1))))
       return false;
@@ -992,12 +993,13 @@ cudaError_t launch_expert_gated(const ExpertGatedArgs& a, const DeviceInfo& dev,
   p.saved_kind = a.saved_kind;
   p.ring = a.ring;
   p.whole_a = p.whole_b = whole(a.C);
+  const Cut c = cut_rows(dev, a.offsets, a.N, a.E, p.mblocks, a.C);
   CUtensorMap w_map;
-  Maps x_maps;
-  if (!gated_map(&w_map, a.weights, a.E, a.F, a.C) || !rows_maps(&x_maps, a.x, a.N, a.C))
+  Maps x_maps{};
+  if (!gated_map(&w_map, a.weights, a.E, a.F, a.C) ||
+      !rows_maps(&x_maps, a.x, a.N, a.C, c.tile_rows))
     return cudaErrorInvalidValue;
-  return launch(kKernels[a.act == kActSilu ? 0 : 1], kGated, w_map, x_maps, p,
-                cut_rows(dev, a.offsets, a.N, a.E, p.mblocks, a.C), dev, stream);
+  return launch(kKernels[a.act == kActSilu ? 0 : 1], kGated, w_map, x_maps, p, c, dev, stream);
 }
 
 cudaError_t launch_expert_rows(const ExpertRowsArgs& a, const DeviceInfo& dev,
@@ -1015,15 +1017,16 @@ cudaError_t launch_expert_rows(const ExpertRowsArgs& a, const DeviceInfo& dev,
   p.ring = a.ring;
   p.whole_a = whole(a.transposed ? a.M : a.K);
   p.whole_b = whole(a.K);
+  const Cut c = cut_rows(dev, a.offsets, a.N, a.E, p.mblocks, a.K);
   CUtensorMap w_map;
-  Maps x_maps;
+  Maps x_maps{};
   if (!(a.transposed ? matrices_map(&w_map, a.weights, a.E, a.K, a.M)
                      : matrices_map(&w_map, a.weights, a.E, a.M, a.K)) ||
-      !rows_maps(&x_maps, a.x, a.N, a.K))
+      !rows_maps(&x_maps, a.x, a.N, a.K, c.tile_rows))
     return cudaErrorInvalidValue;
   const Form form = a.transposed ? kRowsT : kRows;
-  return launch(kKernels[a.transposed ? 3 : 2], form, w_map, x_maps, p,
-                cut_rows(dev, a.offsets, a.N, a.E, p.mblocks, a.K), dev, stream);
+  return launch(kKernels[a.transposed ? 3 : 2], form, w_map, x_maps, p, c, dev,
+                stream);
 }
 
 cudaError_t launch_expert_weights(const ExpertWeightsArgs& a, const DeviceInfo& dev,
