@@ -27,13 +27,15 @@
 //
 // Persistent, warp-specialized, one CTA per SM, 11 warps:
 //   warp 0      producer: this CTA's operand boxes of a 128-deep block into a stage ring
-//   warp 1      TMEM allocation; in the even CTA the MMA issuer
+//   warp 1      TMEM allocation; in the even CTA the MMA issuer (in both loops the whole warp
+//               runs and one elected lane issues)
 //   warps 2..9  epilogue; two accumulators, so the next tile's MMAs run meanwhile. The
 //               lanes of TMEM are columns of the result: 32 rows at a time are turned
 //               over in shared memory and leave in 16-byte pieces of whole row parts.
 //               Two groups of four warps take every other 32 rows: one warp per scheduler
 //               waits for its own shuffles and reciprocals most of the time
-//   warp 10     kWeights: the zeros above; else zeros in the rows that no expert owns
+//   warp 10     kWeights: the zeros above; else zeros in the rows that no expert owns, with
+//               the other warps' help once they are done
 // Sums are FP32; results are rounded once.
 #include "experts.cuh"
 
@@ -114,7 +116,6 @@ struct Tile {
   int e, row0, rows, m0, c0;
 };
 
-
 // The experts in the order of their tiles' cost, the largest first (see Walk).
 struct Table {
   const int* first;  // [E+1] first row of each expert
@@ -162,7 +163,7 @@ __device__ __forceinline__ Tile tile_at(const Params& p, int tile, int& at, cons
 // clusters take turns forwards and backwards, so that what the first pays more in one turn
 // it pays less in the next, and the last turn, which some clusters do not have, is of the
 // cheapest tiles (1013 tokens, 6 of 60 experts, unevenly loaded, gated and kept in 8 bits:
-// 70 us in the order of the experts).
+// 81 us in the order of the experts, 74 like this).
 struct Walk {
   int me, clusters, tiles, base = 0;
   bool back = false;
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t drain_bar;              // even CTA: MMAs before an abort are done
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
+  __shared__ int zero_next;    // rows without an expert that have been handed out
   __shared__ int part_failed;  // a pair's sum did not come (first pair of a cluster)
   volatile int* abort_v = &abort_flag;
 
@@ -231,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&drain_bar), 1);
     abort_flag = 0;
     part_failed = 0;
+    zero_next = 0;
     mbar_fence_init();
     tma_prefetch_map(&a_map);
     tma_prefetch_map(&b_maps.map[0]);
@@ -268,6 +271,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Rows of an MMA's N side.
   auto width_of = [&](const Tile& t) {
     return kForm == kWeights ? p.tile_rows : (t.rows + 31) & ~31;
+  };
+
+  // Zeros in the rows that no expert owns: rows are handed out one by one, to the spare warp
+  // from the start and to the others when they have nothing else to do (8000 tokens with 6 of
+  // 60 experts, nine choices of ten without one, gated and kept in 8 bits: 133 us by the
+  // spare warp alone, 115 like this).
+  auto zero_rows = [&]() {
+    const int before = s_first[0], none = before + p.N - s_first[p.E];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    while (true) {
+      int64_t i = 0;
+      if (lane == 0) i = blockIdx.x + static_cast<int64_t>(atomicAdd(&zero_next, 1)) * gridDim.x;
+      i = __shfl_sync(0xffffffffu, i, 0);
+      if (i >= none) break;
+      const size_t r = static_cast<size_t>(i < before ? i : s_first[p.E] + (i - before));
+      uint4* o = reinterpret_cast<uint4*>(p.out + r * p.M);
+      for (int c = lane; c < p.M / 8; c += 32) o[c] = zero;
+      if (kForm == kGated && p.saved_kind == kSavedBf16) {
+        uint4* k = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.saved) + r * 2 * p.M);
+        for (int c = lane; c < p.M / 4; c += 32) k[c] = zero;
+      } else if (kForm == kGated && p.saved_kind == kSaved8) {
+        uint4* k = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.saved) + r * 2 * p.M);
+        for (int c = lane; c < p.M / 8; c += 32) k[c] = zero;
+        const int groups = 2 * ((p.M + kGroup8 - 1) / kGroup8);
+        for (int c = lane; c < groups; c += 32) p.exponents[r * groups + c] = 0;
+      }
+    }
   };
 
   bool joined = false;  // whether this warp has met the others of the cluster for the sums
@@ -498,23 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else {
-      // ---------------- rows that no expert owns ----------------
-      const int before = s_first[0], end = s_first[p.E];
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      for (int i = blockIdx.x; i < before + p.N - end; i += gridDim.x) {
-        const size_t r = static_cast<size_t>(i < before ? i : end + (i - before));
-        uint4* o = reinterpret_cast<uint4*>(p.out + r * p.M);
-        for (int c = lane; c < p.M / 8; c += 32) o[c] = zero;
-        if (kForm == kGated && p.saved_kind == kSavedBf16) {
-          uint4* k = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.saved) + r * 2 * p.M);
-          for (int c = lane; c < p.M / 4; c += 32) k[c] = zero;
-        } else if (kForm == kGated && p.saved_kind == kSaved8) {
-          uint4* k = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.saved) + r * 2 * p.M);
-          for (int c = lane; c < p.M / 8; c += 32) k[c] = zero;
-          const int groups = 2 * ((p.M + kGroup8 - 1) / kGroup8);
-          for (int c = lane; c < groups; c += 32) p.exponents[r * groups + c] = 0;
-        }
-      }
+      zero_rows();
     }
   } else {
     // ---------------- epilogue (warps 2..9) ----------------
@@ -769,6 +783,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
     cluster_sync();
   }
+  __syncwarp();
+  if (kForm != kWeights) zero_rows();
   // Neither CTA may leave while the pair's MMAs could still read its shared memory or
   // write its TMEM, or while its peer could still signal it.
   tc_fence_before();
@@ -803,9 +819,7 @@ constexpr int kMaxDevices = 64;
 constexpr int kMaxParts = 4;
 int g_clusters[kMaxDevices][kMaxParts];
 
-int resident(const DeviceInfo& dev, int parts) {
-  return std::max(1, g_clusters[dev.device][parts - 1]);
-}
+int resident(const DeviceInfo& dev, int parts) { return g_clusters[dev.device][parts - 1]; }
 
 // How a call is cut: rows (kWeights: columns) of a tile and pairs that share a sum.
 struct Cut {
@@ -835,6 +849,9 @@ bool sums_fit(int parts, int rows, int stages) {
   return (parts - 1) * rows * 512 <= stages * stage_bytes(rows);
 }
 
+// Stages of such tiles beside the widest chunks.
+int stages_of(int rows) { return std::min(kMaxStages, 3 * 65536 / stage_bytes(rows)); }
+
 // `tiles(rows)` for tiles of at most `rows` rows. Whole waves count: as many tiles as pairs
 // are resident run at once.
 template <typename Tiles>
@@ -844,8 +861,8 @@ Cut cut(const DeviceInfo& dev, int blocks, int most_rows, int most_parts, Tiles 
   for (int rows = std::min(kTileRows, most_rows); rows >= 64 || best_cycles == INT64_MAX;
        rows -= 32)
     for (int parts = 1; parts <= most_parts && parts <= blocks; ++parts) {
-      const int64_t n = tiles(rows), at_once = resident(dev, parts);
-      if (parts > 1 && (n > at_once || !sums_fit(parts, rows, std::min(kMaxStages, 196608 / stage_bytes(rows))))) continue;
+      const int64_t n = tiles(rows), at_once = std::max(resident(dev, parts), parts == 1 ? 1 : 0);
+      if (parts > 1 && (n > at_once || !sums_fit(parts, rows, stages_of(rows)))) continue;
       const int64_t waves = ceil_div(n, at_once);
       const int64_t cycles = waves * tile_cycles(blocks, rows, parts);
       if (cycles < best_cycles) {
@@ -871,7 +888,7 @@ Cut cut_rows(const DeviceInfo& dev, const int32_t* offsets, int N, int E, int mb
   // even the most tiles that there can be leave pairs idle.
   Cut c{all, 1, most_row_tiles(N, E, mblocks, all)};
   for (int parts = 2; parts <= kMaxParts && parts <= ceil_div(K, kBlockK); ++parts)
-    if (c.tiles <= resident(dev, parts) && sums_fit(parts, all, std::min(kMaxStages, 196608 / stage_bytes(all)))) c.parts = parts;
+    if (c.tiles <= resident(dev, parts) && sums_fit(parts, all, stages_of(all))) c.parts = parts;
   return c;
 }
 
@@ -889,7 +906,7 @@ cudaError_t launch(Kernel kernel, Form form, const CUtensorMap& a_map, const Map
                       experts_table_bytes(p.E);
   if (!sums_fit(p.parts, p.tile_rows, p.stages)) p.parts = 1;  // (a wide table of experts)
   const int clusters = static_cast<int>(
-      p.parts > 1 ? c.tiles : std::min<int64_t>(resident(dev, 1), c.tiles));
+      p.parts > 1 ? c.tiles : std::min<int64_t>(std::max(1, resident(dev, 1)), c.tiles));
   return launch_dependent_clusters(2 * p.parts, kernel, dim3(2 * p.parts * clusters),
                                    dim3(kThreads), smem, stream, a_map, b_maps, p);
 }
@@ -1050,7 +1067,8 @@ cudaError_t launch_expert_weights(const ExpertWeightsArgs& a, const DeviceInfo& 
   p.whole_b = whole(a.C) && c.tile_rows % 128 == 0;  // (a half begins at a whole piece)
   CUtensorMap g_map;
   Maps x_maps{};
-  if (!sums_map(&g_map, a.grad, a.N, a.M, p.whole_a) || !sums_map(&x_maps.map[0], a.x, a.N, a.C, p.whole_b))
+  if (!sums_map(&g_map, a.grad, a.N, a.M, p.whole_a) ||
+      !sums_map(&x_maps.map[0], a.x, a.N, a.C, p.whole_b))
     return cudaErrorInvalidValue;
   return launch(kKernels[4], kWeights, g_map, x_maps, p, c, dev, stream);
 }
