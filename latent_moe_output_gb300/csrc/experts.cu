@@ -126,11 +126,12 @@ struct Table {
 };
 
 // Rows of an expert's tiles: the fewest tiles of at most tile_rows rows, all of one size.
+// (One tile as a rule, and no division: every CTA asks this of every expert.)
 __device__ __forceinline__ int tiles_of(const Params& p, int n) {
-  return (n + p.tile_rows - 1) / p.tile_rows;
+  return n <= p.tile_rows ? (n > 0) : (n + p.tile_rows - 1) / p.tile_rows;
 }
 __device__ __forceinline__ int tile_size(int n, int tiles) {
-  return ((n + tiles - 1) / tiles + 31) & ~31;
+  return ((tiles <= 1 ? n : (n + tiles - 1) / tiles) + 31) & ~31;
 }
 
 // Tile `tile` of the order: the features of one pass over an expert's rows, then the next
@@ -152,7 +153,8 @@ __device__ __forceinline__ Tile tile_at(const Params& p, int tile, int& at, cons
     while (s.unit[at + 1] <= unit) ++at;
     t.e = s.order[at];
     const int n = s.first[t.e + 1] - s.first[t.e], i = unit - s.unit[at];
-    const int size = tile_size(n, tiles_of(p, n));
+    const int tiles = (n + p.tile_rows - 1) / p.tile_rows;
+    const int size = ((n + tiles - 1) / tiles + 31) & ~31;  // (tile_size without its branch)
     t.row0 = s.first[t.e] + i * size;
     t.rows = min(size, n - i * size);
     t.m0 = (tile - unit * p.mblocks) * (kForm == kGated ? 128 : 256);

@@ -40,12 +40,14 @@ __device__ __forceinline__ void load_experts(const int32_t* offsets, int N, int 
 // with a block barrier.
 template <typename Units>
 __device__ __forceinline__ void sum_units(int count, int* s_unit, Units units) {
+  for (int i = threadIdx.x; i < count; i += blockDim.x) s_unit[i] = units(i);
+  __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    const int per = (count + 32) / 32;
+    const int per = (count + 32) / 32;  // each lane takes a contiguous part
     const int lo = min(count + 1, lane * per), hi = min(count + 1, lo + per);
     int sum = 0;
-    for (int i = lo; i < hi && i < count; ++i) sum += units(i);
+    for (int i = lo; i < min(hi, count); ++i) sum += s_unit[i];
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -54,8 +56,9 @@ __device__ __forceinline__ void sum_units(int count, int* s_unit, Units units) {
     }
     int run = incl - sum;
     for (int i = lo; i < hi; ++i) {
+      const int own = i < count ? s_unit[i] : 0;
       s_unit[i] = run;
-      if (i < count) run += units(i);
+      run += own;
     }
   }
   __syncthreads();

@@ -241,7 +241,10 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
 
 }  // namespace
 
-// One wave of CTAs for rows of several experts. With one matrix, 16 rows a pass, of which
+// Two waves of CTAs for rows of several experts (8 of 256 experts of 2 x 1024 x 2048, 512
+// CTAs: 24 us against 20 of the tensor-core kernel; 2 tokens with 4 of 32 experts of 2 x 512
+// x 2048, 256 CTAs: 11.6 against 13.1; 8 with 4 of 8, 2 x 256 x 1024: 6.7 against 9.2). With
+// one matrix, 16 rows a pass, of which
 // all but the first read the weights from L2: the passes' time at 6.8 TB/s against that of
 // the tensor-core kernel, 1.5 us more to begin with and 0.2 us per 128 columns (both
 // measured, us: 58.7 MB of weights, 16 and 24 rows 13.5 and 20 against 16.7; 29 MB, 16 rows
@@ -250,7 +253,7 @@ bool few_rows(const int32_t* offsets, int N, int E, int M, int C, bool gated,
               const DeviceInfo& dev) {
   const int64_t per = gated ? kRowsPerCta / 2 : kRowsPerCta;
   const int64_t blocks = (M + per - 1) / per;
-  if (offsets != nullptr) return N <= 16 && std::min(N, E) * blocks <= dev.num_sms;
+  if (offsets != nullptr) return N <= 32 && std::min(N, E) * blocks <= 2 * dev.num_sms;
   const double passes = (N + 15) / 16;
   const double bytes = (gated ? 4.0 : 2.0) * M * C;
   return N <= 64 && passes * bytes / 6.8e6 <= 1.5 + 0.2 * ((C + 127) / 128);
