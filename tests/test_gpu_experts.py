@@ -653,3 +653,45 @@ def test_call_from_a_thread_without_a_context():
     assert got == [Status.OK]
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def random_shape(seed):
+    """N, E, M, C and counts over the ranges where the kernels' choices change."""
+    import random
+
+    r = random.Random(seed)
+    log = lambda lo, hi: int(round(lo * (hi / lo) ** r.random()))  # noqa: E731
+    N, M, C = log(1, 4000), 8 * log(1, 300), 8 * log(1, 300)
+    if r.random() < 0.4:
+        return N, 1, M, C, None, 0
+    E = log(1, 300)
+    M, C = min(M, 8 * (8000 // E + 1)), min(C, 1024)
+    cuts = sorted(r.randint(0, N) for _ in range(E - 1))
+    start, end = (r.randint(0, N // 8), N - r.randint(0, N // 8)) if r.random() < 0.5 else (0, N)
+    cuts = [min(max(c, start), end) for c in cuts]
+    edges = [start] + cuts + [end]
+    return N, E, M, C, [b - a for a, b in zip(edges[:-1], edges[1:])], start
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_shapes_of_integers(seed):
+    N, E, M, C, counts, start = random_shape(seed)
+    F = max(8, M // 16 * 8)
+    g = gen(seed)
+    offsets = None if counts is None else offs(*counts, start=start)
+    x, w, dy = ints(N, C, g=g), ints(E, M, C, g=g), ints(N, M, g=g)
+    same(lt.expert_matmul(x, w, offsets, out=nan(N, M)), er.matmul(x, w, offsets)[0], "out")
+    got = lt.expert_matmul_backward(dy, x, w, offsets, grad_x=nan(N, C), grad_weights=nan(E, M, C))
+    for a, b in zip(got, er.matmul_backward(dy, x, w, offsets)):
+        same(a, b, "gradient")
+    up = ints(E, 2 * F, C, g=g, most=1)
+    pre = er.matmul(x, up, offsets)[0].unflatten(1, (2, F))
+    saved = nan(N, 2, F) if seed % 2 else lt.Checkpoint8.empty(N, 2, F)
+    hidden = lt.expert_gated(x, up, offsets, hidden=nan(N, F), saved=saved)
+    if seed % 2:
+        same(saved, pre, "saved")
+    else:
+        same(lt.dequantize8(saved), er.dequantize8(*er.quantize8(pre)), "saved")
+    want = er.act(pre[:, 0], "silu") * pre[:, 1]
+    br.assert_within(hidden, want, br.bf16_bound(want, act_error(pre[:, 0], "silu", want)))
+    latent_tail_check()
