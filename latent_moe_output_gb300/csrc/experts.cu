@@ -188,6 +188,35 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
   return true;
 }
 
+// What a producer has issued (words, in shared memory).
+struct Issued {
+  uint32_t blocks;
+  uint32_t bytes[kMaxStages];  // of the last block in a stage, on full_bar (0: on tail_bar)
+  uint32_t tails[kMaxStages];  // blocks in a stage on tail_bar
+};
+
+// Waits, in the even CTA, for the copies of both CTAs of a pair. The two may have issued
+// different numbers of blocks when a wait ran out, and a barrier completes only with as many
+// bytes as the even CTA expected: what the odd CTA has issued beyond the even one is expected
+// here, and what it has not issued is taken off. A CTA issues a block only after the MMAs of
+// the one before it in the stage, so no more than the last `stages` blocks are open.
+__device__ __noinline__ void drain_copies(uint64_t* full_bar, int stages, const Issued& even,
+                                          const Issued& odd) {
+  const int own = static_cast<int>(even.blocks), other = static_cast<int>(odd.blocks);
+  const int most = max(own, other);
+  for (int it = max(0, most - stages); it < most; ++it) {
+    const int s = it % stages;
+    const uint32_t bar = smem_u32(&full_bar[s]);
+    if (it >= own) {
+      if (odd.bytes[s] == 0) continue;
+      mbar_arrive_expect_tx(bar, odd.bytes[s]);
+    } else if (it >= other && even.bytes[s] != 0) {
+      mbar_complete_tx(bar, even.bytes[s]);
+    }
+    wait_drain(bar, static_cast<uint32_t>(it / stages) & 1u);
+  }
+}
+
 __device__ __forceinline__ void group_barrier(int group) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
@@ -208,6 +237,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int abort_flag;
   __shared__ int zero_next;    // rows without an expert that have been handed out
   __shared__ int part_failed;  // a pair's sum did not come (first pair of a cluster)
+  // For the wind-down after a wait that ran out (see drain_copies): blocks that this CTA's
+  // producer has issued, the bytes of the last one in each stage that count on the even CTA's
+  // full_bar, and the blocks in each stage that counted on this CTA's tail_bar.
+  __shared__ Issued issued, odd_issued;  // (odd_issued: in the even CTA, the odd one's)
+  __shared__ int wind_down;              // a wait ran out in some CTA of the cluster
   volatile int* abort_v = &abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -236,6 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&drain_bar), 1);
     abort_flag = 0;
+    issued = Issued{};
+    wind_down = 0;
     part_failed = 0;
     zero_next = 0;
     mbar_fence_init();
@@ -309,8 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
       // ---------------- producer (this CTA's halves; the whole warp, one lane issues) ------
       int at = 0, s = 0;
-      uint32_t round = 0, tails = 0, tail_phase = 0;
-      int issued = 0;
+      uint32_t round = 0;
+      int blocks = 0;
       const int copied = static_cast<int>(min(static_cast<int64_t>(tiles), p.ring.copied));
       bool alive = true;
       for (Walk walk(cluster, n_clusters, copied); alive && walk.more(); walk.next()) {
@@ -329,11 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t a = ring + static_cast<uint32_t>(s * p.stage_bytes), b = a + kOperandBytes;
           const int k0 = kb * kBlockK;
           const bool tail = kForm == kWeights && kb == nkb - 1 && needs_zeros(t);
-          if (tail) {
-            tails |= 1u << s;
-            tail_phase ^= 1u << s;
-          }
           const bool issue = elect_one();
+          ++blocks;
+          if (issue) {
+            issued.blocks = blocks;
+            issued.bytes[s] = tail ? 0 : bytes;
+            if (tail) ++issued.tails[s];
+          }
           if (issue && tail) {
             // Completes on this CTA's own barrier, for the warp that puts the zeros in.
             const uint32_t bar = smem_u32(&tail_bar[s]);
@@ -396,19 +434,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
-          ++issued;
           if (++s == stages) {
             s = 0;
             ++round;
           }
         }
-      }
-      if (*abort_v && lane == 0) {  // copies in flight land before the CTA's shared memory goes
-        if (rank == 0)  // the even CTA's barriers count both CTAs' copies
-          for (int it = max(0, issued - stages); it < issued; ++it)
-            wait_drain(smem_u32(&full_bar[it % stages]), static_cast<uint32_t>(it / stages) & 1u);
-        for (int i = 0; i < stages; ++i)  // the last tail of each stage
-          if (tails >> i & 1u) wait_drain(smem_u32(&tail_bar[i]), (tail_phase >> i & 1u) ^ 1u);
       }
     }
     __syncwarp();
@@ -805,13 +835,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   pdl_launch_dependents();
-  if (warp == 1 && rank == 0 && *abort_v && elect_one()) {
-    // The MMAs issued before the abort: a commit behind them, waited for.
-    umma_commit_pair(smem_u32(&drain_bar), 0x1 << even);
-    wait_drain(smem_u32(&drain_bar), 0);
-  }
+  // A wait that ran out in one CTA: all of its cluster wind down with it, as what is in
+  // flight may be theirs. (The producer may have ended before: what it issued is waited for
+  // here, when no role runs any more.)
+  if (*abort_v && threadIdx.x < static_cast<unsigned>(2 * p.parts))
+    st_dsmem_u32(map_to_rank(smem_u32(&wind_down), threadIdx.x), 1);
   __syncwarp();
   cluster_sync();
+  if (*const_cast<volatile int*>(&wind_down) != 0) {
+    if (rank == 1 && threadIdx.x < sizeof(Issued) / 4)
+      st_dsmem_u32(map_to_rank(smem_u32(&odd_issued) + threadIdx.x * 4, even),
+                   reinterpret_cast<const volatile uint32_t*>(&issued)[threadIdx.x]);
+    __syncwarp();
+    cluster_sync();
+    if (warp == 1 && rank == 0 && elect_one()) {
+      // The MMAs issued before the abort: a commit behind them, waited for.
+      umma_commit_pair(smem_u32(&drain_bar), 0x1 << even);
+      wait_drain(smem_u32(&drain_bar), 0);
+    }
+    if (threadIdx.x == 0) {
+      if (rank == 0) drain_copies(full_bar, stages, issued, odd_issued);
+      for (int s = 0; s < stages; ++s)  // the last tail of each stage
+        if (issued.tails[s] != 0) wait_drain(smem_u32(&tail_bar[s]), (issued.tails[s] - 1) & 1u);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
