@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
           for (int h = 0; h < 2; ++h) a[u][m][h] = in ? ld_stream_v4(w[m][h] + c) : zero;
 #pragma unroll
         for (int n = 0; n < kTiles; ++n)
-          b[u][n] = in && has[n] ? __ldg(reinterpret_cast<const uint4*>(x[n] + c)) : zero;
+          b[u][n] = in && has[n] ? ld_global_v4(x[n] + c) : zero;
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)

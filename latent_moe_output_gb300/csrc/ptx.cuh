@@ -472,6 +472,18 @@ __device__ __forceinline__ uint4 ld_l2_v4(const void* p) {
   return v;
 }
 
+// 16-byte load of what the work before on the stream may still be writing when the kernel
+// starts: behind pdl_wait() it stays there, as volatile asm does not change places. (__ldg
+// promises memory that nothing writes while the kernel runs, so the compiler may move it
+// above the wait.)
+__device__ __forceinline__ uint4 ld_global_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // 16-byte store marked streaming (evict first): output that is written once and
 // not read again by this kernel, so it does not displace re-read operands in L2.
 // 8-byte store to global memory.
