@@ -513,6 +513,16 @@ LT_API lt_status latent_tail_expert_gated(const uint16_t* x, const uint16_t* wei
                                           lt_stream stream);
 
 /*
+ * Diagnostic as latent_tail_selftest_expert_matmul_timeout (below), for the waits of
+ * latent_tail_expert_gated: each element of hidden and of what is kept is the call's result
+ * or untouched.
+ */
+LT_API lt_status latent_tail_selftest_expert_gated_timeout(
+    const uint16_t* x, const uint16_t* weights, const int32_t* offsets, uint16_t* hidden,
+    void* saved, uint8_t* saved_exponents, int N, int E, int F, int C, lt_activation activation,
+    lt_saved saved_kind, int copied_tiles, unsigned int limit_us, lt_stream stream);
+
+/*
  * Bytes of device workspace latent_tail_expert_gated_backward needs: the gradient at both
  * projections, [N, 2F] bf16. Returns 0 for N <= 0 or invalid shapes. Host-only.
  */
@@ -570,6 +580,16 @@ LT_API lt_status latent_tail_expert_matmul_backward(const uint16_t* grad_out, co
                                                     const int32_t* offsets, uint16_t* grad_x,
                                                     uint16_t* grad_weights, int N, int E, int M,
                                                     int C, lt_stream stream);
+
+/*
+ * Diagnostic as latent_tail_selftest_expert_matmul_timeout, for the waits of
+ * latent_tail_expert_matmul_backward (of the kernel of each gradient): each element of a
+ * gradient is the call's result or untouched.
+ */
+LT_API lt_status latent_tail_selftest_expert_matmul_backward_timeout(
+    const uint16_t* grad_out, const uint16_t* x, const uint16_t* weights, const int32_t* offsets,
+    uint16_t* grad_x, uint16_t* grad_weights, int N, int E, int M, int C, int copied_tiles,
+    unsigned int limit_us, lt_stream stream);
 
 /*
  * Activations in 8 bits: per row and 16 columns (fewer behind the last multiple of 16) a

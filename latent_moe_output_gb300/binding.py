@@ -86,6 +86,9 @@ _SIGNATURES = {
         + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint, ctypes.c_void_p]),
     "latent_tail_expert_gated": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int] * 6
                                  + [ctypes.c_void_p]),
+    "latent_tail_selftest_expert_gated_timeout": (
+        ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int] * 7
+        + [ctypes.c_uint, ctypes.c_void_p]),
     "latent_tail_expert_gated_backward_workspace_size": (ctypes.c_size_t, [ctypes.c_int] * 2),
     "latent_tail_expert_gated_backward": (ctypes.c_int, [ctypes.c_void_p] * 9
                                           + [ctypes.c_int] * 6
@@ -97,6 +100,9 @@ _SIGNATURES = {
         + [ctypes.c_uint, ctypes.c_void_p]),
     "latent_tail_expert_matmul_backward": (ctypes.c_int, [ctypes.c_void_p] * 6
                                            + [ctypes.c_int] * 4 + [ctypes.c_void_p]),
+    "latent_tail_selftest_expert_matmul_backward_timeout": (
+        ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int] * 5
+        + [ctypes.c_uint, ctypes.c_void_p]),
     "latent_tail_quantize8": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_int] * 2
                               + [ctypes.c_void_p]),
     "latent_tail_dequantize8": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_int] * 2

@@ -88,15 +88,10 @@ lt_status expert_matmul(const uint16_t* x, const uint16_t* weights, const int32_
   return launch_status(launch_expert_rows(a, *dev, raw(stream)));
 }
 
-}  // namespace
-
-extern "C" {
-
-LT_API lt_status latent_tail_expert_gated(const uint16_t* x, const uint16_t* weights,
-                                          const int32_t* offsets, uint16_t* hidden, void* saved,
-                                          uint8_t* saved_exponents, int N, int E, int F, int C,
-                                          lt_activation activation, lt_saved saved_kind,
-                                          lt_stream stream) {
+lt_status expert_gated(const uint16_t* x, const uint16_t* weights, const int32_t* offsets,
+                       uint16_t* hidden, void* saved, uint8_t* saved_exponents, int N, int E, int F,
+                       int C, lt_activation activation, lt_saved saved_kind,
+                       const RingLimits& ring, lt_stream stream) {
   lt_status st = check_sizes(N, E, F, C, offsets);
   if (st != LT_OK) return st;
   if (F > kMaxWidth / 2 || !known(activation)) return LT_ERR_INVALID_ARG;
@@ -114,8 +109,69 @@ LT_API lt_status latent_tail_expert_gated(const uint16_t* x, const uint16_t* wei
   const lt::DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev, Operator::kExperts)) != LT_OK) return st;
   const ExpertGatedArgs a{x, weights, offsets, hidden, saved, saved_exponents, N, E, F, C,
-                          activation, saved_kind, RingLimits{}};
+                          activation, saved_kind, ring};
   return launch_status(launch_expert_gated(a, *dev, raw(stream)));
+}
+
+lt_status expert_matmul_backward(const uint16_t* grad_out, const uint16_t* x,
+                                 const uint16_t* weights, const int32_t* offsets, uint16_t* grad_x,
+                                 uint16_t* grad_weights, int N, int E, int M, int C,
+                                 const RingLimits& ring, lt_stream stream) {
+  lt_status st = check_sizes(N, E, M, C, offsets);
+  if (st != LT_OK) return st;
+  if (N == 0) return zero_weights(grad_weights, E, M, C, stream);
+  if (grad_x == nullptr && grad_weights == nullptr) return LT_ERR_INVALID_ARG;
+  if ((st = check_ptrs({grad_out})) != LT_OK) return st;
+  if ((grad_x != nullptr && weights == nullptr) || (grad_weights != nullptr && x == nullptr))
+    return LT_ERR_INVALID_ARG;
+  if ((st = check_optional({x, weights, offsets, grad_x, grad_weights})) != LT_OK) return st;
+  const size_t w_bytes = E * bytes_of(M, C, 2);
+  if (!disjoint({span(grad_x, bytes_of(N, C, 2)), span(grad_weights, w_bytes)},
+                {span(grad_out, bytes_of(N, M, 2)), span(x, bytes_of(N, C, 2)),
+                 span(weights, w_bytes), span(offsets, bytes_of(E + 1, 4, 1))}))
+    return LT_ERR_INVALID_ARG;
+  const lt::DeviceInfo* dev = nullptr;
+  if ((st = current_device(&dev, Operator::kExperts)) != LT_OK) return st;
+  if (grad_x != nullptr) {
+    const ExpertRowsArgs r{grad_out, weights, offsets, grad_x, N, E, C, M, true, ring};
+    if ((st = launch_status(launch_expert_rows(r, *dev, raw(stream)))) != LT_OK) return st;
+  }
+  if (grad_weights != nullptr) {
+    const ExpertWeightsArgs w{grad_out, x, offsets, grad_weights, N, E, M, C, ring};
+    st = launch_status(launch_expert_weights(w, *dev, raw(stream)));
+  }
+  return st;
+}
+
+// Limits of a self-test of expired waits.
+lt_status test_limits(int copied_tiles, unsigned int limit_us, RingLimits* ring) {
+  if (copied_tiles < 0 || limit_us < 1 || limit_us > 1000000) return LT_ERR_INVALID_ARG;
+  *ring = RingLimits{copied_tiles, static_cast<uint64_t>(limit_us) * 1000u};
+  return LT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+LT_API lt_status latent_tail_expert_gated(const uint16_t* x, const uint16_t* weights,
+                                          const int32_t* offsets, uint16_t* hidden, void* saved,
+                                          uint8_t* saved_exponents, int N, int E, int F, int C,
+                                          lt_activation activation, lt_saved saved_kind,
+                                          lt_stream stream) {
+  return expert_gated(x, weights, offsets, hidden, saved, saved_exponents, N, E, F, C, activation,
+                      saved_kind, RingLimits{}, stream);
+}
+
+LT_API lt_status latent_tail_selftest_expert_gated_timeout(
+    const uint16_t* x, const uint16_t* weights, const int32_t* offsets, uint16_t* hidden,
+    void* saved, uint8_t* saved_exponents, int N, int E, int F, int C, lt_activation activation,
+    lt_saved saved_kind, int copied_tiles, unsigned int limit_us, lt_stream stream) {
+  RingLimits ring;
+  const lt_status st = test_limits(copied_tiles, limit_us, &ring);
+  return st != LT_OK ? st
+                     : expert_gated(x, weights, offsets, hidden, saved, saved_exponents, N, E, F, C,
+                                    activation, saved_kind, ring, stream);
 }
 
 LT_API size_t latent_tail_expert_gated_backward_workspace_size(int N, int F) {
@@ -182,9 +238,9 @@ LT_API lt_status latent_tail_expert_matmul(const uint16_t* x, const uint16_t* we
 LT_API lt_status latent_tail_selftest_expert_matmul_timeout(
     const uint16_t* x, const uint16_t* weights, const int32_t* offsets, uint16_t* out, int N,
     int E, int M, int C, int copied_tiles, unsigned int limit_us, lt_stream stream) {
-  if (copied_tiles < 0 || limit_us < 1 || limit_us > 1000000) return LT_ERR_INVALID_ARG;
-  const RingLimits ring{copied_tiles, static_cast<uint64_t>(limit_us) * 1000u};
-  return expert_matmul(x, weights, offsets, out, N, E, M, C, ring, stream);
+  RingLimits ring;
+  const lt_status st = test_limits(copied_tiles, limit_us, &ring);
+  return st != LT_OK ? st : expert_matmul(x, weights, offsets, out, N, E, M, C, ring, stream);
 }
 
 LT_API lt_status latent_tail_expert_matmul_backward(const uint16_t* grad_out, const uint16_t* x,
@@ -192,30 +248,19 @@ LT_API lt_status latent_tail_expert_matmul_backward(const uint16_t* grad_out, co
                                                     const int32_t* offsets, uint16_t* grad_x,
                                                     uint16_t* grad_weights, int N, int E, int M,
                                                     int C, lt_stream stream) {
-  lt_status st = check_sizes(N, E, M, C, offsets);
-  if (st != LT_OK) return st;
-  if (N == 0) return zero_weights(grad_weights, E, M, C, stream);
-  if (grad_x == nullptr && grad_weights == nullptr) return LT_ERR_INVALID_ARG;
-  if ((st = check_ptrs({grad_out})) != LT_OK) return st;
-  if ((grad_x != nullptr && weights == nullptr) || (grad_weights != nullptr && x == nullptr))
-    return LT_ERR_INVALID_ARG;
-  if ((st = check_optional({x, weights, offsets, grad_x, grad_weights})) != LT_OK) return st;
-  const size_t w_bytes = E * bytes_of(M, C, 2);
-  if (!disjoint({span(grad_x, bytes_of(N, C, 2)), span(grad_weights, w_bytes)},
-                {span(grad_out, bytes_of(N, M, 2)), span(x, bytes_of(N, C, 2)),
-                 span(weights, w_bytes), span(offsets, bytes_of(E + 1, 4, 1))}))
-    return LT_ERR_INVALID_ARG;
-  const lt::DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev, Operator::kExperts)) != LT_OK) return st;
-  if (grad_x != nullptr) {
-    const ExpertRowsArgs r{grad_out, weights, offsets, grad_x, N, E, C, M, true, RingLimits{}};
-    if ((st = launch_status(launch_expert_rows(r, *dev, raw(stream)))) != LT_OK) return st;
-  }
-  if (grad_weights != nullptr) {
-    const ExpertWeightsArgs w{grad_out, x, offsets, grad_weights, N, E, M, C, RingLimits{}};
-    st = launch_status(launch_expert_weights(w, *dev, raw(stream)));
-  }
-  return st;
+  return expert_matmul_backward(grad_out, x, weights, offsets, grad_x, grad_weights, N, E, M, C,
+                                RingLimits{}, stream);
+}
+
+LT_API lt_status latent_tail_selftest_expert_matmul_backward_timeout(
+    const uint16_t* grad_out, const uint16_t* x, const uint16_t* weights, const int32_t* offsets,
+    uint16_t* grad_x, uint16_t* grad_weights, int N, int E, int M, int C, int copied_tiles,
+    unsigned int limit_us, lt_stream stream) {
+  RingLimits ring;
+  const lt_status st = test_limits(copied_tiles, limit_us, &ring);
+  return st != LT_OK ? st
+                     : expert_matmul_backward(grad_out, x, weights, offsets, grad_x, grad_weights,
+                                              N, E, M, C, ring, stream);
 }
 
 LT_API lt_status latent_tail_quantize8(const uint16_t* x, int8_t* values, uint8_t* exponents,
