@@ -217,6 +217,31 @@ __device__ __noinline__ void drain_copies(uint64_t* full_bar, int stages, const 
   }
 }
 
+// mbar_wait for the copy of a block that the producer may come to much later: the limit
+// begins again whenever `blocks`, what it has issued, has grown.
+__device__ __forceinline__ bool wait_behind(uint32_t bar, uint32_t parity, uint32_t* err,
+                                            volatile int* abort_flag, uint64_t limit_ns,
+                                            const volatile uint32_t* blocks) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = global_timer_ns();
+  uint32_t seen = *blocks;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    const uint32_t now = *blocks;
+    if (now != seen) {
+      seen = now;
+      t0 = global_timer_ns();
+    } else if (global_timer_ns() - t0 > limit_ns) {
+      atomicOr(err, kErrWaitTimeout);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
 __device__ __forceinline__ void group_barrier(int group) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
@@ -543,8 +568,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!needs_zeros(t) || end != nkb) continue;
         const int s = (it - 1) % stages;
         const int from = t.rows - (blocks_of(t) - 1) * kBlockK, to = (from + 15) & ~15;
-        alive = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tail_bar[s]), phase >> s & 1u, p.err,
-                                                  abort_v, p.ring.limit_ns));
+        // The blocks before this one may take any time; the limit is of the one wait.
+        alive = __all_sync(0xffffffffu,
+                           wait_behind(smem_u32(&tail_bar[s]), phase >> s & 1u, p.err, abort_v,
+                                       p.ring.limit_ns, &issued.blocks));
         if (!alive) break;
         phase ^= 1u << s;
         // Four boxes of 128 rows of 128 bytes (the swizzle stays within a row).

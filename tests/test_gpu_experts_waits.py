@@ -179,3 +179,19 @@ def test_gradients_of_a_product(lib, N, E, M, C, counts):
             again = lt.expert_matmul_backward(dy, x, w, offsets)
             assert all(torch.equal(a, b) for a, b in zip(again, want))
             latent_tail_check()
+
+
+def test_a_limit_is_of_one_wait_and_not_of_the_work_before_it(lib):
+    """Tiles whose rows end inside an MMA's 16 come last here, 3 ms of healthy work after the
+    first; a wait may take 1 ms."""
+    counts, M, C = (16384, 8), 16384, 16384
+    N, E = sum(counts), len(counts)
+    g = gen(1)
+    offsets = offs(*counts)
+    x, dy = ints(N, C, g=g), ints(N, M, g=g)
+    want = lt.expert_matmul_backward(dy, x, None, offsets)[1]
+    got = marked(E, M, C)
+    status = ended_by(lambda: lib.latent_tail_selftest_expert_matmul_backward_timeout(
+        ptr(dy), ptr(x), 0, ptr(offsets), 0, ptr(got), N, E, M, C, ALL, 1000, stream()))
+    assert status == Status.OK
+    assert torch.equal(got, want)
