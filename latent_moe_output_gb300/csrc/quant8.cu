@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedGradArg
     float dg[8], du[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      dg[j] = d[j] * u[j] * slope[j];
+      dg[j] = d[j] * slope[j] * u[j];  // (a' is 0 far out, where d u may pass FP32's range)
       du[j] = d[j] * act[j];
     }
     uint16_t* dst = a.grad_pre + row * 2 * a.F + f;
