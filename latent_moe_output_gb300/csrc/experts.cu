@@ -930,30 +930,40 @@ int64_t tile_cycles(int blocks, int rows, int parts) {
          (parts > 1 ? 2500 + (parts - 1) * (2500 + 20 * rows) : 0);
 }
 
-// Bytes of a stage of tiles of `rows` rows.
-int stage_bytes(int rows) {
-  return static_cast<int>(kOperandBytes) + (rows / 2 + 31) / 32 * 8192;
+// The stages of a form's tiles of `rows` rows (kWeights: columns).
+struct Ring {
+  int stages, stage_bytes;
+};
+
+// As many stages as fit beside the chunks, the experts' table and static shared memory.
+Ring ring_of(Form form, int saved_kind, int rows, int E, const DeviceInfo& dev) {
+  const int bytes = form == kWeights
+                        ? static_cast<int>(2 * kOperandBytes)
+                        : static_cast<int>(kOperandBytes) + (rows / 2 + 31) / 32 * 8192;
+  const int rest = dev.max_smem_optin - 1024 - 1024 - kGroups * turn_bytes(form, saved_kind) -
+                   experts_table_bytes(E);
+  return Ring{std::min(kMaxStages, rest / bytes), bytes};
 }
 
-// Whether the stages hold the sums of a tile's other pairs.
-bool sums_fit(int parts, int rows, int stages) {
-  return (parts - 1) * rows * 512 <= stages * stage_bytes(rows);
+// Whether the stages hold the sums of a tile's other pairs, beside the widest chunks of the
+// form: the order of a sum does not depend on what is kept.
+bool sums_fit(Form form, int parts, int rows, int E, const DeviceInfo& dev) {
+  const Ring ring = ring_of(form, kSavedBf16, rows, E, dev);
+  return (parts - 1) * rows * 512 <= ring.stages * ring.stage_bytes;
 }
-
-// Stages of such tiles beside the widest chunks.
-int stages_of(int rows) { return std::min(kMaxStages, 3 * 65536 / stage_bytes(rows)); }
 
 // `tiles(rows)` for tiles of at most `rows` rows. Whole waves count: as many tiles as pairs
 // are resident run at once.
 template <typename Tiles>
-Cut cut(const DeviceInfo& dev, int blocks, int most_rows, int most_parts, Tiles tiles) {
+Cut cut(const DeviceInfo& dev, Form form, int E, int blocks, int most_rows, int most_parts,
+        Tiles tiles) {
   Cut best{};
   int64_t best_cycles = INT64_MAX;
   for (int rows = std::min(kTileRows, most_rows); rows >= 64 || best_cycles == INT64_MAX;
        rows -= 32)
     for (int parts = 1; parts <= most_parts && parts <= blocks; ++parts) {
       const int64_t n = tiles(rows), at_once = std::max(resident(dev, parts), parts == 1 ? 1 : 0);
-      if (parts > 1 && (n > at_once || !sums_fit(parts, rows, stages_of(rows)))) continue;
+      if (parts > 1 && (n > at_once || !sums_fit(form, parts, rows, E, dev))) continue;
       const int64_t waves = ceil_div(n, at_once);
       const int64_t cycles = waves * tile_cycles(blocks, rows, parts);
       if (cycles < best_cycles) {
@@ -969,17 +979,18 @@ int64_t most_row_tiles(int N, int E, int mblocks, int rows) {
   return (static_cast<int64_t>(std::min(N, E)) + N / rows) * mblocks;
 }
 
-Cut cut_rows(const DeviceInfo& dev, const int32_t* offsets, int N, int E, int mblocks, int K) {
+Cut cut_rows(const DeviceInfo& dev, Form form, const int32_t* offsets, int N, int E, int mblocks,
+             int K) {
   const int all = (std::min(N, kTileRows) + 31) & ~31;
   if (offsets == nullptr)  // tiles of one size, as the kernel cuts them
-    return cut(dev, ceil_div(K, kBlockK), all, kMaxParts, [&](int rows) {
+    return cut(dev, form, E, ceil_div(K, kBlockK), all, kMaxParts, [&](int rows) {
       return static_cast<int64_t>(ceil_div(N, rows)) * mblocks;
     });
   // The experts' counts are not known here: full tiles, and several pairs per sum where
   // even the most tiles that there can be leave pairs idle.
   Cut c{all, 1, most_row_tiles(N, E, mblocks, all)};
   for (int parts = 2; parts <= kMaxParts && parts <= ceil_div(K, kBlockK); ++parts)
-    if (c.tiles <= resident(dev, parts) && sums_fit(parts, all, stages_of(all))) c.parts = parts;
+    if (c.tiles <= resident(dev, parts) && sums_fit(form, parts, all, E, dev)) c.parts = parts;
   return c;
 }
 
@@ -989,13 +1000,11 @@ cudaError_t launch(Kernel kernel, Form form, const CUtensorMap& a_map, const Map
   p.turn = turn_bytes(form, p.saved_kind);
   p.tile_rows = c.tile_rows;
   p.parts = c.parts;
-  p.stage_bytes = form == kWeights ? 2 * kOperandBytes : stage_bytes(c.tile_rows);
-  // As many stages as fit beside the chunks, the experts' table and static shared memory.
-  const int rest = dev.max_smem_optin - 1024 - 1024 - kGroups * p.turn - experts_table_bytes(p.E);
-  p.stages = std::min(kMaxStages, rest / p.stage_bytes);
+  const Ring ring = ring_of(form, p.saved_kind, c.tile_rows, p.E, dev);
+  p.stages = ring.stages;
+  p.stage_bytes = ring.stage_bytes;
   const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + kGroups * p.turn +
                       experts_table_bytes(p.E);
-  if (!sums_fit(p.parts, p.tile_rows, p.stages)) p.parts = 1;  // (a wide table of experts)
   const int clusters = static_cast<int>(
       p.parts > 1 ? c.tiles : std::min<int64_t>(std::max(1, resident(dev, 1)), c.tiles));
   return launch_dependent_clusters(2 * p.parts, kernel, dim3(2 * p.parts * clusters),
@@ -1101,7 +1110,7 @@ cudaError_t launch_expert_gated(const ExpertGatedArgs& a, const DeviceInfo& dev,
   p.saved_kind = a.saved_kind;
   p.ring = a.ring;
   p.whole_a = p.whole_b = whole(a.C);
-  const Cut c = cut_rows(dev, a.offsets, a.N, a.E, p.mblocks, a.C);
+  const Cut c = cut_rows(dev, kGated, a.offsets, a.N, a.E, p.mblocks, a.C);
   CUtensorMap w_map;
   Maps x_maps{};
   if (!gated_map(&w_map, a.weights, a.E, a.F, a.C) ||
@@ -1125,14 +1134,14 @@ cudaError_t launch_expert_rows(const ExpertRowsArgs& a, const DeviceInfo& dev,
   p.ring = a.ring;
   p.whole_a = whole(a.transposed ? a.M : a.K);
   p.whole_b = whole(a.K);
-  const Cut c = cut_rows(dev, a.offsets, a.N, a.E, p.mblocks, a.K);
+  const Form form = a.transposed ? kRowsT : kRows;
+  const Cut c = cut_rows(dev, form, a.offsets, a.N, a.E, p.mblocks, a.K);
   CUtensorMap w_map;
   Maps x_maps{};
   if (!(a.transposed ? matrices_map(&w_map, a.weights, a.E, a.K, a.M)
                      : matrices_map(&w_map, a.weights, a.E, a.M, a.K)) ||
       !rows_maps(&x_maps, a.x, a.N, a.K, c.tile_rows))
     return cudaErrorInvalidValue;
-  const Form form = a.transposed ? kRowsT : kRows;
   return launch(kKernels[a.transposed ? 3 : 2], form, w_map, x_maps, p, c, dev,
                 stream);
 }
@@ -1149,9 +1158,10 @@ cudaError_t launch_expert_weights(const ExpertWeightsArgs& a, const DeviceInfo& 
   p.mblocks = ceil_div(a.M, 256);
   const int mean = ceil_div(a.N, a.E);
   const int most_parts = a.offsets == nullptr ? kMaxParts : 1;  // (of blocks known here)
-  const Cut c = cut(dev, ceil_div(mean, kBlockK), (a.C + 31) & ~31, most_parts, [&](int cols) {
-    return static_cast<int64_t>(a.E) * p.mblocks * ceil_div(a.C, cols);
-  });
+  const Cut c = cut(dev, kWeights, a.E, ceil_div(mean, kBlockK), (a.C + 31) & ~31, most_parts,
+                    [&](int cols) {
+                      return static_cast<int64_t>(a.E) * p.mblocks * ceil_div(a.C, cols);
+                    });
   p.cblocks = ceil_div(a.C, c.tile_rows);
   p.ring = a.ring;
   p.whole_a = whole(a.M);

@@ -58,3 +58,14 @@ def test_gradient_where_the_gate_is_off_and_the_rest_is_large(act, save):
     got = gx.double()
     assert torch.isfinite(got[ok]).all()
     assert ((got - want).abs() <= bound + br.UBF * (want.abs() + bound))[ok].all()
+
+
+@pytest.mark.parametrize("N,M,C", [(65536, 512, 768), (65536, 256, 1920), (16377, 3840, 120)])
+def test_sums_over_many_rows_that_four_pairs_share(N, M, C):
+    """Integers whose sums stay below 2^24: exact, whatever the order."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(N + M)
+    x, dy = (torch.randint(-3, 4, (N, n), generator=g, device="cuda").to(BF16) for n in (C, M))
+    _, gw = lt.expert_matmul_backward(dy, x, None)
+    latent_tail_check()
+    assert torch.equal(gw[0], (dy.double().t() @ x.double()).to(BF16))
