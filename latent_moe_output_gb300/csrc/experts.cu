@@ -935,12 +935,17 @@ struct Ring {
   int stages, stage_bytes;
 };
 
-// As many stages as fit beside the chunks, the experts' table and static shared memory.
+// More than the kernels' static shared memory (setup_experts would fail with less).
+constexpr int kStaticBytes = 512;
+
+// As many stages as fit beside the chunks, the experts' table and static shared memory: of
+// 64 KB three, but two where a gated block keeps its projections in bf16 for more than 297
+// experts.
 Ring ring_of(Form form, int saved_kind, int rows, int E, const DeviceInfo& dev) {
   const int bytes = form == kWeights
                         ? static_cast<int>(2 * kOperandBytes)
                         : static_cast<int>(kOperandBytes) + (rows / 2 + 31) / 32 * 8192;
-  const int rest = dev.max_smem_optin - 1024 - 1024 - kGroups * turn_bytes(form, saved_kind) -
+  const int rest = dev.max_smem_optin - kStaticBytes - 1024 - kGroups * turn_bytes(form, saved_kind) -
                    experts_table_bytes(E);
   return Ring{std::min(kMaxStages, rest / bytes), bytes};
 }
@@ -1069,7 +1074,7 @@ cudaError_t setup_experts(const DeviceInfo& dev) {
   for (Kernel k : kKernels) {
     const cudaError_t e = cudaFuncSetAttribute(
         reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
-        dev.max_smem_optin - 1024);
+        dev.max_smem_optin - kStaticBytes);
     if (e != cudaSuccess) return e;
   }
   // (clusters of several pairs do not always fill every SM: the parts of the GPU that a
@@ -1083,7 +1088,7 @@ cudaError_t setup_experts(const DeviceInfo& dev) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms) / ctas * ctas);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(dev.max_smem_optin) - 1024;
+    cfg.dynamicSmemBytes = static_cast<size_t>(dev.max_smem_optin) - kStaticBytes;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;

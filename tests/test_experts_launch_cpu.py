@@ -112,3 +112,12 @@ def test_what_is_kept_does_not_change_the_order_of_a_sum(run, N, F, C):
     """The same pairs per sum whether projections are kept or not."""
     launches = run(*(f"gated,{N},1,{F},{C},{kind}" for kind in range(3)))
     assert len({launch[:2] for launch in launches}) == 1 and launches[0][1] > 2
+
+
+@pytest.mark.parametrize("E,stages", [(1, 3), (254, 3), (256, 3), (297, 3), (298, 2), (1024, 2)])
+def test_stages_beside_what_is_kept(run, E, stages):
+    """64 KB per stage beside the chunk buffers of projections kept in bf16 and the table."""
+    _, _, _, smem = run(f"gated,65536,{E},1024,2048,1")[0]
+    table = ((E + 1) * 12 + 15) // 16 * 16
+    assert smem == 1024 + stages * 65536 + 2 * 15360 + table
+    assert smem + 512 <= 232448
