@@ -87,7 +87,7 @@ class _ExpertFFN(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, up, down, offsets, activation, save):
         N, F = x.shape[0], up.shape[1] // 2
-        grads = any(ctx.needs_input_grad[:3])
+        grads = save is not None and any(ctx.needs_input_grad[:3])
         kept = None
         if grads:
             kept = torch.empty(N, 2, F, dtype=torch.bfloat16, device=x.device) \
@@ -138,10 +138,13 @@ def expert_ffn(x, up, down, offsets=None, activation: str = "silu", save: str = 
 
     ``save`` says what the backward pass reads: "bf16" keeps x and both projections in
     bf16, "8bit" the projections in 8 bits, "all8bit" x too (per row 2C + 4F, 2C + 2.13F
-    and 1.06C + 2.13F bytes). The product of the block is computed again from them."""
+    and 1.06C + 2.13F bytes). The product of the block is computed again from them. Nothing
+    is kept where gradients are off (``torch.no_grad``, ``torch.inference_mode``)."""
     if save not in _SAVE:
         raise ValueError(f"save: expected one of {_SAVE}, got {save!r}")
-    return _ExpertFFN.apply(x, up, down, offsets, activation, save)
+    # (within the function gradients are always off, and needs_input_grad goes by the tensors)
+    return _ExpertFFN.apply(x, up, down, offsets, activation,
+                            save if torch.is_grad_enabled() else None)
 
 
 def dispatch_rows(x, expert_ids, E: int) -> _block.Dispatched:

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import latent_moe_output_gb300 as lt
+from latent_moe_output_gb300 import autograd as lta
 from latent_moe_output_gb300.binding import latent_tail_check
 
 import block_reference as br
@@ -69,3 +70,43 @@ def test_sums_over_many_rows_that_four_pairs_share(N, M, C):
     _, gw = lt.expert_matmul_backward(dy, x, None)
     latent_tail_check()
     assert torch.equal(gw[0], (dy.double().t() @ x.double()).to(BF16))
+
+
+# --------------------------------------------------------------- under autograd
+def ffn_leaves(N, C, F, M, E, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    new = lambda *s, scale=1.0: (torch.randn(*s, generator=g, device="cuda") * scale).to(  # noqa: E731
+        BF16).requires_grad_(True)
+    return (new(N, C), new(E, 2 * F, C, scale=C ** -0.5), new(E, M, F, scale=F ** -0.5),
+            torch.randn(N, M, generator=g, device="cuda").to(BF16))
+
+
+@pytest.mark.parametrize("save", ["bf16", "8bit", "all8bit"])
+def test_an_evaluation_pass_takes_no_memory_for_a_backward_pass(save):
+    N, C, F, M = 4096, 256, 512, 256
+    x, up, down, _ = ffn_leaves(N, C, F, M, 1, seed=1)
+    want = lta.expert_ffn(x, up, down, save=save).detach()
+    for mode in (torch.no_grad, torch.inference_mode):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        with mode():
+            out = lta.expert_ffn(x, up, down, save=save)
+        torch.cuda.synchronize()
+        # hidden and out, in the allocator's pieces of 2 MB at most
+        assert torch.cuda.max_memory_allocated() - before <= 2 * N * (F + M) + (4 << 20)
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_under_activation_checkpointing(reentrant):
+    """The first pass, without gradients in the one form, gives the same bits."""
+    from torch.utils.checkpoint import checkpoint
+
+    a, b = (ffn_leaves(300, 136, 72, 200, 1, seed=2) for _ in range(2))
+    lta.expert_ffn(*a[:3], save="8bit").backward(a[3])
+    out = checkpoint(lambda *t: lta.expert_ffn(*t, save="8bit"), *b[:3], use_reentrant=reentrant)
+    out.backward(b[3])
+    for s, t in zip(a[:3], b[:3]):
+        assert torch.equal(s.grad, t.grad)
