@@ -90,13 +90,14 @@ class DecodeBlock:
                                 residual_out=residual, next_out=self.next)
 
 
-def train_step(weights, x, expert_ids, expert_weights, shared, residual, residual_scale=1.0):
-    """The block with bf16 experts, their projections kept in 8 bits, under autograd (the
-    tail in torch operations: its kernels have no backward pass). Returns (residual, next
-    input)."""
+def train_step(weights, x, expert_ids, expert_weights, shared, residual, residual_scale=1.0,
+               save="bf16"):
+    """The block with bf16 experts under autograd (the tail in torch operations: its kernels
+    have no backward pass). ``save``: what the experts keep for the backward pass, as for
+    ``autograd.expert_ffn``. Returns (residual, next input)."""
     w = weights
     d = lta.dispatch_rows(x, expert_ids, w["up"].shape[0])
-    rows = lta.expert_ffn(d.rows, w["up"], w["down"], d.offsets)
+    rows = lta.expert_ffn(d.rows, w["up"], w["down"], d.offsets, save=save)
     routed = lta.combine_rows(rows, d.position, expert_weights).float()
     latent = routed * torch.rsqrt(routed.square().mean(-1, keepdim=True) + EPS) * w["latent_norm"]
     out = latent.to(torch.bfloat16) @ w["W"].t() + shared

@@ -131,14 +131,17 @@ class _ExpertFFN(torch.autograd.Function):
         return grad_x, grad_up, grad_down, None, None, None
 
 
-def expert_ffn(x, up, down, offsets=None, activation: str = "silu", save: str = "8bit"):
+def expert_ffn(x, up, down, offsets=None, activation: str = "silu", save: str = "bf16"):
     """A gated feed-forward block for rows sorted by expert (or, without ``offsets``, one
     dense block): ``expert_matmul(expert_gated(x, up), down)`` with gradients for x [N, C],
     up [E, 2F, C] and down [E, M, F].
 
     ``save`` says what the backward pass reads: "bf16" keeps x and both projections in
     bf16, "8bit" the projections in 8 bits, "all8bit" x too (per row 2C + 4F, 2C + 2.13F
-    and 1.06C + 2.13F bytes). The product of the block is computed again from them. Nothing
+    and 1.06C + 2.13F bytes). The product of the block is computed again from them for the
+    gradient of down: from 8 bits it is not quite the product that went forward. Error of the
+    gradients of x, up and down for normal values, as a share of their norms: 0.34, 0.34 and
+    0.35 % with "bf16", 0.9, 0.9 and 1.1 % with "8bit", 0.9, 1.2 and 1.1 % with "all8bit". Nothing
     is kept where gradients are off (``torch.no_grad``, ``torch.inference_mode``)."""
     if save not in _SAVE:
         raise ValueError(f"save: expected one of {_SAVE}, got {save!r}")

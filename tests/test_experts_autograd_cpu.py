@@ -64,3 +64,33 @@ def test_what_is_kept_for_a_backward_pass(calls, mode, save, kind, quantized):
         out = lta.expert_ffn(*tensors(True, True, True), save=save)
     assert out.requires_grad
     assert isinstance(calls.saved[0], kind) and calls.quantized == quantized
+
+
+def test_bits_are_given_up_only_where_the_caller_says_so(calls):
+    lta.expert_ffn(*tensors(True, True, True))
+    assert calls.saved[0].dtype == torch.bfloat16 and calls.quantized == 0
+
+
+def test_the_training_example_keeps_bf16_unless_told_otherwise(calls, monkeypatch):
+    """(its other operators replaced by ones that pass their input on)"""
+    import importlib.util
+    from pathlib import Path
+
+    spec = importlib.util.spec_from_file_location(
+        "latent_moe_block_cpu",
+        Path(__file__).resolve().parents[1] / "examples" / "latent_moe_block.py")
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    monkeypatch.setattr(lta, "dispatch_rows",
+                        lambda x, ids, E: types.SimpleNamespace(rows=x, offsets=None, position=ids))
+    monkeypatch.setattr(lta, "combine_rows", lambda rows, position, weights: rows)
+    monkeypatch.setattr(lta, "residual_norm",
+                        lambda out, residual, post, nxt, eps, gate, residual_scale: (out, out))
+    x, up, down = tensors(True, True, True)
+    w = dict(up=up, down=down, latent_norm=torch.ones(24), post=None, next=None, gate=None,
+             W=torch.ones(40, 24, dtype=torch.bfloat16))
+    args = (w, x, None, None, torch.zeros(4, 40, dtype=torch.bfloat16), None)
+    example.train_step(*args)
+    example.train_step(*args, save="8bit")
+    assert isinstance(calls.saved[0], torch.Tensor) and calls.saved[0].dtype == torch.bfloat16
+    assert isinstance(calls.saved[1], tuple)
