@@ -474,10 +474,13 @@ LT_API lt_status latent_tail_selftest_residual_norm_backward_timeout(
  * as the shared expert. In all of them
  *   offsets [E+1] int32 (rows of expert e: offsets[e] .. offsets[e+1]-1) or NULL with
  *   E == 1 (every row). Offsets are cut to [0, N] and to their running maximum; rows
- *   that no expert owns give zeros, and experts without rows zero gradients.
+ *   that no expert owns give zeros, and experts without rows zero gradients. For some
+ *   of the experts of a dispatch offsets may point into its array, at a multiple of
+ *   four experts (16-byte alignment, as for every pointer).
  * Sums are FP32 on the tensor cores, results are rounded once to bf16; the order of a
- * sum, and with it the last bits of a result, depends on the sizes (N, E, F or M, C)
- * alone, not on the offsets.
+ * sum, and with it the last bits of a result, depends on the sizes (N, E, F or M, C),
+ * on whether offsets are given and on the device, not on the offsets themselves nor on
+ * what is kept.
  * Limits: 0 <= N <= 2^24, 1 <= E <= 1024, C, M and 2F multiples of 8 from 8 to 65536
  * (F a multiple of 8).
  * With N == 0 the gradients of weights are zeros.
@@ -601,7 +604,10 @@ LT_API lt_status latent_tail_selftest_expert_matmul_backward_timeout(
  * so that a value is off by at most 1/127 of its group's largest magnitude (half a unit;
  * the largest magnitude is at least 63.5 units). Groups below 2^-126 * 63.5 round to that
  * power of two. (Where the values are FP32, as in latent_tail_expert_gated, magnitudes
- * below 2^-133 count as zeros.)
+ * below 2^-133 count as zeros.) At the other end, in a group whose largest magnitude is at
+ * least 127.5 * 2^121 (of bf16 values its largest alone, 255/128 * 2^127), magnitudes from
+ * 63.5 * 2^122 on (that one and the one below) round to 64 * 2^122 = 2^128, which reads back
+ * as an infinity.
  *   x [T, C] bf16; values [T, C], exponents [T, ceil(C/16)].
  * Limits: 0 <= T <= 2^24, C a multiple of 8 from 8 to 65536.
  */
@@ -611,8 +617,8 @@ LT_API lt_status latent_tail_quantize8(const uint16_t* x, int8_t* values, uint8_
 /*
  * out[t,c] = values[t,c] * 2^(exponents[t,g]-127) in bf16, which holds it exactly (values
  * of -128, which latent_tail_quantize8 does not write, too); zeros for exponent 0 and NaNs
- * for 255. Products past bf16's range, which latent_tail_quantize8 does not write either,
- * give infinities.
+ * for 255. Products past bf16's range give infinities (latent_tail_quantize8 writes them
+ * for the largest magnitudes alone, as above).
  */
 LT_API lt_status latent_tail_dequantize8(const int8_t* values, const uint8_t* exponents,
                                          uint16_t* out, int T, int C, lt_stream stream);

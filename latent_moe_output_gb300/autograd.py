@@ -141,8 +141,8 @@ def expert_ffn(x, up, down, offsets=None, activation: str = "silu", save: str = 
     and 1.06C + 2.13F bytes). The product of the block is computed again from them for the
     gradient of down: from 8 bits it is not quite the product that went forward. Error of the
     gradients of x, up and down for normal values, as a share of their norms: 0.34, 0.34 and
-    0.35 % with "bf16", 0.9, 0.9 and 1.1 % with "8bit", 0.9, 1.2 and 1.1 % with "all8bit". Nothing
-    is kept where gradients are off (``torch.no_grad``, ``torch.inference_mode``)."""
+    0.35 % with "bf16", 0.9, 0.9 and 1.1 % with "8bit", 0.9, 1.2 and 1.1 % with "all8bit".
+    Nothing is kept where gradients are off (``torch.no_grad``, ``torch.inference_mode``)."""
     if save not in _SAVE:
         raise ValueError(f"save: expected one of {_SAVE}, got {save!r}")
     # (within the function gradients are always off, and needs_input_grad goes by the tensors)

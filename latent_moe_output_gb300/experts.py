@@ -30,7 +30,8 @@ GROUP8 = 16  # columns that share an exponent
 class Checkpoint8(NamedTuple):
     """Activations in 8 bits: ``values * 2 ** (exponents - 127)``, one exponent per 16
     columns of the last dimension. Exponent 0 is a group of zeros, 255 one that held an
-    infinity or a NaN (read back as NaNs). See latent_tail_quantize8."""
+    infinity or a NaN (read back as NaNs). bf16's two largest magnitudes read back as
+    infinities in a group that holds the largest. See latent_tail_quantize8."""
 
     values: torch.Tensor     # [..., C] int8
     exponents: torch.Tensor  # [..., ceil(C / 16)] uint8
@@ -70,8 +71,9 @@ def _saved(saved, N, F, i):
 def expert_gated(x, weights, offsets=None, activation="silu", hidden=None, saved=None,
                  stream=None):
     """hidden[r] = a(g) * u with g = weights[e, :F] @ x[r] and u = weights[e, F:] @ x[r] for
-    the rows r of expert e (``offsets`` of ``dispatch``, or of some of its experts; None
-    with one matrix: every row); zeros for rows that no expert owns.
+    the rows r of expert e (``offsets`` of ``dispatch``, or of some of its experts: a slice
+    that begins at a multiple of four experts, or a copy of another, for the alignment to 16
+    bytes; None with one matrix: every row); zeros for rows that no expert owns.
 
     x [N, C] bf16, weights [E, 2F, C] bf16, activation "silu" or "gelu" (its tanh form).
     ``saved`` takes g and u for the backward pass: a bf16 tensor [N, 2, F], or

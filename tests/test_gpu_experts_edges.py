@@ -5,7 +5,7 @@ import torch
 
 import latent_moe_output_gb300 as lt
 from latent_moe_output_gb300 import autograd as lta
-from latent_moe_output_gb300.binding import latent_tail_check
+from latent_moe_output_gb300.binding import LatentTailError, Status, latent_tail_check
 
 import block_reference as br
 import experts_reference as er
@@ -110,3 +110,61 @@ def test_under_activation_checkpointing(reentrant):
     out.backward(b[3])
     for s, t in zip(a[:3], b[:3]):
         assert torch.equal(s.grad, t.grad)
+
+
+# ------------------------------------------------------ what the documentation says
+def test_offsets_of_some_experts():
+    """Experts 4 to 7 of a dispatch by a slice of its offsets, and 3 to 6 by a copy of one: the
+    other experts' rows are zeros, and the slice that is not aligned is refused."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    counts = [5, 0, 9, 30, 2, 17, 0, 40, 11]
+    offsets = torch.tensor([sum(counts[:i]) for i in range(10)], dtype=torch.int32, device="cuda")
+    N, M, C = sum(counts), 72, 136
+    x = torch.randint(-3, 4, (N, C), generator=g, device="cuda").to(BF16)
+    w = torch.randint(-3, 4, (9, M, C), generator=g, device="cuda").to(BF16)
+    whole = lt.expert_matmul(x, w, offsets)
+    for first, of in ((4, offsets[4:9]), (3, offsets[3:8].clone())):
+        a, b = sum(counts[:first]), sum(counts[:first + 4])
+        out = lt.expert_matmul(x, w[first:first + 4], of)
+        assert torch.equal(out[a:b], whole[a:b])
+        assert not out[:a].any() and not out[b:].any()
+    with pytest.raises(LatentTailError) as e:
+        lt.expert_matmul(x, w[3:7], offsets[3:8])
+    assert e.value.status == Status.ALIGNMENT
+
+
+def test_bits_do_not_depend_on_the_offsets_or_on_what_is_kept():
+    """The same rows and weights with other offsets around them, kept or not."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    N, E, F, C = 700, 3, 136, 712
+    x = torch.randn(N, C, generator=g, device="cuda").to(BF16)
+    w = (torch.randn(1, 2 * F, C, generator=g, device="cuda") * C ** -0.5).to(BF16)
+    w = w.expand(E, 2 * F, C).contiguous()
+    want = None
+    for cuts in ((0, 700, 700, 700), (0, 1, 690, 700), (0, 0, 350, 700), (0, 256, 512, 700)):
+        offsets = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+        for saved in (None, torch.empty(N, 2, F, dtype=BF16, device="cuda"),
+                      lt.Checkpoint8.empty(N, 2, F)):
+            hidden = lt.expert_gated(x, w, offsets, saved=saved)
+            want = hidden if want is None else want
+            assert torch.equal(hidden, want)
+
+
+def test_largest_values_in_8_bits():
+    """255/128 * 2^127 and the value below it, beside the largest, round to 64 units of 2^122:
+    infinities when read back, as documented; everything below them is finite."""
+    top = torch.tensor([0x7F7F, 0x7F7E, 0x7F7D, 0x7F00, 0x3F80], dtype=torch.int16).view(BF16)
+    x = torch.zeros(2, 16, dtype=BF16)
+    x[0, :5], x[1, 0], x[1, 1:4] = top, -top[1], top[2:]  # (with the largest, and without)
+    kept = lt.quantize8(x.cuda())
+    back = lt.dequantize8(kept).cpu()
+    inf = float("inf")
+    assert kept.exponents.tolist() == [[249], [248]]
+    assert kept.values[0, :5].tolist() == [64, 64, 63, 32, 0]
+    assert kept.values[1, :4].tolist() == [-127, 126, 64, 0]  # (126.5 units: to the even one)
+    assert back[0, :5].tolist()[:2] == [inf, inf] and torch.isfinite(back[0, 2:]).all()
+    assert torch.isfinite(back[1]).all()
+    q, e = er.quantize8(x.double())
+    assert torch.equal(kept.values.cpu(), q) and torch.equal(kept.exponents.cpu(), e)
