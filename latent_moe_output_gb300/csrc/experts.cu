@@ -923,7 +923,10 @@ struct Cut {
 // 128 and 64 rows 16.6, 13.0 and 16.2; 128 rows of 7168, 2 x 2048 weight rows, one to three
 // pairs per sum 28.9, 22.7 and 21.5; 64 rows of them 23.3, 18.4 and 17.8). A block of 128
 // columns takes about its MMAs' time, four cycles a row, and no less than the weights need
-// to come in.
+// to come in. It counts neither the bytes of narrower tiles, nor rows that span one line more
+// for their pitch, nor a tile's stores, and is too low where these bind: both products of the
+// gradient of 777 rows (5128 columns, F = 1000) take 22 us each, by this 13; a tile of the
+// weights' gradient of 60 experts of 91 rows 7300 cycles, by this 2800.
 int64_t tile_cycles(int blocks, int rows, int parts) {
   const int64_t block = std::max<int64_t>(570, 240 + 21 * rows / 5);
   return ceil_div(blocks, parts) * block + 1500 +
@@ -945,8 +948,8 @@ Ring ring_of(Form form, int saved_kind, int rows, int E, const DeviceInfo& dev) 
   const int bytes = form == kWeights
                         ? static_cast<int>(2 * kOperandBytes)
                         : static_cast<int>(kOperandBytes) + (rows / 2 + 31) / 32 * 8192;
-  const int rest = dev.max_smem_optin - kStaticBytes - 1024 - kGroups * turn_bytes(form, saved_kind) -
-                   experts_table_bytes(E);
+  const int rest = dev.max_smem_optin - kStaticBytes - 1024 -
+                   kGroups * turn_bytes(form, saved_kind) - experts_table_bytes(E);
   return Ring{std::min(kMaxStages, rest / bytes), bytes};
 }
 

@@ -104,6 +104,7 @@ constexpr int experts_table_bytes(int E) { return ((E + 1) * 12 + 15) & ~15; }
 // Both activations are g * sigmoid(s(g)): SiLU with s = g, the tanh form of GELU with
 // s = sqrt(8 / pi) (g + 0.044715 g^3), as 0.5 (1 + tanh(y)) = sigmoid(2 y). The cubic
 // takes g cut to +-32, where the sigmoid is 0 or 1 in FP32, so that it cannot overflow.
+// (The division gives 0 for denominators past 2^126, where the sigmoid is below 2^-126.)
 __device__ __forceinline__ float sigmoid(float s) {
   return __fdividef(1.f, 1.f + __expf(-s));
 }

@@ -11,6 +11,7 @@
 // long as both operands agree, so the eight columns of a lane are its columns of two
 // fragments, and no shuffle or shared memory lies between a load and its product. In the
 // gated form fragment row g is a gate row and g + 8 the up row of the same feature.
+// Two fragments of rows take all 128 registers that 512 threads leave, and spill one or two.
 // Measured: one row of 7168 against 2 x 2048 weight rows 11.6 us, 75 % of a copy's rate (one
 // wave of 128 CTAs, 2 to 3 us of it to begin and end); half as many loads in flight per lane
 // 16.0, an L2 prefetch of the weights before the wait for the kernel before 13.7 against 12.5

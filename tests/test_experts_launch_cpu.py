@@ -68,7 +68,7 @@ for call in sys.argv[2:]:
     print(int(st))
 """
 
-BOX = (76, 36, 23, 15)  # a GB300's: clusters of 2, 4, 6 and 8 CTAs that are resident at once
+RESIDENT = (76, 36, 23, 15)  # a GB300's: clusters of 2, 4, 6 and 8 CTAs that are resident at once
 
 
 @pytest.fixture(scope="module")
@@ -79,10 +79,10 @@ def run(tmp_path_factory):
     where = tmp_path_factory.mktemp("runtime")
     (where / "fake.c").write_text(FAKE_RUNTIME)
     fake = where / "fake.so"
-    subprocess.run(["gcc", "-shared", "-fPIC", f"-I{build.cuda_home() / 'include'}", "-o", str(fake),
-                    str(where / "fake.c")], check=True)
+    subprocess.run(["gcc", "-shared", "-fPIC", f"-I{build.cuda_home() / 'include'}", "-o",
+                    str(fake), str(where / "fake.c")], check=True)
 
-    def child(*calls, clusters=BOX):
+    def child(*calls, clusters=RESIDENT):
         """(grid, cluster, block, shared memory) of each launch"""
         env = dict(os.environ, LD_PRELOAD=str(fake),
                    **{f"CLUSTERS{2 * (i + 1)}": str(n) for i, n in enumerate(clusters)})
@@ -102,7 +102,7 @@ def run(tmp_path_factory):
 def test_a_sum_over_many_rows_is_shared_as_it_was_cut(run, N, M, C, tiles, resident4):
     """Tiles of 256 x 128, each shared by four pairs: the ring holds the three other pairs'
     sums, 3 * 128 * 512 bytes, in its three stages of 64 KB."""
-    grid, cluster, _, smem = run(f"weights,{N},{M},{C}", clusters=BOX[:3] + (resident4,))[0]
+    grid, cluster, _, smem = run(f"weights,{N},{M},{C}", clusters=RESIDENT[:3] + (resident4,))[0]
     assert (cluster, grid) == (8, tiles * 8)
     assert smem >= 3 * 128 * 512
 
